@@ -98,7 +98,9 @@ typedef enum {
   SPEC_ERR_UNSUPPORTED = 3
 } spec_status;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* SPEC_F16 is a type of key-value caches (spec_paged_attention, spec_cache_*);
+ * logits are float32 or bfloat16. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
 
 /* Per-sequence (or per-tree) policy arrays, device memory.
  *   temperature [B]: 0 -> greedy; > 0 -> softmax(z / T); NaN, < 0 or inf ->
@@ -143,7 +145,15 @@ typedef struct {
                                             drafts, every token -1; on the tree walk
                                             path the tree: 0 accepted nodes, every
                                             path entry and token -1 */
-#define SPEC_FLAG_BAD_TREE 64u           /* parent[0] != -1 or parent[n] not in [0, n) */
+#define SPEC_FLAG_BAD_TREE 64u           /* parent[0] != -1 or parent[n] not in [0, n);
+                                            a path that does not ascend from the root */
+#define SPEC_FLAG_BAD_PAGE 128u          /* a page id outside the cache, or a page given
+                                            back more often than it was taken */
+#define SPEC_FLAG_BAD_LENGTH 256u        /* tokens that do not fit the page table's row,
+                                            or a count outside its range */
+#define SPEC_FLAG_NO_PAGES 512u          /* the pool has too few free pages */
+#define SPEC_FLAG_BAD_SEQUENCE 1024u     /* a fork's source or target that is no
+                                            sequence, or a target that is not empty */
 
 /* Bytes of workspace spec_verify_chain needs for B sequences of gamma drafts
  * (0 for a negative size, V < 1 or an unknown dtype). */
@@ -407,6 +417,182 @@ spec_status spec_typical_accept(
 spec_status spec_tree_rerank(const int32_t *parent, const float *confidence, int T, int N, int m,
                              int32_t *out_nodes, int32_t *out_parent, float *out_value,
                              int32_t *out_count, uint32_t *out_flags, spec_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged key-value cache around a verification: attention of the new tokens
+ * (one, a chain of drafts or a tree of them) over the cache's pages, and the
+ * upkeep of the pages.  wineandchord.com "推测解码：接受规则、状态与收益边界"
+ * asks that the accepted prefix is committed and the rest of the state rolled
+ * back; these entry points do that to the cache on the device, from the
+ * outputs of spec_verify_chain and spec_verify_tree.
+ *
+ * A step of a decode loop: spec_cache_resize (pages for the new tokens); in
+ * each layer spec_cache_append and spec_paged_attention (with the words of
+ * spec_tree_mask); spec_verify_tree; spec_cache_compact; spec_cache_resize
+ * (pages behind the accepted path given back).
+ * ------------------------------------------------------------------------- */
+
+/* Keys and values of num_layers layers in num_pages pages of page_size tokens.
+ * Element (layer, page, token, head, d) of the keys is at
+ * k + layer*k_layer_stride + page*k_page_stride + token*k_token_stride +
+ * head*k_head_stride + d (strides in elements, offsets in 64 bits); the values
+ * alike.  Any order of the strided dimensions is taken ([page, token, head, d]
+ * or [page, head, token, d], keys and values interleaved).
+ * dtype: SPEC_F32, SPEC_BF16 or SPEC_F16.  head_dim: a multiple of 16 bytes, at
+ * most 256 elements.  page_size: 1..65536, not only powers of two.  k, v and
+ * every stride of a dimension larger than one are multiples of 16 bytes, and no
+ * such stride is shorter than head_dim; otherwise SPEC_ERR_UNSUPPORTED. */
+typedef struct {
+  void *k, *v;
+  int64_t k_layer_stride, k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_layer_stride, v_page_stride, v_token_stride, v_head_stride;
+  spec_dtype dtype;
+  int num_layers, num_pages, page_size, num_heads, head_dim;
+} spec_kv_cache;
+
+/* The page tables of B sequences: entry i of sequence b, at table[b*ld + i], is
+ * the page of its tokens i*page_size .. (i+1)*page_size - 1.  Only entries of
+ * tokens that are read or written are looked at.  max_pages >= 1, ld >=
+ * max_pages, max_pages * page_size < 2^31 - 8192. */
+typedef struct {
+  const int32_t *table;
+  int64_t ld;
+  int max_pages;
+} spec_page_table;
+
+/* Bytes of workspace spec_paged_attention needs: partial results of key ranges
+ * that are split over thread blocks.  Does not depend on the lengths.  0 for
+ * sizes that spec_paged_attention refuses. */
+size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int num_kv_heads,
+                                           int head_dim, spec_dtype dtype);
+
+/* Attention of N new tokens of each of B sequences over their pages, which
+ * already hold the new tokens' keys and values (spec_cache_append):
+ *   out[b,n,h] = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q[b,n,h] . k_j),
+ * over the keys j that token n sees, with head h / (num_q_heads / num_heads) of
+ * the cache.  Sequence b has context_len[b] tokens before the new ones; new
+ * token m is at place context_len[b] + m of the page table.  Token n sees
+ *   - every context token, and
+ *   - new token m iff bit m of its tree_mask row is set, or m <= n without one.
+ * window > 0: of those, only keys with place(token n) - place(key) < window or
+ * place(key) < sinks; the place of a context token is its index, that of new
+ * token m is context_len[b] + position[b,m] (its depth; without position: m).
+ * A token that sees no key has out 0 and out_lse -infinity.  Keys and values
+ * that a token does not see do not affect it, whatever they hold.
+ *
+ * q [B, N, num_q_heads, head_dim] of the cache's dtype, strides in elements,
+ *    16-byte aligned as the cache.  num_q_heads: a multiple of cache.num_heads.
+ * cache: num_layers 1.  context_len [B]: >= 0.
+ * num_new [B] (nullable): sequence b has only num_new[b] <= N new tokens (0: it
+ *    is left out); out and out_lse of the others are not written.
+ * tree_mask (nullable) [B, N, (N+63)/64] words as spec_tree_mask writes them,
+ *    sequence b at b*mask_seq_stride words (0: one tree for all).
+ * position (nullable) [B, N], sequence b at b*position_seq_stride; read with a
+ *    window only; values are clamped into [0, N).  Required with window and
+ *    tree_mask.
+ * scale: finite, > 0.  window <= 0: off.  sinks >= 0.
+ * out [B, N, num_q_heads, head_dim] of the cache's dtype, contiguous, 16-byte
+ *    aligned.  out_lse (nullable) float [B, N, num_q_heads]: ln sum_j w_j.
+ * out_flags [B] (nullable): SPEC_FLAG_BAD_LENGTH (num_new outside [0, N], taken
+ *    as clamped; or a sequence whose tokens do not fit its table row: its
+ *    tokens see nothing), SPEC_FLAG_BAD_PAGE (its keys are not seen).  Costs a
+ *    launch of its own.
+ * Products of bf16 and f16 run on the tensor cores with float32 sums; the
+ * weights are rounded to the cache's type before they meet the values.  float32
+ * caches are computed in float32.  1 <= N <= 4096.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (a head_dim, alignment or
+ * stride not listed above) before any launch.  B = 0 is a no-op.  Two launches. */
+spec_status spec_paged_attention(
+    const void *q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, spec_kv_cache cache, spec_page_table pages, const int32_t *context_len,
+    const int32_t *num_new, int B, int N, const uint64_t *tree_mask, int64_t mask_seq_stride,
+    const int32_t *position, int64_t position_seq_stride, float scale, int window, int sinks,
+    void *out, float *out_lse, uint32_t *out_flags, void *workspace, size_t workspace_bytes,
+    spec_stream_t stream);
+
+/* Writes the keys and values of new tokens: in every layer, token n of sequence
+ * b, n < num_new[b] (NULL: N), to place context_len[b] + n of its pages.
+ *
+ * k_new, v_new [num_layers, B, N, num_heads, head_dim] of the cache's dtype;
+ *    strides in elements, aligned as the cache's.  They do not overlap the cache.
+ * Two places on one page slot (sequences that share a page behind their common
+ * tokens) leave either token there; spec_cache_fork makes no such pages.
+ * out_flags [B] (nullable): SPEC_FLAG_BAD_LENGTH (the sequence's tokens are not
+ * written, or num_new is clamped into [0, N]), SPEC_FLAG_BAD_PAGE (the page's
+ * tokens are not written).  Costs a launch of its own.
+ * 0 <= N <= 4096; B * N < 2^28.  One launch. */
+spec_status spec_cache_append(
+    const void *k_new, int64_t k_layer_stride, int64_t k_seq_stride, int64_t k_token_stride,
+    int64_t k_head_stride, const void *v_new, int64_t v_layer_stride, int64_t v_seq_stride,
+    int64_t v_token_stride, int64_t v_head_stride, spec_kv_cache cache, spec_page_table pages,
+    const int32_t *context_len, const int32_t *num_new, int B, int N, uint32_t *out_flags,
+    spec_stream_t stream);
+
+/* Moves the accepted path of a verified tree together: in every layer, place
+ * context_len[b] + i takes the row of place context_len[b] + path[b,i] for
+ * i = 1..num_accepted[b]; the other rows stay as they are.
+ *
+ * path [B, width] and num_accepted [B] as spec_verify_tree writes them (node
+ *    ids, the root 0 first, ascending); num_accepted -1: nothing is accepted,
+ *    not even the root.
+ * out_context_len [B]: context_len[b] + num_accepted[b] + 1, or context_len[b]
+ *    where nothing is accepted or a flag below other than BAD_PAGE is set.  May
+ *    not be context_len itself.
+ * out_flags [B] (nullable): SPEC_FLAG_BAD_TREE (num_accepted outside
+ *    [-1, width), or a path that does not ascend from 0), SPEC_FLAG_BAD_LENGTH
+ *    (a node outside the table row): nothing is moved; SPEC_FLAG_BAD_PAGE: the
+ *    rows from or to that page are not moved.
+ * 1 <= width <= 4097.  One launch. */
+spec_status spec_cache_compact(spec_kv_cache cache, spec_page_table pages,
+                               const int32_t *context_len, const int32_t *path, int width,
+                               const int32_t *num_accepted, int B, int32_t *out_context_len,
+                               uint32_t *out_flags, spec_stream_t stream);
+
+/* A pool of num_pages pages shared by B sequences, in device memory:
+ * page_table [B, max_pages] (ld_table >= max_pages), page_count [B] entries in
+ * use, ref_count [num_pages] sequences that hold each page, free_list
+ * [num_pages] of which the first free_count[0] entries are the free pages.  The
+ * operators below keep unused entries of page_table and free_list at -1. */
+typedef struct {
+  int32_t *page_table;
+  int64_t ld_table;
+  int max_pages;
+  int32_t *page_count, *ref_count, *free_list, *free_count;
+  int num_seqs, num_pages, page_size;
+} spec_page_pool;
+
+/* Gives each sequence the pages of length[b] tokens, ceil(length / page_size).
+ * Entries behind them are given back first: a page that no sequence holds any
+ * more goes to the end of the free list, in the order of (sequence, entry).
+ * Then sequences that need more take pages from the list's end, in ascending
+ * order, as long as the list holds the demand of the sequence and of all before
+ * it; the others keep their pages and get SPEC_FLAG_NO_PAGES.  length 0 frees a
+ * sequence.
+ * out_flags [B] (nullable): also SPEC_FLAG_BAD_LENGTH (a length below 0 or above
+ * max_pages pages: the sequence keeps its pages), SPEC_FLAG_BAD_PAGE.
+ * 0 <= B <= 4096 and B * max_pages < 2^30.  One launch. */
+spec_status spec_cache_resize(spec_page_pool pool, const int32_t *length, uint32_t *out_flags,
+                              spec_stream_t stream);
+
+/* Bytes of workspace spec_cache_fork needs for F forks (0: F outside 0..4096). */
+size_t spec_cache_fork_workspace_size(int F);
+
+/* Lets sequence dst[f] go on from the context_len[src[f]] tokens of sequence
+ * src[f], f < F: full pages are shared (ref_count + 1), the rows of a last,
+ * partly filled page are copied to a page of its own in every layer, popped from
+ * the list's end in the order of the forks.  dst[f] must hold no pages before
+ * the call; context_len[dst[f]] is set.  Sources are read as they are before the
+ * call; a source may be forked many times.
+ * out_flags [F] (nullable): SPEC_FLAG_BAD_SEQUENCE (an index outside
+ * [0, num_seqs), a dst that holds pages, or that a lower f names too),
+ * SPEC_FLAG_BAD_LENGTH (fewer pages than tokens), SPEC_FLAG_NO_PAGES (the list
+ * holds too few for the forks up to f): the fork is not made;
+ * SPEC_FLAG_BAD_PAGE: that entry becomes -1.
+ * cache: pages and page size of the pool.  context_len [num_seqs] is read and
+ * written.  workspace: 4-byte aligned.  0 <= F <= 4096.  Two launches. */
+spec_status spec_cache_fork(spec_page_pool pool, spec_kv_cache cache, int32_t *context_len,
+                            const int32_t *src, const int32_t *dst, int F, uint32_t *out_flags,
+                            void *workspace, size_t workspace_bytes, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -18,6 +18,7 @@ SPEC_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
+SPEC_F16 = 2
 
 FLAG_BAD_TOKEN = 1
 FLAG_ZERO_Q = 2
@@ -26,6 +27,10 @@ FLAG_DEGENERATE_RESIDUAL = 8
 FLAG_DEPTH = 16
 FLAG_TIMEOUT = 32
 FLAG_BAD_TREE = 64
+FLAG_BAD_PAGE = 128
+FLAG_BAD_LENGTH = 256
+FLAG_NO_PAGES = 512
+FLAG_BAD_SEQUENCE = 1024
 
 EXPORTS = (
     "spec_verify_chain_workspace_size",
@@ -41,6 +46,13 @@ EXPORTS = (
     "spec_status_string",
     "spec_set_profile_events",
     "spec_set_wait_limit",
+    "spec_paged_attention_workspace_size",
+    "spec_paged_attention",
+    "spec_cache_append",
+    "spec_cache_compact",
+    "spec_cache_resize",
+    "spec_cache_fork_workspace_size",
+    "spec_cache_fork",
 )
 
 
@@ -49,8 +61,29 @@ class spec_policy(ctypes.Structure):
                 ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
 
 
+class spec_kv_cache(ctypes.Structure):
+    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+                + [(f"{x}_{dim}_stride", ctypes.c_int64) for x in "kv"
+                   for dim in ("layer", "page", "token", "head")]
+                + [(name, ctypes.c_int) for name in
+                   ("dtype", "num_layers", "num_pages", "page_size", "num_heads", "head_dim")])
+
+
+class spec_page_table(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("ld", ctypes.c_int64), ("max_pages", ctypes.c_int)]
+
+
+class spec_page_pool(ctypes.Structure):
+    _fields_ = ([("page_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64),
+                 ("max_pages", ctypes.c_int)]
+                + [(name, ctypes.c_void_p) for name in
+                   ("page_count", "ref_count", "free_list", "free_count")]
+                + [(name, ctypes.c_int) for name in ("num_seqs", "num_pages", "page_size")])
+
+
 _p = ctypes.c_void_p
 _i = ctypes.c_int
+_f = ctypes.c_float
 _i64 = ctypes.c_int64
 _u64 = ctypes.c_uint64
 _sz = ctypes.c_size_t
@@ -107,6 +140,25 @@ def load():
     lib.spec_set_profile_events.restype = _i
     lib.spec_set_wait_limit.argtypes = [_i64]
     lib.spec_set_wait_limit.restype = _i
+    lib.spec_paged_attention_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+    lib.spec_paged_attention_workspace_size.restype = _sz
+    lib.spec_paged_attention.argtypes = [
+        _p, _i64, _i64, _i64, _i, spec_kv_cache, spec_page_table, _p, _p, _i, _i, _p, _i64, _p,
+        _i64, _f, _i, _i, _p, _p, _p, _p, _sz, _p]
+    lib.spec_paged_attention.restype = _i
+    lib.spec_cache_append.argtypes = [
+        _p, _i64, _i64, _i64, _i64, _p, _i64, _i64, _i64, _i64, spec_kv_cache, spec_page_table,
+        _p, _p, _i, _i, _p, _p]
+    lib.spec_cache_append.restype = _i
+    lib.spec_cache_compact.argtypes = [spec_kv_cache, spec_page_table, _p, _p, _i, _p, _i, _p, _p,
+                                       _p]
+    lib.spec_cache_compact.restype = _i
+    lib.spec_cache_resize.argtypes = [spec_page_pool, _p, _p, _p]
+    lib.spec_cache_resize.restype = _i
+    lib.spec_cache_fork_workspace_size.argtypes = [_i]
+    lib.spec_cache_fork_workspace_size.restype = _sz
+    lib.spec_cache_fork.argtypes = [spec_page_pool, spec_kv_cache, _p, _p, _p, _i, _p, _p, _sz, _p]
+    lib.spec_cache_fork.restype = _i
     _lib = lib
     return lib
 

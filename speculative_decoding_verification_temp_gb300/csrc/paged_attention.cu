@@ -1,0 +1,818 @@
+// Attention of few new tokens over a paged cache: 16 rows of 16-bit types per
+// unit on warp-level matrix instructions, 8 rows of float32 on the FMA pipes,
+// and the join of the pieces of cut units.
+//
+// Both kernels read every key and value once per row tile and are bound by HBM
+// for one token; each of the four warps of a CTA streams its own quarter of
+// each key tile through a ring of its own in shared memory (cp.async, 16 bytes
+// a piece, so a row may start on any page) and keeps its own running maximum,
+// sum and output in registers, so that no barrier is on the stream.  The warps'
+// results meet in shared memory at the end of a unit.
+//
+// A weight is 2^(s c - m) with c = scale log2(e) and m the running maximum of
+// s c, rounded once and then used as it is: the weights of all keys, the sums
+// and the logarithm refer to the same float32 m.
+#include "paged_attention.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int kSms = 152;       // GB300
+constexpr int kAttnThreads = 128;
+constexpr int kAttnWarps = 4;
+constexpr int kJoinWarps = 4;
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t to, const char *from, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int n>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+template <class E>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<Bf16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma<F16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four outputs of one row: stored as the cache's type.
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(Bf16::pack(v.x, v.y), Bf16::pack(v.z, v.w));
+}
+__device__ __forceinline__ void store4(__half *p, float4 v) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(F16::pack(v.x, v.y), F16::pack(v.z, v.w));
+}
+__device__ __forceinline__ float as_f32(float x) { return x; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
+
+// Address of row r of a unit in [B, N, Hq] rows.
+__device__ __forceinline__ long long out_row(const AttnParams &p, int b, int h, int r) {
+  const int n = r / p.G, g = r - n * p.G;
+  return (static_cast<long long>(b) * p.S.N + n) * (p.C.heads * p.G) + h * p.G + g;
+}
+
+// ln of the weights' sum, from m and l of a row (base 2).
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+// Keys whose values hold infinities or NaNs, in slices that some row does not
+// see whole: their values entered the products as zero, so that 0 * inf does
+// not reach rows that do not see them.  What they add to the rows that do is an
+// infinity or a NaN whatever the weight, and is added here: four outputs of
+// token n, from the slices (kSlice keys) of tiles [i0, i1).  Reached only when
+// such a value was found.
+template <class TE, int kSlice>
+__device__ __noinline__ float4 nonfinite_values(const AttnParams &p, const UnitWalk &u, int n,
+                                                int d, float4 acc) {
+  float *a = reinterpret_cast<float *>(&acc);
+  for (int i = u.i0; i < u.i1; ++i) {
+    const int t0 = key_tile(u.k, i) * p.tile;
+    for (int at0 = t0; at0 < t0 + p.tile && at0 < u.k.end; at0 += kSlice) {
+      bool whole = all_seen(p, u.k, u.r0, at0, kSlice);
+      for (int at = at0; at < at0 + kSlice && whole; ++at)
+        whole = at < u.k.end && page_ok(p.C, page_at(p.S, u.b, at / p.C.page_size));
+      if (whole) continue;
+      for (int at = at0; at < min(at0 + kSlice, u.k.end); ++at) {
+        const int index = at / p.C.page_size, page = page_at(p.S, u.b, index);
+        if (!page_ok(p.C, page) || !sees(p, u.k, u.b, n, at)) continue;
+        const TE *v = reinterpret_cast<const TE *>(p.C.v + page * p.C.v_page +
+                                                   (at - index * p.C.page_size) * p.C.v_token +
+                                                   u.h * p.C.v_head);
+        for (int j = 0; j < 4; ++j) {
+          const float x = as_f32(v[d + j]);
+          if (!isfinite(x)) a[j] += x;
+        }
+      }
+    }
+  }
+  return acc;
+}
+
+// Adds the warps' results of a unit (o_s: each warp's R x DP outputs at
+// warp_floats apart; ml_s: m and l of each warp's rows) and writes the unit's
+// rows, or its piece of them.
+template <class TE, int R, int DP, int kSlice>
+__device__ __forceinline__ void write_unit(const AttnParams &p, const UnitWalk &u,
+                                           const float *o_s, int warp_floats,
+                                           const float (*ml_s)[2][R], bool bad) {
+  const int live = u.live_rows(p);
+  const bool whole = u.whole();
+  float *slot = p.part + piece_slot(u) * slot_floats(p.rows, p.D);
+  for (int i = threadIdx.x; i < R * (DP / 4); i += kAttnThreads) {
+    const int row = i / (DP / 4), d = i % (DP / 4) * 4;
+    if (row >= live || d >= p.D) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, ml_s[w][0][row]);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      const float m = ml_s[w][0][row];
+      if (m == -INFINITY) continue;
+      const float f = fast_exp2(m - M);
+      const float4 x = *reinterpret_cast<const float4 *>(o_s + w * warp_floats + row * DP + d);
+      l += f * ml_s[w][1][row];
+      o.x += f * x.x;
+      o.y += f * x.y;
+      o.z += f * x.z;
+      o.w += f * x.w;
+    }
+    if (bad) o = nonfinite_values<TE, kSlice>(p, u, (u.r0 + row) / p.G, d, o);
+    if (whole) {
+      const long long at = out_row(p, u.b, u.h, u.r0 + row);
+      const float r = l == 0.f ? 0.f : 1.f / l;
+      store4(static_cast<TE *>(p.out) + at * p.D + d,
+             make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+      if (d == 0 && p.lse) p.lse[at] = row_lse(M, l);
+    } else {
+      store4(slot + 2 * p.rows + static_cast<size_t>(row) * p.D + d, o);
+      if (d == 0) {
+        slot[row] = M;
+        slot[p.rows + row] = l;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit types, 16 rows per unit
+// ---------------------------------------------------------------------------
+
+// DP: head_dim padded to 64, 128 or 256; KT: keys per warp and tile; ST: tiles
+// in a warp's ring.  Shared rows of DP elements hold their 16-byte pieces
+// permuted within each 128 bytes (piece ^ row mod 8), so that the eight rows of
+// an 8x8 matrix load meet eight different banks.
+template <int DP, int KT, int ST>
+struct Rows16 {
+  static constexpr int kTile = kAttnWarps * KT;
+  static constexpr int kRow = DP * 2;
+  static constexpr int kStage = 2 * KT * kRow;  // keys, then values
+  static constexpr int kRing = ST * kStage;
+  static constexpr int kSmem = 16 * kRow + kAttnWarps * kRing;
+  static_assert(kRing >= 16 * DP * 4, "a warp's outputs fit its ring");
+};
+
+template <class E, int DP, int KT, int ST>
+__global__ void __launch_bounds__(kAttnThreads) rows16_kernel(const __grid_constant__ AttnParams p) {
+  using L = Rows16<DP, KT, ST>;
+  using TE = typename E::T;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ float ml_s[kAttnWarps][2][16];
+  __shared__ uint32_t valid_s[kAttnWarps][ST];
+  __shared__ int bad_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  char *q_s = smem;
+  char *ring = smem + 16 * L::kRow + warp * L::kRing;
+  const uint32_t q_at = smem_u32(q_s), ring_at = smem_u32(ring);
+  if (p.D < DP) {
+    // pieces behind head_dim are never copied to: zero for good
+    for (int i = tid; i < L::kSmem / 16; i += kAttnThreads)
+      reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+  }
+  if (tid == 0) bad_s = 0;
+  const Line line = find_run<kAttnThreads>(p);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (line.w0 == line.w1) {
+    if (tid == 0) write_join(p, line, nullptr);
+    return;
+  }
+  UnitWalk u;
+  u.start(p, line);
+  if (tid == 0) write_join(p, line, &u);
+
+  // piece of a row that this lane copies, and the row of it among each batch
+  constexpr int kPieces = DP / 8, kBatch = 32 / kPieces;
+  const int piece = lane % kPieces, sub = lane / kPieces;
+  const bool has_piece = piece * 8 < p.D;
+  const float c = p.scale_log2;
+
+  for (long long w = line.w0;;) {
+    // this lane's key of the next tile to copy
+    int pid = -1, in_page = 0;
+    auto look_up = [&](int i) {
+      pid = -1;
+      const int at = key_tile(u.k, i) * L::kTile + warp * KT + lane;
+      if (i < u.i1 && lane < KT && at < u.k.end) {
+        const int index = at / p.C.page_size;
+        in_page = at - index * p.C.page_size;
+        pid = page_at(p.S, u.b, index);
+      }
+    };
+    auto copy_tile = [&](int i) {
+      if (i < u.i1) {
+        const int st = (i - u.i0) % ST;
+        const bool ok = page_ok(p.C, pid);
+        const long long ko = ok ? pid * p.C.k_page + in_page * p.C.k_token + u.h * p.C.k_head : 0;
+        const long long vo = ok ? pid * p.C.v_page + in_page * p.C.v_token + u.h * p.C.v_head : 0;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
+        if (lane == 0) valid_s[warp][st] = valid;
+        const uint32_t at = ring_at + st * L::kStage;
+#pragma unroll
+        for (int it = 0; it < KT / kBatch; ++it) {
+          const int row = it * kBatch + sub;
+          const long long kr = __shfl_sync(0xFFFFFFFFu, ko, row);
+          const long long vr = __shfl_sync(0xFFFFFFFFu, vo, row);
+          const bool real = (valid >> row) & 1u;
+          const uint32_t to = at + row * L::kRow + ((piece ^ (row & 7)) << 4);
+          if (has_piece) {
+            copy16(to, p.C.k + kr + piece * 16, real);
+            copy16(to + KT * L::kRow, p.C.v + vr + piece * 16, real);
+          }
+        }
+        look_up(i + 1);
+      }
+      copy_commit();
+    };
+    look_up(u.i0);
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) copy_tile(u.i0 + s);
+
+    // the queries
+    const int live = u.live_rows(p);
+    for (int i = tid; i < 16 * kPieces; i += kAttnThreads) {
+      const int row = i / kPieces, pc = i % kPieces;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (row < live && pc * 8 < p.D) {
+        const int r = u.r0 + row, n = r / p.G, g = r - n * p.G;
+        x = *reinterpret_cast<const uint4 *>(p.q + u.b * p.q_seq + n * p.q_token +
+                                             (u.h * p.G + g) * p.q_head + pc * 16);
+      }
+      *reinterpret_cast<uint4 *>(q_s + row * L::kRow + ((pc ^ (row & 7)) << 4)) = x;
+    }
+    __syncthreads();
+    uint32_t qf[DP / 16][4];
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+      const int row = (lane & 7) + ((lane >> 3) & 1) * 8, pc = k * 2 + (lane >> 4);
+      ldsm4(qf[k], q_at + row * L::kRow + ((pc ^ (row & 7)) << 4));
+    }
+    const int n0 = (u.r0 + min(lane / 4, live - 1)) / p.G;
+    const int n1 = (u.r0 + min(lane / 4 + 8, live - 1)) / p.G;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float o[DP / 8][4];
+#pragma unroll
+    for (int j = 0; j < DP / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    bool bad = false;
+
+    for (int i = u.i0; i < u.i1; ++i) {
+      copy_wait<ST - 2>();
+      __syncwarp();
+      copy_tile(i + ST - 1);
+      const int st = (i - u.i0) % ST;
+      const uint32_t valid = valid_s[warp][st];
+      if (valid == 0u) continue;
+      const int at0 = key_tile(u.k, i) * L::kTile + warp * KT;
+      const uint32_t k_at = ring_at + st * L::kStage, v_at = k_at + KT * L::kRow;
+      float s[KT / 8][4];
+#pragma unroll
+      for (int j = 0; j < KT / 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < DP / 16; ++k) {
+#pragma unroll
+        for (int j = 0; j < KT / 16; ++j) {
+          uint32_t b[4];
+          const int row = j * 16 + ((lane >> 4) << 3) + (lane & 7), pc = k * 2 + ((lane >> 3) & 1);
+          ldsm4(b, k_at + row * L::kRow + ((pc ^ (row & 7)) << 4));
+          mma<E>(s[2 * j], qf[k], b[0], b[1]);
+          mma<E>(s[2 * j + 1], qf[k], b[2], b[3]);
+        }
+      }
+      constexpr uint32_t kAll = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
+      if (valid != kAll || !all_seen(p, u.k, u.r0, at0, KT)) {
+#pragma unroll
+        for (int j = 0; j < KT / 8; ++j) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = j * 8 + (lane & 3) * 2 + e;
+            const bool there = (valid >> key) & 1u;
+            if (!there || !sees(p, u.k, u.b, n0, at0 + key)) s[j][e] = -INFINITY;
+            if (!there || !sees(p, u.k, u.b, n1, at0 + key)) s[j][2 + e] = -INFINITY;
+          }
+        }
+        // infinities and NaNs among the values: zero here, see nonfinite_values
+        for (int t = lane; t < KT * kPieces; t += 32) {
+          uint4 *x = reinterpret_cast<uint4 *>(ring + st * L::kStage + KT * L::kRow + t * 16);
+          uint32_t v[4] = {x->x, x->y, x->z, x->w};
+          bool found = false;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if ((v[y] & E::kExp) == E::kExp) v[y] &= 0xFFFF0000u, found = true;
+            if (((v[y] >> 16) & E::kExp) == E::kExp) v[y] &= 0xFFFFu, found = true;
+          }
+          if (found) {
+            *x = make_uint4(v[0], v[1], v[2], v[3]);
+            bad = true;
+          }
+        }
+        __syncwarp();
+      }
+      float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < KT / 8; ++j) {
+        x0 = fmaxf(x0, fmaxf(s[j][0], s[j][1]));
+        x1 = fmaxf(x1, fmaxf(s[j][2], s[j][3]));
+      }
+#pragma unroll
+      for (int x = 1; x <= 2; x <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, x));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, x));
+      }
+      x0 = fmaxf(m0, x0 * c);
+      x1 = fmaxf(m1, x1 * c);
+      if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+        const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - x0);
+        const float f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - x1);
+        m0 = x0;
+        m1 = x1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int j = 0; j < DP / 8; ++j) {
+          o[j][0] *= f0;
+          o[j][1] *= f0;
+          o[j][2] *= f1;
+          o[j][3] *= f1;
+        }
+      }
+      // a row that has seen nothing yet keeps weights of zero
+      const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+      for (int j = 0; j < KT / 8; ++j) {
+        s[j][0] = fast_exp2(fmaf(s[j][0], c, -u0));
+        s[j][1] = fast_exp2(fmaf(s[j][1], c, -u0));
+        s[j][2] = fast_exp2(fmaf(s[j][2], c, -u1));
+        s[j][3] = fast_exp2(fmaf(s[j][3], c, -u1));
+        l0 += s[j][0] + s[j][1];
+        l1 += s[j][2] + s[j][3];
+      }
+#pragma unroll
+      for (int j = 0; j < KT / 16; ++j) {
+        // the matrix product takes the weights in the cache's type: each is off
+        // by at most half a step of that type, as the values themselves are
+        const uint32_t a[4] = {E::pack(s[2 * j][0], s[2 * j][1]), E::pack(s[2 * j][2], s[2 * j][3]),
+                               E::pack(s[2 * j + 1][0], s[2 * j + 1][1]),
+                               E::pack(s[2 * j + 1][2], s[2 * j + 1][3])};
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+          uint32_t b[4];
+          const int row = j * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), pc = d * 2 + (lane >> 4);
+          ldsm4t(b, v_at + row * L::kRow + ((pc ^ (row & 7)) << 4));
+          mma<E>(o[2 * d], a, b[0], b[1]);
+          mma<E>(o[2 * d + 1], a, b[2], b[3]);
+        }
+      }
+    }
+
+    // the unit's end: the warps' results meet in shared memory
+    copy_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int x = 1; x <= 2; x <<= 1) {
+      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, x);
+      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, x);
+    }
+    float *o_w = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int j = 0; j < DP / 8; ++j) {
+      const int d = j * 8 + (lane & 3) * 2, row = lane / 4;
+      *reinterpret_cast<float2 *>(o_w + row * DP + d) = make_float2(o[j][0], o[j][1]);
+      *reinterpret_cast<float2 *>(o_w + (row + 8) * DP + d) = make_float2(o[j][2], o[j][3]);
+    }
+    if ((lane & 3) == 0) {
+      ml_s[warp][0][lane / 4] = m0;
+      ml_s[warp][0][lane / 4 + 8] = m1;
+      ml_s[warp][1][lane / 4] = l0;
+      ml_s[warp][1][lane / 4 + 8] = l1;
+    }
+    if (bad) bad_s = 1;
+    __syncthreads();
+    write_unit<TE, 16, DP, KT>(p, u, reinterpret_cast<const float *>(smem + 16 * L::kRow),
+                               L::kRing / 4, ml_s, bad_s != 0);
+    w += u.i1 - u.i0;
+    if (w >= line.w1) break;
+    __syncthreads();
+    if (tid == 0) bad_s = 0;
+    if (p.D < DP) {
+      // the outputs were laid over the pieces that stay zero
+      for (int i = lane; i < 16 * DP / 4; i += 32)
+        reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+    u.next(p, line);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// float32, 8 rows per unit
+// ---------------------------------------------------------------------------
+
+// A lane takes one key of its warp's tile (or one of 32 / KT parts of it) for
+// the scores and some of the head's dimensions for the outputs.  Rows of keys
+// are 16 bytes longer than their data, so that eight lanes on eight rows meet
+// different banks.
+template <int DP>
+struct Rows8 {
+  static constexpr int KT = 2048 / DP;  // 32, 16, 8 keys per warp and tile
+  static constexpr int ST = 2;
+  static constexpr int kTile = kAttnWarps * KT;
+  static constexpr int kKeyRow = DP * 4 + 16, kValRow = DP * 4;
+  static constexpr int kStage = KT * (kKeyRow + kValRow);
+  static constexpr int kRing = ST * kStage;
+  static constexpr int kWeights = KT * 8 * 4;
+  static constexpr int kSmem = 8 * DP * 4 + kAttnWarps * (kRing + kWeights);
+  static_assert(kRing >= 8 * DP * 4, "a warp's outputs fit its ring");
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kAttnThreads) rows8_kernel(const __grid_constant__ AttnParams p) {
+  using L = Rows8<DP>;
+  constexpr int KT = L::KT, ST = L::ST, R = 8;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ float ml_s[kAttnWarps][2][R];
+  __shared__ uint32_t valid_s[kAttnWarps][ST];
+  __shared__ int bad_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float *q_s = reinterpret_cast<float *>(smem);
+  char *rings = smem + R * DP * 4;
+  char *ring = rings + warp * L::kRing;
+  float *p_s = reinterpret_cast<float *>(rings + kAttnWarps * L::kRing) + warp * KT * R;
+  const uint32_t ring_at = smem_u32(ring);
+  if (tid == 0) bad_s = 0;
+  const Line line = find_run<kAttnThreads>(p);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (line.w0 == line.w1) {
+    if (tid == 0) write_join(p, line, nullptr);
+    return;
+  }
+  UnitWalk u;
+  u.start(p, line);
+  if (tid == 0) write_join(p, line, &u);
+
+  constexpr int kPieces = DP / 4;                            // of a row, 16 bytes each
+  constexpr int kLanes = kPieces < 32 ? kPieces : 32;        // lanes on one row
+  constexpr int kBatch = 32 / kLanes, kOwn = kPieces / kLanes;  // rows at once, pieces a lane
+  const int piece = lane % kLanes, sub = lane / kLanes;
+  const int pieces = p.D / 4;
+  const float c = p.scale_log2;
+  const int key = lane % KT, part = lane / KT;
+
+  for (long long w = line.w0;;) {
+    auto copy_tile = [&](int i) {
+      if (i < u.i1) {
+        const int st = (i - u.i0) % ST;
+        const int at = key_tile(u.k, i) * L::kTile + warp * KT + lane;
+        int pid = -1, in_page = 0;
+        if (lane < KT && at < u.k.end) {
+          const int index = at / p.C.page_size;
+          in_page = at - index * p.C.page_size;
+          pid = page_at(p.S, u.b, index);
+        }
+        const bool ok = page_ok(p.C, pid);
+        const long long ko = ok ? pid * p.C.k_page + in_page * p.C.k_token + u.h * p.C.k_head : 0;
+        const long long vo = ok ? pid * p.C.v_page + in_page * p.C.v_token + u.h * p.C.v_head : 0;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
+        if (lane == 0) valid_s[warp][st] = valid;
+        const uint32_t to = ring_at + st * L::kStage;
+#pragma unroll 4
+        for (int r0 = 0; r0 < KT; r0 += kBatch) {
+          const int row = r0 + sub;
+          const long long kr = __shfl_sync(0xFFFFFFFFu, ko, row);
+          const long long vr = __shfl_sync(0xFFFFFFFFu, vo, row);
+          const bool real = (valid >> row) & 1u;
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            const int pc = piece + j * kLanes;
+            if (pc < pieces) {
+              copy16(to + row * L::kKeyRow + pc * 16, p.C.k + kr + pc * 16, real);
+              copy16(to + KT * L::kKeyRow + row * L::kValRow + pc * 16, p.C.v + vr + pc * 16, real);
+            }
+          }
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < ST - 1; ++s) copy_tile(u.i0 + s);
+    const int live = u.live_rows(p);
+    for (int i = tid; i < R * kPieces; i += kAttnThreads) {
+      const int row = i / kPieces, pc = i % kPieces;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < live && pc < pieces) {
+        const int r = u.r0 + row, n = r / p.G, g = r - n * p.G;
+        x = *reinterpret_cast<const float4 *>(p.q + u.b * p.q_seq + n * p.q_token +
+                                              (u.h * p.G + g) * p.q_head + pc * 16);
+      }
+      *reinterpret_cast<float4 *>(q_s + row * DP + pc * 4) = x;
+    }
+    __syncthreads();
+    float m[R], l[R], o[R][4 * kOwn];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4 * kOwn; ++j) o[r][j] = 0.f;
+    }
+    bool bad = false;
+
+    for (int i = u.i0; i < u.i1; ++i) {
+      copy_wait<ST - 2>();
+      __syncwarp();
+      copy_tile(i + ST - 1);
+      const int st = (i - u.i0) % ST;
+      const uint32_t valid = valid_s[warp][st];
+      if (valid == 0u) continue;
+      const int at0 = key_tile(u.k, i) * L::kTile + warp * KT;
+      const float *k_s = reinterpret_cast<const float *>(ring + st * L::kStage);
+      float *v_s = reinterpret_cast<float *>(ring + st * L::kStage + KT * L::kKeyRow);
+      float s[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = 0.f;
+      for (int pc = part; pc < pieces; pc += 32 / KT) {
+        const float4 x = *reinterpret_cast<const float4 *>(k_s + key * (L::kKeyRow / 4) + pc * 4);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 y = *reinterpret_cast<const float4 *>(q_s + r * DP + pc * 4);
+          s[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[r]))));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int x = KT; x < 32; x <<= 1) s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], x);
+      constexpr uint32_t kAll = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
+      if (valid != kAll || !all_seen(p, u.k, u.r0, at0, KT)) {
+        const bool there = (valid >> key) & 1u;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (!there || !sees(p, u.k, u.b, (u.r0 + min(r, live - 1)) / p.G, at0 + key))
+            s[r] = -INFINITY;
+        for (int t = lane; t < KT * pieces; t += 32) {
+          float4 *x = reinterpret_cast<float4 *>(v_s + t / pieces * DP + t % pieces * 4);
+          float4 y = *x;
+          float *z = reinterpret_cast<float *>(&y);
+          bool found = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!isfinite(z[e])) z[e] = 0.f, found = true;
+          if (found) *x = y, bad = true;
+        }
+      }
+      bool up = false;
+      float f[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x = s[r];
+#pragma unroll
+        for (int y = 1; y < KT; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, y));
+        x = fmaxf(m[r], x * c);
+        f[r] = m[r] == -INFINITY ? 0.f : fast_exp2(m[r] - x);
+        up |= x > m[r];
+        m[r] = x;
+        s[r] = fast_exp2(fmaf(s[r], c, x == -INFINITY ? 0.f : -x));
+      }
+      if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          l[r] *= f[r];
+#pragma unroll
+          for (int j = 0; j < 4 * kOwn; ++j) o[r][j] *= f[r];
+        }
+      }
+      if (part == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) l[r] += s[r];
+        *reinterpret_cast<float4 *>(p_s + key * R) = make_float4(s[0], s[1], s[2], s[3]);
+        *reinterpret_cast<float4 *>(p_s + key * R + 4) = make_float4(s[4], s[5], s[6], s[7]);
+      }
+      __syncwarp();
+#pragma unroll 4
+      for (int k0 = 0; k0 < KT; k0 += kBatch) {
+        const int kk = k0 + sub;
+        const float4 a = *reinterpret_cast<const float4 *>(p_s + kk * R);
+        const float4 b = *reinterpret_cast<const float4 *>(p_s + kk * R + 4);
+        const float wt[R] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+          const int pc = piece + j * kLanes;
+          if (pc >= pieces) continue;
+          const float4 v = *reinterpret_cast<const float4 *>(v_s + kk * DP + pc * 4);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            o[r][4 * j] = fmaf(wt[r], v.x, o[r][4 * j]);
+            o[r][4 * j + 1] = fmaf(wt[r], v.y, o[r][4 * j + 1]);
+            o[r][4 * j + 2] = fmaf(wt[r], v.z, o[r][4 * j + 2]);
+            o[r][4 * j + 3] = fmaf(wt[r], v.w, o[r][4 * j + 3]);
+          }
+        }
+      }
+    }
+
+    copy_wait<0>();
+    __syncwarp();
+    float *o_w = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] = warp_sum(l[r]);
+#pragma unroll
+      for (int j = 0; j < 4 * kOwn; ++j)
+#pragma unroll
+        for (int x = kLanes; x < 32; x <<= 1)
+          o[r][j] += __shfl_xor_sync(0xFFFFFFFFu, o[r][j], x);
+      if (sub == 0) {
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+          store4(o_w + r * DP + (piece + j * kLanes) * 4,
+                 make_float4(o[r][4 * j], o[r][4 * j + 1], o[r][4 * j + 2], o[r][4 * j + 3]));
+      }
+      if (lane == 0) {
+        ml_s[warp][0][r] = m[r];
+        ml_s[warp][1][r] = l[r];
+      }
+    }
+    if (bad) bad_s = 1;
+    __syncthreads();
+    write_unit<float, R, DP, KT>(p, u, reinterpret_cast<const float *>(rings), L::kRing / 4, ml_s,
+                                 bad_s != 0);
+    w += u.i1 - u.i0;
+    if (w >= line.w1) break;
+    __syncthreads();
+    if (tid == 0) bad_s = 0;
+    u.next(p, line);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the join
+// ---------------------------------------------------------------------------
+
+// One warp per row of a cut unit: its pieces in the order of their keys.
+template <class TE>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.y * kJoinWarps + warp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const JoinDesc d = p.join[blockIdx.x];
+  if (d.pieces_end < 0) return;
+  if (d.r0 + row >= seq_new(p.S, d.b) * p.G || row >= p.rows) return;
+  const int first = static_cast<int>(blockIdx.x) - 1, count = d.pieces_end - first + 1;
+  const size_t per_slot = slot_floats(p.rows, p.D);
+  auto slot = [&](int i) { return p.part + (2 * (first + i) + (i == 0 ? 1 : 0)) * per_slot; };
+  float M = -INFINITY;
+  for (int i = lane; i < count; i += 32) M = fmaxf(M, slot(i)[row]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
+  float l = 0.f;
+  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    float f = 0.f, lp = 0.f;
+    if (i0 + lane < count) {
+      const float *s = slot(i0 + lane);
+      const float m = s[row];
+      if (m != -INFINITY) {
+        f = fast_exp2(m - M);
+        lp = f * s[p.rows + row];
+      }
+    }
+    for (int j = 0; j < min(32, count - i0); ++j) {
+      const float w = __shfl_sync(0xFFFFFFFFu, f, j);
+      l += __shfl_sync(0xFFFFFFFFu, lp, j);
+      const float *s = slot(i0 + j) + 2 * p.rows + static_cast<size_t>(row) * p.D;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int at = (lane + 32 * x) * 4;
+        if (at >= p.D) continue;
+        const float4 v = *reinterpret_cast<const float4 *>(s + at);
+        o[x].x += w * v.x;
+        o[x].y += w * v.y;
+        o[x].z += w * v.z;
+        o[x].w += w * v.w;
+      }
+    }
+  }
+  const long long at = out_row(p, d.b, d.h, d.r0 + row);
+  const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int e = (lane + 32 * x) * 4;
+    if (e < p.D)
+      store4(static_cast<TE *>(p.out) + at * p.D + e,
+             make_float4(o[x].x * r, o[x].y * r, o[x].z * r, o[x].w * r));
+  }
+  if (lane == 0 && p.lse) p.lse[at] = row_lse(M, l);
+}
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+
+struct AttnPlan {
+  int ctas, rows, tile;
+};
+
+AttnPlan attention_plan(int N, int G, int D, int dtype) {
+  (void)N;
+  (void)G;
+  if (dtype == SPEC_F32)
+    return {kSms, 8, D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile)};
+  if (D <= 64) return {2 * kSms, 16, 128};
+  if (D <= 128) return {2 * kSms, 16, 64};
+  return {kSms, 16, 64};
+}
+
+template <class K>
+cudaError_t start(K kernel, size_t smem, const AttnParams &p, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<p.ctas, kAttnThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <class E>
+cudaError_t start16(const AttnParams &p, cudaStream_t stream) {
+  if (p.D <= 64) return start(rows16_kernel<E, 64, 32, 3>, Rows16<64, 32, 3>::kSmem, p, stream);
+  if (p.D <= 128) return start(rows16_kernel<E, 128, 16, 3>, Rows16<128, 16, 3>::kSmem, p, stream);
+  return start(rows16_kernel<E, 256, 16, 3>, Rows16<256, 16, 3>::kSmem, p, stream);
+}
+
+size_t align16(size_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace
+
+size_t attention_workspace_bytes(int N, int G, int D, int dtype) {
+  const AttnPlan plan = attention_plan(N, G, D, dtype);
+  return align16(plan.ctas * sizeof(JoinDesc)) +
+         2 * plan.ctas * slot_floats(plan.rows, D) * sizeof(float);
+}
+
+cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream) {
+  const AttnPlan plan = attention_plan(p.S.N, p.G, p.D, dtype);
+  p.ctas = plan.ctas;
+  p.rows = plan.rows;
+  p.tile = plan.tile;
+  p.min_tiles = 1;
+  p.join = static_cast<JoinDesc *>(workspace);
+  p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                     align16(plan.ctas * sizeof(JoinDesc)));
+  cudaError_t e;
+  if (dtype == SPEC_F32) {
+    if (p.D <= 64) {
+      e = start(rows8_kernel<64>, Rows8<64>::kSmem, p, stream);
+    } else if (p.D <= 128) {
+      e = start(rows8_kernel<128>, Rows8<128>::kSmem, p, stream);
+    } else {
+      e = start(rows8_kernel<256>, Rows8<256>::kSmem, p, stream);
+    }
+  } else {
+    e = dtype == SPEC_BF16 ? start16<Bf16>(p, stream) : start16<F16>(p, stream);
+  }
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.ctas, (p.rows + kJoinWarps - 1) / kJoinWarps);
+  if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinWarps * 32, 0, stream, p);
+  if (dtype == SPEC_BF16)
+    return launch_behind(join_kernel<__nv_bfloat16>, grid, kJoinWarps * 32, 0, stream, p);
+  return launch_behind(join_kernel<__half>, grid, kJoinWarps * 32, 0, stream, p);
+}
+
+}  // namespace sv

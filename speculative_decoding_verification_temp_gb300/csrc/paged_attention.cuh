@@ -1,0 +1,300 @@
+// Attention of new tokens over a paged key-value cache: what its kernels share.
+//
+// The rows of a (sequence, head of the cache) are its new tokens times the
+// group of query heads that read this head: row r is token r / G, query head
+// h * G + r % G.  A unit is a tile of R rows with all the keys that one of them
+// may see, cut into tiles of T keys.  The units' key tiles, laid end to end
+// (sequences, then heads, then row tiles), are one line of work that is cut
+// into equal runs, one per CTA, whatever the lengths of the sequences are: a
+// CTA's run holds whole units, which it finishes, and at most one unit's end
+// and one unit's beginning, which it leaves as partial results (running
+// maximum, sum and unnormalised output of each row).  A second kernel joins
+// the partial results of each unit that was cut, in the order of its keys, so
+// results do not depend on timing.  The line is laid out on the device from
+// the lengths, so a captured launch follows lengths that change.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv_cache.cuh"
+
+namespace sv {
+
+struct AttnParams {
+  const char *q;
+  long long q_seq, q_token, q_head;  // bytes
+  KvCache C;
+  KvSeqs S;
+  const uint64_t *mask;
+  long long mask_seq;
+  int words;
+  const int32_t *position;
+  long long position_seq;
+  int G, D;
+  float scale, scale_log2;
+  int window, sinks;
+  void *out;
+  float *lse;
+  float *part;  // partial results, two slots per CTA
+  struct JoinDesc *join;
+  int ctas, rows, tile;  // R and T
+  int min_tiles;         // a CTA's run is at least this long (where there is as much)
+};
+
+// A cut unit, written by the CTA that holds its first cut; its pieces are those
+// of CTAs cta - 1 .. pieces_end.  pieces_end -1: no unit's cuts start here.
+struct JoinDesc {
+  int b, h, r0, pieces_end;
+};
+
+size_t attention_workspace_bytes(int N, int G, int D, int dtype);
+cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream);
+// The tensor-memory form; rows of up to 2 * 128 per unit.
+cudaError_t launch_attention_wide(const AttnParams &p, int dtype, cudaStream_t stream);
+
+// The keys that the rows [r0, r0 + R) of sequence b may see: tiles
+// [0, sink_tiles) and then `lo` and those behind it; at least one tile, which
+// may hold no visible key.
+struct KeyRange {
+  int ctx, n_new;   // n_new: new tokens, 0 where the sequence does not fit
+  int end;          // keys at or behind it are seen by no row
+  int sink_tiles, lo, count;
+};
+
+__device__ __forceinline__ KeyRange key_range(const AttnParams &p, int ctx, int n_new, bool fits,
+                                              int r0) {
+  KeyRange k;
+  k.ctx = ctx;
+  k.n_new = n_new;
+  k.end = 0;
+  int first = 0;
+  if (fits) {
+    const int n_lo = r0 / p.G;
+    const int n_hi = min((r0 + p.rows - 1) / p.G, n_new - 1);
+    k.end = p.mask ? ctx + n_new : ctx + n_hi + 1;
+    if (p.window) first = max(0, (p.mask || p.position ? ctx : ctx + n_lo) - p.window + 1);
+  }
+  k.lo = first / p.tile;
+  k.sink_tiles = p.window ? min((min(p.sinks, k.end) + p.tile - 1) / p.tile, k.lo) : 0;
+  k.count = max(1, k.sink_tiles + (k.end + p.tile - 1) / p.tile - k.lo);
+  return k;
+}
+
+__device__ __forceinline__ int key_tile(const KeyRange &k, int i) {
+  return i < k.sink_tiles ? i : k.lo + i - k.sink_tiles;
+}
+
+// Key tiles of one head of a sequence.
+__device__ __forceinline__ long long head_work(const AttnParams &p, int ctx, int n_new, bool fits) {
+  long long w = 0;
+  for (int r0 = 0; r0 < n_new * p.G; r0 += p.rows) w += key_range(p, ctx, n_new, fits, r0).count;
+  return w;
+}
+
+struct Line {
+  long long w0, w1;     // this CTA's run
+  long long total;
+  int ctas;             // CTAs with work
+  int b;                // the sequence that holds w0
+  long long in_seq;     // w0 within it
+};
+
+__device__ __forceinline__ long long run_start(long long cta, long long total, int ctas) {
+  return cta * total / ctas;
+}
+
+// The line of work, by all threads of the CTA (kT of them).
+template <int kT>
+__device__ __forceinline__ Line find_run(const AttnParams &p) {
+  __shared__ long long warp_s[kT / 32 + 1];
+  __shared__ long long found_s[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.S.B + kT - 1) / kT;
+  const int b0 = min(tid * per, p.S.B), b1 = min(b0 + per, p.S.B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
+    mine += p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n));
+  }
+  long long x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_s[warp] = x;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kT / 32; ++w) {
+    const long long v = warp_s[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  before += x - mine;
+  Line L;
+  L.total = total;
+  const long long most = (total + p.min_tiles - 1) / p.min_tiles;
+  L.ctas = static_cast<int>(most < p.ctas ? (most > 0 ? most : 1) : p.ctas);
+  const bool busy = total > 0 && static_cast<int>(blockIdx.x) < L.ctas;
+  L.w0 = busy ? run_start(blockIdx.x, total, L.ctas) : 0;
+  L.w1 = busy ? run_start(blockIdx.x + 1ll, total, L.ctas) : 0;
+  if (busy && before <= L.w0 && L.w0 < before + mine) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
+      const long long w = p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n));
+      if (L.w0 < at + w) {
+        found_s[0] = b;
+        found_s[1] = L.w0 - at;
+        break;
+      }
+      at += w;
+    }
+  }
+  __syncthreads();
+  L.b = busy ? static_cast<int>(found_s[0]) : 0;
+  L.in_seq = busy ? found_s[1] : 0;
+  return L;
+}
+
+// Walks the units of a run.
+struct UnitWalk {
+  int b, h, r0;
+  KeyRange k;
+  bool fits;
+  long long a;    // the unit's first tile on the line
+  int i0, i1;     // the run's tiles of the unit
+
+  __device__ __forceinline__ void load_seq(const AttnParams &p) {
+    k.ctx = __ldg(p.S.ctx + b);
+    k.n_new = seq_new(p.S, b);
+    fits = seq_fits(p.S, p.C, k.ctx, k.n_new);
+  }
+  __device__ __forceinline__ void start(const AttnParams &p, const Line &L) {
+    b = L.b;
+    load_seq(p);
+    const long long per_head = head_work(p, k.ctx, k.n_new, fits);
+    h = static_cast<int>(L.in_seq / per_head);
+    long long left = L.in_seq - h * per_head;
+    for (r0 = 0;; r0 += p.rows) {
+      k = key_range(p, k.ctx, k.n_new, fits, r0);
+      if (left < k.count) break;
+      left -= k.count;
+    }
+    a = L.w0 - left;
+    i0 = static_cast<int>(left);
+    i1 = static_cast<int>(min(static_cast<long long>(k.count), L.w1 - a));
+  }
+  // The next unit; the caller has checked that the run goes on behind this one.
+  __device__ __forceinline__ void next(const AttnParams &p, const Line &L) {
+    a += k.count;
+    r0 += p.rows;
+    if (r0 >= k.n_new * p.G) {
+      r0 = 0;
+      if (++h == p.C.heads) {
+        h = 0;
+        do {
+          ++b;
+          load_seq(p);
+        } while (k.n_new == 0);
+      }
+    }
+    k = key_range(p, k.ctx, k.n_new, fits, r0);
+    i0 = 0;
+    i1 = static_cast<int>(min(static_cast<long long>(k.count), L.w1 - a));
+  }
+  __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == k.count; }
+  // Rows of the unit that exist.
+  __device__ __forceinline__ int live_rows(const AttnParams &p) const {
+    return min(p.rows, k.n_new * p.G - r0);
+  }
+};
+
+// Slot of the workspace for this CTA's piece of a cut unit.
+__device__ __forceinline__ int piece_slot(const UnitWalk &u) {
+  return 2 * blockIdx.x + (u.i0 > 0 ? 0 : 1);
+}
+__host__ __device__ __forceinline__ size_t slot_floats(int R, int D) {
+  return static_cast<size_t>(R) * (D + 2);
+}
+
+// Writes this CTA's join descriptor, before or after its run: the unit that its
+// first tile cuts, if no CTA before it cuts that unit.
+__device__ __forceinline__ void write_join(const AttnParams &p, const Line &L, const UnitWalk *u) {
+  JoinDesc d = {0, 0, 0, -1};
+  if (u && u->i0 > 0 && run_start(blockIdx.x - 1ll, L.total, L.ctas) <= u->a) {
+    d.b = u->b;
+    d.h = u->h;
+    d.r0 = u->r0;
+    const long long last = u->a + u->k.count - 1;
+    long long c = last * L.ctas / L.total;  // the CTA that holds the last tile, or next to it
+    while (run_start(c, L.total, L.ctas) > last) --c;
+    while (c + 1 < L.ctas && run_start(c + 1, L.total, L.ctas) <= last) ++c;
+    d.pieces_end = static_cast<int>(c);
+  }
+  p.join[blockIdx.x] = d;
+}
+
+// The place of new token m behind the context, for windows.
+__device__ __forceinline__ int clamp_pos(const AttnParams &p, int b, int m) {
+  if (!p.position) return m;
+  return min(max(__ldg(p.position + static_cast<long long>(b) * p.position_seq + m), 0),
+             p.S.N - 1);
+}
+// Whether new token n sees the key at index `at` of the sequence.
+__device__ __forceinline__ bool sees(const AttnParams &p, const KeyRange &k, int b, int n, int at) {
+  int place = at;
+  if (at >= k.ctx) {
+    const int m = at - k.ctx;
+    if (m >= k.n_new) return false;
+    if (p.mask) {
+      const uint64_t w = __ldg(reinterpret_cast<const unsigned long long *>(p.mask) +
+                               static_cast<long long>(b) * p.mask_seq +
+                               static_cast<long long>(n) * p.words + (m >> 6));
+      if (!((w >> (m & 63)) & 1ull)) return false;
+    } else if (m > n) {
+      return false;
+    }
+    if (p.window) place = k.ctx + clamp_pos(p, b, m);
+  }
+  if (p.window && place >= p.sinks && k.ctx + clamp_pos(p, b, n) - place >= p.window) return false;
+  return true;
+}
+
+// Whether every row of the unit (from row r0 on) sees all of the keys
+// [at, at + n).
+__device__ __forceinline__ bool all_seen(const AttnParams &p, const KeyRange &k, int r0, int at,
+                                         int n) {
+  if (at + n > k.ctx && (p.mask || at + n - 1 > k.ctx + r0 / p.G)) return false;
+  if (!p.window) return true;
+  if (at + n > k.ctx) return false;
+  // before the last place that a new token can have
+  return at + n <= p.sinks || at > k.ctx + p.S.N - 1 - p.window;
+}
+
+// ---------------------------------------------------------------------------
+// element types
+// ---------------------------------------------------------------------------
+
+struct Bf16 {
+  using T = __nv_bfloat16;
+  static __device__ __forceinline__ float to(T x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+  static constexpr uint32_t kExp = 0x7F80u;  // all ones: infinity or NaN
+};
+struct F16 {
+  using T = __half;
+  static __device__ __forceinline__ float to(T x) { return __half2float(x); }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+  static constexpr uint32_t kExp = 0x7C00u;
+};
+
+}  // namespace sv

@@ -186,6 +186,7 @@ spec_status spec_paged_attention(
   p.sinks = sinks;
   p.out = out;
   p.lse = out_lse;
+  p.flags = out_flags;
   if (out_flags) {
     const cudaError_t e = sv::launch_kv_flags(p.S, p.C, false, out_flags, st);
     if (e != cudaSuccess) return map_cuda(e);

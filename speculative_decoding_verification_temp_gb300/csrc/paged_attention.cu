@@ -23,22 +23,6 @@ constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = 4;
 constexpr int kJoinWarps = 4;
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 bytes from global to shared memory, or 16 zero bytes.
-__device__ __forceinline__ void copy16(uint32_t to, const char *from, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
-               "r"(real ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copy_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int n>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -69,62 +53,6 @@ __device__ __forceinline__ void mma<F16>(float (&c)[4], const uint32_t (&a)[4], 
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four outputs of one row: stored as the cache's type.
-__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
-  *reinterpret_cast<uint2 *>(p) = make_uint2(Bf16::pack(v.x, v.y), Bf16::pack(v.z, v.w));
-}
-__device__ __forceinline__ void store4(__half *p, float4 v) {
-  *reinterpret_cast<uint2 *>(p) = make_uint2(F16::pack(v.x, v.y), F16::pack(v.z, v.w));
-}
-__device__ __forceinline__ float as_f32(float x) { return x; }
-__device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
-
-// Address of row r of a unit in [B, N, Hq] rows.
-__device__ __forceinline__ long long out_row(const AttnParams &p, int b, int h, int r) {
-  const int n = r / p.G, g = r - n * p.G;
-  return (static_cast<long long>(b) * p.S.N + n) * (p.C.heads * p.G) + h * p.G + g;
-}
-
-// ln of the weights' sum, from m and l of a row (base 2).
-__device__ __forceinline__ float row_lse(float m, float l) {
-  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-}
-
-// Keys whose values hold infinities or NaNs, in slices that some row does not
-// see whole: their values entered the products as zero, so that 0 * inf does
-// not reach rows that do not see them.  What they add to the rows that do is an
-// infinity or a NaN whatever the weight, and is added here: four outputs of
-// token n, from the slices (kSlice keys) of tiles [i0, i1).  Reached only when
-// such a value was found.
-template <class TE, int kSlice>
-__device__ __noinline__ float4 nonfinite_values(const AttnParams &p, const UnitWalk &u, int n,
-                                                int d, float4 acc) {
-  float *a = reinterpret_cast<float *>(&acc);
-  for (int i = u.i0; i < u.i1; ++i) {
-    const int t0 = key_tile(u.k, i) * p.tile;
-    for (int at0 = t0; at0 < t0 + p.tile && at0 < u.k.end; at0 += kSlice) {
-      bool whole = all_seen(p, u.k, u.r0, at0, kSlice);
-      for (int at = at0; at < at0 + kSlice && whole; ++at)
-        whole = at < u.k.end && page_ok(p.C, page_at(p.S, u.b, at / p.C.page_size));
-      if (whole) continue;
-      for (int at = at0; at < min(at0 + kSlice, u.k.end); ++at) {
-        const int index = at / p.C.page_size, page = page_at(p.S, u.b, index);
-        if (!page_ok(p.C, page) || !sees(p, u.k, u.b, n, at)) continue;
-        const TE *v = reinterpret_cast<const TE *>(p.C.v + page * p.C.v_page +
-                                                   (at - index * p.C.page_size) * p.C.v_token +
-                                                   u.h * p.C.v_head);
-        for (int j = 0; j < 4; ++j) {
-          const float x = as_f32(v[d + j]);
-          if (!isfinite(x)) a[j] += x;
-        }
-      }
-    }
-  }
-  return acc;
 }
 
 // Adds the warps' results of a unit (o_s: each warp's R x DP outputs at
@@ -200,6 +128,7 @@ __global__ void __launch_bounds__(kAttnThreads) rows16_kernel(const __grid_const
   __shared__ float ml_s[kAttnWarps][2][16];
   __shared__ uint32_t valid_s[kAttnWarps][ST];
   __shared__ int bad_s;
+  __shared__ long long warp_s[kAttnWarps], found_s[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   char *q_s = smem;
   char *ring = smem + 16 * L::kRow + warp * L::kRing;
@@ -210,7 +139,7 @@ __global__ void __launch_bounds__(kAttnThreads) rows16_kernel(const __grid_const
       reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
   }
   if (tid == 0) bad_s = 0;
-  const Line line = find_run<kAttnThreads>(p);
+  const Line line = find_run<kAttnThreads>(p, warp_s, found_s);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (line.w0 == line.w1) {
     if (tid == 0) write_join(p, line, nullptr);
@@ -332,15 +261,10 @@ __global__ void __launch_bounds__(kAttnThreads) rows16_kernel(const __grid_const
         // infinities and NaNs among the values: zero here, see nonfinite_values
         for (int t = lane; t < KT * kPieces; t += 32) {
           uint4 *x = reinterpret_cast<uint4 *>(ring + st * L::kStage + KT * L::kRow + t * 16);
-          uint32_t v[4] = {x->x, x->y, x->z, x->w};
-          bool found = false;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if ((v[y] & E::kExp) == E::kExp) v[y] &= 0xFFFF0000u, found = true;
-            if (((v[y] >> 16) & E::kExp) == E::kExp) v[y] &= 0xFFFFu, found = true;
-          }
-          if (found) {
-            *x = make_uint4(v[0], v[1], v[2], v[3]);
+          const uint4 v = make_uint4(finite_or_zero<E>(x->x), finite_or_zero<E>(x->y),
+                                     finite_or_zero<E>(x->z), finite_or_zero<E>(x->w));
+          if (v.x != x->x || v.y != x->y || v.z != x->z || v.w != x->w) {
+            *x = v;
             bad = true;
           }
         }
@@ -471,6 +395,7 @@ __global__ void __launch_bounds__(kAttnThreads) rows8_kernel(const __grid_consta
   __shared__ float ml_s[kAttnWarps][2][R];
   __shared__ uint32_t valid_s[kAttnWarps][ST];
   __shared__ int bad_s;
+  __shared__ long long warp_s[kAttnWarps], found_s[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *q_s = reinterpret_cast<float *>(smem);
   char *rings = smem + R * DP * 4;
@@ -478,7 +403,7 @@ __global__ void __launch_bounds__(kAttnThreads) rows8_kernel(const __grid_consta
   float *p_s = reinterpret_cast<float *>(rings + kAttnWarps * L::kRing) + warp * KT * R;
   const uint32_t ring_at = smem_u32(ring);
   if (tid == 0) bad_s = 0;
-  const Line line = find_run<kAttnThreads>(p);
+  const Line line = find_run<kAttnThreads>(p, warp_s, found_s);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (line.w0 == line.w1) {
     if (tid == 0) write_join(p, line, nullptr);
@@ -748,16 +673,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 
 struct AttnPlan {
   int ctas, rows, tile;
+  bool wide;
 };
 
 AttnPlan attention_plan(int N, int G, int D, int dtype) {
-  (void)N;
-  (void)G;
   if (dtype == SPEC_F32)
-    return {kSms, 8, D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile)};
-  if (D <= 64) return {2 * kSms, 16, 128};
-  if (D <= 128) return {2 * kSms, 16, 64};
-  return {kSms, 16, 64};
+    return {kSms, 8,
+            D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile), false};
+  if (N * G > 16 && (D == 64 || D == 128)) return {kSms, N * G > 128 ? 256 : 128, 128, true};
+  if (D <= 64) return {2 * kSms, 16, Rows16<64, 32, 3>::kTile, false};
+  if (D <= 128) return {2 * kSms, 16, Rows16<128, 16, 3>::kTile, false};
+  return {kSms, 16, Rows16<256, 16, 3>::kTile, false};
 }
 
 template <class K>
@@ -804,6 +730,8 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
     } else {
       e = start(rows8_kernel<256>, Rows8<256>::kSmem, p, stream);
     }
+  } else if (plan.wide) {
+    e = launch_attention_wide(p, dtype, stream);
   } else {
     e = dtype == SPEC_BF16 ? start16<Bf16>(p, stream) : start16<F16>(p, stream);
   }

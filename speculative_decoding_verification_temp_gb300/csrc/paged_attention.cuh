@@ -36,6 +36,7 @@ struct AttnParams {
   int window, sinks;
   void *out;
   float *lse;
+  uint32_t *flags;
   float *part;  // partial results, two slots per CTA
   struct JoinDesc *join;
   int ctas, rows, tile;  // R and T
@@ -50,7 +51,7 @@ struct JoinDesc {
 
 size_t attention_workspace_bytes(int N, int G, int D, int dtype);
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream);
-// The tensor-memory form; rows of up to 2 * 128 per unit.
+// Units of 128 or 256 rows (p.rows), head_dim 64 or 128, 16-bit types.
 cudaError_t launch_attention_wide(const AttnParams &p, int dtype, cudaStream_t stream);
 
 // The keys that the rows [r0, r0 + R) of sequence b may see: tiles
@@ -106,9 +107,8 @@ __device__ __forceinline__ long long run_start(long long cta, long long total, i
 
 // The line of work, by all threads of the CTA (kT of them).
 template <int kT>
-__device__ __forceinline__ Line find_run(const AttnParams &p) {
-  __shared__ long long warp_s[kT / 32 + 1];
-  __shared__ long long found_s[2];
+__device__ __forceinline__ Line find_run(const AttnParams &p, long long (&warp_s)[kT / 32],
+                                         long long (&found_s)[2]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.S.B + kT - 1) / kT;
   const int b0 = min(tid * per, p.S.B), b1 = min(b0 + per, p.S.B);
@@ -296,5 +296,86 @@ struct F16 {
   }
   static constexpr uint32_t kExp = 0x7C00u;
 };
+
+// Four outputs of one row: stored as the cache's type.
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(Bf16::pack(v.x, v.y), Bf16::pack(v.z, v.w));
+}
+__device__ __forceinline__ void store4(__half *p, float4 v) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(F16::pack(v.x, v.y), F16::pack(v.z, v.w));
+}
+__device__ __forceinline__ float as_f32(float x) { return x; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_f32(__half x) { return __half2float(x); }
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t to, const char *from, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int n>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+// A 32-bit word of two 16-bit values with infinities and NaNs set to zero.
+template <class E>
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t v) {
+  if ((v & E::kExp) == E::kExp) v &= 0xFFFF0000u;
+  if (((v >> 16) & E::kExp) == E::kExp) v &= 0xFFFFu;
+  return v;
+}
+
+// Address of row r of a unit in [B, N, Hq] rows.
+__device__ __forceinline__ long long out_row(const AttnParams &p, int b, int h, int r) {
+  const int n = r / p.G, g = r - n * p.G;
+  return (static_cast<long long>(b) * p.S.N + n) * (p.C.heads * p.G) + h * p.G + g;
+}
+
+// ln of the weights' sum, from m and l of a row (base 2).
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+// Keys whose values hold infinities or NaNs, in slices that some row does not
+// see whole: their values entered the products as zero, so that 0 * inf does
+// not reach rows that do not see them.  What they add to the rows that do is an
+// infinity or a NaN whatever the weight, and is added here: four outputs of
+// token n, from the slices (kSlice keys) of tiles [i0, i1).  Reached only when
+// such a value was found.
+template <class TE, int kSlice>
+static __device__ __noinline__ float4 nonfinite_values(const AttnParams &p, const UnitWalk &u, int n,
+                                                int d, float4 acc) {
+  float *a = reinterpret_cast<float *>(&acc);
+  for (int i = u.i0; i < u.i1; ++i) {
+    const int t0 = key_tile(u.k, i) * p.tile;
+    for (int at0 = t0; at0 < t0 + p.tile && at0 < u.k.end; at0 += kSlice) {
+      bool whole = all_seen(p, u.k, u.r0, at0, kSlice);
+      for (int at = at0; at < at0 + kSlice && whole; ++at)
+        whole = at < u.k.end && page_ok(p.C, page_at(p.S, u.b, at / p.C.page_size));
+      if (whole) continue;
+      for (int at = at0; at < min(at0 + kSlice, u.k.end); ++at) {
+        const int index = at / p.C.page_size, page = page_at(p.S, u.b, index);
+        if (!page_ok(p.C, page) || !sees(p, u.k, u.b, n, at)) continue;
+        const TE *v = reinterpret_cast<const TE *>(p.C.v + page * p.C.v_page +
+                                                   (at - index * p.C.page_size) * p.C.v_token +
+                                                   u.h * p.C.v_head);
+        for (int j = 0; j < 4; ++j) {
+          const float x = as_f32(v[d + j]);
+          if (!isfinite(x)) a[j] += x;
+        }
+      }
+    }
+  }
+  return acc;
+}
 
 }  // namespace sv

@@ -121,7 +121,7 @@ struct Rows16 {
 };
 
 template <class E, int DP, int KT, int ST>
-__global__ void __launch_bounds__(kAttnThreads) rows16_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel(const __grid_constant__ AttnParams p) {
   using L = Rows16<DP, KT, ST>;
   using TE = typename E::T;
   extern __shared__ __align__(128) char smem[];
@@ -388,7 +388,7 @@ struct Rows8 {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kAttnThreads) rows8_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_constant__ AttnParams p) {
   using L = Rows8<DP>;
   constexpr int KT = L::KT, ST = L::ST, R = 8;
   extern __shared__ __align__(128) char smem[];
@@ -673,18 +673,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 
 struct AttnPlan {
   int ctas, rows, tile;
-  bool wide;
 };
 
-AttnPlan attention_plan(int N, int G, int D, int dtype) {
+AttnPlan narrow_plan(int D, int dtype) {
   if (dtype == SPEC_F32)
     return {kSms, 8,
-            D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile), false};
-  if (N * G > 16 && (D == 64 || D == 128)) return {kSms, N * G > 128 ? 256 : 128, 128, true};
-  if (D <= 64) return {2 * kSms, 16, Rows16<64, 32, 3>::kTile, false};
-  if (D <= 128) return {2 * kSms, 16, Rows16<128, 16, 3>::kTile, false};
-  return {kSms, 16, Rows16<256, 16, 3>::kTile, false};
+            D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile)};
+  if (D <= 64) return {2 * kSms, 16, Rows16<64, 32, 3>::kTile};
+  if (D <= 128) return {2 * kSms, 16, Rows16<128, 16, 3>::kTile};
+  return {kSms, 16, Rows16<256, 16, 3>::kTile};
 }
+
+bool wide_sizes(int G, int D, int dtype) {
+  return dtype != SPEC_F32 && (D == 64 || D == 128) && G <= 128;
+}
+int wide_tiles(int N, int G) { return N * G > wide_tile_rows(G) ? 2 : 1; }
+AttnPlan wide_plan(int N, int G) { return {kSms, wide_tiles(N, G) * wide_tile_rows(G), 128}; }
 
 template <class K>
 cudaError_t start(K kernel, size_t smem, const AttnParams &p, cudaStream_t stream) {
@@ -706,14 +710,23 @@ size_t align16(size_t x) { return (x + 15) / 16 * 16; }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int N, int G, int D, int dtype) {
-  const AttnPlan plan = attention_plan(N, G, D, dtype);
+size_t plan_bytes(const AttnPlan &plan, int D) {
   return align16(plan.ctas * sizeof(JoinDesc)) +
          2 * plan.ctas * slot_floats(plan.rows, D) * sizeof(float);
 }
 
+size_t attention_workspace_bytes(int N, int G, int D, int dtype) {
+  const size_t narrow = plan_bytes(narrow_plan(D, dtype), D);
+  const size_t wide = wide_sizes(G, D, dtype) ? plan_bytes(wide_plan(N, G), D) : 0;
+  return narrow > wide ? narrow : wide;
+}
+
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream) {
-  const AttnPlan plan = attention_plan(p.S.N, p.G, p.D, dtype);
+  const int P = p.C.page_size;
+  WideMaps maps;
+  const bool wide = wide_sizes(p.G, p.D, dtype) && (P % 128 == 0 || (P >= 8 && 128 % P == 0)) &&
+                    wide_maps(p, dtype, &maps);
+  const AttnPlan plan = wide ? wide_plan(p.S.N, p.G) : narrow_plan(p.D, dtype);
   p.ctas = plan.ctas;
   p.rows = plan.rows;
   p.tile = plan.tile;
@@ -730,8 +743,8 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
     } else {
       e = start(rows8_kernel<256>, Rows8<256>::kSmem, p, stream);
     }
-  } else if (plan.wide) {
-    e = launch_attention_wide(p, dtype, stream);
+  } else if (wide) {
+    e = launch_attention_wide(p, wide_tiles(p.S.N, p.G), maps, dtype, stream);
   } else {
     e = dtype == SPEC_BF16 ? start16<Bf16>(p, stream) : start16<F16>(p, stream);
   }

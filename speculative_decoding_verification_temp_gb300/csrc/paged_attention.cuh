@@ -14,6 +14,7 @@
 // the lengths, so a captured launch follows lengths that change.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -51,8 +52,19 @@ struct JoinDesc {
 
 size_t attention_workspace_bytes(int N, int G, int D, int dtype);
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream);
-// Units of 128 or 256 rows (p.rows), head_dim 64 or 128, 16-bit types.
-cudaError_t launch_attention_wide(const AttnParams &p, int dtype, cudaStream_t stream);
+// The form on tensor memory: `tiles` (1 or 2) tiles of wide_tile_rows(G) rows
+// per unit, head_dim 64 or 128, 16-bit types.  wide_maps: false where the
+// tensors cannot be described to TMA.
+struct WideMaps {
+  CUtensorMap k, v, q;
+  // coordinate of a box: page * k_page + head * k_head + token * k_token, ...
+  int k_page, k_head, k_token, v_page, v_head, v_token, q_seq, q_head;
+};
+// Rows of a tile: whole tokens, at most 128 rows.
+inline int wide_tile_rows(int G) { return 128 / G * G; }
+bool wide_maps(const AttnParams &p, int dtype, WideMaps *maps);
+cudaError_t launch_attention_wide(const AttnParams &p, int tiles, const WideMaps &maps, int dtype,
+                                  cudaStream_t stream);
 
 // The keys that the rows [r0, r0 + R) of sequence b may see: tiles
 // [0, sink_tiles) and then `lo` and those behind it; at least one tile, which
@@ -281,6 +293,7 @@ __device__ __forceinline__ bool all_seen(const AttnParams &p, const KeyRange &k,
 struct Bf16 {
   using T = __nv_bfloat16;
   static __device__ __forceinline__ float to(T x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ T from(float x) { return __float2bfloat16_rn(x); }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -290,6 +303,7 @@ struct Bf16 {
 struct F16 {
   using T = __half;
   static __device__ __forceinline__ float to(T x) { return __half2float(x); }
+  static __device__ __forceinline__ T from(float x) { return __float2half_rn(x); }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);
@@ -352,7 +366,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // token n, from the slices (kSlice keys) of tiles [i0, i1).  Reached only when
 // such a value was found.
 template <class TE, int kSlice>
-static __device__ __noinline__ float4 nonfinite_values(const AttnParams &p, const UnitWalk &u, int n,
+static __device__ __noinline__ float4 nonfinite_values(const AttnParams &p, const UnitWalk u, int n,
                                                 int d, float4 acc) {
   float *a = reinterpret_cast<float *>(&acc);
   for (int i = u.i0; i < u.i1; ++i) {

@@ -12,6 +12,8 @@
 // A weight is 2^(s c - m) with c = scale log2(e) and m the running maximum of
 // s c, rounded once and then used as it is: the weights of all keys, the sums
 // and the logarithm refer to the same float32 m.
+#include <algorithm>
+
 #include "paged_attention.cuh"
 
 namespace sv {
@@ -21,7 +23,7 @@ namespace {
 constexpr int kSms = 152;       // GB300
 constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = 4;
-constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = 128, kJoinRows = 4;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -61,10 +63,10 @@ __device__ __forceinline__ void mma<F16>(float (&c)[4], const uint32_t (&a)[4], 
 template <class TE, int R, int DP, int kSlice>
 __device__ __forceinline__ void write_unit(const AttnParams &p, const UnitWalk &u,
                                            const float *o_s, int warp_floats,
-                                           const float (*ml_s)[2][R], bool bad) {
+                                           const float (*ml_s)[2][R], bool bad, int worker) {
   const int live = u.live_rows(p);
   const bool whole = u.whole();
-  float *slot = p.part + piece_slot(u) * slot_floats(p.rows, p.D);
+  float *slot = p.part + piece_slot(u, worker) * slot_floats(p.rows, p.D);
   for (int i = threadIdx.x; i < R * (DP / 4); i += kAttnThreads) {
     const int row = i / (DP / 4), d = i % (DP / 4) * 4;
     if (row >= live || d >= p.D) continue;
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
   __shared__ float ml_s[kAttnWarps][2][16];
   __shared__ uint32_t valid_s[kAttnWarps][ST];
   __shared__ int bad_s;
-  __shared__ long long warp_s[kAttnWarps], found_s[2];
+  __shared__ RunScratch<kAttnThreads, 1> run_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   char *q_s = smem;
   char *ring = smem + 16 * L::kRow + warp * L::kRing;
@@ -139,15 +141,14 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
       reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
   }
   if (tid == 0) bad_s = 0;
-  const Line line = find_run<kAttnThreads>(p, warp_s, found_s);
+  Line lines[1];
+  find_runs(p, run_s, blockIdx.x, 0, lines);
+  const Line &line = lines[0];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (line.w0 == line.w1) {
-    if (tid == 0) write_join(p, line, nullptr);
-    return;
-  }
   UnitWalk u;
-  u.start(p, line);
-  if (tid == 0) write_join(p, line, &u);
+  const bool busy = u.start(p, line);
+  if (tid == 0) write_join(p, line, busy ? &u : nullptr);
+  if (!busy) return;
 
   // piece of a row that this lane copies, and the row of it among each batch
   constexpr int kPieces = DP / 8, kBatch = 32 / kPieces;
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
   const bool has_piece = piece * 8 < p.D;
   const float c = p.scale_log2;
 
-  for (long long w = line.w0;;) {
+  for (;;) {
     // this lane's key of the next tile to copy
     int pid = -1, in_page = 0;
     auto look_up = [&](int i) {
@@ -351,9 +352,8 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
     if (bad) bad_s = 1;
     __syncthreads();
     write_unit<TE, 16, DP, KT>(p, u, reinterpret_cast<const float *>(smem + 16 * L::kRow),
-                               L::kRing / 4, ml_s, bad_s != 0);
-    w += u.i1 - u.i0;
-    if (w >= line.w1) break;
+                               L::kRing / 4, ml_s, bad_s != 0, line.worker);
+    if (!u.next(p, line)) break;
     __syncthreads();
     if (tid == 0) bad_s = 0;
     if (p.D < DP) {
@@ -362,7 +362,6 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
         reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
       __syncwarp();
     }
-    u.next(p, line);
   }
 }
 
@@ -395,7 +394,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_con
   __shared__ float ml_s[kAttnWarps][2][R];
   __shared__ uint32_t valid_s[kAttnWarps][ST];
   __shared__ int bad_s;
-  __shared__ long long warp_s[kAttnWarps], found_s[2];
+  __shared__ RunScratch<kAttnThreads, 1> run_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *q_s = reinterpret_cast<float *>(smem);
   char *rings = smem + R * DP * 4;
@@ -403,15 +402,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_con
   float *p_s = reinterpret_cast<float *>(rings + kAttnWarps * L::kRing) + warp * KT * R;
   const uint32_t ring_at = smem_u32(ring);
   if (tid == 0) bad_s = 0;
-  const Line line = find_run<kAttnThreads>(p, warp_s, found_s);
+  Line lines[1];
+  find_runs(p, run_s, blockIdx.x, 0, lines);
+  const Line &line = lines[0];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (line.w0 == line.w1) {
-    if (tid == 0) write_join(p, line, nullptr);
-    return;
-  }
   UnitWalk u;
-  u.start(p, line);
-  if (tid == 0) write_join(p, line, &u);
+  const bool busy = u.start(p, line);
+  if (tid == 0) write_join(p, line, busy ? &u : nullptr);
+  if (!busy) return;
 
   constexpr int kPieces = DP / 4;                            // of a row, 16 bytes each
   constexpr int kLanes = kPieces < 32 ? kPieces : 32;        // lanes on one row
@@ -421,7 +419,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_con
   const float c = p.scale_log2;
   const int key = lane % KT, part = lane / KT;
 
-  for (long long w = line.w0;;) {
+  for (;;) {
     auto copy_tile = [&](int i) {
       if (i < u.i1) {
         const int st = (i - u.i0) % ST;
@@ -598,12 +596,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_con
     if (bad) bad_s = 1;
     __syncthreads();
     write_unit<float, R, DP, KT>(p, u, reinterpret_cast<const float *>(rings), L::kRing / 4, ml_s,
-                                 bad_s != 0);
-    w += u.i1 - u.i0;
-    if (w >= line.w1) break;
+                                 bad_s != 0, line.worker);
+    if (!u.next(p, line)) break;
     __syncthreads();
     if (tid == 0) bad_s = 0;
-    u.next(p, line);
   }
 }
 
@@ -611,60 +607,123 @@ __global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_con
 // the join
 // ---------------------------------------------------------------------------
 
-// One warp per row of a cut unit: its pieces in the order of their keys.
+// The rows of a cut unit, kJoinRows per CTA.  Units of few pieces: a warp per
+// row.  Units of many: the CTA's warps share the pieces of one row after the
+// other, and their sums are added in order.  A warp has eight pieces in flight.
 template <class TE>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float m_s[kWarps], l_s[kWarps];
+  __shared__ float4 o_s[kWarps][64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.y * kJoinWarps + warp;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinDesc d = p.join[blockIdx.x];
   if (d.pieces_end < 0) return;
-  if (d.r0 + row >= seq_new(p.S, d.b) * p.G || row >= p.rows) return;
+  const int rows = min(p.rows, seq_new(p.S, d.b) * p.G - d.r0);
   const int first = static_cast<int>(blockIdx.x) - 1, count = d.pieces_end - first + 1;
   const size_t per_slot = slot_floats(p.rows, p.D);
   auto slot = [&](int i) { return p.part + (2 * (first + i) + (i == 0 ? 1 : 0)) * per_slot; };
-  float M = -INFINITY;
-  for (int i = lane; i < count; i += 32) M = fmaxf(M, slot(i)[row]);
+  // pieces from, from + step, ... of a row
+  auto gather = [&](int row, int from, int step, float &M, float &l, float4 (&o)[2]) {
+    M = -INFINITY;
+    l = 0.f;
+    o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = from; i0 < count; i0 += 8 * step) {
+      float m[8], lp[8];
+      float4 v[8][2];
+      float top = M;
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
-  float l = 0.f;
-  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int i0 = 0; i0 < count; i0 += 32) {
-    float f = 0.f, lp = 0.f;
-    if (i0 + lane < count) {
-      const float *s = slot(i0 + lane);
-      const float m = s[row];
-      if (m != -INFINITY) {
-        f = fast_exp2(m - M);
-        lp = f * s[p.rows + row];
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * step;
+        m[j] = -INFINITY;
+        if (i >= count) continue;
+        const float *s = slot(i);
+        m[j] = s[row];
+        lp[j] = s[p.rows + row];
+        const float *from_o = s + 2 * p.rows + static_cast<size_t>(row) * p.D;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if ((lane + 32 * x) * 4 < p.D)
+            v[j][x] = *reinterpret_cast<const float4 *>(from_o + (lane + 32 * x) * 4);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, m[j]);
+      if (M > -INFINITY && top > M) {
+        const float f = fast_exp2(M - top);
+        l *= f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) o[x].x *= f, o[x].y *= f, o[x].z *= f, o[x].w *= f;
+      }
+      M = top;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (m[j] == -INFINITY) continue;
+        const float f = fast_exp2(m[j] - M);
+        l += f * lp[j];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if ((lane + 32 * x) * 4 >= p.D) continue;
+          o[x].x += f * v[j][x].x;
+          o[x].y += f * v[j][x].y;
+          o[x].z += f * v[j][x].z;
+          o[x].w += f * v[j][x].w;
+        }
       }
     }
-    for (int j = 0; j < min(32, count - i0); ++j) {
-      const float w = __shfl_sync(0xFFFFFFFFu, f, j);
-      l += __shfl_sync(0xFFFFFFFFu, lp, j);
-      const float *s = slot(i0 + j) + 2 * p.rows + static_cast<size_t>(row) * p.D;
+  };
+  auto finish = [&](int row, float M, float l, const float4 (&o)[2]) {
+    const long long at = out_row(p, d.b, d.h, d.r0 + row);
+    const float r = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int at = (lane + 32 * x) * 4;
-        if (at >= p.D) continue;
-        const float4 v = *reinterpret_cast<const float4 *>(s + at);
-        o[x].x += w * v.x;
-        o[x].y += w * v.y;
-        o[x].z += w * v.z;
-        o[x].w += w * v.w;
-      }
+    for (int x = 0; x < 2; ++x) {
+      const int e = (lane + 32 * x) * 4;
+      if (e < p.D)
+        store4(static_cast<TE *>(p.out) + at * p.D + e,
+               make_float4(o[x].x * r, o[x].y * r, o[x].z * r, o[x].w * r));
     }
+    if (lane == 0 && p.lse) p.lse[at] = row_lse(M, l);
+  };
+  const int row0 = blockIdx.y * kJoinRows;
+  float M, l;
+  float4 o[2];
+  if (count <= 16) {
+    for (int row = row0 + warp; row < min(row0 + kJoinRows, rows); row += kWarps) {
+      gather(row, 0, 1, M, l, o);
+      finish(row, M, l, o);
+    }
+    return;
   }
-  const long long at = out_row(p, d.b, d.h, d.r0 + row);
-  const float r = l == 0.f ? 0.f : 1.f / l;
+  for (int row = row0; row < min(row0 + kJoinRows, rows); ++row) {
+    gather(row, warp, kWarps, M, l, o);
+    if (lane == 0) {
+      m_s[warp] = M;
+      l_s[warp] = l;
+    }
+    o_s[warp][lane] = o[0];
+    o_s[warp][lane + 32] = o[1];
+    __syncthreads();
+    if (warp == 0) {
+      M = fmaxf(fmaxf(m_s[0], m_s[1]), fmaxf(m_s[2], m_s[3]));
+      l = 0.f;
+      o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int e = (lane + 32 * x) * 4;
-    if (e < p.D)
-      store4(static_cast<TE *>(p.out) + at * p.D + e,
-             make_float4(o[x].x * r, o[x].y * r, o[x].z * r, o[x].w * r));
+      for (int w = 0; w < kWarps; ++w) {
+        if (m_s[w] == -INFINITY) continue;
+        const float f = fast_exp2(m_s[w] - M);
+        l += f * l_s[w];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float4 v = o_s[w][lane + 32 * x];
+          o[x].x += f * v.x;
+          o[x].y += f * v.y;
+          o[x].z += f * v.z;
+          o[x].w += f * v.w;
+        }
+      }
+      finish(row, M, l, o);
+    }
+    __syncthreads();
   }
-  if (lane == 0 && p.lse) p.lse[at] = row_lse(M, l);
 }
 
 // ---------------------------------------------------------------------------
@@ -672,30 +731,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 // ---------------------------------------------------------------------------
 
 struct AttnPlan {
-  int ctas, rows, tile;
+  int workers, rows, tile, unit_cost;
 };
 
 AttnPlan narrow_plan(int D, int dtype) {
   if (dtype == SPEC_F32)
     return {kSms, 8,
-            D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile)};
-  if (D <= 64) return {2 * kSms, 16, Rows16<64, 32, 3>::kTile};
-  if (D <= 128) return {2 * kSms, 16, Rows16<128, 16, 3>::kTile};
-  return {kSms, 16, Rows16<256, 16, 3>::kTile};
+            D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile), 1};
+  if (D <= 64) return {2 * kSms, 16, Rows16<64, 32, 3>::kTile, 1};
+  if (D <= 128) return {2 * kSms, 16, Rows16<128, 16, 3>::kTile, 1};
+  return {kSms, 16, Rows16<256, 16, 3>::kTile, 1};
 }
 
 bool wide_sizes(int G, int D, int dtype) {
   return dtype != SPEC_F32 && (D == 64 || D == 128) && G <= 128;
 }
-int wide_tiles(int N, int G) { return N * G > wide_tile_rows(G) ? 2 : 1; }
-AttnPlan wide_plan(int N, int G) { return {kSms, wide_tiles(N, G) * wide_tile_rows(G), 128}; }
+AttnPlan wide_plan(int N, int G) {
+  // two row tiles that share their keys, or a row tile for each of two streams
+  if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 128, 2};
+  return {2 * kSms, wide_tile_rows(G), 128, 1};
+}
 
 template <class K>
 cudaError_t start(K kernel, size_t smem, const AttnParams &p, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  kernel<<<p.ctas, kAttnThreads, smem, stream>>>(p);
+  kernel<<<p.workers, kAttnThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -711,8 +773,8 @@ size_t align16(size_t x) { return (x + 15) / 16 * 16; }
 }  // namespace
 
 size_t plan_bytes(const AttnPlan &plan, int D) {
-  return align16(plan.ctas * sizeof(JoinDesc)) +
-         2 * plan.ctas * slot_floats(plan.rows, D) * sizeof(float);
+  return align16(plan.workers * sizeof(JoinDesc)) +
+         2 * plan.workers * slot_floats(plan.rows, D) * sizeof(float);
 }
 
 size_t attention_workspace_bytes(int N, int G, int D, int dtype) {
@@ -723,17 +785,23 @@ size_t attention_workspace_bytes(int N, int G, int D, int dtype) {
 
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream) {
   const int P = p.C.page_size;
+  auto take = [&](const AttnPlan &plan) {
+    p.workers = plan.workers;
+    p.rows = plan.rows;
+    p.tile = plan.tile;
+    p.unit_cost = plan.unit_cost;
+    p.min_run = 1;
+  };
   WideMaps maps;
-  const bool wide = wide_sizes(p.G, p.D, dtype) && (P % 128 == 0 || (P >= 8 && 128 % P == 0)) &&
-                    wide_maps(p, dtype, &maps);
-  const AttnPlan plan = wide ? wide_plan(p.S.N, p.G) : narrow_plan(p.D, dtype);
-  p.ctas = plan.ctas;
-  p.rows = plan.rows;
-  p.tile = plan.tile;
-  p.min_tiles = 1;
+  bool wide = wide_sizes(p.G, p.D, dtype) && (P % 128 == 0 || (P >= 8 && 128 % P == 0));
+  if (wide) {
+    take(wide_plan(p.S.N, p.G));
+    wide = wide_maps(p, dtype, &maps);
+  }
+  if (!wide) take(narrow_plan(p.D, dtype));
   p.join = static_cast<JoinDesc *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                     align16(plan.ctas * sizeof(JoinDesc)));
+                                     align16(p.workers * sizeof(JoinDesc)));
   cudaError_t e;
   if (dtype == SPEC_F32) {
     if (p.D <= 64) {
@@ -744,16 +812,17 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
       e = start(rows8_kernel<256>, Rows8<256>::kSmem, p, stream);
     }
   } else if (wide) {
-    e = launch_attention_wide(p, wide_tiles(p.S.N, p.G), maps, dtype, stream);
+    e = launch_attention_wide(p, maps, dtype, stream);
   } else {
     e = dtype == SPEC_BF16 ? start16<Bf16>(p, stream) : start16<F16>(p, stream);
   }
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.ctas, (p.rows + kJoinWarps - 1) / kJoinWarps);
-  if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinWarps * 32, 0, stream, p);
+  // no unit has more rows than a sequence
+  const dim3 grid(p.workers, (std::min(p.rows, p.S.N * p.G) + kJoinRows - 1) / kJoinRows);
+  if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinThreads, 0, stream, p);
   if (dtype == SPEC_BF16)
-    return launch_behind(join_kernel<__nv_bfloat16>, grid, kJoinWarps * 32, 0, stream, p);
-  return launch_behind(join_kernel<__half>, grid, kJoinWarps * 32, 0, stream, p);
+    return launch_behind(join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, stream, p);
+  return launch_behind(join_kernel<__half>, grid, kJoinThreads, 0, stream, p);
 }
 
 }  // namespace sv

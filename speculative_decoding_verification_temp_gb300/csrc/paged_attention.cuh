@@ -4,14 +4,16 @@
 // group of query heads that read this head: row r is token r / G, query head
 // h * G + r % G.  A unit is a tile of R rows with all the keys that one of them
 // may see, cut into tiles of T keys.  The units' key tiles, laid end to end
-// (sequences, then heads, then row tiles), are one line of work that is cut
-// into equal runs, one per CTA, whatever the lengths of the sequences are: a
-// CTA's run holds whole units, which it finishes, and at most one unit's end
-// and one unit's beginning, which it leaves as partial results (running
-// maximum, sum and unnormalised output of each row).  A second kernel joins
-// the partial results of each unit that was cut, in the order of its keys, so
-// results do not depend on timing.  The line is laid out on the device from
-// the lengths, so a captured launch follows lengths that change.
+// (sequences, then heads, then row tiles; a unit's end takes some places more,
+// for what a unit costs beside its keys), are one line of work that is cut into
+// equal runs, one per worker (a CTA, or one of its two streams), whatever the
+// lengths of the sequences are: a worker's run holds whole units, which it
+// finishes, and at most one unit's end and one unit's beginning, which it leaves
+// as partial results (running maximum, sum and unnormalised output of each row).
+// A second kernel joins the partial results of each unit that was cut, in the
+// order of its keys, so results do not depend on timing.  The line is laid out
+// on the device from the lengths, so a captured launch follows lengths that
+// change.
 #pragma once
 
 #include <cuda.h>
@@ -38,22 +40,24 @@ struct AttnParams {
   void *out;
   float *lse;
   uint32_t *flags;
-  float *part;  // partial results, two slots per CTA
+  float *part;  // partial results, two slots per worker
   struct JoinDesc *join;
-  int ctas, rows, tile;  // R and T
-  int min_tiles;         // a CTA's run is at least this long (where there is as much)
+  int workers, rows, tile;  // at most; R and T
+  int unit_cost;            // places on the line behind a unit's key tiles
+  int min_run;              // a worker's run is at least this long (where there is as much)
 };
 
-// A cut unit, written by the CTA that holds its first cut; its pieces are those
-// of CTAs cta - 1 .. pieces_end.  pieces_end -1: no unit's cuts start here.
+// A cut unit, written by the worker that holds its first cut; its pieces are
+// those of the worker before it .. pieces_end.  pieces_end -1: no unit's cuts
+// start here.
 struct JoinDesc {
   int b, h, r0, pieces_end;
 };
 
 size_t attention_workspace_bytes(int N, int G, int D, int dtype);
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream);
-// The form on tensor memory: `tiles` (1 or 2) tiles of wide_tile_rows(G) rows
-// per unit, head_dim 64 or 128, 16-bit types.  wide_maps: false where the
+// The form on tensor memory: one or two tiles of wide_tile_rows(G) rows per unit
+// (p.rows), head_dim 64 or 128, 16-bit types.  wide_maps: false where the
 // tensors cannot be described to TMA.
 struct WideMaps {
   CUtensorMap k, v, q;
@@ -63,7 +67,7 @@ struct WideMaps {
 // Rows of a tile: whole tokens, at most 128 rows.
 inline int wide_tile_rows(int G) { return 128 / G * G; }
 bool wide_maps(const AttnParams &p, int dtype, WideMaps *maps);
-cudaError_t launch_attention_wide(const AttnParams &p, int tiles, const WideMaps &maps, int dtype,
+cudaError_t launch_attention_wide(const AttnParams &p, const WideMaps &maps, int dtype,
                                   cudaStream_t stream);
 
 // The keys that the rows [r0, r0 + R) of sequence b may see: tiles
@@ -98,29 +102,39 @@ __device__ __forceinline__ int key_tile(const KeyRange &k, int i) {
   return i < k.sink_tiles ? i : k.lo + i - k.sink_tiles;
 }
 
-// Key tiles of one head of a sequence.
+// Places of one head of a sequence.
 __device__ __forceinline__ long long head_work(const AttnParams &p, int ctx, int n_new, bool fits) {
   long long w = 0;
-  for (int r0 = 0; r0 < n_new * p.G; r0 += p.rows) w += key_range(p, ctx, n_new, fits, r0).count;
+  for (int r0 = 0; r0 < n_new * p.G; r0 += p.rows)
+    w += key_range(p, ctx, n_new, fits, r0).count + p.unit_cost;
   return w;
 }
 
+// A worker's run.
 struct Line {
-  long long w0, w1;     // this CTA's run
+  long long w0, w1;     // empty: no work
   long long total;
-  int ctas;             // CTAs with work
+  int worker, workers;  // of `workers` with work
   int b;                // the sequence that holds w0
   long long in_seq;     // w0 within it
 };
 
-__device__ __forceinline__ long long run_start(long long cta, long long total, int ctas) {
-  return cta * total / ctas;
+__device__ __forceinline__ long long run_start(long long worker, long long total, int workers) {
+  return worker * total / workers;
 }
 
-// The line of work, by all threads of the CTA (kT of them).
-template <int kT>
-__device__ __forceinline__ Line find_run(const AttnParams &p, long long (&warp_s)[kT / 32],
-                                         long long (&found_s)[2]) {
+// Shared memory that find_runs works in.
+template <int kT, int kW>
+struct RunScratch {
+  long long sums[kT / 32];
+  long long found[kW][2];
+};
+
+// The runs of kW workers of a CTA (first, first + step, ...), by all its kT
+// threads.
+template <int kT, int kW>
+__device__ __forceinline__ void find_runs(const AttnParams &p, RunScratch<kT, kW> &x, int first,
+                                          int step, Line (&L)[kW]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.S.B + kT - 1) / kT;
   const int b0 = min(tid * per, p.S.B), b1 = min(b0 + per, p.S.B);
@@ -129,46 +143,53 @@ __device__ __forceinline__ Line find_run(const AttnParams &p, long long (&warp_s
     const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
     mine += p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n));
   }
-  long long x = mine;
+  long long before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
+    const long long y = __shfl_up_sync(0xFFFFFFFFu, before, o);
+    if (lane >= o) before += y;
   }
-  if (lane == 31) warp_s[warp] = x;
+  if (lane == 31) x.sums[warp] = before;
   __syncthreads();
-  long long before = 0, total = 0;
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < kT / 32; ++w) {
-    const long long v = warp_s[w];
+    const long long v = x.sums[w];
     if (w < warp) before += v;
     total += v;
   }
-  before += x - mine;
-  Line L;
-  L.total = total;
-  const long long most = (total + p.min_tiles - 1) / p.min_tiles;
-  L.ctas = static_cast<int>(most < p.ctas ? (most > 0 ? most : 1) : p.ctas);
-  const bool busy = total > 0 && static_cast<int>(blockIdx.x) < L.ctas;
-  L.w0 = busy ? run_start(blockIdx.x, total, L.ctas) : 0;
-  L.w1 = busy ? run_start(blockIdx.x + 1ll, total, L.ctas) : 0;
-  if (busy && before <= L.w0 && L.w0 < before + mine) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
-      const long long w = p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n));
-      if (L.w0 < at + w) {
-        found_s[0] = b;
-        found_s[1] = L.w0 - at;
-        break;
+  before -= mine;
+  const long long most = (total + p.min_run - 1) / p.min_run;
+  const int workers = static_cast<int>(most < p.workers ? (most > 0 ? most : 1) : p.workers);
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    L[i].total = total;
+    L[i].workers = workers;
+    L[i].worker = first + i * step;
+    const bool busy = total > 0 && L[i].worker < workers;
+    L[i].w0 = busy ? run_start(L[i].worker, total, workers) : 0;
+    L[i].w1 = busy ? run_start(L[i].worker + 1ll, total, workers) : 0;
+    if (busy && before <= L[i].w0 && L[i].w0 < before + mine) {
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
+        const long long w = p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n));
+        if (L[i].w0 < at + w) {
+          x.found[i][0] = b;
+          x.found[i][1] = L[i].w0 - at;
+          break;
+        }
+        at += w;
       }
-      at += w;
     }
   }
   __syncthreads();
-  L.b = busy ? static_cast<int>(found_s[0]) : 0;
-  L.in_seq = busy ? found_s[1] : 0;
-  return L;
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    const bool busy = L[i].w0 < L[i].w1;
+    L[i].b = busy ? static_cast<int>(x.found[i][0]) : 0;
+    L[i].in_seq = busy ? x.found[i][1] : 0;
+  }
 }
 
 // Walks the units of a run.
@@ -176,7 +197,7 @@ struct UnitWalk {
   int b, h, r0;
   KeyRange k;
   bool fits;
-  long long a;    // the unit's first tile on the line
+  long long a;    // the unit's first place on the line
   int i0, i1;     // the run's tiles of the unit
 
   __device__ __forceinline__ void load_seq(const AttnParams &p) {
@@ -184,7 +205,9 @@ struct UnitWalk {
     k.n_new = seq_new(p.S, b);
     fits = seq_fits(p.S, p.C, k.ctx, k.n_new);
   }
-  __device__ __forceinline__ void start(const AttnParams &p, const Line &L) {
+  // The first unit; false: the run has no tiles.
+  __device__ __forceinline__ bool start(const AttnParams &p, const Line &L) {
+    if (L.w0 == L.w1) return false;
     b = L.b;
     load_seq(p);
     const long long per_head = head_work(p, k.ctx, k.n_new, fits);
@@ -192,16 +215,18 @@ struct UnitWalk {
     long long left = L.in_seq - h * per_head;
     for (r0 = 0;; r0 += p.rows) {
       k = key_range(p, k.ctx, k.n_new, fits, r0);
-      if (left < k.count) break;
-      left -= k.count;
+      if (left < k.count + p.unit_cost) break;
+      left -= k.count + p.unit_cost;
     }
     a = L.w0 - left;
     i0 = static_cast<int>(left);
     i1 = static_cast<int>(min(static_cast<long long>(k.count), L.w1 - a));
+    return i0 < i1 || next(p, L);
   }
-  // The next unit; the caller has checked that the run goes on behind this one.
-  __device__ __forceinline__ void next(const AttnParams &p, const Line &L) {
-    a += k.count;
+  // The next unit; false: the run ends before it.
+  __device__ __forceinline__ bool next(const AttnParams &p, const Line &L) {
+    a += k.count + p.unit_cost;
+    if (a >= L.w1) return false;
     r0 += p.rows;
     if (r0 >= k.n_new * p.G) {
       r0 = 0;
@@ -216,6 +241,7 @@ struct UnitWalk {
     k = key_range(p, k.ctx, k.n_new, fits, r0);
     i0 = 0;
     i1 = static_cast<int>(min(static_cast<long long>(k.count), L.w1 - a));
+    return true;
   }
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == k.count; }
   // Rows of the unit that exist.
@@ -224,29 +250,30 @@ struct UnitWalk {
   }
 };
 
-// Slot of the workspace for this CTA's piece of a cut unit.
-__device__ __forceinline__ int piece_slot(const UnitWalk &u) {
-  return 2 * blockIdx.x + (u.i0 > 0 ? 0 : 1);
+// Slot of the workspace for a worker's piece of a cut unit.
+__device__ __forceinline__ int piece_slot(const UnitWalk &u, int worker) {
+  return 2 * worker + (u.i0 > 0 ? 0 : 1);
 }
 __host__ __device__ __forceinline__ size_t slot_floats(int R, int D) {
   return static_cast<size_t>(R) * (D + 2);
 }
 
-// Writes this CTA's join descriptor, before or after its run: the unit that its
-// first tile cuts, if no CTA before it cuts that unit.
+// Writes a worker's join descriptor: the unit that its first tile cuts, if no
+// worker before it cuts that unit.  u: its first unit, or NULL.
 __device__ __forceinline__ void write_join(const AttnParams &p, const Line &L, const UnitWalk *u) {
+  if (L.worker >= p.workers) return;
   JoinDesc d = {0, 0, 0, -1};
-  if (u && u->i0 > 0 && run_start(blockIdx.x - 1ll, L.total, L.ctas) <= u->a) {
+  if (u && u->i0 > 0 && run_start(L.worker - 1ll, L.total, L.workers) <= u->a) {
     d.b = u->b;
     d.h = u->h;
     d.r0 = u->r0;
     const long long last = u->a + u->k.count - 1;
-    long long c = last * L.ctas / L.total;  // the CTA that holds the last tile, or next to it
-    while (run_start(c, L.total, L.ctas) > last) --c;
-    while (c + 1 < L.ctas && run_start(c + 1, L.total, L.ctas) <= last) ++c;
+    long long c = last * L.workers / L.total;  // the worker of the last tile, or next to it
+    while (run_start(c, L.total, L.workers) > last) --c;
+    while (c + 1 < L.workers && run_start(c + 1, L.total, L.workers) <= last) ++c;
     d.pieces_end = static_cast<int>(c);
   }
-  p.join[blockIdx.x] = d;
+  p.join[L.worker] = d;
 }
 
 // The place of new token m behind the context, for windows.
@@ -360,11 +387,11 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 }
 
 // Keys whose values hold infinities or NaNs, in slices that some row does not
-// see whole: their values entered the products as zero, so that 0 * inf does
-// not reach rows that do not see them.  What they add to the rows that do is an
-// infinity or a NaN whatever the weight, and is added here: four outputs of
-// token n, from the slices (kSlice keys) of tiles [i0, i1).  Reached only when
-// such a value was found.
+// see whole: their values enter the products as zero where some row does not
+// see them, so that 0 * inf does not reach that row.  What they add to the rows
+// that do is an infinity or a NaN whatever the weight, and is added here: four
+// outputs of token n, from the slices (kSlice keys) of tiles [i0, i1).  Reached
+// only when such a value was found.
 template <class TE, int kSlice>
 static __device__ __noinline__ float4 nonfinite_values(const AttnParams &p, const UnitWalk u, int n,
                                                 int d, float4 acc) {

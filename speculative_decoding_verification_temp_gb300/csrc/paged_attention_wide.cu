@@ -1,31 +1,30 @@
 // Attention over a paged cache on the fifth-generation tensor cores: 16-bit
 // types, head_dim 64 or 128, pages of 8, 16, 32, 64 or a multiple of 128 tokens,
-// units of 128 or 256 rows (new tokens times the query heads of a group).
+// rows in tiles of at most 128 (new tokens times the query heads of a group).
 //
-// Two streams of work share a CTA: with 256 rows each takes half of the rows
-// and all key tiles, with 128 rows each takes all rows and every second key
-// tile, and their results are added at the end.  For a tile of 128 keys a
-// stream computes S = Q K^T into tensor memory (128 lanes of rows x 128
-// columns), one thread per row turns S into weights in place (the running
-// maximum, the sum, 2^(s c - m) packed into the first half of S's columns), and
-// O += P V takes them from there as the A operand.  While one stream is in its
-// softmax the other's products run.
+// For a tile of 128 keys a stream of work computes S = Q K^T into tensor memory
+// (128 lanes of rows x 128 columns); one thread per row turns S into weights in
+// place (the running maximum, the sum, 2^(s c - m) packed into the first half of
+// S's columns), and O += P V takes them from there as the A operand.  Two
+// streams share a CTA, so that the products of one run while the other is in its
+// softmax:
+//   solo_kernel  units of one row tile; each stream has units, keys and values
+//                of its own
+//   pair_kernel  units of two row tiles, one per stream, that share the keys and
+//                values
 //
-// Warps 0-3 and 4-7: the softmax of stream 0 and 1; warps without rows only
-// pass their barriers, so few rows cost few instructions.  Warps 8 and 9: keys
-// and values by TMA, one box per page, into a ring of entries of 128 rows; warp
-// 10: the queries' boxes.  One thread of warp 11 issues every product.  Copies
-// and products meet at mbarriers; every wait is bounded.
-//
-// Shared rows are 128-byte pieces in the 128-byte swizzle.  An entry of keys or
-// values is groups of eight tokens, each with its panels of 64 elements one
-// behind another, so that one box holds a page whole whatever its size; rows of
-// K are K-major for S = Q K^T, rows of V are N-major for O += P V, without a
-// transpose.  A tile of queries is its panels one behind another, rows token by
-// token with the group's heads, as many whole tokens as 128 rows hold.
+// Keys and values come by TMA, one box per page, into a ring of entries of 128
+// rows; every hand-over is an mbarrier, every wait is bounded.  Shared rows are
+// 128-byte pieces in the 128-byte swizzle.  An entry of keys or values is groups
+// of eight tokens, each with its panels of 64 elements one behind another, so
+// that one box holds a page whole whatever its size; rows of K are K-major for
+// S = Q K^T, rows of V are N-major for O += P V, without a transpose.  A tile of
+// queries is its panels one behind another, rows token by token with the
+// group's heads, as many whole tokens as 128 rows hold.
 //
 // One token is bound by HBM: 64 KB of keys and values a tile at head_dim 128
-// arrive in about 3000 cycles of an SM, their products take 512 of them.
+// arrive in about 3000 cycles of an SM, their products take 850 of them (Q K^T
+// reads both operands from shared memory, 64 cycles a step of 16).
 #include <climits>
 #include <numeric>
 
@@ -35,8 +34,7 @@ namespace sv {
 
 namespace {
 
-constexpr int kSoft = 256;          // softmax threads
-constexpr int kWideThreads = 384;   // three warpgroups
+constexpr int kWideThreads = 384;  // three warpgroups
 // Registers of a softmax thread and of the others: 2 * 128 * 208 + 128 * 88 are
 // the 384 * 168 that the CTA is launched with.
 constexpr int kSoftRegs = 208, kRestRegs = 88;
@@ -48,39 +46,15 @@ constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 // rescaled.  Weights above one have the same relative rounding.
 constexpr float kSlack = 8.f;
 
-template <int D, int NQ>
-struct WideShape {
-  static constexpr int kRow = 128;                    // bytes of a row in a panel
+// Bytes of an entry of 128 rows.
+template <int D>
+struct Entry {
+  static constexpr int kRow = 128;              // of a row in a panel
   static constexpr int kPanels = D / 64;
-  static constexpr int kPanel = 8 * kRow;             // 8 rows of 64 elements
-  static constexpr int kGroup = kPanels * kPanel;     // 8 rows
-  static constexpr int kEntry = kTileKeys / 8 * kGroup;
-  static constexpr int kQPanel = 128 * kRow;          // of queries: 128 rows
-  // queries of 256 rows, or of this unit and the next
-  static constexpr int kQ = 2 * kEntry;
-  static constexpr int kRing = D == 128 ? 5 : 12;  // what 227 KB hold beside them
+  static constexpr int kPanel = 8 * kRow;       // 8 rows of 64 elements
+  static constexpr int kGroup = kPanels * kPanel;
+  static constexpr int kBytes = kTileKeys / 8 * kGroup;
 };
-
-template <int D, int NQ>
-struct WideCtl {
-  using W = WideShape<D, NQ>;
-  unsigned long long full[W::kRing], empty[W::kRing], s_full[2], p_full[2], o_done[2], q_full[2],
-      q_empty[2], meet, drain;
-  long long warp_s[kWideThreads / 32], found_s[2];
-  alignas(16) uint32_t valid[kValidRing][4];
-  uint32_t tmem;
-  int dead, bad;
-  float ml[NQ == 1 ? 2 : 1][2][NQ == 1 ? 128 : 1];
-};
-
-template <int D, int NQ>
-constexpr int wide_smem() {
-  return WideShape<D, NQ>::kQ + WideShape<D, NQ>::kRing * WideShape<D, NQ>::kEntry +
-         static_cast<int>(sizeof(WideCtl<D, NQ>));
-}
-static_assert(wide_smem<128, 2>() <= 227 * 1024 && wide_smem<128, 1>() <= 227 * 1024 &&
-                  wide_smem<64, 2>() <= 227 * 1024 && wide_smem<64, 1>() <= 227 * 1024,
-              "shared memory of a CTA");
 
 __device__ __forceinline__ void bar_init(const void *bar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -168,6 +142,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 __device__ __forceinline__ void mma_commit(const void *bar) {
@@ -259,11 +242,6 @@ __device__ __forceinline__ constexpr uint32_t mma_idesc<F16>(int n, bool b_n_maj
          (8u << 24);
 }
 
-// Place in the order of a unit's entries, with 128 rows, of the values of its
-// tile i of n: K0 K1 V0 K2 V1 K3 ... V(n-2) V(n-1); the keys of tile i > 0 are
-// at 2 i - 1.  With 256 rows the order is K0 V0 K1 V1 ...
-__device__ __forceinline__ int value_entry(int i, int n) { return i + 1 < n ? 2 * i + 2 : 2 * i + 1; }
-
 // The top bit of each of two 16-bit values that is an infinity or a NaN.
 template <class E>
 __device__ __forceinline__ uint32_t nonfinite_bits(uint32_t v) {
@@ -313,505 +291,727 @@ __device__ __forceinline__ uint32_t seen_word(const AttnParams &p, const KeyRang
   return w | block;
 }
 
-}  // namespace
+// What a masked tile of values needs before its product: tokens that were not
+// copied (not in `valid`) become zero, and so do infinities and NaNs, which
+// nonfinite_values adds to the rows that see them.  Thread t of `threads`; tokens
+// from `from` on.
+template <class E, int D>
+__device__ __forceinline__ void clean_values(char *entry, uint4 valid, int from, int t, int threads,
+                                             int *bad) {
+  using W = Entry<D>;
+  bool found = false;
+#pragma unroll 4
+  for (int i = from / 8 * (W::kGroup / 16) + t; i < W::kBytes / 16; i += threads) {
+    uint4 *x = reinterpret_cast<uint4 *>(entry + i * 16);
+    const uint4 y = *x;
+    const int key = i / (W::kGroup / 16) * 8 + i / 8 % 8;
+    const uint32_t word = key < 64 ? (key < 32 ? valid.x : valid.y) : (key < 96 ? valid.z : valid.w);
+    if (!((word >> (key & 31)) & 1u)) {
+      *x = make_uint4(0, 0, 0, 0);
+    } else if (nonfinite_bits<E>(y.x) | nonfinite_bits<E>(y.y) | nonfinite_bits<E>(y.z) |
+               nonfinite_bits<E>(y.w)) {
+      *x = make_uint4(finite_or_zero<E>(y.x), finite_or_zero<E>(y.y), finite_or_zero<E>(y.z),
+                      finite_or_zero<E>(y.w));
+      found = true;
+    }
+  }
+  if (found) *reinterpret_cast<volatile int *>(bad) = 1;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 
-template <class E, int D, int NQ>
-__global__ void __launch_bounds__(kWideThreads, 1)
-    wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideMaps maps) {
-  using W = WideShape<D, NQ>;
-  using Ctl = WideCtl<D, NQ>;
+// The first token of a masked tile that clean_values has to look at: those
+// before it are copied and every row sees them.
+__device__ __forceinline__ int clean_from(const AttnParams &p, const KeyRange &k, int r0, int at0,
+                                          uint4 valid) {
+  if (p.window) return 0;
+  const int from = min(max((p.mask ? k.ctx : k.ctx + r0 / p.G + 1) - at0, 0), kTileKeys);
+  const uint32_t missing = (low_bits(from) & ~valid.x) | (low_bits(from - 32) & ~valid.y) |
+                           (low_bits(from - 64) & ~valid.z) | (low_bits(from - 96) & ~valid.w);
+  return missing ? 0 : from;
+}
+
+__device__ __forceinline__ bool tile_masked(const AttnParams &p, const UnitWalk &u, int at0,
+                                            uint4 valid) {
+  return (valid.x & valid.y & valid.z & valid.w) != 0xFFFFFFFFu ||
+         !all_seen(p, u.k, u.r0, at0, kTileKeys);
+}
+
+// One row per thread: the scores of a tile become weights, m and l go on, the
+// row's outputs so far are rescaled where m is raised (`first`: there are none).
+template <class E, int D>
+__device__ __forceinline__ void softmax_tile(const AttnParams &p, const UnitWalk &u, int n, bool mine,
+                                             bool masked, uint4 valid, int at0, uint32_t s_at,
+                                             uint32_t o_at, bool first, float &m, float &l) {
+  const float c = p.scale_log2;
+  tc_after();
+  uint32_t s[4][32];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) tm_load32(s[j], s_at + j * 32);
+  tm_wait_ld();
+  if (masked) {
+    const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t vis = seen_word(p, u.k, u.b, n, at0 + j * 32, in[j]);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!((vis >> e) & 1u)) s[j][e] = __float_as_uint(-INFINITY);
+    }
+  }
+  float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+      x[j] = max3(x[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
+  const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
+  const bool raise = mine && top > m + kSlack;
+  if (__any_sync(0xFFFFFFFFu, raise)) {
+    const float to = raise ? top : m;
+    const float f = m == -INFINITY ? 0.f : fast_exp2(m - to);
+    l *= f;
+    m = to;
+    if (!first) {
+      // the products before S's are complete: O is whole
+#pragma unroll 1
+      for (int d = 0; d < D; d += 16) {
+        uint32_t o[16];
+        tm_load16(o, o_at + d);
+        tm_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tm_store16(o_at + d, o);
+      }
+    }
+  }
+  const float sub = m == -INFINITY ? 0.f : -m;
+  const float2 c2 = make_float2(c, c), sub2 = make_float2(sub, sub);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t packed[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float2 y =
+          fma2(make_float2(__uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1])), c2, sub2);
+      y.x = fast_exp2(y.x);
+      y.y = fast_exp2(y.y);
+      sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+      // the product takes the weights in the cache's type: each is off by at
+      // most half a step of that type, as the values themselves are
+      packed[e / 2] = E::pack(y.x, y.y);
+    }
+    tm_store16(s_at + j * 16, packed);
+  }
+  sum[0] = add2(sum[0], sum[1]);
+  l += sum[0].x + sum[0].y;
+  tm_wait_st();
+}
+
+// Eight outputs of a row.
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  store4(p, make_float4(v[0], v[1], v[2], v[3]));
+  store4(p + 4, make_float4(v[4], v[5], v[6], v[7]));
+}
+template <class E>
+__device__ __forceinline__ void store8(typename E::T *p, const float (&v)[8]) {
+  *reinterpret_cast<uint4 *>(p) = make_uint4(E::pack(v[0], v[1]), E::pack(v[2], v[3]),
+                                             E::pack(v[4], v[5]), E::pack(v[6], v[7]));
+}
+
+// A row's end: its outputs from tensor memory, divided by the sum, or its piece
+// of a cut unit.  By whole warps; `mine`: the row exists.
+template <class E, int D>
+__device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u, int worker, int row,
+                                          int n, bool mine, uint32_t o_at, float m, float l,
+                                          bool bad) {
   using TE = typename E::T;
-  // all shared memory is this array, so its alignment is the swizzle's
-  extern __shared__ __align__(1024) char wide_s[];
-  char *q_s = wide_s, *ring = wide_s + W::kQ;
-  Ctl &ctl = *reinterpret_cast<Ctl *>(ring + W::kRing * W::kEntry);
-  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const bool whole = u.whole();
+  float *slot = p.part + piece_slot(u, worker) * slot_floats(p.rows, D);
+  float *slot_o = slot + 2 * p.rows + static_cast<size_t>(row) * D;
+  const long long at = mine ? out_row(p, u.b, u.h, u.r0 + row) : 0;
+  TE *out = static_cast<TE *>(p.out) + at * D;
+  const float norm = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f);
+  tc_after();
+#pragma unroll 1
+  for (int d = 0; d < D; d += 32) {
+    __syncwarp();
+    uint32_t o[32];
+    tm_load32(o, o_at + d);
+    tm_wait_ld();
+    if (mine) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = l == 0.f ? 0.f : __uint_as_float(o[e + i]) * norm;
+        if (whole) {
+          store8<E>(out + d + e, v);
+        } else {
+          store8(slot_o + d + e, v);
+        }
+      }
+    }
+  }
+  if (bad && mine && l != 0.f) {
+    for (int d = 0; d < D; d += 4) {
+      const float4 v =
+          nonfinite_values<TE, kTileKeys>(p, u, n, d, make_float4(0.f, 0.f, 0.f, 0.f));
+      const float x[4] = {v.x, v.y, v.z, v.w};
+      for (int e = 0; e < 4; ++e) {
+        if (x[e] == 0.f) continue;
+        if (whole) {
+          out[d + e] = E::from(E::to(out[d + e]) + x[e]);
+        } else {
+          slot_o[d + e] += x[e];
+        }
+      }
+    }
+  }
+  if (mine) {
+    if (!whole) {
+      slot[row] = m;
+      slot[p.rows + row] = l;
+    } else if (p.lse) {
+      p.lse[at] = row_lse(m, l);
+    }
+  }
+  __syncwarp();
+  tc_before();
+}
 
-  if (tid == 0) {
-    for (int i = 0; i < W::kRing; ++i) {
-      bar_init(&ctl.full[i], 1);
-      bar_init(&ctl.empty[i], 1);
-    }
-    for (int g = 0; g < 2; ++g) {
-      bar_init(&ctl.s_full[g], 1);
-      bar_init(&ctl.p_full[g], 4);
-      bar_init(&ctl.o_done[g], 1);
-      bar_init(&ctl.q_full[g], 1);
-      bar_init(&ctl.q_empty[g], 1);
-    }
-    bar_init(&ctl.meet, kSoft / 32);
-    bar_init(&ctl.drain, 1);
-    ctl.dead = 0;
-    ctl.bad = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+// The boxes of a tile of keys or values, one per page and lane.
+struct BoxLoader {
+  const CUtensorMap *map;
+  int unit_page, unit_head, unit_token;
+  int box, boxes, shift;  // tokens of a box, boxes of a tile, log2(tokens)
+
+  __device__ __forceinline__ BoxLoader(const AttnParams &p, const WideMaps &maps, bool values) {
+    map = values ? &maps.v : &maps.k;
+    unit_page = values ? maps.v_page : maps.k_page;
+    unit_head = values ? maps.v_head : maps.k_head;
+    unit_token = values ? maps.v_token : maps.k_token;
+    box = min(p.C.page_size, kTileKeys);
+    boxes = kTileKeys / box;
+    shift = 31 - __clz(box);
   }
-  const Line line = find_run<kWideThreads>(p, ctl.warp_s, ctl.found_s);  // also a barrier
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (line.w0 == line.w1) {
-    if (tid == 0) write_join(p, line, nullptr);
-    return;
+  // This lane's page of tile i of the unit, -1 where it has none.
+  __device__ __forceinline__ int page(const AttnParams &p, const UnitWalk &u, int i, int lane) const {
+    const int at = key_tile(u.k, u.i0 + i) * kTileKeys + lane * box;
+    if (lane >= boxes || i >= u.i1 - u.i0 || at >= u.k.end) return -1;
+    return page_at(p.S, u.b, p.C.page_size <= kTileKeys ? at >> shift : at / p.C.page_size);
   }
+  // Which of the 32 tokens from 32 * j of the tile at at0 on are copied.
+  __device__ __forceinline__ uint32_t valid_word(const UnitWalk &u, uint32_t pages, int at0,
+                                                 int j) const {
+    if (pages == low_bits(boxes) && at0 + kTileKeys <= u.k.end) return 0xFFFFFFFFu;
+    uint32_t word = 0u;
+    for (int k = 0; k < 32; k += box)
+      if ((pages >> ((j * 32 + k) >> shift)) & 1u) word |= low_bits(box) << k;
+    return word & low_bits(u.k.end - at0 - j * 32);
+  }
+  // By a whole warp, into an entry that is free.
+  template <int D>
+  __device__ __forceinline__ void load(const AttnParams &p, const UnitWalk &u, int at0, int page_id,
+                                       uint32_t pages, uint32_t entry, const void *full,
+                                       int lane) const {
+    using W = Entry<D>;
+    __syncwarp();
+    if (lane == 0) bar_expect(full, __popc(pages) * box * W::kRow * W::kPanels);
+    __syncwarp();
+    if ((pages >> lane) & 1u) {
+      const int token = p.C.page_size <= kTileKeys ? 0 : at0 % p.C.page_size;
+      box_load(entry + lane * (box >> 3) * W::kGroup, map, full, 0, 0, 0, 0,
+               page_id * unit_page + u.h * unit_head + token * unit_token);
+    }
+  }
+};
+
+// S = Q K^T of a tile, by a whole warp; qpanel: bytes of a panel of queries.
+template <class E, int D>
+__device__ __forceinline__ void issue_scores(uint32_t s, uint32_t q_at, int qpanel, uint32_t k_at) {
+  using W = Entry<D>;
+  constexpr uint32_t idesc = mma_idesc<E>(kTileKeys, false);
+  // a descriptor's address counts 16 bytes
+  const uint64_t a = smem_desc(q_at, 16, 1024), b = smem_desc(k_at, 16, W::kGroup);
+  tc_after();
+  if (elect_one()) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      mma_ss(s, a + ((k >> 2) * qpanel + (k & 3) * 32) / 16,
+             b + ((k >> 2) * W::kPanel + (k & 3) * 32) / 16, idesc, k > 0);
+  }
+  __syncwarp();
+}
+// O (+)= P V.
+template <class E, int D>
+__device__ __forceinline__ void issue_outputs(uint32_t o, uint32_t p_at, uint32_t v_at, bool first) {
+  using W = Entry<D>;
+  constexpr uint32_t idesc = mma_idesc<E>(D, true);
+  const uint64_t b = smem_desc(v_at, W::kPanel, W::kGroup);
+  tc_after();
+  if (elect_one()) {
+#pragma unroll
+    for (int k = 0; k < kTileKeys / 16; ++k)
+      mma_ts(o, p_at + k * 8, b + k * 2 * W::kGroup / 16, idesc, !first || k > 0);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void issue_commit(const void *bar) {
+  if (elect_one()) mma_commit(bar);
+  __syncwarp();
+}
+
+__device__ __forceinline__ uint32_t tm_alloc(void *slot, int warp) {
   if (warp == 11) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_u32(&ctl.tmem))
+                     smem_u32(slot))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = ctl.tmem;
-  UnitWalk u;
-  u.start(p, line);
-  if (tid == 0) write_join(p, line, &u);
-
-  if (warp < 8) {
-    // -------------------------------------------------------------- softmax
-    more_regs<kSoftRegs>();
-    const int g = warp >> 2;
-    const int lane_row = tid & 127;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256;
-    const float c = p.scale_log2;
-    const int tile_rows = NQ == 2 ? p.rows / 2 : p.rows;
-    uint32_t n_s = 0, n_o[2] = {0, 0}, n_meet = 0;
-    int tiles_before = 0;  // of this CTA, for the rings
-    bool ok = true;
-    for (long long w = line.w0; ok;) {
-      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
-      const int row = NQ == 2 ? g * tile_rows + lane_row : lane_row;
-      const int rows = NQ == 2 ? min(tile_rows, live - g * tile_rows) : live;  // of the stream
-      const bool mine = lane_row < rows;
-      const int n = (u.r0 + min(row, live - 1)) / p.G;
-      const bool active = rows > 0;
-      const bool works = (lane_row & ~31) < rows;  // this warp has rows
-      float m = -INFINITY, l = 0.f;
-      for (int i = NQ == 2 ? 0 : g; active && i < n_tiles; i += NQ == 2 ? 1 : 2) {
-        if (!(ok = warp_wait(&ctl.s_full[g], n_s++ & 1u, &ctl.dead))) break;
-        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
-        const uint4 valid =
-            *reinterpret_cast<const uint4 *>(ctl.valid[(tiles_before + i) % kValidRing]);
-        const bool masked = (valid.x & valid.y & valid.z & valid.w) != 0xFFFFFFFFu ||
-                            !all_seen(p, u.k, u.r0, at0, kTileKeys);
-        if (works) {
-          tc_after();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tm_load32(s[j], s_at + j * 32);
-          tm_wait_ld();
-          if (masked) {
-            const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t vis = seen_word(p, u.k, u.b, n, at0 + j * 32, in[j]);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((vis >> e) & 1u)) s[j][e] = __float_as_uint(-INFINITY);
-            }
-          }
-          float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              x[j] = max3(x[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
-          const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
-          const bool raise = mine && top > m + kSlack;
-          if (__any_sync(0xFFFFFFFFu, raise)) {
-            const float to = raise ? top : m;
-            const float f = m == -INFINITY ? 0.f : fast_exp2(m - to);
-            l *= f;
-            m = to;
-            if (i >= (NQ == 2 ? 1 : 2)) {
-              // the products before S's are complete: O is whole
-#pragma unroll 1
-              for (int d = 0; d < D; d += 16) {
-                uint32_t o[16];
-                tm_load16(o, o_at + g * 128 + d);
-                tm_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tm_store16(o_at + g * 128 + d, o);
-              }
-            }
-          }
-          const float sub = m == -INFINITY ? 0.f : -m;
-          const float2 c2 = make_float2(c, c), sub2 = make_float2(sub, sub);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t packed[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 y = fma2(make_float2(__uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1])), c2,
-                              sub2);
-              y.x = fast_exp2(y.x);
-              y.y = fast_exp2(y.y);
-              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
-              // the product takes the weights in the cache's type: each is off
-              // by at most half a step of that type, as the values themselves are
-              packed[e / 2] = E::pack(y.x, y.y);
-            }
-            tm_store16(s_at + j * 16, packed);
-          }
-          sum[0] = add2(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
-          tm_wait_st();
-        }
-        if (masked && (NQ == 1 || g == 0)) {
-          // Rows of the value tile that some row of the unit does not see: those
-          // that were not copied become zero, and so do infinities and NaNs,
-          // which nonfinite_values adds to the rows that see them.  With 256 rows
-          // the first stream does it, whose product with the tile comes first.
-          const int e = NQ == 2 ? 2 * (tiles_before + i) + 1 : 2 * tiles_before + value_entry(i, n_tiles);
-          const int slot = e % W::kRing;
-          if (!(ok = warp_wait(&ctl.full[slot], (e / W::kRing) & 1, &ctl.dead))) break;
-          bool found = false;
-          char *at = ring + slot * W::kEntry + lane_row * 16;
-          const int key0 = (lane_row * 16 / W::kGroup) * 8 + lane_row / 8 % 8;
-#pragma unroll 4
-          for (int t = 0; t < W::kEntry / 2048; ++t) {
-            const int key = key0 + t * 2048 / W::kGroup * 8;
-            uint4 *x = reinterpret_cast<uint4 *>(at + t * 2048);
-            const uint4 y = *x;
-            const uint32_t word = key < 64 ? (key < 32 ? valid.x : valid.y)
-                                           : (key < 96 ? valid.z : valid.w);
-            if (!((word >> (key & 31)) & 1u)) {
-              *x = make_uint4(0, 0, 0, 0);
-            } else if (nonfinite_bits<E>(y.x) | nonfinite_bits<E>(y.y) | nonfinite_bits<E>(y.z) |
-                       nonfinite_bits<E>(y.w)) {
-              *x = make_uint4(finite_or_zero<E>(y.x), finite_or_zero<E>(y.y), finite_or_zero<E>(y.z),
-                              finite_or_zero<E>(y.w));
-              found = true;
-            }
-          }
-          if (found) *reinterpret_cast<volatile int *>(&ctl.bad) = 1;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&ctl.p_full[g]);
-      }
-      if (!ok) break;
-      tiles_before += n_tiles;
-
-      // the unit's end
-      const bool whole = u.whole();
-      float *slot = p.part + piece_slot(u) * slot_floats(p.rows, D);
-      const long long out_at = mine ? out_row(p, u.b, u.h, u.r0 + row) : 0;
-      const int d_from = NQ == 2 ? 0 : g * (D / 2), d_to = NQ == 2 ? D : d_from + D / 2;
-      float w0 = 1.f, w1 = 0.f;  // weights of the streams' outputs
-      if constexpr (NQ == 2) {
-        if (active && !(ok = warp_wait(&ctl.o_done[g], n_o[g]++ & 1u, &ctl.dead))) break;
-      } else {
-        ctl.ml[g][0][lane_row] = m;
-        ctl.ml[g][1][lane_row] = l;
-        __syncwarp();
-        if (lane == 0) bar_arrive(&ctl.meet);
-        if (!(ok = warp_wait(&ctl.meet, n_meet++ & 1u, &ctl.dead))) break;
-        if (!(ok = warp_wait(&ctl.o_done[0], n_o[0]++ & 1u, &ctl.dead))) break;
-        if (n_tiles > 1 && !(ok = warp_wait(&ctl.o_done[1], n_o[1]++ & 1u, &ctl.dead))) break;
-        const float m0 = ctl.ml[0][0][lane_row], m1 = ctl.ml[1][0][lane_row];
-        m = fmaxf(m0, m1);
-        w0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - m);
-        w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - m);
-        l = (w0 == 0.f ? 0.f : w0 * ctl.ml[0][1][lane_row]) +
-            (w1 == 0.f ? 0.f : w1 * ctl.ml[1][1][lane_row]);
-      }
-      if (active && works) {
-        tc_after();
-        const float norm = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        const bool bad = *reinterpret_cast<volatile int *>(&ctl.bad) != 0;
-#pragma unroll 1
-        for (int d = d_from; d < d_to; d += 32) {
-          __syncwarp();
-          uint32_t o[32];
-          tm_load32(o, o_at + (NQ == 2 ? g * 128 : 0) + d);
-          if constexpr (NQ == 1) {
-            uint32_t o1[32];
-            tm_load32(o1, o_at + 128 + d);
-            tm_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float a = w0 == 0.f ? 0.f : w0 * __uint_as_float(o[e]);
-              const float b = w1 == 0.f ? 0.f : w1 * __uint_as_float(o1[e]);
-              o[e] = __float_as_uint(a + b);
-            }
-          } else {
-            tm_wait_ld();
-          }
-          if (mine) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                     __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-              if (l == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (whole) {
-                v = make_float4(v.x * norm, v.y * norm, v.z * norm, v.w * norm);
-                store4(static_cast<TE *>(p.out) + out_at * D + d + e, v);
-              } else {
-                store4(slot + 2 * p.rows + static_cast<size_t>(row) * D + d + e, v);
-              }
-            }
-          }
-        }
-        if (bad && mine && l != 0.f) {
-          for (int d = d_from; d < d_to; d += 4) {
-            const float4 v =
-                nonfinite_values<TE, kTileKeys>(p, u, n, d, make_float4(0.f, 0.f, 0.f, 0.f));
-            const float x[4] = {v.x, v.y, v.z, v.w};
-            for (int e = 0; e < 4; ++e) {
-              if (x[e] == 0.f) continue;
-              if (whole) {
-                TE *o = static_cast<TE *>(p.out) + out_at * D + d + e;
-                *o = E::from(E::to(*o) + x[e]);
-              } else {
-                slot[2 * p.rows + static_cast<size_t>(row) * D + d + e] += x[e];
-              }
-            }
-          }
-        }
-        if (mine && d_from == 0) {
-          if (!whole) {
-            slot[row] = m;
-            slot[p.rows + row] = l;
-          } else if (p.lse) {
-            p.lse[out_at] = row_lse(m, l);
-          }
-        }
-      }
-      __syncwarp();
-      tc_before();
-      if constexpr (NQ == 1) {
-        // both halves have been read before either stream's next output begins
-        if (lane == 0) bar_arrive(&ctl.meet);
-        if (!(ok = warp_wait(&ctl.meet, n_meet++ & 1u, &ctl.dead))) break;
-      }
-      w += n_tiles;
-      if (w >= line.w1) break;
-      u.next(p, line);
-    }
-  } else {
-    fewer_regs<kRestRegs>();
-    if (warp < 10) {
-      // ----------------------------------------------------- keys and values
-      const bool values = warp == 9;
-      const CUtensorMap *map = values ? &maps.v : &maps.k;
-      const int unit_page = values ? maps.v_page : maps.k_page;
-      const int unit_head = values ? maps.v_head : maps.k_head;
-      const int unit_token = values ? maps.v_token : maps.k_token;
-      const uint32_t ring_at = smem_u32(ring);
-      const int box = min(p.C.page_size, kTileKeys);  // tokens of a box
-      const int boxes = kTileKeys / box;              // of a tile, one per lane
-      const uint32_t all = low_bits(boxes);
-      const int shift = 31 - __clz(box);
-      uint32_t last = 0;
-      int tiles_before = 0;
-      bool ok = true;
-      auto look_up = [&](int i) {  // this lane's page of tile i of the unit
-        const int at = key_tile(u.k, u.i0 + i) * kTileKeys + lane * box;
-        if (lane >= boxes || i >= u.i1 - u.i0 || at >= u.k.end) return -1;
-        return page_at(p.S, u.b, p.C.page_size <= kTileKeys ? at >> shift : at / p.C.page_size);
-      };
-      for (long long w = line.w0; ok;) {
-        const int n_tiles = u.i1 - u.i0;
-        // a tile's pages are looked up two tiles ahead
-        int page = look_up(0), next = look_up(1);
-        for (int i = 0; i < n_tiles; ++i) {
-          const int behind = look_up(i + 2);
-          const uint32_t e =
-              2 * tiles_before + (NQ == 2 ? 2 * i + (values ? 1 : 0)
-                                          : (values ? value_entry(i, n_tiles) : max(2 * i - 1, 0)));
-          const int slot = e % W::kRing;
-          if (!(ok = warp_wait(&ctl.empty[slot], ((e / W::kRing) & 1u) ^ 1u, &ctl.dead))) break;
-          const bool there = page_ok(p.C, page);
-          const uint32_t pages = __ballot_sync(0xFFFFFFFFu, there);
-          const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
-          if (!values && lane < 4) {
-            uint32_t word = 0xFFFFFFFFu;
-            if (pages != all || at0 + kTileKeys > u.k.end) {
-              word = 0u;
-              for (int k = 0; k < 32; k += box)
-                if ((pages >> ((lane * 32 + k) >> shift)) & 1u) word |= low_bits(box) << k;
-              word &= low_bits(u.k.end - at0 - lane * 32);
-            }
-            ctl.valid[(tiles_before + i) % kValidRing][lane] = word;
-          }
-          __syncwarp();
-          if (lane == 0) bar_expect(&ctl.full[slot], __popc(pages) * box * W::kRow * W::kPanels);
-          __syncwarp();
-          if (there) {
-            const int token = p.C.page_size <= kTileKeys ? 0 : at0 % p.C.page_size;
-            box_load(ring_at + slot * W::kEntry + lane * (box >> 3) * W::kGroup, map,
-                     &ctl.full[slot], 0, 0, 0, 0, page * unit_page + u.h * unit_head + token * unit_token);
-          }
-          last = e;
-          page = next;
-          next = behind;
-        }
-        if (!ok) break;
-        tiles_before += n_tiles;
-        w += n_tiles;
-        if (w >= line.w1) break;
-        u.next(p, line);
-      }
-      // the products wait for every entry; where a wait gave up, its copies are
-      // given time to land before the CTA ends
-      for (uint32_t e = last + 1 > W::kRing ? last + 1 - W::kRing : 0; !ok && e <= last; ++e)
-        bar_linger(&ctl.full[e % W::kRing], (e / W::kRing) & 1u);
-    } else if (warp == 10) {
-      // -------------------------------------------------------------- queries
-      const uint32_t q_at = smem_u32(q_s);
-      const int tile_rows = NQ == 2 ? p.rows / 2 : p.rows;
-      uint32_t unit = 0;
-      bool ok = true;
-      for (long long w = line.w0;;) {
-        const int live = u.live_rows(p);
-        const int buf = NQ == 1 ? unit & 1 : 0;
-        const uint32_t use = NQ == 1 ? unit >> 1 : unit;
-        // once the products of the unit before have read theirs
-        if (!(ok = warp_wait(&ctl.q_empty[buf], (use & 1u) ^ 1u, &ctl.dead))) break;
-        if (lane == 0) {
-          const int tiles = NQ == 2 && live > tile_rows ? 2 : 1;
-          bar_expect(&ctl.q_full[buf], tiles * tile_rows * W::kRow * W::kPanels);
-          for (int t = 0; t < tiles; ++t)
-            for (int x = 0; x < W::kPanels; ++x)
-              box_load(q_at + (buf + t) * W::kEntry + x * W::kQPanel, &maps.q, &ctl.q_full[buf], 0, 0,
-                       (u.r0 + t * tile_rows) / p.G, x, u.b * maps.q_seq + u.h * maps.q_head);
-        }
-        __syncwarp();
-        ++unit;
-        w += u.i1 - u.i0;
-        if (w >= line.w1) break;
-        u.next(p, line);
-      }
-      for (int b = 0; !ok && b < 2; ++b) {
-        const uint32_t uses = NQ == 1 ? (unit + 1 - b) / 2 : (b == 0 ? unit : 0);
-        if (uses > 0) bar_linger(&ctl.q_full[b], (uses - 1) & 1u);
-      }
-    } else if (lane == 0) {
-      // ------------------------------------------------------------- products
-      const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(q_s);
-      constexpr uint32_t s_idesc = mma_idesc<E>(kTileKeys, false), o_idesc = mma_idesc<E>(D, true);
-      uint32_t taken = 0, n_p[2] = {0, 0}, unit = 0;
-      bool ok = true;
-      // Waits for the next entry of the ring; its place.
-      auto take = [&]() {
-        const int slot = taken % W::kRing;
-        ok = bar_wait(&ctl.full[slot], (taken / W::kRing) & 1u, &ctl.dead);
-        ++taken;
-        return slot;
-      };
-      auto scores = [&](int g, int buf, int slot) {
-        // a descriptor's address counts 16 bytes
-        const uint64_t a = smem_desc(q_at + buf * W::kEntry, 16, 1024);
-        const uint64_t b = smem_desc(ring_at + slot * W::kEntry, 16, W::kGroup);
-        tc_after();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + g * 128, a + ((k >> 2) * W::kQPanel + (k & 3) * 32) / 16,
-                 b + ((k >> 2) * W::kPanel + (k & 3) * 32) / 16, s_idesc, k > 0);
-        mma_commit(&ctl.s_full[g]);
-      };
-      auto outputs = [&](int g, int slot, bool first) {
-        ok = bar_wait(&ctl.p_full[g], n_p[g]++ & 1u, &ctl.dead);
-        if (!ok) return;
-        tc_after();
-        const uint64_t b = smem_desc(ring_at + slot * W::kEntry, W::kPanel, W::kGroup);
-#pragma unroll
-        for (int k = 0; k < kTileKeys / 16; ++k)
-          mma_ts(tmem + 256 + g * 128, tmem + g * 128 + k * 8, b + k * 2 * W::kGroup / 16, o_idesc,
-                 !first || k > 0);
-      };
-      for (long long w = line.w0; ok;) {
-        const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
-        const int buf = NQ == 1 ? unit & 1 : 0;
-        const uint32_t use = NQ == 1 ? unit >> 1 : unit;
-        int slot = take();
-        if (!ok || !(ok = bar_wait(&ctl.q_full[buf], use & 1u, &ctl.dead))) break;
-        ++unit;
-        if constexpr (NQ == 2) {
-          const int streams = live > p.rows / 2 ? 2 : 1;
-          for (int g = 0; g < streams; ++g) scores(g, g, slot);
-          mma_commit(&ctl.empty[slot]);
-          if (n_tiles == 1) mma_commit(&ctl.q_empty[0]);
-          for (int i = 0; ok && i < n_tiles; ++i) {
-            const int val_slot = take();
-            if (!ok) break;
-            const bool more = i + 1 < n_tiles;
-            for (int g = 0; g < streams; ++g) {
-              outputs(g, val_slot, i == 0);
-              if (!ok) break;
-              if (!more) mma_commit(&ctl.o_done[g]);
-              if (g == streams - 1) mma_commit(&ctl.empty[val_slot]);
-              if (more) {
-                if (g == 0) slot = take();
-                if (!ok) break;
-                scores(g, g, slot);
-                if (g == streams - 1) {
-                  mma_commit(&ctl.empty[slot]);
-                  if (i + 2 == n_tiles) mma_commit(&ctl.q_empty[0]);
-                }
-              }
-            }
-          }
-        } else {
-          scores(0, buf, slot);
-          mma_commit(&ctl.empty[slot]);
-          if (n_tiles > 1) {
-            slot = take();
-            if (!ok) break;
-            scores(1, buf, slot);
-            mma_commit(&ctl.empty[slot]);
-          }
-          if (n_tiles <= 2) mma_commit(&ctl.q_empty[buf]);
-          for (int i = 0; ok && i < n_tiles; ++i) {
-            const int g = i & 1;
-            slot = take();
-            if (!ok) break;
-            outputs(g, slot, i < 2);
-            if (!ok) break;
-            mma_commit(&ctl.empty[slot]);
-            if (i + 2 >= n_tiles) mma_commit(&ctl.o_done[g]);
-            if (i + 2 < n_tiles) {
-              slot = take();
-              if (!ok) break;
-              scores(g, buf, slot);
-              mma_commit(&ctl.empty[slot]);
-              if (i + 3 == n_tiles) mma_commit(&ctl.q_empty[buf]);
-            }
-          }
-        }
-        if (!ok) break;
-        w += n_tiles;
-        if (w >= line.w1) break;
-        u.next(p, line);
-      }
-      // nothing is in flight when the tensor memory goes back
-      mma_commit(&ctl.drain);
-      bar_linger(&ctl.drain, 0u);
-    }
-  }
+  return *reinterpret_cast<volatile uint32_t *>(slot);
+}
+__device__ __forceinline__ void tm_free(uint32_t tmem, int warp) {
   __syncwarp();
   tc_before();
   __syncthreads();
   tc_after();
   if (warp == 11)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-  if (tid == 0 && ctl.dead && p.flags) {
-    // a wait gave up: the outputs of the run's sequences are not to be used
-    UnitWalk v;
-    v.start(p, line);
-    for (long long w = line.w0;;) {
+}
+
+// A wait gave up: the outputs of the run's sequences are not to be used.
+__device__ __forceinline__ void flag_run(const AttnParams &p, const Line &line) {
+  UnitWalk v;
+  if (p.flags && v.start(p, line)) do {
       atomicOr(p.flags + v.b, SPEC_FLAG_TIMEOUT);
-      w += v.i1 - v.i0;
-      if (w >= line.w1) break;
-      v.next(p, line);
+    } while (v.next(p, line));
+}
+
+// ---------------------------------------------------------------------------
+// two streams with units of their own
+// ---------------------------------------------------------------------------
+
+// QR: rows of queries that are copied, 32 or 128.  The products read 128: what
+// lies behind is another buffer, whose rows make results that nobody reads.
+template <int D, int QR>
+struct SoloCtl {
+  static constexpr int kRing = D == 128 ? (QR == 32 ? 3 : 2) : 6;  // entries of a stream
+  struct Stream {
+    unsigned long long full[kRing], empty[kRing], s_full, p_full, o_done, q_full, q_empty, drain;
+    alignas(16) uint32_t valid[kValidRing][4];
+  } stream[2];
+  RunScratch<kWideThreads, 2> runs;
+  uint32_t tmem;
+  int dead, bad;
+};
+template <int D, int QR>
+struct SoloShape {
+  static constexpr int kQPanel = QR * 128, kQ = Entry<D>::kPanels * kQPanel;  // of a stream
+  static constexpr int kRing = SoloCtl<D, QR>::kRing;
+  static constexpr int kEntries = 2 * kQ;  // where the rings begin
+  static constexpr int kCtl = kEntries + 2 * kRing * Entry<D>::kBytes;
+  static constexpr int kSmem = kCtl + static_cast<int>(sizeof(SoloCtl<D, QR>));
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+}  // namespace
+
+template <class E, int D, int QR>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    solo_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideMaps maps) {
+  using W = Entry<D>;
+  using Shape = SoloShape<D, QR>;
+  using Ctl = SoloCtl<D, QR>;
+  constexpr int kRing = Shape::kRing;
+  // all shared memory is this array, so its alignment is the swizzle's
+  extern __shared__ __align__(1024) char wide_s[];
+  Ctl &ctl = *reinterpret_cast<Ctl *>(wide_s + Shape::kCtl);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+
+  if (tid < 2) {
+    auto &st = ctl.stream[tid];
+    for (int i = 0; i < kRing; ++i) {
+      bar_init(&st.full[i], 1);
+      bar_init(&st.empty[i], 1);
+    }
+    bar_init(&st.s_full, 1);
+    bar_init(&st.p_full, 4);
+    bar_init(&st.o_done, 1);
+    bar_init(&st.q_full, 1);
+    bar_init(&st.q_empty, 1);
+    bar_init(&st.drain, 1);
+    ctl.dead = 0;
+    ctl.bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  Line lines[2];
+  // a barrier as well; consecutive workers on different CTAs
+  find_runs(p, ctl.runs, blockIdx.x, gridDim.x, lines);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // of this warp's stream
+  const int g = warp < 8 ? warp >> 2 : warp & 1;
+  const Line line = g ? lines[1] : lines[0];
+  UnitWalk u;
+  const bool busy = u.start(p, line);
+  if (lane == 0 && (warp == 8 || warp == 9)) write_join(p, line, busy ? &u : nullptr);
+  if (lines[0].w0 == lines[0].w1 && lines[1].w0 == lines[1].w1) return;
+  const uint32_t tmem = tm_alloc(&ctl.tmem, warp);
+  auto &st = ctl.stream[g];
+  const uint32_t s_at = tmem + g * 128, o_at = tmem + 256 + g * 128;
+  const uint32_t q_at = smem_u32(wide_s) + g * Shape::kQ;
+  char *ring = wide_s + Shape::kEntries + g * kRing * W::kBytes;
+  const uint32_t ring_at = smem_u32(ring);
+  bool ok = true;
+
+  if (warp < 8) {
+    // -------------------------------------------------------------- softmax
+    more_regs<kSoftRegs>();
+    const int part = warp & 3, row = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
+    uint32_t tiles = 0, units = 0;
+    if (busy) do {
+        const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+        const bool mine = row < live, works = part * 32 < live;
+        const int n = (u.r0 + min(row, live - 1)) / p.G;
+        const int idle = 4 - min((live + 31) / 32, 4);  // warps without rows
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < n_tiles; ++i, ++tiles) {
+          if (!(ok = warp_wait(&st.s_full, tiles & 1u, &ctl.dead))) break;
+          const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+          const uint4 valid = *reinterpret_cast<const uint4 *>(st.valid[tiles % kValidRing]);
+          const bool masked = tile_masked(p, u, at0, valid);
+          if (works)
+            softmax_tile<E, D>(p, u, n, mine, masked, valid, at0, s_at + lanes, o_at + lanes, i == 0,
+                               m, l);
+          if (masked && (idle == 0 || !works)) {
+            const uint32_t e = 2 * tiles + 1;
+            if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+            clean_values<E, D>(ring + e % kRing * W::kBytes, valid,
+                               clean_from(p, u.k, u.r0, at0, valid),
+                               idle == 0 ? row : row - (4 - idle) * 32, idle == 0 ? 128 : idle * 32,
+                               &ctl.bad);
+          }
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&st.p_full);
+        }
+        if (!ok || !(ok = warp_wait(&st.o_done, units++ & 1u, &ctl.dead))) break;
+        if (works)
+          write_row<E, D>(p, u, line.worker, row, n, mine, o_at + lanes, m, l,
+                          *reinterpret_cast<volatile int *>(&ctl.bad) != 0);
+      } while (u.next(p, line));
+  } else {
+    fewer_regs<kRestRegs>();
+    if (warp < 10) {
+    // ------------------------------------------------ queries, keys, values
+    const BoxLoader keys(p, maps, false), values(p, maps, true);
+    uint32_t tiles = 0, units = 0;
+    if (busy) do {
+        const int n_tiles = u.i1 - u.i0;
+        int page = keys.page(p, u, 0, lane), next = keys.page(p, u, 1, lane);
+        for (int i = 0; ok && i < n_tiles; ++i, ++tiles) {
+          // a tile's pages are looked up two tiles ahead
+          const int behind = keys.page(p, u, i + 2, lane);
+          const uint32_t pages = __ballot_sync(0xFFFFFFFFu, page_ok(p.C, page));
+          const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+          uint32_t e = 2 * tiles;
+          if (!(ok = warp_wait(&st.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, &ctl.dead))) break;
+          if (lane < 4) st.valid[tiles % kValidRing][lane] = keys.valid_word(u, pages, at0, lane);
+          keys.load<D>(p, u, at0, page, pages, ring_at + e % kRing * W::kBytes, &st.full[e % kRing],
+                       lane);
+          if (i == 0) {
+            // once the products of the unit before have read theirs
+            if (!(ok = warp_wait(&st.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
+            ++units;
+            if (lane == 0) {
+              bar_expect(&st.q_full, min(p.rows, QR) / p.G * p.G * W::kRow * W::kPanels);
+              for (int x = 0; x < W::kPanels; ++x)
+                box_load(q_at + x * Shape::kQPanel, &maps.q, &st.q_full, 0, 0, u.r0 / p.G, x,
+                         u.b * maps.q_seq + u.h * maps.q_head);
+            }
+          }
+          ++e;
+          if (!(ok = warp_wait(&st.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, &ctl.dead))) break;
+          values.load<D>(p, u, at0, page, pages, ring_at + e % kRing * W::kBytes,
+                         &st.full[e % kRing], lane);
+          page = next;
+          next = behind;
+        }
+      } while (ok && u.next(p, line));
+    // the products wait for every copy; where a wait gave up, the copies are
+    // given time to land before the CTA ends
+    if (!ok) {
+      for (uint32_t e = 2 * tiles > kRing ? 2 * tiles - kRing : 0; e < 2 * tiles + 1; ++e)
+        bar_linger(&st.full[e % kRing], (e / kRing) & 1u);
+      if (units > 0) bar_linger(&st.q_full, (units - 1) & 1u);
+    }
+    } else {
+    // ------------------------------------------------------------- products
+    uint32_t tiles = 0, units = 0;
+    if (busy) do {
+        const int n_tiles = u.i1 - u.i0;
+        for (int i = 0; i < n_tiles; ++i, ++tiles) {
+          uint32_t e = 2 * tiles;
+          if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+          if (i == 0 && !(ok = warp_wait(&st.q_full, units++ & 1u, &ctl.dead))) break;
+          issue_scores<E, D>(s_at, q_at, Shape::kQPanel, ring_at + e % kRing * W::kBytes);
+          issue_commit(&st.s_full);
+          issue_commit(&st.empty[e % kRing]);
+          if (i + 1 == n_tiles) issue_commit(&st.q_empty);
+          ++e;
+          if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+          if (!(ok = warp_wait(&st.p_full, tiles & 1u, &ctl.dead))) break;
+          issue_outputs<E, D>(o_at, s_at, ring_at + e % kRing * W::kBytes, i == 0);
+          if (i + 1 == n_tiles) issue_commit(&st.o_done);
+          issue_commit(&st.empty[e % kRing]);
+        }
+      } while (ok && u.next(p, line));
+    // nothing is in flight when the tensor memory goes back
+    issue_commit(&st.drain);
+    bar_linger(&st.drain, 0u);
     }
   }
+  tm_free(tmem, warp);
+  if (ctl.dead && tid < 2) flag_run(p, tid ? lines[1] : lines[0]);
 }
 
 namespace {
+
+// ---------------------------------------------------------------------------
+// two streams that share keys and values
+// ---------------------------------------------------------------------------
+
+template <int D>
+struct PairCtl {
+  static constexpr int kRing = D == 128 ? 5 : 12;  // what 227 KB hold beside the queries
+  // checked: an entry of values is ready for its products
+  unsigned long long full[kRing], empty[kRing], checked[kRing], s_full[2], p_full[2], o_done[2],
+      q_full, q_empty, drain;
+  alignas(16) uint32_t valid[kValidRing][4];
+  RunScratch<kWideThreads, 1> runs;
+  uint32_t tmem;
+  int dead, bad;
+};
+template <int D>
+struct PairShape {
+  static constexpr int kQPanel = 128 * 128, kQ = Entry<D>::kPanels * kQPanel;  // of a row tile
+  static constexpr int kRing = PairCtl<D>::kRing;
+  static constexpr int kEntries = 2 * kQ;
+  static constexpr int kCtl = kEntries + kRing * Entry<D>::kBytes;
+  static constexpr int kSmem = kCtl + static_cast<int>(sizeof(PairCtl<D>));
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+}  // namespace
+
+template <class E, int D>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    pair_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideMaps maps) {
+  using W = Entry<D>;
+  using Shape = PairShape<D>;
+  using Ctl = PairCtl<D>;
+  constexpr int kRing = Shape::kRing;
+  extern __shared__ __align__(1024) char wide_s[];
+  char *ring = wide_s + Shape::kEntries;
+  Ctl &ctl = *reinterpret_cast<Ctl *>(wide_s + Shape::kCtl);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const int tile_rows = p.rows / 2;
+
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      bar_init(&ctl.full[i], 1);
+      bar_init(&ctl.empty[i], 2);  // the products and the check are done with it
+      bar_init(&ctl.checked[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      bar_init(&ctl.s_full[g], 1);
+      bar_init(&ctl.p_full[g], 4);
+      bar_init(&ctl.o_done[g], 1);
+    }
+    bar_init(&ctl.q_full, 1);
+    bar_init(&ctl.q_empty, 1);
+    bar_init(&ctl.drain, 1);
+    ctl.dead = 0;
+    ctl.bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  Line lines[1];
+  find_runs(p, ctl.runs, blockIdx.x, 0, lines);  // a barrier as well
+  const Line &line = lines[0];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  UnitWalk u;
+  const bool busy = u.start(p, line);
+  if (tid == 0) write_join(p, line, busy ? &u : nullptr);
+  if (!busy) return;
+  const uint32_t tmem = tm_alloc(&ctl.tmem, warp);
+  const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(wide_s);
+  uint32_t tiles = 0, units = 0;
+  bool ok = true;
+
+  if (warp < 8) {
+    // -------------------------------------------------------------- softmax
+    more_regs<kSoftRegs>();
+    const int g = warp >> 2, part = warp & 3, tile_row = tid & 127, row = g * tile_rows + tile_row;
+    const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
+    const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * 128;
+    uint32_t seen = 0, ended = 0;  // tiles and units of this stream
+    do {
+      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+      const int rows = min(tile_rows, live - g * tile_rows);  // of this stream
+      const bool mine = tile_row < rows, works = part * 32 < rows;
+      const int n = (u.r0 + min(row, live - 1)) / p.G;
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; rows > 0 && i < n_tiles; ++i) {
+        if (!(ok = warp_wait(&ctl.s_full[g], seen++ & 1u, &ctl.dead))) break;
+        if (works) {
+          const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+          const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.valid[(tiles + i) % kValidRing]);
+          softmax_tile<E, D>(p, u, n, mine, tile_masked(p, u, at0, valid), valid, at0, s_at, o_at,
+                             i == 0, m, l);
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&ctl.p_full[g]);
+      }
+      if (!ok) break;
+      tiles += n_tiles;
+      if (rows > 0) {
+        if (!(ok = warp_wait(&ctl.o_done[g], ended++ & 1u, &ctl.dead))) break;
+        if (works)
+          write_row<E, D>(p, u, line.worker, row, n, mine, o_at, m, l,
+                          *reinterpret_cast<volatile int *>(&ctl.bad) != 0);
+      }
+    } while (u.next(p, line));
+  } else {
+    fewer_regs<kRestRegs>();
+    if (warp < 10) {
+    // ------------------------------ warp 8: keys and queries, warp 9: values
+    const bool values = warp == 9;
+    const BoxLoader boxes(p, maps, values);
+    do {
+      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+      // a tile's pages are looked up two tiles ahead
+      int page = boxes.page(p, u, 0, lane), next = boxes.page(p, u, 1, lane);
+      for (int i = 0; ok && i < n_tiles; ++i, ++tiles) {
+        const int behind = boxes.page(p, u, i + 2, lane);
+        const uint32_t pages = __ballot_sync(0xFFFFFFFFu, page_ok(p.C, page));
+        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+        const uint32_t e = 2 * tiles + (values ? 1 : 0);
+        if (!(ok = warp_wait(&ctl.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, &ctl.dead))) break;
+        if (!values && lane < 4)
+          ctl.valid[tiles % kValidRing][lane] = boxes.valid_word(u, pages, at0, lane);
+        boxes.load<D>(p, u, at0, page, pages, ring_at + e % kRing * W::kBytes, &ctl.full[e % kRing],
+                      lane);
+        if (!values && i == 0) {
+          // once the products of the unit before have read theirs
+          if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
+          ++units;
+          if (lane == 0) {
+            const int used = live > tile_rows ? 2 : 1;
+            bar_expect(&ctl.q_full, used * tile_rows * W::kRow * W::kPanels);
+            for (int t = 0; t < used; ++t)
+              for (int x = 0; x < W::kPanels; ++x)
+                box_load(q_at + t * Shape::kQ + x * Shape::kQPanel, &maps.q, &ctl.q_full, 0, 0,
+                         (u.r0 + t * tile_rows) / p.G, x, u.b * maps.q_seq + u.h * maps.q_head);
+          }
+        }
+        page = next;
+        next = behind;
+      }
+    } while (ok && u.next(p, line));
+    // the products wait for every copy; where a wait gave up, the copies are
+    // given time to land before the CTA ends
+    if (!ok) {
+      for (uint32_t e = 2 * tiles > kRing ? 2 * tiles - kRing : 0; e < 2 * tiles + 2; ++e)
+        bar_linger(&ctl.full[e % kRing], (e / kRing) & 1u);
+      if (units > 0) bar_linger(&ctl.q_full, (units - 1) & 1u);
+    }
+    } else if (warp == 10) {
+    // -------------------------------------------------- values made ready
+    do {
+      const int n_tiles = u.i1 - u.i0;
+      for (int i = 0; i < n_tiles; ++i, ++tiles) {
+        uint32_t e = 2 * tiles;
+        if (!(ok = warp_wait(&ctl.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+        const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.valid[tiles % kValidRing]);
+        if (lane == 0) {
+          bar_arrive(&ctl.checked[e % kRing]);  // every entry is a phase of its place
+          bar_arrive(&ctl.empty[e % kRing]);
+        }
+        ++e;
+        // only an entry that has landed is this warp's to release
+        if (!(ok = warp_wait(&ctl.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+        if (tile_masked(p, u, at0, valid)) {
+          clean_values<E, D>(ring + e % kRing * W::kBytes, valid,
+                             clean_from(p, u.k, u.r0, at0, valid), lane, 32, &ctl.bad);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&ctl.checked[e % kRing]);
+          bar_arrive(&ctl.empty[e % kRing]);
+        }
+      }
+    } while (ok && u.next(p, line));
+    } else {
+    // ------------------------------------------------------------- products
+    uint32_t made[2] = {0, 0};  // tiles of each stream
+    auto take = [&](uint32_t e) {  // an entry that has landed
+      ok = warp_wait(&ctl.full[e % kRing], (e / kRing) & 1u, &ctl.dead);
+      return ring_at + e % kRing * W::kBytes;
+    };
+    auto scores = [&](int g, uint32_t k_at) {
+      issue_scores<E, D>(tmem + g * 128, q_at + g * Shape::kQ, Shape::kQPanel, k_at);
+      issue_commit(&ctl.s_full[g]);
+    };
+    do {
+      const int n_tiles = u.i1 - u.i0, streams = u.live_rows(p) > tile_rows ? 2 : 1;
+      uint32_t k_at = take(2 * tiles);
+      if (!ok || !(ok = warp_wait(&ctl.q_full, units++ & 1u, &ctl.dead))) break;
+      for (int g = 0; g < streams; ++g) scores(g, k_at);
+      issue_commit(&ctl.empty[2 * tiles % kRing]);
+      if (n_tiles == 1) issue_commit(&ctl.q_empty);
+      for (int i = 0; ok && i < n_tiles; ++i, ++tiles) {
+        const uint32_t e = 2 * tiles + 1;
+        const bool more = i + 1 < n_tiles;
+        const uint32_t v_at = take(e);
+        if (!ok || !(ok = warp_wait(&ctl.checked[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+        for (int g = 0; ok && g < streams; ++g) {
+          if (!(ok = warp_wait(&ctl.p_full[g], made[g]++ & 1u, &ctl.dead))) break;
+          issue_outputs<E, D>(tmem + 256 + g * 128, tmem + g * 128, v_at, i == 0);
+          if (!more) issue_commit(&ctl.o_done[g]);
+          if (g == streams - 1) issue_commit(&ctl.empty[e % kRing]);
+          if (more) {
+            if (g == 0) k_at = take(e + 1);
+            if (!ok) break;
+            scores(g, k_at);
+            if (g == streams - 1) {
+              issue_commit(&ctl.empty[(e + 1) % kRing]);
+              if (i + 2 == n_tiles) issue_commit(&ctl.q_empty);
+            }
+          }
+        }
+      }
+    } while (ok && u.next(p, line));
+    // nothing is in flight when the tensor memory goes back
+    issue_commit(&ctl.drain);
+    bar_linger(&ctl.drain, 0u);
+    }
+  }
+  tm_free(tmem, warp);
+  if (ctl.dead && tid == 0) flag_run(p, line);
+}
+
+namespace {
+
+bool wide_pairs(const AttnParams &p) { return p.rows > wide_tile_rows(p.G); }
+int wide_ctas(const AttnParams &p) { return wide_pairs(p) ? p.workers : p.workers / 2; }
+// Few rows leave room for an entry more in each ring.
+int solo_query_rows(const AttnParams &p) { return p.S.N * p.G <= 32 ? 32 : 128; }
 
 // cuTensorMapEncodeTiled of the installed driver; the library does not link to it.
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -885,20 +1085,23 @@ bool cache_map(CUtensorMap *map, Origin *o, int dtype, const KvCache &C, int D, 
   return encode_map(map, dtype, base, dims, steps, box);
 }
 
-template <class E, int D, int NQ>
-cudaError_t start_wide(const AttnParams &p, const WideMaps &maps, cudaStream_t stream) {
-  constexpr int smem = wide_smem<D, NQ>();
-  const cudaError_t e = cudaFuncSetAttribute(wide_kernel<E, D, NQ>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <class K>
+cudaError_t start_wide(K kernel, int smem, const AttnParams &p, const WideMaps &maps,
+                       cudaStream_t stream) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  wide_kernel<E, D, NQ><<<p.ctas, kWideThreads, smem, stream>>>(p, maps);
+  kernel<<<wide_ctas(p), kWideThreads, smem, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
-template <class E>
-cudaError_t start_wide(const AttnParams &p, int tiles, const WideMaps &maps, cudaStream_t stream) {
-  if (p.D == 64) return tiles == 2 ? start_wide<E, 64, 2>(p, maps, stream) : start_wide<E, 64, 1>(p, maps, stream);
-  return tiles == 2 ? start_wide<E, 128, 2>(p, maps, stream) : start_wide<E, 128, 1>(p, maps, stream);
+template <class E, int D>
+cudaError_t start_wide(const AttnParams &p, const WideMaps &maps, cudaStream_t stream) {
+  if (wide_pairs(p))
+    return start_wide(pair_kernel<E, D>, PairShape<D>::kSmem, p, maps, stream);
+  if (solo_query_rows(p) == 32)
+    return start_wide(solo_kernel<E, D, 32>, SoloShape<D, 32>::kSmem, p, maps, stream);
+  return start_wide(solo_kernel<E, D, 128>, SoloShape<D, 128>::kSmem, p, maps, stream);
 }
 
 }  // namespace
@@ -924,15 +1127,17 @@ bool wide_maps(const AttnParams &p, int dtype, WideMaps *maps) {
   const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(p.G), static_cast<cuuint64_t>(p.S.N),
                               static_cast<cuuint64_t>(p.D / 64), static_cast<cuuint64_t>(q.count)};
   const long long steps[4] = {p.G > 1 ? p.q_head : row, p.S.N > 1 ? p.q_token : row, 128, q.step};
-  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.G),
-                             static_cast<cuuint32_t>(wide_tile_rows(p.G) / p.G), 1, 1};
+  const int rows = wide_pairs(p) ? 128 : solo_query_rows(p);
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(rows / p.G),
+                             1, 1};
   return encode_map(&maps->q, dtype, p.q, dims, steps, box);
 }
 
-cudaError_t launch_attention_wide(const AttnParams &p, int tiles, const WideMaps &maps, int dtype,
+cudaError_t launch_attention_wide(const AttnParams &p, const WideMaps &maps, int dtype,
                                   cudaStream_t stream) {
-  return dtype == SPEC_BF16 ? start_wide<Bf16>(p, tiles, maps, stream)
-                            : start_wide<F16>(p, tiles, maps, stream);
+  if (dtype == SPEC_BF16)
+    return p.D == 64 ? start_wide<Bf16, 64>(p, maps, stream) : start_wide<Bf16, 128>(p, maps, stream);
+  return p.D == 64 ? start_wide<F16, 64>(p, maps, stream) : start_wide<F16, 128>(p, maps, stream);
 }
 
 }  // namespace sv

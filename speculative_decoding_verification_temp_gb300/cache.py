@@ -27,18 +27,19 @@ _KV_DTYPES = {torch.float32: _abi.SPEC_F32, torch.bfloat16: _abi.SPEC_BF16,
 def _on(x, dev, name):
     if not isinstance(x, torch.Tensor) or x.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
-    return x
 
 
 def _forward_only(*tensors):
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        raise ValueError("the cache operators have no gradient: call them under torch.no_grad()")
+    for t in tensors:
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(
+                "the cache operators have no gradient: call them under torch.no_grad()")
 
 
 def _ints(x, shape, dev, name):
     """An int32 tensor of `shape` on dev, contiguous; another integer type is converted."""
     _on(x, dev, name)
-    if tuple(x.shape) != shape:
+    if x.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(x.shape)}")
     if x.dtype != torch.int32:
         if x.is_floating_point() or x.is_complex() or x.dtype == torch.bool:
@@ -50,7 +51,7 @@ def _ints(x, shape, dev, name):
 def _inplace(x, shape, dev, name):
     """An int32 tensor that the call writes: no conversion, which would write a copy."""
     _on(x, dev, name)
-    if x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous():
+    if x.dtype != torch.int32 or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)}")
     return x
 
@@ -62,43 +63,50 @@ def _cache(k, v, layers):
         raise ValueError("k_cache must be a CUDA tensor")
     _on(v, k.device, "v_cache")
     _forward_only(k, v)
-    shape, dt = k.shape, k.dtype
-    if dt not in _KV_DTYPES or v.dtype != dt:
+    shape, code, ks, vs = k.shape, _KV_DTYPES.get(k.dtype), k.stride(), v.stride()
+    if code is None or v.dtype != k.dtype:
         raise ValueError("k_cache and v_cache must both be float32, bfloat16 or float16")
-    if v.shape != shape or len(shape) != 4 and not (layers and len(shape) == 5):
+    dims = len(shape)
+    if v.shape != shape or dims != 4 and not (layers and dims == 5):
         raise ValueError("k_cache and v_cache must be [%snum_pages, page_size, num_heads, head_dim]"
                          % ("num_layers, " if layers else ""))
-    ks, vs = k.stride(), v.stride()
     if shape[-1] > 1 and (ks[-1] != 1 or vs[-1] != 1):
         raise ValueError("the last dimension of the caches must be contiguous")
-    if len(shape) == 4:
-        ks, vs, n = (0, *ks), (0, *vs), 1
-    else:
-        n = shape[0]
-    return _abi.spec_kv_cache(k.data_ptr(), v.data_ptr(), *ks[:4], *vs[:4], _KV_DTYPES[dt], n,
-                              *shape[-4:])
+    if dims == 4:
+        return _abi.spec_kv_cache(k.data_ptr(), v.data_ptr(), 0, ks[0], ks[1], ks[2], 0, vs[0],
+                                  vs[1], vs[2], code, 1, *shape)
+    return _abi.spec_kv_cache(k.data_ptr(), v.data_ptr(), *ks[:4], *vs[:4], code, *shape)
 
 
 def _table(page_table, B, dev):
     _on(page_table, dev, "page_table")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError(f"page_table must be [{B}, max_pages]")
     if page_table.dtype != torch.int32:
-        page_table = _ints(page_table, tuple(page_table.shape), dev, "page_table")
-    if page_table.stride(1) != 1 or page_table.stride(0) < page_table.shape[1]:
+        page_table = _ints(page_table, tuple(shape), dev, "page_table")
+    ld, step = page_table.stride()
+    if step != 1 or ld < shape[1]:
         page_table = page_table.contiguous()
-    return page_table, _abi.spec_page_table(page_table.data_ptr(), page_table.stride(0),
-                                            page_table.shape[1])
+        ld = shape[1]
+    return page_table, _abi.spec_page_table(page_table.data_ptr(), ld, shape[1])
+
+
+# the current stream's handle, without a Stream object where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _run(dev, fn, *args):
     """fn(*args, stream) on dev's current stream, with dev the current device."""
-    if dev.index == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            code = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(code)
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
+    if code:
+        _check(code)
 
 
 def _ptr(x):
@@ -127,11 +135,13 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
     dev = k_cache.device
     _on(q, dev, "q")
     _forward_only(q)
-    if q.dim() != 4 or q.shape[3] != cache.head_dim or q.dtype != k_cache.dtype:
+    if q.dim() != 4 or q.shape[3] != k_cache.shape[3] or q.dtype != k_cache.dtype:
         raise ValueError("q must be [B, N, num_q_heads, head_dim] with the cache's type")
-    B, N, Hq, D = q.shape
-    if q.stride(3) != 1:
+    B, N, Hq, D = shape = q.shape
+    strides = q.stride()
+    if strides[3] != 1:
         q = q.contiguous()
+        strides = q.stride()
     page_table, table = _table(page_table, B, dev)
     context_len = _ints(context_len, (B,), dev, "context_len")
     if num_new is not None:
@@ -149,10 +159,10 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
         pos_stride = N if position.dim() == 2 else 0
         position = _ints(position, (B, N) if position.dim() == 2 else (N,), dev, "position")
     if out is None:
-        out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
     else:
         _on(out, dev, "out")
-        if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        if out.shape != shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be a contiguous tensor like q")
     lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev) if return_lse else None
     flags = torch.empty(B, dtype=torch.int32, device=dev) if return_flags else None
@@ -161,10 +171,10 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
     # of the caching allocator, ordered on this stream and kept by a graph that
     # captures the call: never shared with calls on other streams
     ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    _run(dev, lib.spec_paged_attention, q.data_ptr(), *q.stride()[:3], Hq, cache, table,
-         context_len.data_ptr(), _ptr(num_new), B, N, _ptr(tree_mask), mask_stride,
+    _run(dev, lib.spec_paged_attention, q.data_ptr(), strides[0], strides[1], strides[2], Hq, cache,
+         table, context_len.data_ptr(), _ptr(num_new), B, N, _ptr(tree_mask), mask_stride,
          _ptr(position), pos_stride, D ** -0.5 if scale is None else float(scale), int(window),
-         int(sinks), out.data_ptr(), _ptr(lse), _ptr(flags), ws.data_ptr(), ws.numel())
+         int(sinks), out.data_ptr(), _ptr(lse), _ptr(flags), ws.data_ptr(), max(nbytes, 16))
     return AttentionResult(out, lse, flags)
 
 

@@ -2,6 +2,8 @@
 // by the operators on it.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace sv {
@@ -64,6 +66,30 @@ __device__ __forceinline__ bool page_ok(const KvCache &C, int page) {
 // those of the new tokens alone).  One launch.
 cudaError_t launch_kv_flags(const KvSeqs &S, const KvCache &C, bool new_only, uint32_t *flags,
                             cudaStream_t stream);
+
+// Launch of a kernel with much dynamic shared memory.  It is allowed to use that
+// once per device (done: a bit each), since the call for it costs a good part of
+// a launch's host time; a context that has forgotten it is told again.
+template <typename... KP, typename... A>
+cudaError_t launch_large(void (*kernel)(KP...), std::atomic<uint64_t> &done, int grid, int threads,
+                         int smem, cudaStream_t stream, const A &...args) {
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  for (;;) {
+    const bool told = (done.load(std::memory_order_relaxed) & bit) != 0;
+    if (!told) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      done.fetch_or(bit, std::memory_order_relaxed);
+    }
+    kernel<<<grid, threads, smem, stream>>>(args...);
+    e = cudaGetLastError();
+    if (e != cudaErrorInvalidValue || !told) return e;
+    done.fetch_and(~bit, std::memory_order_relaxed);
+  }
+}
 
 // Launch with programmatic stream serialisation: the kernel may start while
 // the previous one on the stream drains, and waits for it at its own

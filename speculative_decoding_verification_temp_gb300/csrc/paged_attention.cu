@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
         }
       }
       constexpr uint32_t kAll = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
-      if (valid != kAll || !all_seen(p, u.k, u.r0, at0, KT)) {
+      if (valid != kAll || !all_seen(p, u.k, at0, KT)) {
 #pragma unroll
         for (int j = 0; j < KT / 8; ++j) {
 #pragma unroll
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_con
 #pragma unroll
         for (int x = KT; x < 32; x <<= 1) s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], x);
       constexpr uint32_t kAll = KT == 32 ? 0xFFFFFFFFu : (1u << KT) - 1u;
-      if (valid != kAll || !all_seen(p, u.k, u.r0, at0, KT)) {
+      if (valid != kAll || !all_seen(p, u.k, at0, KT)) {
         const bool there = (valid >> key) & 1u;
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -731,16 +731,19 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // ---------------------------------------------------------------------------
 
 struct AttnPlan {
-  int workers, rows, tile, unit_cost;
+  int workers, rows, tile_log2, unit_cost;
 };
 
+constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
+
 AttnPlan narrow_plan(int D, int dtype) {
-  if (dtype == SPEC_F32)
-    return {kSms, 8,
-            D <= 64 ? Rows8<64>::kTile : (D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile), 1};
-  if (D <= 64) return {2 * kSms, 16, Rows16<64, 32, 3>::kTile, 1};
-  if (D <= 128) return {2 * kSms, 16, Rows16<128, 16, 3>::kTile, 1};
-  return {kSms, 16, Rows16<256, 16, 3>::kTile, 1};
+  if (dtype == SPEC_F32) {
+    if (D <= 64) return {kSms, 8, log2_of(Rows8<64>::kTile), 1};
+    return {kSms, 8, log2_of(D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile), 1};
+  }
+  if (D <= 64) return {2 * kSms, 16, log2_of(Rows16<64, 32, 3>::kTile), 1};
+  if (D <= 128) return {2 * kSms, 16, log2_of(Rows16<128, 16, 3>::kTile), 1};
+  return {kSms, 16, log2_of(Rows16<256, 16, 3>::kTile), 1};
 }
 
 bool wide_sizes(int G, int D, int dtype) {
@@ -748,24 +751,21 @@ bool wide_sizes(int G, int D, int dtype) {
 }
 AttnPlan wide_plan(int N, int G) {
   // two row tiles that share their keys, or a row tile for each of two streams
-  if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 128, 2};
-  return {2 * kSms, wide_tile_rows(G), 128, 1};
+  if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 7, 2};
+  return {2 * kSms, wide_tile_rows(G), 7, 1};
 }
 
-template <class K>
-cudaError_t start(K kernel, size_t smem, const AttnParams &p, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  kernel<<<p.workers, kAttnThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+template <auto kKernel>
+cudaError_t start(size_t smem, const AttnParams &p, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  return launch_large(kKernel, done, p.workers, kAttnThreads, static_cast<int>(smem), stream, p);
 }
 
 template <class E>
 cudaError_t start16(const AttnParams &p, cudaStream_t stream) {
-  if (p.D <= 64) return start(rows16_kernel<E, 64, 32, 3>, Rows16<64, 32, 3>::kSmem, p, stream);
-  if (p.D <= 128) return start(rows16_kernel<E, 128, 16, 3>, Rows16<128, 16, 3>::kSmem, p, stream);
-  return start(rows16_kernel<E, 256, 16, 3>, Rows16<256, 16, 3>::kSmem, p, stream);
+  if (p.D <= 64) return start<rows16_kernel<E, 64, 32, 3>>(Rows16<64, 32, 3>::kSmem, p, stream);
+  if (p.D <= 128) return start<rows16_kernel<E, 128, 16, 3>>(Rows16<128, 16, 3>::kSmem, p, stream);
+  return start<rows16_kernel<E, 256, 16, 3>>(Rows16<256, 16, 3>::kSmem, p, stream);
 }
 
 size_t align16(size_t x) { return (x + 15) / 16 * 16; }
@@ -788,9 +788,8 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
   auto take = [&](const AttnPlan &plan) {
     p.workers = plan.workers;
     p.rows = plan.rows;
-    p.tile = plan.tile;
+    p.tile_log2 = plan.tile_log2;
     p.unit_cost = plan.unit_cost;
-    p.min_run = 1;
   };
   WideMaps maps;
   bool wide = wide_sizes(p.G, p.D, dtype) && (P % 128 == 0 || (P >= 8 && 128 % P == 0));
@@ -805,11 +804,11 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
   cudaError_t e;
   if (dtype == SPEC_F32) {
     if (p.D <= 64) {
-      e = start(rows8_kernel<64>, Rows8<64>::kSmem, p, stream);
+      e = start<rows8_kernel<64>>(Rows8<64>::kSmem, p, stream);
     } else if (p.D <= 128) {
-      e = start(rows8_kernel<128>, Rows8<128>::kSmem, p, stream);
+      e = start<rows8_kernel<128>>(Rows8<128>::kSmem, p, stream);
     } else {
-      e = start(rows8_kernel<256>, Rows8<256>::kSmem, p, stream);
+      e = start<rows8_kernel<256>>(Rows8<256>::kSmem, p, stream);
     }
   } else if (wide) {
     e = launch_attention_wide(p, maps, dtype, stream);

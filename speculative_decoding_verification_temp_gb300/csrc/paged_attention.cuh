@@ -42,9 +42,8 @@ struct AttnParams {
   uint32_t *flags;
   float *part;  // partial results, two slots per worker
   struct JoinDesc *join;
-  int workers, rows, tile;  // at most; R and T
-  int unit_cost;            // places on the line behind a unit's key tiles
-  int min_run;              // a worker's run is at least this long (where there is as much)
+  int workers, rows, tile_log2;  // at most; R; T as a power of two
+  int unit_cost;                 // places on the line behind a unit's key tiles
 };
 
 // A cut unit, written by the worker that holds its first cut; its pieces are
@@ -76,25 +75,28 @@ cudaError_t launch_attention_wide(const AttnParams &p, const WideMaps &maps, int
 struct KeyRange {
   int ctx, n_new;   // n_new: new tokens, 0 where the sequence does not fit
   int end;          // keys at or behind it are seen by no row
+  int all;          // keys before it are seen by every row, but for the window
   int sink_tiles, lo, count;
 };
 
 __device__ __forceinline__ KeyRange key_range(const AttnParams &p, int ctx, int n_new, bool fits,
                                               int r0) {
+  const int round = (1 << p.tile_log2) - 1;
   KeyRange k;
   k.ctx = ctx;
   k.n_new = n_new;
-  k.end = 0;
+  k.end = k.all = 0;
   int first = 0;
   if (fits) {
-    const int n_lo = r0 / p.G;
-    const int n_hi = min((r0 + p.rows - 1) / p.G, n_new - 1);
+    const int n_lo = r0 == 0 ? 0 : r0 / p.G;
+    const int n_hi = r0 + p.rows >= n_new * p.G ? n_new - 1 : (r0 + p.rows - 1) / p.G;
     k.end = p.mask ? ctx + n_new : ctx + n_hi + 1;
+    k.all = p.mask ? ctx : ctx + n_lo + 1;
     if (p.window) first = max(0, (p.mask || p.position ? ctx : ctx + n_lo) - p.window + 1);
   }
-  k.lo = first / p.tile;
-  k.sink_tiles = p.window ? min((min(p.sinks, k.end) + p.tile - 1) / p.tile, k.lo) : 0;
-  k.count = max(1, k.sink_tiles + (k.end + p.tile - 1) / p.tile - k.lo);
+  k.lo = first >> p.tile_log2;
+  k.sink_tiles = p.window ? min((min(p.sinks, k.end) + round) >> p.tile_log2, k.lo) : 0;
+  k.count = max(1, k.sink_tiles + ((k.end + round) >> p.tile_log2) - k.lo);
   return k;
 }
 
@@ -102,26 +104,40 @@ __device__ __forceinline__ int key_tile(const KeyRange &k, int i) {
   return i < k.sink_tiles ? i : k.lo + i - k.sink_tiles;
 }
 
+// Quotient of two whole numbers that are mostly small.
+__device__ __forceinline__ long long div_small(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 // Places of one head of a sequence.
 __device__ __forceinline__ long long head_work(const AttnParams &p, int ctx, int n_new, bool fits) {
+  const int rows = n_new * p.G;
+  if (rows == 0) return 0;
+  if (rows <= p.rows || p.mask || !fits) {  // its row tiles have the same keys
+    const int tiles = rows <= p.rows ? 1 : (rows + p.rows - 1) / p.rows;
+    return static_cast<long long>(tiles) * (key_range(p, ctx, n_new, fits, 0).count + p.unit_cost);
+  }
   long long w = 0;
-  for (int r0 = 0; r0 < n_new * p.G; r0 += p.rows)
+  for (int r0 = 0; r0 < rows; r0 += p.rows)
     w += key_range(p, ctx, n_new, fits, r0).count + p.unit_cost;
   return w;
 }
 
-// A worker's run.
+// A worker's run.  The line's places are dealt out in order, one more to each of
+// the first `more` workers.
 struct Line {
   long long w0, w1;     // empty: no work
-  long long total;
+  long long per, more;
   int worker, workers;  // of `workers` with work
   int b;                // the sequence that holds w0
   long long in_seq;     // w0 within it
-};
 
-__device__ __forceinline__ long long run_start(long long worker, long long total, int workers) {
-  return worker * total / workers;
-}
+  __device__ __forceinline__ long long start_of(long long w) const { return w * per + min(w, more); }
+  __device__ __forceinline__ long long worker_of(long long place) const {
+    const long long cut = more * (per + 1);
+    return place < cut ? div_small(place, per + 1) : more + div_small(place - cut, per);
+  }
+};
 
 // Shared memory that find_runs works in.
 template <int kT, int kW>
@@ -136,8 +152,8 @@ template <int kT, int kW>
 __device__ __forceinline__ void find_runs(const AttnParams &p, RunScratch<kT, kW> &x, int first,
                                           int step, Line (&L)[kW]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.S.B + kT - 1) / kT;
-  const int b0 = min(tid * per, p.S.B), b1 = min(b0 + per, p.S.B);
+  const int chunk = (p.S.B + kT - 1) / kT;
+  const int b0 = min(tid * chunk, p.S.B), b1 = min(b0 + chunk, p.S.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
@@ -159,16 +175,17 @@ __device__ __forceinline__ void find_runs(const AttnParams &p, RunScratch<kT, kW
     total += v;
   }
   before -= mine;
-  const long long most = (total + p.min_run - 1) / p.min_run;
-  const int workers = static_cast<int>(most < p.workers ? (most > 0 ? most : 1) : p.workers);
+  const int workers = total < p.workers ? (total > 0 ? static_cast<int>(total) : 1) : p.workers;
+  const long long per = div_small(total, workers);
 #pragma unroll
   for (int i = 0; i < kW; ++i) {
-    L[i].total = total;
+    L[i].per = per;
+    L[i].more = total - per * workers;
     L[i].workers = workers;
     L[i].worker = first + i * step;
     const bool busy = total > 0 && L[i].worker < workers;
-    L[i].w0 = busy ? run_start(L[i].worker, total, workers) : 0;
-    L[i].w1 = busy ? run_start(L[i].worker + 1ll, total, workers) : 0;
+    L[i].w0 = busy ? L[i].start_of(L[i].worker) : 0;
+    L[i].w1 = busy ? L[i].start_of(L[i].worker + 1ll) : 0;
     if (busy && before <= L[i].w0 && L[i].w0 < before + mine) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
@@ -211,7 +228,7 @@ struct UnitWalk {
     b = L.b;
     load_seq(p);
     const long long per_head = head_work(p, k.ctx, k.n_new, fits);
-    h = static_cast<int>(L.in_seq / per_head);
+    h = static_cast<int>(div_small(L.in_seq, per_head));
     long long left = L.in_seq - h * per_head;
     for (r0 = 0;; r0 += p.rows) {
       k = key_range(p, k.ctx, k.n_new, fits, r0);
@@ -263,15 +280,11 @@ __host__ __device__ __forceinline__ size_t slot_floats(int R, int D) {
 __device__ __forceinline__ void write_join(const AttnParams &p, const Line &L, const UnitWalk *u) {
   if (L.worker >= p.workers) return;
   JoinDesc d = {0, 0, 0, -1};
-  if (u && u->i0 > 0 && run_start(L.worker - 1ll, L.total, L.workers) <= u->a) {
+  if (u && u->i0 > 0 && L.start_of(L.worker - 1ll) <= u->a) {
     d.b = u->b;
     d.h = u->h;
     d.r0 = u->r0;
-    const long long last = u->a + u->k.count - 1;
-    long long c = last * L.workers / L.total;  // the worker of the last tile, or next to it
-    while (run_start(c, L.total, L.workers) > last) --c;
-    while (c + 1 < L.workers && run_start(c + 1, L.total, L.workers) <= last) ++c;
-    d.pieces_end = static_cast<int>(c);
+    d.pieces_end = static_cast<int>(L.worker_of(u->a + u->k.count - 1));
   }
   p.join[L.worker] = d;
 }
@@ -302,11 +315,9 @@ __device__ __forceinline__ bool sees(const AttnParams &p, const KeyRange &k, int
   return true;
 }
 
-// Whether every row of the unit (from row r0 on) sees all of the keys
-// [at, at + n).
-__device__ __forceinline__ bool all_seen(const AttnParams &p, const KeyRange &k, int r0, int at,
-                                         int n) {
-  if (at + n > k.ctx && (p.mask || at + n - 1 > k.ctx + r0 / p.G)) return false;
+// Whether every row of the unit sees all of the keys [at, at + n).
+__device__ __forceinline__ bool all_seen(const AttnParams &p, const KeyRange &k, int at, int n) {
+  if (at + n > k.all) return false;
   if (!p.window) return true;
   if (at + n > k.ctx) return false;
   // before the last place that a new token can have
@@ -397,9 +408,9 @@ static __device__ __noinline__ float4 nonfinite_values(const AttnParams &p, cons
                                                 int d, float4 acc) {
   float *a = reinterpret_cast<float *>(&acc);
   for (int i = u.i0; i < u.i1; ++i) {
-    const int t0 = key_tile(u.k, i) * p.tile;
-    for (int at0 = t0; at0 < t0 + p.tile && at0 < u.k.end; at0 += kSlice) {
-      bool whole = all_seen(p, u.k, u.r0, at0, kSlice);
+    const int t0 = key_tile(u.k, i) << p.tile_log2;
+    for (int at0 = t0; at0 < t0 + (1 << p.tile_log2) && at0 < u.k.end; at0 += kSlice) {
+      bool whole = all_seen(p, u.k, at0, kSlice);
       for (int at = at0; at < at0 + kSlice && whole; ++at)
         whole = at < u.k.end && page_ok(p.C, page_at(p.S, u.b, at / p.C.page_size));
       if (whole) continue;

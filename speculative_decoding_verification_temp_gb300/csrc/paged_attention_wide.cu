@@ -321,10 +321,10 @@ __device__ __forceinline__ void clean_values(char *entry, uint4 valid, int from,
 
 // The first token of a masked tile that clean_values has to look at: those
 // before it are copied and every row sees them.
-__device__ __forceinline__ int clean_from(const AttnParams &p, const KeyRange &k, int r0, int at0,
+__device__ __forceinline__ int clean_from(const AttnParams &p, const KeyRange &k, int at0,
                                           uint4 valid) {
   if (p.window) return 0;
-  const int from = min(max((p.mask ? k.ctx : k.ctx + r0 / p.G + 1) - at0, 0), kTileKeys);
+  const int from = min(max(k.all - at0, 0), kTileKeys);
   const uint32_t missing = (low_bits(from) & ~valid.x) | (low_bits(from - 32) & ~valid.y) |
                            (low_bits(from - 64) & ~valid.z) | (low_bits(from - 96) & ~valid.w);
   return missing ? 0 : from;
@@ -333,7 +333,7 @@ __device__ __forceinline__ int clean_from(const AttnParams &p, const KeyRange &k
 __device__ __forceinline__ bool tile_masked(const AttnParams &p, const UnitWalk &u, int at0,
                                             uint4 valid) {
   return (valid.x & valid.y & valid.z & valid.w) != 0xFFFFFFFFu ||
-         !all_seen(p, u.k, u.r0, at0, kTileKeys);
+         !all_seen(p, u.k, at0, kTileKeys);
 }
 
 // One row per thread: the scores of a tile become weights, m and l go on, the
@@ -345,25 +345,23 @@ __device__ __forceinline__ void softmax_tile(const AttnParams &p, const UnitWalk
   const float c = p.scale_log2;
   tc_after();
   uint32_t s[4][32];
+  float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
+  tm_load32(s[0], s_at);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) tm_load32(s[j], s_at + j * 32);
-  tm_wait_ld();
-  if (masked) {
-    const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 4; ++j) {
+    tm_wait_ld();
+    if (j < 3) tm_load32(s[j + 1], s_at + (j + 1) * 32);
+    if (masked) {
       const uint32_t vis = seen_word(p, u.k, u.b, n, at0 + j * 32, in[j]);
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         if (!((vis >> e) & 1u)) s[j][e] = __float_as_uint(-INFINITY);
     }
-  }
-  float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int e = 0; e < 32; e += 2)
       x[j] = max3(x[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
+  }
   const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
   const bool raise = mine && top > m + kSlack;
   if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -562,17 +560,16 @@ __device__ __forceinline__ void issue_commit(const void *bar) {
   __syncwarp();
 }
 
-__device__ __forceinline__ uint32_t tm_alloc(void *slot, int warp) {
-  if (warp == 11) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
-                     smem_u32(slot))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
+// By the warp that frees it; other warps see the address behind a barrier.
+__device__ __forceinline__ void tm_alloc(void *slot) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                   smem_u32(slot))
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   tc_before();
-  __syncthreads();
-  tc_after();
-  return *reinterpret_cast<volatile uint32_t *>(slot);
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ void tm_free(uint32_t tmem, int warp) {
   __syncwarp();
@@ -648,8 +645,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     ctl.bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 11) tm_alloc(&ctl.tmem);
+  if (warp == 8 && lane == 0) {
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+    prefetch_map(&maps.q);
+  }
+  __syncwarp();
   Line lines[2];
-  // a barrier as well; consecutive workers on different CTAs
+  // barriers as well; consecutive workers on different CTAs
   find_runs(p, ctl.runs, blockIdx.x, gridDim.x, lines);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // of this warp's stream
@@ -658,8 +662,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   UnitWalk u;
   const bool busy = u.start(p, line);
   if (lane == 0 && (warp == 8 || warp == 9)) write_join(p, line, busy ? &u : nullptr);
-  if (lines[0].w0 == lines[0].w1 && lines[1].w0 == lines[1].w1) return;
-  const uint32_t tmem = tm_alloc(&ctl.tmem, warp);
+  tc_after();
+  const uint32_t tmem = ctl.tmem;
+  if (lines[0].w0 == lines[0].w1 && lines[1].w0 == lines[1].w1) {
+    tm_free(tmem, warp);
+    return;
+  }
   auto &st = ctl.stream[g];
   const uint32_t s_at = tmem + g * 128, o_at = tmem + 256 + g * 128;
   const uint32_t q_at = smem_u32(wide_s) + g * Shape::kQ;
@@ -691,7 +699,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const uint32_t e = 2 * tiles + 1;
             if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
             clean_values<E, D>(ring + e % kRing * W::kBytes, valid,
-                               clean_from(p, u.k, u.r0, at0, valid),
+                               clean_from(p, u.k, at0, valid),
                                idle == 0 ? row : row - (4 - idle) * 32, idle == 0 ? 128 : idle * 32,
                                &ctl.bad);
           }
@@ -839,15 +847,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     ctl.bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 11) tm_alloc(&ctl.tmem);
+  if (warp == 8 && lane == 0) {
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+    prefetch_map(&maps.q);
+  }
+  __syncwarp();
   Line lines[1];
-  find_runs(p, ctl.runs, blockIdx.x, 0, lines);  // a barrier as well
+  find_runs(p, ctl.runs, blockIdx.x, 0, lines);  // barriers as well
   const Line &line = lines[0];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   UnitWalk u;
   const bool busy = u.start(p, line);
   if (tid == 0) write_join(p, line, busy ? &u : nullptr);
-  if (!busy) return;
-  const uint32_t tmem = tm_alloc(&ctl.tmem, warp);
+  tc_after();
+  const uint32_t tmem = ctl.tmem;
+  if (!busy) {  // the same for every thread
+    tm_free(tmem, warp);
+    return;
+  }
   const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(wide_s);
   uint32_t tiles = 0, units = 0;
   bool ok = true;
@@ -948,7 +967,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (!(ok = warp_wait(&ctl.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
         if (tile_masked(p, u, at0, valid)) {
           clean_values<E, D>(ring + e % kRing * W::kBytes, valid,
-                             clean_from(p, u.k, u.r0, at0, valid), lane, 32, &ctl.bad);
+                             clean_from(p, u.k, at0, valid), lane, 32, &ctl.bad);
         }
         __syncwarp();
         if (lane == 0) {
@@ -1085,23 +1104,18 @@ bool cache_map(CUtensorMap *map, Origin *o, int dtype, const KvCache &C, int D, 
   return encode_map(map, dtype, base, dims, steps, box);
 }
 
-template <class K>
-cudaError_t start_wide(K kernel, int smem, const AttnParams &p, const WideMaps &maps,
-                       cudaStream_t stream) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kernel<<<wide_ctas(p), kWideThreads, smem, stream>>>(p, maps);
-  return cudaGetLastError();
+template <auto kKernel>
+cudaError_t start_wide(int smem, const AttnParams &p, const WideMaps &maps, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  return launch_large(kKernel, done, wide_ctas(p), kWideThreads, smem, stream, p, maps);
 }
 
 template <class E, int D>
 cudaError_t start_wide(const AttnParams &p, const WideMaps &maps, cudaStream_t stream) {
-  if (wide_pairs(p))
-    return start_wide(pair_kernel<E, D>, PairShape<D>::kSmem, p, maps, stream);
+  if (wide_pairs(p)) return start_wide<pair_kernel<E, D>>(PairShape<D>::kSmem, p, maps, stream);
   if (solo_query_rows(p) == 32)
-    return start_wide(solo_kernel<E, D, 32>, SoloShape<D, 32>::kSmem, p, maps, stream);
-  return start_wide(solo_kernel<E, D, 128>, SoloShape<D, 128>::kSmem, p, maps, stream);
+    return start_wide<solo_kernel<E, D, 32>>(SoloShape<D, 32>::kSmem, p, maps, stream);
+  return start_wide<solo_kernel<E, D, 128>>(SoloShape<D, 128>::kSmem, p, maps, stream);
 }
 
 }  // namespace

@@ -499,7 +499,7 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  *    launch of its own.
  * Products of bf16 and f16 run on the tensor cores with float32 sums; the
  * weights are rounded to the cache's type before they meet the values.  float32
- * caches are computed in float32.  1 <= N <= 4096.
+ * caches are computed in float32.  1 <= N <= 4096.  workspace: 32-byte aligned.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (a head_dim, alignment or
  * stride not listed above) before any launch.  B = 0 is a no-op.  Two launches. */
 spec_status spec_paged_attention(

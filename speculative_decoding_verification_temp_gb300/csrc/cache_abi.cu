@@ -162,7 +162,7 @@ spec_status spec_paged_attention(
       !stride_ok(q_head_stride, num_q_heads, cache.head_dim, esize))
     return SPEC_ERR_UNSUPPORTED;
   const int group = num_q_heads / cache.num_heads;
-  if (!workspace || !aligned16(workspace) ||
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0 ||
       workspace_bytes < sv::attention_workspace_bytes(N, group, cache.head_dim, cache.dtype))
     return SPEC_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -95,7 +95,7 @@ __device__ __forceinline__ void write_unit(const AttnParams &p, const UnitWalk &
              make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
       if (d == 0 && p.lse) p.lse[at] = row_lse(M, l);
     } else {
-      store4(slot + 2 * p.rows + static_cast<size_t>(row) * p.D + d, o);
+      store4(slot + slot_stats(p.rows) + static_cast<size_t>(row) * p.D + d, o);
       if (d == 0) {
         slot[row] = M;
         slot[p.rows + row] = l;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const float *s = slot(i);
         m[j] = s[row];
         lp[j] = s[p.rows + row];
-        const float *from_o = s + 2 * p.rows + static_cast<size_t>(row) * p.D;
+        const float *from_o = s + slot_stats(p.rows) + static_cast<size_t>(row) * p.D;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if ((lane + 32 * x) * 4 < p.D)
@@ -768,12 +768,12 @@ cudaError_t start16(const AttnParams &p, cudaStream_t stream) {
   return start<rows16_kernel<E, 256, 16, 3>>(Rows16<256, 16, 3>::kSmem, p, stream);
 }
 
-size_t align16(size_t x) { return (x + 15) / 16 * 16; }
+size_t align32(size_t x) { return (x + 31) / 32 * 32; }
 
 }  // namespace
 
 size_t plan_bytes(const AttnPlan &plan, int D) {
-  return align16(plan.workers * sizeof(JoinDesc)) +
+  return align32(plan.workers * sizeof(JoinDesc)) +
          2 * plan.workers * slot_floats(plan.rows, D) * sizeof(float);
 }
 
@@ -800,7 +800,7 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
   if (!wide) take(narrow_plan(p.D, dtype));
   p.join = static_cast<JoinDesc *>(workspace);
   p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                     align16(p.workers * sizeof(JoinDesc)));
+                                     align32(p.workers * sizeof(JoinDesc)));
   cudaError_t e;
   if (dtype == SPEC_F32) {
     if (p.D <= 64) {

@@ -271,8 +271,10 @@ struct UnitWalk {
 __device__ __forceinline__ int piece_slot(const UnitWalk &u, int worker) {
   return 2 * worker + (u.i0 > 0 ? 0 : 1);
 }
+// A slot: m of each row, l of each row, padding to 32 bytes, the rows' outputs.
+__host__ __device__ __forceinline__ size_t slot_stats(int R) { return (2 * R + 7) / 8 * 8; }
 __host__ __device__ __forceinline__ size_t slot_floats(int R, int D) {
-  return static_cast<size_t>(R) * (D + 2);
+  return (slot_stats(R) + static_cast<size_t>(R) * D + 7) / 8 * 8;
 }
 
 // Writes a worker's join descriptor: the unit that its first tile cuts, if no

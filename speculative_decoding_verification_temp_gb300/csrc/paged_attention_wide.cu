@@ -242,23 +242,15 @@ __device__ __forceinline__ constexpr uint32_t mma_idesc<F16>(int n, bool b_n_maj
          (8u << 24);
 }
 
-// The top bit of each of two 16-bit values that is an infinity or a NaN.
-template <class E>
-__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t v) {
-  constexpr uint32_t exps = E::kExp * 0x10001u, ones = (E::kExp & (0u - E::kExp)) * 0x10001u;
-  return ((v & exps) + ones) & 0x80008000u;
-}
-
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-// Which of the 32 keys from `at` on token n sees (sees() for all of them), of
-// those in `valid`.
+// Which of the 32 keys from `at` on token n sees (sees() for all of them).
 __device__ __forceinline__ uint32_t seen_word(const AttnParams &p, const KeyRange &k, int b, int n,
-                                              int at, uint32_t valid) {
+                                              int at) {
   const uint32_t in_ctx = low_bits(k.ctx - at);
-  uint32_t w = valid & in_ctx, block = valid & ~in_ctx;
+  uint32_t w = in_ctx, block = ~in_ctx;
   const int place = p.window ? k.ctx + clamp_pos(p, b, n) : 0;
   if (p.window) w &= low_bits(p.sinks - at) | ~low_bits(place - p.window + 1 - at);
   if (block) {
@@ -299,23 +291,50 @@ template <class E, int D>
 __device__ __forceinline__ void clean_values(char *entry, uint4 valid, int from, int t, int threads,
                                              int *bad) {
   using W = Entry<D>;
-  bool found = false;
-#pragma unroll 4
-  for (int i = from / 8 * (W::kGroup / 16) + t; i < W::kBytes / 16; i += threads) {
-    uint4 *x = reinterpret_cast<uint4 *>(entry + i * 16);
-    const uint4 y = *x;
-    const int key = i / (W::kGroup / 16) * 8 + i / 8 % 8;
+  constexpr int kPer = W::kGroup / 16;  // pieces of eight tokens
+  constexpr uint32_t exps = E::kExp * 0x10001u, ones = (E::kExp & (0u - E::kExp)) * 0x10001u;
+  auto key_of = [](int i) { return i / kPer * 8 + i / 8 % 8; };
+  auto piece = [&](int i) { return reinterpret_cast<uint4 *>(entry + i * 16); };
+  const int count = __popc(valid.x) + __popc(valid.y) + __popc(valid.z) + __popc(valid.w);
+  const bool prefix = valid.x == low_bits(count) && valid.y == low_bits(count - 32) &&
+                      valid.z == low_bits(count - 64) && valid.w == low_bits(count - 96);
+  int i = from / 8 * kPer + t;
+  // tokens that were copied, four pieces at once; an exponent of all ones
+  // carries into the sign's place
+  const int copied = prefix ? count / 8 * kPer : 0;
+  for (; i + 3 * threads < copied; i += 4 * threads) {
+    uint32_t found = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 y = *piece(i + j * threads);
+      found |= ((y.x & exps) + ones) | ((y.y & exps) + ones) | ((y.z & exps) + ones) |
+               ((y.w & exps) + ones);
+    }
+    if (!(found & 0x80008000u)) continue;
+    for (int j = 0; j < 4; ++j) {
+      uint4 *x = piece(i + j * threads);
+      *x = make_uint4(finite_or_zero<E>(x->x), finite_or_zero<E>(x->y), finite_or_zero<E>(x->z),
+                      finite_or_zero<E>(x->w));
+    }
+    *reinterpret_cast<volatile int *>(bad) = 1;
+  }
+  for (; i < W::kBytes / 16; i += threads) {
+    const int key = key_of(i);
     const uint32_t word = key < 64 ? (key < 32 ? valid.x : valid.y) : (key < 96 ? valid.z : valid.w);
+    uint4 *x = piece(i);
     if (!((word >> (key & 31)) & 1u)) {
       *x = make_uint4(0, 0, 0, 0);
-    } else if (nonfinite_bits<E>(y.x) | nonfinite_bits<E>(y.y) | nonfinite_bits<E>(y.z) |
-               nonfinite_bits<E>(y.w)) {
+      continue;
+    }
+    const uint4 y = *x;
+    if ((((y.x & exps) + ones) | ((y.y & exps) + ones) | ((y.z & exps) + ones) |
+         ((y.w & exps) + ones)) &
+        0x80008000u) {
       *x = make_uint4(finite_or_zero<E>(y.x), finite_or_zero<E>(y.y), finite_or_zero<E>(y.z),
                       finite_or_zero<E>(y.w));
-      found = true;
+      *reinterpret_cast<volatile int *>(bad) = 1;
     }
   }
-  if (found) *reinterpret_cast<volatile int *>(bad) = 1;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
@@ -335,28 +354,38 @@ __device__ __forceinline__ bool tile_masked(const AttnParams &p, const UnitWalk 
   return (valid.x & valid.y & valid.z & valid.w) != 0xFFFFFFFFu ||
          !all_seen(p, u.k, at0, kTileKeys);
 }
+__device__ __forceinline__ uint4 both(uint4 a, uint4 b) {
+  return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
+}
+// Which of the tile's keys token n sees, as far as that is known before its
+// pages are.
+__device__ __forceinline__ uint4 seen_tile(const AttnParams &p, const UnitWalk &u, int n, int at0) {
+  if (all_seen(p, u.k, at0, kTileKeys))
+    return make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
+  return make_uint4(seen_word(p, u.k, u.b, n, at0), seen_word(p, u.k, u.b, n, at0 + 32),
+                    seen_word(p, u.k, u.b, n, at0 + 64), seen_word(p, u.k, u.b, n, at0 + 96));
+}
 
 // One row per thread: the scores of a tile become weights, m and l go on, the
 // row's outputs so far are rescaled where m is raised (`first`: there are none).
+// seen: the keys that the row sees; masked: some are missing in some row.
 template <class E, int D>
-__device__ __forceinline__ void softmax_tile(const AttnParams &p, const UnitWalk &u, int n, bool mine,
-                                             bool masked, uint4 valid, int at0, uint32_t s_at,
-                                             uint32_t o_at, bool first, float &m, float &l) {
-  const float c = p.scale_log2;
+__device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, uint4 seen,
+                                             uint32_t s_at, uint32_t o_at, bool first, float &m,
+                                             float &l) {
   tc_after();
   uint32_t s[4][32];
   float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
+  const uint32_t vis[4] = {seen.x, seen.y, seen.z, seen.w};
   tm_load32(s[0], s_at);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     tm_wait_ld();
     if (j < 3) tm_load32(s[j + 1], s_at + (j + 1) * 32);
     if (masked) {
-      const uint32_t vis = seen_word(p, u.k, u.b, n, at0 + j * 32, in[j]);
 #pragma unroll
       for (int e = 0; e < 32; ++e)
-        if (!((vis >> e) & 1u)) s[j][e] = __float_as_uint(-INFINITY);
+        if (!(vis[j] & (1u << e))) s[j][e] = __float_as_uint(-INFINITY);
     }
 #pragma unroll
     for (int e = 0; e < 32; e += 2)
@@ -406,15 +435,11 @@ __device__ __forceinline__ void softmax_tile(const AttnParams &p, const UnitWalk
   tm_wait_st();
 }
 
-// Eight outputs of a row.
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-  store4(p, make_float4(v[0], v[1], v[2], v[3]));
-  store4(p + 4, make_float4(v[4], v[5], v[6], v[7]));
-}
-template <class E>
-__device__ __forceinline__ void store8(typename E::T *p, const float (&v)[8]) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(E::pack(v[0], v[1]), E::pack(v[2], v[3]),
-                                             E::pack(v[4], v[5]), E::pack(v[6], v[7]));
+// 32 bytes of a row at once: a whole sector.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // A row's end: its outputs from tensor memory, divided by the sum, or its piece
@@ -426,7 +451,8 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
   using TE = typename E::T;
   const bool whole = u.whole();
   float *slot = p.part + piece_slot(u, worker) * slot_floats(p.rows, D);
-  float *slot_o = slot + 2 * p.rows + static_cast<size_t>(row) * D;
+  float *slot_o = slot + slot_stats(p.rows) + static_cast<size_t>(row) * D;
+  const bool wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   const long long at = mine ? out_row(p, u.b, u.h, u.r0 + row) : 0;
   TE *out = static_cast<TE *>(p.out) + at * D;
   const float norm = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f);
@@ -439,14 +465,28 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
     tm_wait_ld();
     if (mine) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        float v[8];
+      for (int i = 0; i < 32; ++i)
+        o[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * norm);
+      if (whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = l == 0.f ? 0.f : __uint_as_float(o[e + i]) * norm;
-        if (whole) {
-          store8<E>(out + d + e, v);
-        } else {
-          store8(slot_o + d + e, v);
+        for (int e = 0; e < 32; e += 16) {
+          uint32_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = E::pack(__uint_as_float(o[e + 2 * i]), __uint_as_float(o[e + 2 * i + 1]));
+          if (wide_out) {
+            store32(out + d + e, v);
+          } else {
+            *reinterpret_cast<uint4 *>(out + d + e) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4 *>(out + d + e + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          const uint32_t v[8] = {o[e],     o[e + 1], o[e + 2], o[e + 3],
+                                 o[e + 4], o[e + 5], o[e + 6], o[e + 7]};
+          store32(slot_o + d + e, v);
         }
       }
     }
@@ -688,13 +728,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int idle = 4 - min((live + 31) / 32, 4);  // warps without rows
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < n_tiles; ++i, ++tiles) {
-          if (!(ok = warp_wait(&st.s_full, tiles & 1u, &ctl.dead))) break;
           const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+          uint4 seen = make_uint4(0, 0, 0, 0);
+          if (works) seen = seen_tile(p, u, n, at0);
+          if (!(ok = warp_wait(&st.s_full, tiles & 1u, &ctl.dead))) break;
           const uint4 valid = *reinterpret_cast<const uint4 *>(st.valid[tiles % kValidRing]);
           const bool masked = tile_masked(p, u, at0, valid);
           if (works)
-            softmax_tile<E, D>(p, u, n, mine, masked, valid, at0, s_at + lanes, o_at + lanes, i == 0,
-                               m, l);
+            softmax_tile<E, D>(p.scale_log2, mine, masked, both(seen, valid), s_at + lanes,
+                               o_at + lanes, i == 0, m, l);
           if (masked && (idle == 0 || !works)) {
             const uint32_t e = 2 * tiles + 1;
             if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
@@ -877,7 +919,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int g = warp >> 2, part = warp & 3, tile_row = tid & 127, row = g * tile_rows + tile_row;
     const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
     const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * 128;
-    uint32_t seen = 0, ended = 0;  // tiles and units of this stream
+    uint32_t turns = 0, ended = 0;  // tiles and units of this stream
     do {
       const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
       const int rows = min(tile_rows, live - g * tile_rows);  // of this stream
@@ -885,12 +927,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const int n = (u.r0 + min(row, live - 1)) / p.G;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; rows > 0 && i < n_tiles; ++i) {
-        if (!(ok = warp_wait(&ctl.s_full[g], seen++ & 1u, &ctl.dead))) break;
+        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+        uint4 seen = make_uint4(0, 0, 0, 0);
+        if (works) seen = seen_tile(p, u, n, at0);
+        if (!(ok = warp_wait(&ctl.s_full[g], turns++ & 1u, &ctl.dead))) break;
         if (works) {
-          const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
           const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.valid[(tiles + i) % kValidRing]);
-          softmax_tile<E, D>(p, u, n, mine, tile_masked(p, u, at0, valid), valid, at0, s_at, o_at,
-                             i == 0, m, l);
+          softmax_tile<E, D>(p.scale_log2, mine, tile_masked(p, u, at0, valid), both(seen, valid),
+                             s_at, o_at, i == 0, m, l);
         }
         tc_before();
         __syncwarp();

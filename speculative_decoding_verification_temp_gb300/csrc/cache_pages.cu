@@ -87,34 +87,48 @@ cudaError_t launch_kv_flags(const KvSeqs &S, const KvCache &C, bool new_only, ui
 // append: slot(ctx + n) of sequence b <- new row n
 // ---------------------------------------------------------------------------
 
-// A CTA takes `tokens` consecutive new tokens of the batch (blockIdx.x) of one
-// layer's keys or values (blockIdx.y); its threads are dealt over the 16-byte
-// pieces of the tokens' heads.
-__global__ void __launch_bounds__(kThreads)
-    append_kernel(KvSeqs S, KvCache C, NewRows R, int tokens) {
-  const int layer = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
+// A warp takes one new token: it finds the token's slot once and then copies the
+// token's keys and values in the layers blockIdx.y, blockIdx.y + gridDim.y, ...,
+// eight 16-byte pieces a lane in flight.
+__global__ void __launch_bounds__(kThreads) append_kernel(KvSeqs S, KvCache C, NewRows R) {
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= S.B * S.N) return;
+  const int b = t / S.N, n = t - b * S.N;
+  const int ctx = __ldg(S.ctx + b), m = seq_new(S, b);
+  if (n >= m || !seq_fits(S, C, ctx, m)) return;
+  const int at = ctx + n, index = at / C.page_size;
+  const int page = page_at(S, b, index);
+  if (!page_ok(C, page)) return;
+  const int in_page = at - index * C.page_size;
   const int per_row = C.row_bytes / 16, per_token = C.heads * per_row;
-  const int first = blockIdx.x * tokens;
-  const int count = min(tokens, S.B * S.N - first);
-  const char *src = is_v ? R.v + layer * R.v_layer : R.k + layer * R.k_layer;
-  char *dst = is_v ? C.v + layer * C.v_layer : C.k + layer * C.k_layer;
-  const long long s_seq = is_v ? R.v_seq : R.k_seq, s_tok = is_v ? R.v_token : R.k_token;
-  const long long s_head = is_v ? R.v_head : R.k_head;
-  const long long d_page = is_v ? C.v_page : C.k_page, d_tok = is_v ? C.v_token : C.k_token;
-  const long long d_head = is_v ? C.v_head : C.k_head;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < count * per_token; i += kThreads) {
-    const int t = i / per_token, r = i - t * per_token;
-    const int h = r / per_row, c = r - h * per_row;
-    const int b = (first + t) / S.N, n = first + t - b * S.N;
-    const int m = seq_new(S, b), ctx = __ldg(S.ctx + b);
-    if (n >= m || !seq_fits(S, C, ctx, m)) continue;
-    const int at = ctx + n, index = at / C.page_size;
-    const int page = page_at(S, b, index);
-    if (!page_ok(C, page)) continue;
-    const uint4 x = load16(src + b * s_seq + n * s_tok + h * s_head + c * 16);
-    store16(dst + page * d_page + (at - index * C.page_size) * d_tok + h * d_head + c * 16, x);
+  const char *k_src = R.k + b * R.k_seq + n * R.k_token, *v_src = R.v + b * R.v_seq + n * R.v_token;
+  char *k_dst = C.k + page * C.k_page + in_page * C.k_token;
+  char *v_dst = C.v + page * C.v_page + in_page * C.v_token;
+  for (int i0 = lane; i0 < per_token; i0 += 128) {
+    long long ks[4], vs[4], kd[4], vd[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * 32, h = i / per_row, c = (i - h * per_row) * 16;
+      ks[j] = h * R.k_head + c;
+      vs[j] = h * R.v_head + c;
+      kd[j] = h * C.k_head + c;
+      vd[j] = h * C.v_head + c;
+    }
+    for (long long layer = blockIdx.y; layer < C.layers; layer += gridDim.y) {
+      uint4 x[4], y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j * 32 < per_token) {
+          x[j] = load16(k_src + layer * R.k_layer + ks[j]);
+          y[j] = load16(v_src + layer * R.v_layer + vs[j]);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j * 32 < per_token) {
+          store16(k_dst + layer * C.k_layer + kd[j], x[j]);
+          store16(v_dst + layer * C.v_layer + vd[j], y[j]);
+        }
+    }
   }
 }
 
@@ -125,10 +139,10 @@ cudaError_t launch_append(const KvSeqs &S, const KvCache &C, const NewRows &R, u
     if (e != cudaSuccess) return e;
   }
   if (S.N == 0) return cudaSuccess;
-  const int per_token = C.heads * (C.row_bytes / 16);
-  const int tokens = max(1, 4 * kThreads / per_token);
-  const dim3 grid((S.B * S.N + tokens - 1) / tokens, 2 * C.layers);
-  append_kernel<<<grid, kThreads, 0, stream>>>(S, C, R, tokens);
+  // two layers a warp where there are enough tokens to fill the card
+  const int tokens = S.B * S.N;
+  const int split = tokens >= 1024 ? (C.layers + 1) / 2 : C.layers;
+  append_kernel<<<dim3((tokens + kWarps - 1) / kWarps, split), kThreads, 0, stream>>>(S, C, R);
   return cudaGetLastError();
 }
 

@@ -23,7 +23,7 @@ namespace {
 constexpr int kSms = 152;       // GB300
 constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = 4;
-constexpr int kJoinThreads = 128, kJoinRows = 4;
+constexpr int kJoinThreads = 128;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -607,8 +607,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_con
 // the join
 // ---------------------------------------------------------------------------
 
-// The rows of a cut unit, kJoinRows per CTA.  Units of few pieces: a warp per
-// row.  Units of many: the CTA's warps share the pieces of one row after the
+// The rows of a cut unit, dealt over gridDim.y CTAs.  Units of two pieces, the
+// most there are in a full batch: a warp takes four rows at once, since a row
+// alone is one round trip to L2 whatever its size.  Units of few pieces: a warp
+// per row.  Units of many: the CTA's warps share the pieces of one row after the
 // other, and their sums are added in order.  A warp has eight pieces in flight.
 template <class TE>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
@@ -619,10 +621,54 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinDesc d = p.join[blockIdx.x];
   if (d.pieces_end < 0) return;
-  const int rows = min(p.rows, seq_new(p.S, d.b) * p.G - d.r0);
+  const int rows = d.rows, Y = gridDim.y;
   const int first = static_cast<int>(blockIdx.x) - 1, count = d.pieces_end - first + 1;
   const size_t per_slot = slot_floats(p.rows, p.D);
   auto slot = [&](int i) { return p.part + (2 * (first + i) + (i == 0 ? 1 : 0)) * per_slot; };
+  if (count == 2 && p.D <= 128) {
+    const float *s[2] = {slot(0), slot(1)};
+    const int at = lane * 4;
+    for (int r = blockIdx.y * kWarps + warp; r < rows; r += 4 * Y * kWarps) {
+      float m[4][2], l[4][2];
+      float4 v[4][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = min(r + j * Y * kWarps, rows - 1);
+          m[j][x] = s[x][row];
+          l[j][x] = s[x][p.rows + row];
+          if (at < p.D)
+            v[j][x] = *reinterpret_cast<const float4 *>(s[x] + slot_stats(p.rows) +
+                                                        static_cast<size_t>(row) * p.D + at);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = r + j * Y * kWarps;
+        if (row >= rows) break;
+        const float M = fmaxf(m[j][0], m[j][1]);
+        float f[2], sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (m[j][x] == -INFINITY) continue;
+          f[x] = fast_exp2(m[j][x] - M);
+          sum += f[x] * l[j][x];
+          o.x += f[x] * v[j][x].x;
+          o.y += f[x] * v[j][x].y;
+          o.z += f[x] * v[j][x].z;
+          o.w += f[x] * v[j][x].w;
+        }
+        const long long to = out_row(p, d.b, d.h, d.r0 + row);
+        const float n = sum == 0.f ? 0.f : 1.f / sum;
+        if (at < p.D)
+          store4(static_cast<TE *>(p.out) + to * p.D + at,
+                 make_float4(o.x * n, o.y * n, o.z * n, o.w * n));
+        if (lane == 0 && p.lse) p.lse[to] = row_lse(M, sum);
+      }
+    }
+    return;
+  }
   // pieces from, from + step, ... of a row
   auto gather = [&](int row, int from, int step, float &M, float &l, float4 (&o)[2]) {
     M = -INFINITY;
@@ -683,17 +729,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
     if (lane == 0 && p.lse) p.lse[at] = row_lse(M, l);
   };
-  const int row0 = blockIdx.y * kJoinRows;
   float M, l;
   float4 o[2];
   if (count <= 16) {
-    for (int row = row0 + warp; row < min(row0 + kJoinRows, rows); row += kWarps) {
+    for (int row = blockIdx.y * kWarps + warp; row < rows; row += Y * kWarps) {
       gather(row, 0, 1, M, l, o);
       finish(row, M, l, o);
     }
     return;
   }
-  for (int row = row0; row < min(row0 + kJoinRows, rows); ++row) {
+  for (int row = blockIdx.y; row < rows; row += Y) {
     gather(row, warp, kWarps, M, l, o);
     if (lane == 0) {
       m_s[warp] = M;
@@ -816,8 +861,7 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
     e = dtype == SPEC_BF16 ? start16<Bf16>(p, stream) : start16<F16>(p, stream);
   }
   if (e != cudaSuccess) return e;
-  // no unit has more rows than a sequence
-  const dim3 grid(p.workers, (std::min(p.rows, p.S.N * p.G) + kJoinRows - 1) / kJoinRows);
+  const dim3 grid(p.workers, std::min(8, std::min(p.rows, p.S.N * p.G)));
   if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinThreads, 0, stream, p);
   if (dtype == SPEC_BF16)
     return launch_behind(join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, stream, p);

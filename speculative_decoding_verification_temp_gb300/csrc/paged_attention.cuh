@@ -50,7 +50,7 @@ struct AttnParams {
 // those of the worker before it .. pieces_end.  pieces_end -1: no unit's cuts
 // start here.
 struct JoinDesc {
-  int b, h, r0, pieces_end;
+  int b, h, r0, rows, pieces_end;
 };
 
 size_t attention_workspace_bytes(int N, int G, int D, int dtype);
@@ -76,6 +76,7 @@ struct KeyRange {
   int ctx, n_new;   // n_new: new tokens, 0 where the sequence does not fit
   int end;          // keys at or behind it are seen by no row
   int all;          // keys before it are seen by every row, but for the window
+  int first;        // keys before it are seen by no row, but for the sinks
   int sink_tiles, lo, count;
 };
 
@@ -85,16 +86,15 @@ __device__ __forceinline__ KeyRange key_range(const AttnParams &p, int ctx, int 
   KeyRange k;
   k.ctx = ctx;
   k.n_new = n_new;
-  k.end = k.all = 0;
-  int first = 0;
+  k.end = k.all = k.first = 0;
   if (fits) {
     const int n_lo = r0 == 0 ? 0 : r0 / p.G;
     const int n_hi = r0 + p.rows >= n_new * p.G ? n_new - 1 : (r0 + p.rows - 1) / p.G;
     k.end = p.mask ? ctx + n_new : ctx + n_hi + 1;
     k.all = p.mask ? ctx : ctx + n_lo + 1;
-    if (p.window) first = max(0, (p.mask || p.position ? ctx : ctx + n_lo) - p.window + 1);
+    if (p.window) k.first = max(0, (p.mask || p.position ? ctx : ctx + n_lo) - p.window + 1);
   }
-  k.lo = first >> p.tile_log2;
+  k.lo = k.first >> p.tile_log2;
   k.sink_tiles = p.window ? min((min(p.sinks, k.end) + round) >> p.tile_log2, k.lo) : 0;
   k.count = max(1, k.sink_tiles + ((k.end + round) >> p.tile_log2) - k.lo);
   return k;
@@ -281,11 +281,12 @@ __host__ __device__ __forceinline__ size_t slot_floats(int R, int D) {
 // worker before it cuts that unit.  u: its first unit, or NULL.
 __device__ __forceinline__ void write_join(const AttnParams &p, const Line &L, const UnitWalk *u) {
   if (L.worker >= p.workers) return;
-  JoinDesc d = {0, 0, 0, -1};
+  JoinDesc d = {0, 0, 0, 0, -1};
   if (u && u->i0 > 0 && L.start_of(L.worker - 1ll) <= u->a) {
     d.b = u->b;
     d.h = u->h;
     d.r0 = u->r0;
+    d.rows = u->live_rows(p);
     d.pieces_end = static_cast<int>(L.worker_of(u->a + u->k.count - 1));
   }
   p.join[L.worker] = d;

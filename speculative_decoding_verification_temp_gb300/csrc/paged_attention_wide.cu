@@ -537,6 +537,8 @@ struct BoxLoader {
   __device__ __forceinline__ int page(const AttnParams &p, const UnitWalk &u, int i, int lane) const {
     const int at = key_tile(u.k, u.i0 + i) * kTileKeys + lane * box;
     if (lane >= boxes || i >= u.i1 - u.i0 || at >= u.k.end) return -1;
+    // between the sinks and the window
+    if (at >= p.sinks && at + box <= u.k.first) return -1;
     return page_at(p.S, u.b, p.C.page_size <= kTileKeys ? at >> shift : at / p.C.page_size);
   }
   // Which of the 32 tokens from 32 * j of the tile at at0 on are copied.
@@ -632,8 +634,10 @@ __device__ __forceinline__ void flag_run(const AttnParams &p, const Line &line) 
 // two streams with units of their own
 // ---------------------------------------------------------------------------
 
-// QR: rows of queries that are copied, 32 or 128.  The products read 128: what
-// lies behind is another buffer, whose rows make results that nobody reads.
+// QR: rows of queries that are copied, 32 or 128.  The products read 128: with
+// 32, those are rows 0..31 of the first stream's and 32..63 of the second's, and
+// what lies before and behind them is other buffers, whose rows make results that
+// nobody reads.
 template <int D, int QR>
 struct SoloCtl {
   static constexpr int kRing = D == 128 ? (QR == 32 ? 3 : 2) : 6;  // entries of a stream
@@ -718,14 +722,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
     more_regs<kSoftRegs>();
-    const int part = warp & 3, row = tid & 127;
+    const int part = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
+    // a stream's only warp of rows is on a quarter of the SM of its own
+    const int row = (tid & 127) - (QR == 32 ? g * 32 : 0);
     uint32_t tiles = 0, units = 0;
     if (busy) do {
         const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
-        const bool mine = row < live, works = part * 32 < live;
-        const int n = (u.r0 + min(row, live - 1)) / p.G;
-        const int idle = 4 - min((live + 31) / 32, 4);  // warps without rows
+        const bool mine = row >= 0 && row < live, works = row >= 0 && (row & ~31) < live;
+        const int n = (u.r0 + min(max(row, 0), live - 1)) / p.G;
+        // warps without rows, and this warp's place among them
+        const int idle = 4 - min((live + 31) / 32, 4);
+        const int helper = QR == 32 ? (part > g ? part - 1 : part) : part - (4 - idle);
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < n_tiles; ++i, ++tiles) {
           const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
@@ -742,8 +750,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
             clean_values<E, D>(ring + e % kRing * W::kBytes, valid,
                                clean_from(p, u.k, at0, valid),
-                               idle == 0 ? row : row - (4 - idle) * 32, idle == 0 ? 128 : idle * 32,
-                               &ctl.bad);
+                               idle == 0 ? tid & 127 : helper * 32 + lane,
+                               idle == 0 ? 128 : idle * 32, &ctl.bad);
           }
           tc_before();
           __syncwarp();
@@ -808,7 +816,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           uint32_t e = 2 * tiles;
           if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
           if (i == 0 && !(ok = warp_wait(&st.q_full, units++ & 1u, &ctl.dead))) break;
-          issue_scores<E, D>(s_at, q_at, Shape::kQPanel, ring_at + e % kRing * W::kBytes);
+          issue_scores<E, D>(s_at, q_at - (QR == 32 ? g * 32 * W::kRow : 0), Shape::kQPanel,
+                             ring_at + e % kRing * W::kBytes);
           issue_commit(&st.s_full);
           issue_commit(&st.empty[e % kRing]);
           if (i + 1 == n_tiles) issue_commit(&st.q_empty);

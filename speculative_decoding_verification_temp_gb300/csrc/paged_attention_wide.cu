@@ -9,7 +9,10 @@
 // streams share a CTA, so that the products of one run while the other is in its
 // softmax:
 //   solo_kernel  units of one row tile; each stream has units, keys and values
-//                of its own
+//                of its own.  Up to 32 rows are given to each of the four
+//                quarters of the lanes, and each quarter weighs a quarter of a
+//                tile's keys: a row's softmax is four threads' work, and the
+//                quarters' results are added at the unit's end.
 //   pair_kernel  units of two row tiles, one per stream, that share the keys and
 //                values
 //
@@ -435,6 +438,65 @@ __device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, ui
   tm_wait_st();
 }
 
+// The same for a quarter of the tile's keys, those of the warp's part: weights of
+// zero for the other quarters' keys.  seen: of the 32 keys.
+template <class E, int D>
+__device__ __forceinline__ void softmax_part(float c, bool mine, bool masked, uint32_t seen,
+                                             int part, uint32_t s_at, uint32_t o_at, bool first,
+                                             float &m, float &l) {
+  tc_after();
+  uint32_t s[32];
+  tm_load32(s, s_at + part * 32);
+  tm_wait_ld();
+  if (masked) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!(seen & (1u << e))) s[e] = __float_as_uint(-INFINITY);
+  }
+  float x[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 32; e += 2)
+    x[(e >> 1) & 1] = max3(x[(e >> 1) & 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+  const float top = fmaxf(x[0], x[1]) * c;
+  const bool raise = mine && top > m + kSlack;
+  if (__any_sync(0xFFFFFFFFu, raise)) {
+    const float to = raise ? top : m;
+    const float f = m == -INFINITY ? 0.f : fast_exp2(m - to);
+    l *= f;
+    m = to;
+    if (!first) {
+#pragma unroll 1
+      for (int d = 0; d < D; d += 16) {
+        uint32_t o[16];
+        tm_load16(o, o_at + d);
+        tm_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tm_store16(o_at + d, o);
+      }
+    }
+  }
+  const float sub = m == -INFINITY ? 0.f : -m;
+  const float2 c2 = make_float2(c, c), sub2 = make_float2(sub, sub);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t packed[16], none[16];
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, sub2);
+    y.x = fast_exp2(y.x);
+    y.y = fast_exp2(y.y);
+    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
+    packed[e / 2] = E::pack(y.x, y.y);
+    none[e / 2] = 0u;
+  }
+#pragma unroll
+  for (int j = 1; j < 4; ++j) tm_store16(s_at + ((part + j) & 3) * 16, none);
+  tm_store16(s_at + part * 16, packed);
+  sum[0] = add2(sum[0], sum[1]);
+  l += sum[0].x + sum[0].y;
+  tm_wait_st();
+}
+
 // 32 bytes of a row at once: a whole sector.
 __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
@@ -516,6 +578,105 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
   }
   __syncwarp();
   tc_before();
+}
+
+// Where the quarters of a split unit's rows meet.
+struct Quarters {
+  static constexpr int kFloats = 1024;  // of a warp: 8 rows of 128, 16 of 64
+  float o[4][kFloats];
+  float ml[4][2][32];
+};
+
+// The end of a unit whose rows are spread over four quarters; by the stream's
+// four warps.  False: a wait gave up.
+template <class E, int D>
+__device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk &u, int worker,
+                                            int part, int lane, uint32_t o_at, float m, float l,
+                                            Quarters &x, const void *meet, uint32_t &met, int *dead,
+                                            const int *bad) {
+  using TE = typename E::T;
+  constexpr int kRows = Quarters::kFloats / D, kPieces = D / 8;
+  const bool whole = u.whole();
+  const int live = u.live_rows(p), t = part * 32 + lane;
+  float *slot = p.part + piece_slot(u, worker) * slot_floats(p.rows, D);
+  x.ml[part][0][lane] = m;
+  x.ml[part][1][lane] = l;
+  tc_after();
+  for (int r0 = 0; r0 < live; r0 += kRows) {
+#pragma unroll 1
+    for (int d = 0; d < D; d += 32) {
+      __syncwarp();
+      uint32_t o[32];
+      tm_load32(o, o_at + d);
+      tm_wait_ld();
+      if (lane >= r0 && lane < r0 + kRows) {
+        float *to = x.o[part] + (lane - r0) * D + d;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<uint4 *>(to + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) bar_arrive(meet);
+    if (!warp_wait(meet, met++ & 1u, dead)) return false;
+    const int row = r0 + t / kPieces, d = t % kPieces * 8;
+    if (row < live) {
+      float M = -INFINITY, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, x.ml[w][0][row]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float mw = x.ml[w][0][row];
+        if (mw == -INFINITY) continue;
+        const float f = fast_exp2(mw - M);
+        sum += f * x.ml[w][1][row];
+        const float *from = x.o[w] + (row - r0) * D + d;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const float4 y = *reinterpret_cast<const float4 *>(from + e);
+          v[e] += f * y.x;
+          v[e + 1] += f * y.y;
+          v[e + 2] += f * y.z;
+          v[e + 3] += f * y.w;
+        }
+      }
+      if (*reinterpret_cast<const volatile int *>(bad)) {
+#pragma unroll 1
+        for (int e = 0; e < 8; e += 4) {
+          const float4 y = nonfinite_values<TE, kTileKeys>(p, u, (u.r0 + row) / p.G, d + e,
+                                                           make_float4(0.f, 0.f, 0.f, 0.f));
+          if (e == 0) {
+            v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
+          } else {
+            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+          }
+        }
+      }
+      if (whole) {
+        const long long at = out_row(p, u.b, u.h, u.r0 + row);
+        const float n = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = sum == 0.f ? 0.f : v[e] * n;
+        *reinterpret_cast<uint4 *>(static_cast<TE *>(p.out) + at * D + d) = make_uint4(
+            E::pack(v[0], v[1]), E::pack(v[2], v[3]), E::pack(v[4], v[5]), E::pack(v[6], v[7]));
+        if (d == 0 && p.lse) p.lse[at] = row_lse(M, sum);
+      } else {
+        float *to = slot + slot_stats(p.rows) + static_cast<size_t>(row) * D + d;
+        store4(to, make_float4(v[0], v[1], v[2], v[3]));
+        store4(to + 4, make_float4(v[4], v[5], v[6], v[7]));
+        if (d == 0) {
+          slot[row] = M;
+          slot[p.rows + row] = sum;
+        }
+      }
+    }
+    // the quarters are read before they are written again
+    __syncwarp();
+    if (lane == 0) bar_arrive(meet);
+    if (!warp_wait(meet, met++ & 1u, dead)) return false;
+  }
+  tc_before();
+  return true;
 }
 
 // The boxes of a tile of keys or values, one per page and lane.
@@ -634,39 +795,39 @@ __device__ __forceinline__ void flag_run(const AttnParams &p, const Line &line) 
 // two streams with units of their own
 // ---------------------------------------------------------------------------
 
-// QR: rows of queries that are copied, 32 or 128.  The products read 128: with
-// 32, those are rows 0..31 of the first stream's and 32..63 of the second's, and
-// what lies before and behind them is other buffers, whose rows make results that
-// nobody reads.
-template <int D, int QR>
+// kSplit: at most 32 rows, spread over the four quarters.
+template <int D, bool kSplit>
 struct SoloCtl {
-  static constexpr int kRing = D == 128 ? (QR == 32 ? 3 : 2) : 6;  // entries of a stream
+  // entries of a stream: what 227 KB hold beside the queries and the quarters
+  static constexpr int kRing = D == 128 ? 2 : (kSplit ? 5 : 6);
   struct Stream {
-    unsigned long long full[kRing], empty[kRing], s_full, p_full, o_done, q_full, q_empty, drain;
+    unsigned long long full[kRing], empty[kRing], s_full, p_full, o_done, q_full, q_empty, meet,
+        drain;
     alignas(16) uint32_t valid[kValidRing][4];
   } stream[2];
   RunScratch<kWideThreads, 2> runs;
   uint32_t tmem;
   int dead, bad;
 };
-template <int D, int QR>
+template <int D, bool kSplit>
 struct SoloShape {
-  static constexpr int kQPanel = QR * 128, kQ = Entry<D>::kPanels * kQPanel;  // of a stream
-  static constexpr int kRing = SoloCtl<D, QR>::kRing;
+  static constexpr int kQPanel = 128 * 128, kQ = Entry<D>::kPanels * kQPanel;  // of a stream
+  static constexpr int kRing = SoloCtl<D, kSplit>::kRing;
   static constexpr int kEntries = 2 * kQ;  // where the rings begin
-  static constexpr int kCtl = kEntries + 2 * kRing * Entry<D>::kBytes;
-  static constexpr int kSmem = kCtl + static_cast<int>(sizeof(SoloCtl<D, QR>));
+  static constexpr int kMeet = kEntries + 2 * kRing * Entry<D>::kBytes;
+  static constexpr int kCtl = kMeet + (kSplit ? 2 * static_cast<int>(sizeof(Quarters)) : 0);
+  static constexpr int kSmem = kCtl + static_cast<int>(sizeof(SoloCtl<D, kSplit>));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
 }  // namespace
 
-template <class E, int D, int QR>
+template <class E, int D, bool kSplit>
 __global__ void __launch_bounds__(kWideThreads, 1)
     solo_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ WideMaps maps) {
   using W = Entry<D>;
-  using Shape = SoloShape<D, QR>;
-  using Ctl = SoloCtl<D, QR>;
+  using Shape = SoloShape<D, kSplit>;
+  using Ctl = SoloCtl<D, kSplit>;
   constexpr int kRing = Shape::kRing;
   // all shared memory is this array, so its alignment is the swizzle's
   extern __shared__ __align__(1024) char wide_s[];
@@ -684,6 +845,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     bar_init(&st.o_done, 1);
     bar_init(&st.q_full, 1);
     bar_init(&st.q_empty, 1);
+    bar_init(&st.meet, 4);
     bar_init(&st.drain, 1);
     ctl.dead = 0;
     ctl.bad = 0;
@@ -724,33 +886,43 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     more_regs<kSoftRegs>();
     const int part = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
-    // a stream's only warp of rows is on a quarter of the SM of its own
-    const int row = (tid & 127) - (QR == 32 ? g * 32 : 0);
-    uint32_t tiles = 0, units = 0;
+    // a split stream's lane holds the same row in every warp
+    const int row = kSplit ? lane : tid & 127;
+    Quarters &quarters = reinterpret_cast<Quarters *>(wide_s + Shape::kMeet)[kSplit ? g : 0];
+    uint32_t tiles = 0, units = 0, met = 0;
     if (busy) do {
         const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
-        const bool mine = row >= 0 && row < live, works = row >= 0 && (row & ~31) < live;
-        const int n = (u.r0 + min(max(row, 0), live - 1)) / p.G;
-        // warps without rows, and this warp's place among them
-        const int idle = 4 - min((live + 31) / 32, 4);
-        const int helper = QR == 32 ? (part > g ? part - 1 : part) : part - (4 - idle);
+        const bool mine = row < live, works = kSplit || part * 32 < live;
+        const int n = (u.r0 + min(row, live - 1)) / p.G;
+        const int idle = kSplit ? 0 : 4 - min((live + 31) / 32, 4);  // warps without rows
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < n_tiles; ++i, ++tiles) {
           const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
           uint4 seen = make_uint4(0, 0, 0, 0);
-          if (works) seen = seen_tile(p, u, n, at0);
+          if (kSplit) {
+            seen.x = all_seen(p, u.k, at0, kTileKeys)
+                         ? 0xFFFFFFFFu
+                         : seen_word(p, u.k, u.b, n, at0 + part * 32);
+          } else if (works) {
+            seen = seen_tile(p, u, n, at0);
+          }
           if (!(ok = warp_wait(&st.s_full, tiles & 1u, &ctl.dead))) break;
           const uint4 valid = *reinterpret_cast<const uint4 *>(st.valid[tiles % kValidRing]);
           const bool masked = tile_masked(p, u, at0, valid);
-          if (works)
+          if (kSplit) {
+            const uint32_t word = part < 2 ? (part == 0 ? valid.x : valid.y)
+                                           : (part == 2 ? valid.z : valid.w);
+            softmax_part<E, D>(p.scale_log2, mine, masked, seen.x & word, part, s_at + lanes,
+                               o_at + lanes, i == 0, m, l);
+          } else if (works) {
             softmax_tile<E, D>(p.scale_log2, mine, masked, both(seen, valid), s_at + lanes,
                                o_at + lanes, i == 0, m, l);
+          }
           if (masked && (idle == 0 || !works)) {
             const uint32_t e = 2 * tiles + 1;
             if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
-            clean_values<E, D>(ring + e % kRing * W::kBytes, valid,
-                               clean_from(p, u.k, at0, valid),
-                               idle == 0 ? tid & 127 : helper * 32 + lane,
+            clean_values<E, D>(ring + e % kRing * W::kBytes, valid, clean_from(p, u.k, at0, valid),
+                               idle == 0 ? tid & 127 : (part - (4 - idle)) * 32 + lane,
                                idle == 0 ? 128 : idle * 32, &ctl.bad);
           }
           tc_before();
@@ -758,9 +930,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (lane == 0) bar_arrive(&st.p_full);
         }
         if (!ok || !(ok = warp_wait(&st.o_done, units++ & 1u, &ctl.dead))) break;
-        if (works)
+        if constexpr (kSplit) {
+          if (!(ok = write_split<E, D>(p, u, line.worker, part, lane, o_at + lanes, m, l, quarters,
+                                       &st.meet, met, &ctl.dead, &ctl.bad)))
+            break;
+        } else if (works) {
           write_row<E, D>(p, u, line.worker, row, n, mine, o_at + lanes, m, l,
                           *reinterpret_cast<volatile int *>(&ctl.bad) != 0);
+        }
       } while (u.next(p, line));
   } else {
     fewer_regs<kRestRegs>();
@@ -786,9 +963,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (!(ok = warp_wait(&st.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
             ++units;
             if (lane == 0) {
-              bar_expect(&st.q_full, min(p.rows, QR) / p.G * p.G * W::kRow * W::kPanels);
-              for (int x = 0; x < W::kPanels; ++x)
-                box_load(q_at + x * Shape::kQPanel, &maps.q, &st.q_full, 0, 0, u.r0 / p.G, x,
+              constexpr int kRows = kSplit ? 32 : 128, kCopies = 128 / kRows;
+              bar_expect(&st.q_full, kCopies * (kRows / p.G * p.G) * W::kRow * W::kPanels);
+              for (int x = 0; x < W::kPanels * kCopies; ++x)
+                box_load(q_at + x / kCopies * Shape::kQPanel + x % kCopies * kRows * W::kRow, &maps.q,
+                         &st.q_full, 0, 0, u.r0 / p.G, x / kCopies,
                          u.b * maps.q_seq + u.h * maps.q_head);
             }
           }
@@ -816,8 +995,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           uint32_t e = 2 * tiles;
           if (!(ok = warp_wait(&st.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
           if (i == 0 && !(ok = warp_wait(&st.q_full, units++ & 1u, &ctl.dead))) break;
-          issue_scores<E, D>(s_at, q_at - (QR == 32 ? g * 32 * W::kRow : 0), Shape::kQPanel,
-                             ring_at + e % kRing * W::kBytes);
+          issue_scores<E, D>(s_at, q_at, Shape::kQPanel, ring_at + e % kRing * W::kBytes);
           issue_commit(&st.s_full);
           issue_commit(&st.empty[e % kRing]);
           if (i + 1 == n_tiles) issue_commit(&st.q_empty);
@@ -1082,8 +1260,7 @@ namespace {
 
 bool wide_pairs(const AttnParams &p) { return p.rows > wide_tile_rows(p.G); }
 int wide_ctas(const AttnParams &p) { return wide_pairs(p) ? p.workers : p.workers / 2; }
-// Few rows leave room for an entry more in each ring.
-int solo_query_rows(const AttnParams &p) { return p.S.N * p.G <= 32 ? 32 : 128; }
+bool solo_splits(const AttnParams &p) { return p.S.N * p.G <= 32; }
 
 // cuTensorMapEncodeTiled of the installed driver; the library does not link to it.
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -1166,9 +1343,9 @@ cudaError_t start_wide(int smem, const AttnParams &p, const WideMaps &maps, cuda
 template <class E, int D>
 cudaError_t start_wide(const AttnParams &p, const WideMaps &maps, cudaStream_t stream) {
   if (wide_pairs(p)) return start_wide<pair_kernel<E, D>>(PairShape<D>::kSmem, p, maps, stream);
-  if (solo_query_rows(p) == 32)
-    return start_wide<solo_kernel<E, D, 32>>(SoloShape<D, 32>::kSmem, p, maps, stream);
-  return start_wide<solo_kernel<E, D, 128>>(SoloShape<D, 128>::kSmem, p, maps, stream);
+  if (solo_splits(p))
+    return start_wide<solo_kernel<E, D, true>>(SoloShape<D, true>::kSmem, p, maps, stream);
+  return start_wide<solo_kernel<E, D, false>>(SoloShape<D, false>::kSmem, p, maps, stream);
 }
 
 }  // namespace
@@ -1194,7 +1371,7 @@ bool wide_maps(const AttnParams &p, int dtype, WideMaps *maps) {
   const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(p.G), static_cast<cuuint64_t>(p.S.N),
                               static_cast<cuuint64_t>(p.D / 64), static_cast<cuuint64_t>(q.count)};
   const long long steps[4] = {p.G > 1 ? p.q_head : row, p.S.N > 1 ? p.q_token : row, 128, q.step};
-  const int rows = wide_pairs(p) ? 128 : solo_query_rows(p);
+  const int rows = !wide_pairs(p) && solo_splits(p) ? 32 : 128;
   const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(rows / p.G),
                              1, 1};
   return encode_map(&maps->q, dtype, p.q, dims, steps, box);

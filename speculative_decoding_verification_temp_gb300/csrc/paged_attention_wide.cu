@@ -582,64 +582,78 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
 
 // Where the quarters of a split unit's rows meet.
 struct Quarters {
-  static constexpr int kFloats = 1024;  // of a warp: 8 rows of 128, 16 of 64
+  static constexpr int kFloats = 1024;  // of a warp
   float o[4][kFloats];
   float ml[4][2][32];
 };
 
 // The end of a unit whose rows are spread over four quarters; by the stream's
-// four warps.  False: a wait gave up.
+// four warps.  Few rows meet at once (8 of 128 outputs, 16 of 64), more rows 32
+// outputs at a time, a row's 16-byte pieces permuted so that eight rows meet
+// eight banks.  False: a wait gave up.
 template <class E, int D>
 __device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk &u, int worker,
                                             int part, int lane, uint32_t o_at, float m, float l,
                                             Quarters &x, const void *meet, uint32_t &met, int *dead,
                                             const int *bad) {
   using TE = typename E::T;
-  constexpr int kRows = Quarters::kFloats / D, kPieces = D / 8;
+  constexpr int kFew = Quarters::kFloats / D;
   const bool whole = u.whole();
   const int live = u.live_rows(p), t = part * 32 + lane;
+  const bool few = live <= kFew;
+  // this thread's eight outputs of a pass
+  const int row = few ? t / (D / 8) : t / 4, d0 = few ? t % (D / 8) * 8 : t % 4 * 8;
+  const int pitch = few ? D : 32, mask = few ? 0 : row & 7;
   float *slot = p.part + piece_slot(u, worker) * slot_floats(p.rows, D);
   x.ml[part][0][lane] = m;
   x.ml[part][1][lane] = l;
   tc_after();
-  for (int r0 = 0; r0 < live; r0 += kRows) {
+  float M = -INFINITY, sum = 0.f, f[4];
+  for (int pass = 0; pass < (few ? 1 : D / 32); ++pass) {
 #pragma unroll 1
-    for (int d = 0; d < D; d += 32) {
+    for (int d = few ? 0 : pass * 32; d < (few ? D : pass * 32 + 32); d += 32) {
       __syncwarp();
       uint32_t o[32];
       tm_load32(o, o_at + d);
       tm_wait_ld();
-      if (lane >= r0 && lane < r0 + kRows) {
-        float *to = x.o[part] + (lane - r0) * D + d;
+      if (lane < live) {
+        float *to = x.o[part] + lane * pitch + (few ? d : 0);
+        const int swap = few ? 0 : lane & 7;
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<uint4 *>(to + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4 *>(to + (e ^ swap) * 4) =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
     }
     __syncwarp();
     if (lane == 0) bar_arrive(meet);
     if (!warp_wait(meet, met++ & 1u, dead)) return false;
-    const int row = r0 + t / kPieces, d = t % kPieces * 8;
     if (row < live) {
-      float M = -INFINITY, sum = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (pass == 0) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, x.ml[w][0][row]);
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, x.ml[w][0][row]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float mw = x.ml[w][0][row];
-        if (mw == -INFINITY) continue;
-        const float f = fast_exp2(mw - M);
-        sum += f * x.ml[w][1][row];
-        const float *from = x.o[w] + (row - r0) * D + d;
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 y = *reinterpret_cast<const float4 *>(from + e);
-          v[e] += f * y.x;
-          v[e + 1] += f * y.y;
-          v[e + 2] += f * y.z;
-          v[e + 3] += f * y.w;
+        for (int w = 0; w < 4; ++w) {
+          const float mw = x.ml[w][0][row];
+          f[w] = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+          if (mw != -INFINITY) sum += f[w] * x.ml[w][1][row];
         }
       }
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (f[w] == 0.f) continue;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 y = *reinterpret_cast<const float4 *>(x.o[w] + row * pitch +
+                                                             (((d0 >> 2) + e) ^ mask) * 4);
+          v[4 * e] += f[w] * y.x;
+          v[4 * e + 1] += f[w] * y.y;
+          v[4 * e + 2] += f[w] * y.z;
+          v[4 * e + 3] += f[w] * y.w;
+        }
+      }
+      const int d = pass * 32 + d0;
       if (*reinterpret_cast<const volatile int *>(bad)) {
 #pragma unroll 1
         for (int e = 0; e < 8; e += 4) {

@@ -9,6 +9,7 @@ cache's device.  They are forward operators: tensors that require gradients are
 refused while autograd records.
 """
 
+import functools
 from collections import namedtuple
 
 import torch
@@ -113,6 +114,11 @@ def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(*sizes):
+    return max(_abi.load().spec_paged_attention_workspace_size(*sizes), 32)
+
+
 def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, num_new=None,
                     tree_mask=None, position=None, window=0, sinks=0, return_lse=False,
                     return_flags=False, out=None):
@@ -166,15 +172,14 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
             raise ValueError("out must be a contiguous tensor like q")
     lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev) if return_lse else None
     flags = torch.empty(B, dtype=torch.int32, device=dev) if return_flags else None
-    lib = _abi.load()
-    nbytes = lib.spec_paged_attention_workspace_size(B, N, Hq, cache.num_heads, D, cache.dtype)
+    nbytes = _attention_bytes(B, N, Hq, cache.num_heads, D, cache.dtype)
     # of the caching allocator, ordered on this stream and kept by a graph that
     # captures the call: never shared with calls on other streams
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    _run(dev, lib.spec_paged_attention, q.data_ptr(), strides[0], strides[1], strides[2], Hq, cache,
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _run(dev, _abi.load().spec_paged_attention, q.data_ptr(), strides[0], strides[1], strides[2], Hq, cache,
          table, context_len.data_ptr(), _ptr(num_new), B, N, _ptr(tree_mask), mask_stride,
          _ptr(position), pos_stride, D ** -0.5 if scale is None else float(scale), int(window),
-         int(sinks), out.data_ptr(), _ptr(lse), _ptr(flags), ws.data_ptr(), max(nbytes, 16))
+         int(sinks), out.data_ptr(), _ptr(lse), _ptr(flags), ws.data_ptr(), nbytes)
     return AttentionResult(out, lse, flags)
 
 
@@ -233,7 +238,8 @@ def cache_compact(k_cache, v_cache, page_table, context_len, path, num_accepted)
     num_accepted = _ints(num_accepted, (B,), dev, "num_accepted")
     page_table, table = _table(page_table, B, dev)
     context_len = _ints(context_len, (B,), dev, "context_len")
-    length, flags = torch.empty((2, B), dtype=torch.int32, device=dev)
+    length = torch.empty(B, dtype=torch.int32, device=dev)
+    flags = torch.empty(B, dtype=torch.int32, device=dev)
     _run(dev, _abi.load().spec_cache_compact, cache, table, context_len.data_ptr(),
          path.data_ptr(), width, num_accepted.data_ptr(), B, length.data_ptr(), flags.data_ptr())
     return CompactResult(length, flags)

@@ -152,88 +152,102 @@ cudaError_t launch_append(const KvSeqs &S, const KvCache &C, const NewRows &R, u
 
 // A path ascends, so path[i] >= i, and a thread that moves the rows of one
 // 16-byte column in ascending order never reads a slot that it has written:
-// step i writes slot i, every later source is above it.  Four sources are
-// loaded before their four targets are stored, for the same reason.  One CTA
-// per sequence and layer's keys or values; the path is checked and staged by
-// each CTA.
+// step i writes slot i, every later source is above it.  Eight sources are
+// loaded before their eight targets are stored, for the same reason.  One CTA
+// per sequence and layer's keys or values.  Each CTA checks the path and finds
+// the byte offsets of the moves' slots, a thread each, into shared memory.
+struct Move {
+  long long from, to;  // from -1: no move
+};
+
 __global__ void __launch_bounds__(kThreads)
     compact_kernel(KvSeqs S, KvCache C, const int32_t *path, int width, const int32_t *accepted,
                    int32_t *out_len, uint32_t *flags) {
-  extern __shared__ int path_s[];
+  extern __shared__ Move move_s[];
   const int b = blockIdx.x, layer = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
   const int ctx = __ldg(S.ctx + b), na = __ldg(accepted + b);
+  const int32_t *nodes = path + static_cast<long long>(b) * width;
+  const long long s_page = is_v ? C.v_page : C.k_page, s_tok = is_v ? C.v_token : C.k_token;
+  const long long s_head = is_v ? C.v_head : C.k_head;
+  const int room = S.max_pages * C.page_size;
   uint32_t f = 0u;
   if (na < -1 || na >= width) f |= SPEC_FLAG_BAD_TREE;
-  int ok = na >= 0 && na < width;
+  bool ok = na >= 0 && na < width;
   if (ok) {
-    for (int i = threadIdx.x; i <= na; i += kThreads)
-      path_s[i] = __ldg(path + static_cast<long long>(b) * width + i);
-  }
-  __syncthreads();
-  if (ok) {
-    int bad = 0, far = 0;
-    for (int i = threadIdx.x; i <= na; i += kThreads) {
-      if (i == 0 ? path_s[0] != 0 : path_s[i] <= path_s[i - 1]) bad = 1;
-      if (ctx < 0 || path_s[i] < 0 || path_s[i] >= S.max_pages * C.page_size - ctx) far = 1;
-    }
-    if (__syncthreads_or(bad)) {
-      f |= SPEC_FLAG_BAD_TREE;
-      ok = 0;
-    } else if (__syncthreads_or(far)) {
-      f |= SPEC_FLAG_BAD_LENGTH;
-      ok = 0;
-    }
-  }
-  if (ok) {
-    char *base = is_v ? C.v + layer * C.v_layer : C.k + layer * C.k_layer;
-    const long long s_page = is_v ? C.v_page : C.k_page, s_tok = is_v ? C.v_token : C.k_token;
-    const long long s_head = is_v ? C.v_head : C.k_head;
-    const int per_row = C.row_bytes / 16, per_token = C.heads * per_row;
-    auto slot = [&](int at, bool &good) {
-      const int index = at / C.page_size;
-      const int page = page_at(S, b, index);
-      good = page_ok(C, page);
-      return good ? page * s_page + (at - index * C.page_size) * s_tok : 0ll;
+    auto slot = [&](int at) {
+      const int index = at / C.page_size, page = page_at(S, b, index);
+      return page_ok(C, page) ? page * s_page + (at - index * C.page_size) * s_tok : -1ll;
     };
-    for (int r = threadIdx.x; r < per_token; r += kThreads) {
-      char *col = base + (r / per_row) * s_head + (r % per_row) * 16;
-      for (int i = 1; i <= na; i += 4) {
-        uint4 x[4];
-        char *to[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          to[j] = nullptr;
-          if (i + j <= na) {
-            const int from = path_s[i + j];
-            bool gs, gd;
-            const long long so = slot(ctx + from, gs), d = slot(ctx + i + j, gd);
-            if (!gs || !gd) f |= SPEC_FLAG_BAD_PAGE;
-            if (gs && gd && from != i + j) {
-              x[j] = load16(col + so);
-              to[j] = col + d;
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (to[j]) store16(to[j], x[j]);
+    int bad = 0, far = 0, lost = 0;
+    for (int i = threadIdx.x; i <= na; i += blockDim.x) {
+      const int node = __ldg(nodes + i);
+      if (i == 0 ? node != 0 : node <= __ldg(nodes + i - 1)) bad = 1;
+      if (ctx < 0 || node < 0 || node >= room - ctx || i >= room - ctx) {
+        far = 1;
+        continue;
       }
+      Move m = {-1, -1};
+      if (node != i && i > 0) {
+        const long long from = slot(ctx + node), to = slot(ctx + i);
+        if (from >= 0 && to >= 0) {
+          m = {from, to};
+        } else {
+          lost = 1;
+        }
+      } else if (i > 0 && slot(ctx + i) < 0) {
+        lost = 1;
+      }
+      move_s[i] = m;
     }
+    bad = __syncthreads_or(bad);
+    far = __syncthreads_or(far);
+    lost = __syncthreads_or(lost);
+    if (bad) {
+      f |= SPEC_FLAG_BAD_TREE;
+    } else if (far) {
+      f |= SPEC_FLAG_BAD_LENGTH;
+    } else if (lost) {
+      f |= SPEC_FLAG_BAD_PAGE;
+    }
+    ok = !bad && !far;
   }
   if (blockIdx.y == 0 && threadIdx.x == 0) {
-    // the first thread walks the whole path (every CTA has a column for it),
-    // so its flags are the sequence's
     out_len[b] = ok ? ctx + na + 1 : ctx;
     if (flags) flags[b] = f;
+  }
+  if (!ok) return;
+  char *base = is_v ? C.v + layer * C.v_layer : C.k + layer * C.k_layer;
+  const int per_row = C.row_bytes / 16, per_token = C.heads * per_row;
+  for (int r = threadIdx.x; r < per_token; r += blockDim.x) {
+    const int h = r / per_row;
+    char *col = base + h * s_head + (r - h * per_row) * 16;
+    for (int i = 1; i <= na; i += 8) {
+      uint4 x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j <= na && move_s[i + j].from >= 0) x[j] = load16(col + move_s[i + j].from);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j <= na && move_s[i + j].from >= 0) store16(col + move_s[i + j].to, x[j]);
+    }
   }
 }
 
 cudaError_t launch_compact(const KvSeqs &S, const KvCache &C, const int32_t *path, int width,
                            const int32_t *accepted, int32_t *out_len, uint32_t *flags,
                            cudaStream_t stream) {
-  compact_kernel<<<dim3(S.B, 2 * C.layers), kThreads, width * sizeof(int), stream>>>(
-      S, C, path, width, accepted, out_len, flags);
+  // a CTA no larger than a token's pieces
+  const int per_token = C.heads * (C.row_bytes / 16);
+  const int threads = per_token >= kThreads ? kThreads : (per_token + 31) / 32 * 32;
+  const size_t smem = static_cast<size_t>(width) * sizeof(Move);
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  compact_kernel<<<dim3(S.B, 2 * C.layers), threads, smem, stream>>>(S, C, path, width, accepted,
+                                                                     out_len, flags);
   return cudaGetLastError();
 }
 

@@ -492,11 +492,12 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  *    tree_mask.
  * scale: finite, > 0.  window <= 0: off.  sinks >= 0.
  * out [B, N, num_q_heads, head_dim] of the cache's dtype, contiguous, 16-byte
- *    aligned.  out_lse (nullable) float [B, N, num_q_heads]: ln sum_j w_j.
+ *    aligned; does not overlap the span of q (SPEC_ERR_INVALID_ARG).  out_lse (nullable) float [B, N, num_q_heads]: ln sum_j w_j.
  * out_flags [B] (nullable): SPEC_FLAG_BAD_LENGTH (num_new outside [0, N], taken
  *    as clamped; or a sequence whose tokens do not fit its table row: its
- *    tokens see nothing), SPEC_FLAG_BAD_PAGE (its keys are not seen).  Costs a
- *    launch of its own.
+ *    tokens see nothing), SPEC_FLAG_BAD_PAGE (its keys are not seen),
+ *    SPEC_FLAG_TIMEOUT (a bounded on-device wait gave up: the sequence's outputs
+ *    are not to be used).  Costs a launch of its own.
  * Products of bf16 and f16 run on the tensor cores with float32 sums; the
  * weights are rounded to the cache's type before they meet the values.  float32
  * caches are computed in float32.  1 <= N <= 4096.  workspace: 32-byte aligned.

@@ -114,6 +114,20 @@ def _ptr(x):
     return None if x is None else x.data_ptr()
 
 
+def _rows(x):
+    """x as rows that the kernels can read: 16-byte aligned and apart, the last
+    dimension contiguous; a copy where they are not (slices at odd offsets,
+    expanded dimensions, transposed heads)."""
+    if x.is_contiguous() and x.data_ptr() % 16 == 0:
+        return x
+    shape, strides, size = x.shape, x.stride(), x.element_size()
+    if x.data_ptr() % 16 == 0 and strides[-1] == 1 and all(
+            n <= 1 or s >= shape[-1] and s * size % 16 == 0
+            for n, s in zip(shape[:-1], strides[:-1])):
+        return x
+    return x.clone(memory_format=torch.contiguous_format)
+
+
 @functools.lru_cache(maxsize=256)
 def _attention_bytes(*sizes):
     return max(_abi.load().spec_paged_attention_workspace_size(*sizes), 32)
@@ -144,10 +158,8 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
     if q.dim() != 4 or q.shape[3] != k_cache.shape[3] or q.dtype != k_cache.dtype:
         raise ValueError("q must be [B, N, num_q_heads, head_dim] with the cache's type")
     B, N, Hq, D = shape = q.shape
+    q = _rows(q)
     strides = q.stride()
-    if strides[3] != 1:
-        q = q.contiguous()
-        strides = q.stride()
     page_table, table = _table(page_table, B, dev)
     context_len = _ints(context_len, (B,), dev, "context_len")
     if num_new is not None:
@@ -205,8 +217,7 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_ne
     if k_new.dtype != k_cache.dtype or v_new.dtype != k_cache.dtype:
         raise ValueError("k_new and v_new must have the cache's type")
     B, N = shape[-4:-2]
-    k_new = k_new if k_new.stride(-1) == 1 else k_new.contiguous()
-    v_new = v_new if v_new.stride(-1) == 1 else v_new.contiguous()
+    k_new, v_new = _rows(k_new), _rows(v_new)
     ks, vs = k_new.stride(), v_new.stride()
     if len(shape) == 4:
         ks, vs = (0, *ks), (0, *vs)

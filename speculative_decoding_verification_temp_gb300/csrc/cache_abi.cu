@@ -161,6 +161,16 @@ spec_status spec_paged_attention(
       !stride_ok(q_token_stride, N, cache.head_dim, esize) ||
       !stride_ok(q_head_stride, num_q_heads, cache.head_dim, esize))
     return SPEC_ERR_UNSUPPORTED;
+  // pieces of a unit read its queries while others write its outputs
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t q1 = q0 + (static_cast<uintptr_t>(B - 1) * (B > 1 ? q_seq_stride : 0) +
+                             static_cast<uintptr_t>(N - 1) * (N > 1 ? q_token_stride : 0) +
+                             static_cast<uintptr_t>(num_q_heads - 1) *
+                                 (num_q_heads > 1 ? q_head_stride : 0) +
+                             cache.head_dim) * esize;
+  const uintptr_t o1 =
+      o0 + static_cast<uintptr_t>(B) * N * num_q_heads * cache.head_dim * esize;
+  if (q0 < o1 && o0 < q1) return SPEC_ERR_INVALID_ARG;
   const int group = num_q_heads / cache.num_heads;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0 ||
       workspace_bytes < sv::attention_workspace_bytes(N, group, cache.head_dim, cache.dtype))
@@ -182,7 +192,9 @@ spec_status spec_paged_attention(
   p.D = cache.head_dim;
   p.scale = scale;
   p.scale_log2 = scale * sv::kLog2e;
-  p.window = window > 0 ? window : 0;
+  // a window that holds every place of a sequence is none
+  const int places = pages.max_pages * cache.page_size + N;
+  p.window = window > 0 && window < places ? window : 0;
   p.sinks = sinks;
   p.out = out;
   p.lse = out_lse;

@@ -255,7 +255,8 @@ __device__ __forceinline__ uint32_t seen_word(const AttnParams &p, const KeyRang
   const uint32_t in_ctx = low_bits(k.ctx - at);
   uint32_t w = in_ctx, block = ~in_ctx;
   const int place = p.window ? k.ctx + clamp_pos(p, b, n) : 0;
-  if (p.window) w &= low_bits(p.sinks - at) | ~low_bits(place - p.window + 1 - at);
+  // the window's first place; no difference of two places leaves 32 bits
+  if (p.window) w &= low_bits(p.sinks - at) | ~low_bits(max(place - p.window + 1, at) - at);
   if (block) {
     const int m0 = at - k.ctx;  // above -32
     block &= low_bits(k.n_new - m0);

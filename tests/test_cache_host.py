@@ -46,7 +46,7 @@ BAD_TABLES = [dict(table=None), dict(max_pages=0), dict(ld=7), dict(max_pages=1 
 
 
 def attention(lib, B=2, N=3, Hq=4, q=P, qs=(12 * 64, 4 * 64, 64), c=None, t=None, ctx=P, mask=None,
-              ms=0, pos=None, ps=0, scale=0.125, window=0, sinks=0, out=P, ws=P, ws_bytes=None):
+              ms=0, pos=None, ps=0, scale=0.125, window=0, sinks=0, out=P << 4, ws=P, ws_bytes=None):
     need = lib.spec_paged_attention_workspace_size(max(B, 0), min(max(N, 1), 4096), 4, 2, 64, 1)
     return lib.spec_paged_attention(q, *qs, Hq, c or cache(), t or table(), ctx, None, B, N, mask, ms,
                                     pos, ps, scale, window, sinks, out, None, None, ws,
@@ -63,11 +63,12 @@ def test_attention_refuses(lib):
     for kw in (dict(B=-1), dict(N=0), dict(N=4097), dict(Hq=0), dict(Hq=3), dict(q=None), dict(out=None),
                dict(ctx=None), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                dict(scale=float("inf")), dict(sinks=-1), dict(ws=None), dict(ws=P + 4),
-               dict(window=4, mask=P), dict(ms=-1), dict(ps=-1), dict(B=1 << 17, N=4096)):
+               dict(window=4, mask=P), dict(ms=-1), dict(ps=-1), dict(B=1 << 17, N=4096),
+               dict(out=P), dict(out=P + 12 * 64 * 2 + 2 * 4 * 64 * 2), dict(q=(P << 4) + 16)):
         assert attention(lib, **kw) == INV, kw
     need = lib.spec_paged_attention_workspace_size(2, 3, 4, 2, 64, 1)
     assert attention(lib, ws_bytes=need - 1) == INV
-    for kw in (dict(q=P + 8), dict(out=P + 8), dict(qs=(12 * 64, 4 * 64, 60)), dict(qs=(0, 4 * 64, 64)),
+    for kw in (dict(q=P + 8), dict(out=(P << 4) + 8), dict(qs=(12 * 64, 4 * 64, 60)), dict(qs=(0, 4 * 64, 64)),
                dict(qs=(12 * 64, 8, 64))):
         assert attention(lib, **kw) == UNS, kw
 

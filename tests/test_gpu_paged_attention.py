@@ -324,3 +324,106 @@ def test_long_chains_from_an_empty_cache():
     """A prompt: every token is new."""
     s = Setup(17, [0, 37], 300, 4, 2, 128, 16, "bf16")
     s.check(s.call())
+
+
+# bf16 and f16 at head_dim 64 and 128 with pages of 8..128 tokens take the tensor
+# memory kernels, other sizes the matrix kernel, float32 the FMA kernel; up to 32
+# rows (new tokens times query heads per head) are split over lane quarters, up to
+# 128 are a row tile, more are pairs of row tiles.
+KERNELS = [("bf16", 1, 8, 2, 128, 16), ("f16", 4, 16, 2, 64, 8), ("bf16", 10, 16, 2, 128, 32),
+           ("f16", 12, 10, 2, 64, 16), ("bf16", 40, 14, 2, 128, 64), ("f16", 70, 8, 2, 64, 16),
+           ("bf16", 3, 6, 2, 72, 16), ("f16", 2, 4, 2, 128, 5), ("bf16", 2, 4, 2, 200, 16),
+           ("f32", 3, 6, 2, 20, 16), ("f32", 1, 4, 2, 128, 3), ("f32", 2, 2, 1, 256, 16)]
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D,page", KERNELS)
+def test_many_short_sequences(dtype, N, Hq, Hkv, D, page):
+    """More units than CTAs: a CTA goes from one to the next."""
+    rng = np.random.default_rng(20)
+    B = 40 if N >= 40 else 420
+    s = Setup(20, rng.integers(0, 50, B), N, Hq, Hkv, D, page, dtype,
+              n_new=rng.integers(0, N + 1, B))
+    s.check(s.call())
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D,page", KERNELS)
+def test_ragged_batches_that_are_cut_anywhere(dtype, N, Hq, Hkv, D, page):
+    rng = np.random.default_rng(21)
+    s = Setup(21, [3, 2500, 0, 127, 128, 129, 900, 1, 1300], N, Hq, Hkv, D, page, dtype)
+    sees = rng.random((9, N, N)) < 0.5
+    res = s.call(tree_mask=s.dev(mask_words(sees)))
+    s.check(res, sees=sees)
+    again = s.call(tree_mask=s.dev(mask_words(sees)))
+    assert torch.equal(res.out, again.out) and torch.equal(res.lse, again.lse)
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D,page", KERNELS)
+def test_windows_in_every_kernel(dtype, N, Hq, Hkv, D, page):
+    s = Setup(22, [0, 5, 700, 333], N, Hq, Hkv, D, page, dtype)
+    position = s.rng.integers(0, N, (4, N))
+    for window, sinks, pos in ((100, 4, None), (30, 200, None), (2 ** 31 - 1, 3, None), (7, 1, position)):
+        res = s.call(window=window, sinks=sinks, position=s.dev(pos))
+        s.check(res, window=window, sinks=sinks, position=pos)
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D,page", KERNELS)
+def test_nothing_to_do(dtype, N, Hq, Hkv, D, page):
+    s = Setup(23, [30, 0, 7], N, Hq, Hkv, D, page, dtype, n_new=[0, 0, 0])
+    out = torch.full(s.q.shape, 3.0, dtype=s.q.dtype, device="cuda")
+    s.call(out=out)
+    assert (out == 3.0).all()
+    none = sv.paged_attention(s.q[:0], s.k, s.v, s.dev(s.table)[:0], s.dev(s.ctx)[:0], return_flags=True)
+    assert none.out.shape[0] == 0 and none.flags.numel() == 0
+
+
+@pytest.mark.parametrize("page", [8, 32, 128, 256, 384, 24])
+@pytest.mark.parametrize("N", [1, 20, 70])
+def test_page_sizes(page, N):
+    s = Setup(24, [0, 100, 383, 384, 900], N, 8, 2, 128, page, "bf16", layout="hnd" if N == 20 else "nhd")
+    s.check(s.call())
+
+
+@pytest.mark.parametrize("Hq,N,D", [(130, 1, 64), (300, 2, 128), (97, 3, 64), (128, 1, 128)])
+def test_many_query_heads_to_one(Hq, N, D):
+    s = Setup(25, [40, 300], N, Hq, 1, D, 16, "bf16")
+    s.check(s.call())
+
+
+def test_queries_that_have_to_be_copied():
+    s = Setup(26, [50, 120], 3, 8, 2, 64, 16, "bf16")
+    want = s.call()
+    flat = torch.zeros(s.q.numel() + 3, dtype=s.q.dtype, device="cuda")
+    odd = flat[3:].view(s.q.shape)
+    odd.copy_(s.q)
+    swapped = s.q.transpose(2, 3).contiguous().transpose(2, 3)
+    for q in (odd, swapped):
+        got = sv.paged_attention(q, s.k, s.v, s.dev(s.table), s.dev(s.ctx))
+        assert torch.equal(got.out, want.out)
+    one = s.q[:1].expand(2, -1, -1, -1)
+    got = sv.paged_attention(one, s.k, s.v, s.dev(s.table), s.dev(s.ctx))
+    assert torch.equal(got.out, sv.paged_attention(one.contiguous(), s.k, s.v, s.dev(s.table),
+                                                   s.dev(s.ctx)).out)
+
+
+def test_refused_tensors():
+    s = Setup(27, [50, 120], 3, 8, 2, 64, 16, "bf16")
+    table, ctx = s.dev(s.table), s.dev(s.ctx)
+    good = dict(q=s.q, k_cache=s.k, v_cache=s.v, page_table=table, context_len=ctx)
+    words = torch.zeros(2, 3, 1, dtype=torch.int64, device="cuda")
+    grad = s.q.clone().requires_grad_()
+    for bad in (dict(q=s.q.float()), dict(q=s.q[:, :, :, :32]), dict(q=s.q[0]), dict(q=s.q.cpu()),
+                dict(v_cache=s.v[:, :, :1]), dict(v_cache=s.v.half()), dict(k_cache=s.k.cpu()),
+                dict(k_cache=s.k[None], v_cache=s.v[None]), dict(page_table=table[:1]),
+                dict(page_table=table.float()), dict(context_len=ctx[:1]), dict(context_len=ctx.float()),
+                dict(num_new=ctx[:1]), dict(tree_mask=words[:, :2]), dict(tree_mask=words.int()),
+                dict(position=ctx), dict(out=s.q[:1]), dict(q=grad),
+                dict(k_cache=s.k.transpose(1, 3).contiguous().transpose(1, 3),
+                     v_cache=s.v.transpose(1, 3).contiguous().transpose(1, 3))):
+        with pytest.raises(ValueError):
+            sv.paged_attention(**(good | bad))
+    for bad in (dict(out=s.q), dict(window=3, tree_mask=words), dict(scale=0.0), dict(sinks=-1),
+                dict(q=s.q[:, :, :7])):
+        with pytest.raises(sv.SpecVerifyError):
+            sv.paged_attention(**(good | bad))
+    with torch.no_grad():
+        assert torch.equal(sv.paged_attention(**(good | dict(q=grad))).out, s.call().out)

@@ -628,14 +628,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (count == 2 && p.D <= 128) {
     const float *s[2] = {slot(0), slot(1)};
     const int at = lane * 4;
-    for (int r = blockIdx.y * kWarps + warp; r < rows; r += 4 * Y * kWarps) {
+    for (int r = (blockIdx.y * kWarps + warp) * 4; r < rows; r += 4 * Y * kWarps) {
       float m[4][2], l[4][2];
       float4 v[4][2];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int row = min(r + j * Y * kWarps, rows - 1);
+          const int row = min(r + j, rows - 1);
           m[j][x] = s[x][row];
           l[j][x] = s[x][p.rows + row];
           if (at < p.D)
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int row = r + j * Y * kWarps;
+        const int row = r + j;
         if (row >= rows) break;
         const float M = fmaxf(m[j][0], m[j][1]);
         float f[2], sum = 0.f;
@@ -794,10 +794,15 @@ AttnPlan narrow_plan(int D, int dtype) {
 bool wide_sizes(int G, int D, int dtype) {
   return dtype != SPEC_F32 && (D == 64 || D == 128) && G <= 128;
 }
-AttnPlan wide_plan(int N, int G) {
-  // two row tiles that share their keys, or a row tile for each of two streams
-  if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 7, 2};
-  return {2 * kSms, wide_tile_rows(G), 7, 1};
+// What a unit costs beside its tiles (queries, the first products and the last,
+// masked tiles, outputs), in tiles, from runs of one launch fitted by their tiles
+// and units: pairs of row tiles 8 (12 to 16 us; 256-node trees at B=16 take 593 us with
+// 9, 603 with 7, 606 with 5, 665 with 2, where the longest of 152 runs is 1.23
+// times the median), single ones 1 at head_dim 128, where HBM hides it, and 2 at
+// 64.
+AttnPlan wide_plan(int N, int G, int D) {
+  if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 7, 8};
+  return {2 * kSms, wide_tile_rows(G), 7, D == 64 ? 2 : 1};
 }
 
 template <auto kKernel>
@@ -824,7 +829,7 @@ size_t plan_bytes(const AttnPlan &plan, int D) {
 
 size_t attention_workspace_bytes(int N, int G, int D, int dtype) {
   const size_t narrow = plan_bytes(narrow_plan(D, dtype), D);
-  const size_t wide = wide_sizes(G, D, dtype) ? plan_bytes(wide_plan(N, G), D) : 0;
+  const size_t wide = wide_sizes(G, D, dtype) ? plan_bytes(wide_plan(N, G, D), D) : 0;
   return narrow > wide ? narrow : wide;
 }
 
@@ -839,7 +844,7 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
   WideMaps maps;
   bool wide = wide_sizes(p.G, p.D, dtype) && (P % 128 == 0 || (P >= 8 && 128 % P == 0));
   if (wide) {
-    take(wide_plan(p.S.N, p.G));
+    take(wide_plan(p.S.N, p.G, p.D));
     wide = wide_maps(p, dtype, &maps);
   }
   if (!wide) take(narrow_plan(p.D, dtype));

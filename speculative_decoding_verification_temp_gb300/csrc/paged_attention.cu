@@ -622,9 +622,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const JoinDesc d = p.join[blockIdx.x];
   if (d.pieces_end < 0) return;
   const int rows = d.rows, Y = gridDim.y;
-  const int first = static_cast<int>(blockIdx.x) - 1, count = d.pieces_end - first + 1;
+  const int step = p.row_lines, first = static_cast<int>(blockIdx.x) - step;
+  const int count = (d.pieces_end - first) / step + 1;
   const size_t per_slot = slot_floats(p.rows, p.D);
-  auto slot = [&](int i) { return p.part + (2 * (first + i) + (i == 0 ? 1 : 0)) * per_slot; };
+  auto slot = [&](int i) { return p.part + (2 * (first + i * step) + (i == 0 ? 1 : 0)) * per_slot; };
   if (count == 2 && p.D <= 128) {
     const float *s[2] = {slot(0), slot(1)};
     const int at = lane * 4;
@@ -791,6 +792,9 @@ AttnPlan narrow_plan(int D, int dtype) {
   return {kSms, 16, log2_of(Rows16<256, 16, 3>::kTile), 1};
 }
 
+// Lines of 19 workers each at least; 152 are a multiple of 2, 4 and 8.
+constexpr int kMaxRowLines = 8;
+
 bool wide_sizes(int G, int D, int dtype) {
   return dtype != SPEC_F32 && (D == 64 || D == 128) && G <= 128;
 }
@@ -840,11 +844,15 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
     p.rows = plan.rows;
     p.tile_log2 = plan.tile_log2;
     p.unit_cost = plan.unit_cost;
+    p.row_lines = 1;
   };
   WideMaps maps;
   bool wide = wide_sizes(p.G, p.D, dtype) && (P % 128 == 0 || (P >= 8 && 128 % P == 0));
   if (wide) {
     take(wide_plan(p.S.N, p.G, p.D));
+    // row tiles of a tree see the same keys; those of a chain end at their own
+    const int tiles = (p.S.N * p.G + p.rows - 1) / p.rows;
+    if (p.mask && tiles <= kMaxRowLines) p.row_lines = tiles;
     wide = wide_maps(p, dtype, &maps);
   }
   if (!wide) take(narrow_plan(p.D, dtype));

@@ -14,6 +14,11 @@
 // order of its keys, so results do not depend on timing.  The line is laid out
 // on the device from the lengths, so a captured launch follows lengths that
 // change.
+//
+// Where a sequence has several row tiles with the same keys (row_lines of them),
+// each has a line and an equal share of the workers of its own: neighbouring
+// workers then go through the same keys at the same time, and HBM is read once
+// for all of them instead of once for each.
 #pragma once
 
 #include <cuda.h>
@@ -44,10 +49,11 @@ struct AttnParams {
   struct JoinDesc *join;
   int workers, rows, tile_log2;  // at most; R; T as a power of two
   int unit_cost;                 // places on the line behind a unit's key tiles
+  int row_lines;                 // 1: all row tiles on one line
 };
 
 // A cut unit, written by the worker that holds its first cut; its pieces are
-// those of the worker before it .. pieces_end.  pieces_end -1: no unit's cuts
+// those of its line's worker before it .. pieces_end.  pieces_end -1: no unit's cuts
 // start here.
 struct JoinDesc {
   int b, h, r0, rows, pieces_end;
@@ -110,9 +116,12 @@ __device__ __forceinline__ long long div_small(long long a, long long b) {
 }
 
 // Places of one head of a sequence.
-__device__ __forceinline__ long long head_work(const AttnParams &p, int ctx, int n_new, bool fits) {
+__device__ __forceinline__ long long head_work(const AttnParams &p, int ctx, int n_new, bool fits,
+                                               int line) {
   const int rows = n_new * p.G;
-  if (rows == 0) return 0;
+  if (rows <= line * p.rows) return 0;
+  if (p.row_lines > 1)
+    return key_range(p, ctx, n_new, fits, line * p.rows).count + p.unit_cost;
   if (rows <= p.rows || p.mask || !fits) {  // its row tiles have the same keys
     const int tiles = rows <= p.rows ? 1 : (rows + p.rows - 1) / p.rows;
     return static_cast<long long>(tiles) * (key_range(p, ctx, n_new, fits, 0).count + p.unit_cost);
@@ -128,12 +137,13 @@ __device__ __forceinline__ long long head_work(const AttnParams &p, int ctx, int
 struct Line {
   long long w0, w1;     // empty: no work
   long long per, more;
-  int worker, workers;  // of `workers` with work
+  int worker, line;     // the line is `worker` modulo row_lines,
+  int turn, turns;      // its run on it the turn-th of those with work
   int b;                // the sequence that holds w0
   long long in_seq;     // w0 within it
 
   __device__ __forceinline__ long long start_of(long long w) const { return w * per + min(w, more); }
-  __device__ __forceinline__ long long worker_of(long long place) const {
+  __device__ __forceinline__ long long turn_of(long long place) const {
     const long long cut = more * (per + 1);
     return place < cut ? div_small(place, per + 1) : more + div_small(place - cut, per);
   }
@@ -152,12 +162,14 @@ template <int kT, int kW>
 __device__ __forceinline__ void find_runs(const AttnParams &p, RunScratch<kT, kW> &x, int first,
                                           int step, Line (&L)[kW]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (with more than one line, of one worker)
+  const int line = p.row_lines == 1 ? 0 : first % p.row_lines;
   const int chunk = (p.S.B + kT - 1) / kT;
   const int b0 = min(tid * chunk, p.S.B), b1 = min(b0 + chunk, p.S.B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
-    mine += p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n));
+    mine += p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n), line);
   }
   long long before = mine;
 #pragma unroll
@@ -175,22 +187,25 @@ __device__ __forceinline__ void find_runs(const AttnParams &p, RunScratch<kT, kW
     total += v;
   }
   before -= mine;
-  const int workers = total < p.workers ? (total > 0 ? static_cast<int>(total) : 1) : p.workers;
-  const long long per = div_small(total, workers);
+  const int most = p.row_lines == 1 ? p.workers : p.workers / p.row_lines;
+  const int turns = total < most ? (total > 0 ? static_cast<int>(total) : 1) : most;
+  const long long per = div_small(total, turns);
 #pragma unroll
   for (int i = 0; i < kW; ++i) {
     L[i].per = per;
-    L[i].more = total - per * workers;
-    L[i].workers = workers;
+    L[i].more = total - per * turns;
+    L[i].turns = turns;
     L[i].worker = first + i * step;
-    const bool busy = total > 0 && L[i].worker < workers;
-    L[i].w0 = busy ? L[i].start_of(L[i].worker) : 0;
-    L[i].w1 = busy ? L[i].start_of(L[i].worker + 1ll) : 0;
+    L[i].line = line;
+    L[i].turn = p.row_lines == 1 ? L[i].worker : L[i].worker / p.row_lines;
+    const bool busy = total > 0 && L[i].turn < turns;
+    L[i].w0 = busy ? L[i].start_of(L[i].turn) : 0;
+    L[i].w1 = busy ? L[i].start_of(L[i].turn + 1ll) : 0;
     if (busy && before <= L[i].w0 && L[i].w0 < before + mine) {
       long long at = before;
       for (int b = b0; b < b1; ++b) {
         const int ctx = __ldg(p.S.ctx + b), n = seq_new(p.S, b);
-        const long long w = p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n));
+        const long long w = p.C.heads * head_work(p, ctx, n, seq_fits(p.S, p.C, ctx, n), line);
         if (L[i].w0 < at + w) {
           x.found[i][0] = b;
           x.found[i][1] = L[i].w0 - at;
@@ -227,10 +242,10 @@ struct UnitWalk {
     if (L.w0 == L.w1) return false;
     b = L.b;
     load_seq(p);
-    const long long per_head = head_work(p, k.ctx, k.n_new, fits);
+    const long long per_head = head_work(p, k.ctx, k.n_new, fits, L.line);
     h = static_cast<int>(div_small(L.in_seq, per_head));
     long long left = L.in_seq - h * per_head;
-    for (r0 = 0;; r0 += p.rows) {
+    for (r0 = L.line * p.rows;; r0 += p.rows) {
       k = key_range(p, k.ctx, k.n_new, fits, r0);
       if (left < k.count + p.unit_cost) break;
       left -= k.count + p.unit_cost;
@@ -245,14 +260,14 @@ struct UnitWalk {
     a += k.count + p.unit_cost;
     if (a >= L.w1) return false;
     r0 += p.rows;
-    if (r0 >= k.n_new * p.G) {
-      r0 = 0;
+    if (p.row_lines > 1 || r0 >= k.n_new * p.G) {
+      r0 = L.line * p.rows;
       if (++h == p.C.heads) {
         h = 0;
         do {
           ++b;
           load_seq(p);
-        } while (k.n_new == 0);
+        } while (k.n_new * p.G <= r0);
       }
     }
     k = key_range(p, k.ctx, k.n_new, fits, r0);
@@ -282,12 +297,13 @@ __host__ __device__ __forceinline__ size_t slot_floats(int R, int D) {
 __device__ __forceinline__ void write_join(const AttnParams &p, const Line &L, const UnitWalk *u) {
   if (L.worker >= p.workers) return;
   JoinDesc d = {0, 0, 0, 0, -1};
-  if (u && u->i0 > 0 && L.start_of(L.worker - 1ll) <= u->a) {
+  if (u && u->i0 > 0 && L.start_of(L.turn - 1ll) <= u->a) {
     d.b = u->b;
     d.h = u->h;
     d.r0 = u->r0;
     d.rows = u->live_rows(p);
-    d.pieces_end = static_cast<int>(L.worker_of(u->a + u->k.count - 1));
+    d.pieces_end =
+        static_cast<int>(L.turn_of(u->a + u->k.count - 1)) * p.row_lines + L.line;
   }
   p.join[L.worker] = d;
 }

@@ -427,3 +427,16 @@ def test_refused_tensors():
             sv.paged_attention(**(good | bad))
     with torch.no_grad():
         assert torch.equal(sv.paged_attention(**(good | dict(q=grad))).out, s.call().out)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 128), (14, 2, 64), (3, 1, 128)])
+def test_trees_of_several_row_tiles(Hq, Hkv, D):
+    """Row tiles with lines of work of their own; sequences with fewer of them."""
+    N, n_new = 100, [100, 3, 0, 64, 33, 100]
+    s = Setup(28, [700, 100, 5, 3000, 0, 90], N, Hq, Hkv, D, 16, "bf16", n_new=n_new)
+    sees = s.rng.random((6, N, N)) < 0.4
+    res = s.call(tree_mask=s.dev(mask_words(sees)))
+    s.check(res, sees=sees)
+    again = s.call(tree_mask=s.dev(mask_words(sees)))
+    for b, n in enumerate(n_new):
+        assert torch.equal(res.out[b, :n], again.out[b, :n])

@@ -1,9 +1,16 @@
-// Attention of few new tokens over a paged cache: 16 rows of 16-bit types per
-// unit on warp-level matrix instructions, 8 rows of float32 on the FMA pipes,
-// and the join of the pieces of cut units.
+// Attention over a paged cache where the tensor-memory kernels do not apply: 16
+// rows of 16-bit types per unit on warp-level matrix instructions (head_dim other
+// than 64 and 128, pages that are no power of two of 8 to 128 tokens nor a
+// multiple of 128, more than 128 query heads to one), 8 rows of float32 on the FMA
+// pipes; and the join of the pieces of cut units.
 //
-// Both kernels read every key and value once per row tile and are bound by HBM
-// for one token; each of the four warps of a CTA streams its own quarter of
+// Each row tile reads its keys and values once.  16-bit, 256 sequences of 1 to
+// 4096 tokens, one token each, 32 query heads on 8 of 128, bound by HBM: 365 us
+// (5.9 TB/s) with pages of 24 tokens, where the tensor-memory kernels take 333 us
+// with pages of 16; many rows are bound by the row tiles' re-reading: 32 trees of
+// 60 nodes 1033 us against 110.
+//
+// In both kernels each of the four warps of a CTA streams its own quarter of
 // each key tile through a ring of its own in shared memory (cp.async, 16 bytes
 // a piece, so a row may start on any page) and keeps its own running maximum,
 // sum and output in registers, so that no barrier is on the stream.  The warps'
@@ -369,13 +376,17 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
 // float32, 8 rows per unit
 // ---------------------------------------------------------------------------
 
-// A lane takes one key of its warp's tile (or one of 32 / KT parts of it) for
-// the scores and some of the head's dimensions for the outputs.  Rows of keys
-// are 16 bytes longer than their data, so that eight lanes on eight rows meet
-// different banks.
+// A lane takes one of 32 / KT parts of a key of its warp's tile for the scores
+// and some of the head's dimensions for the outputs.  Rows of keys are 16 bytes
+// longer than their data, so that lanes on different rows meet different banks.
+// Bound by shared-memory reads: a key's part is met by eight queries, 9 reads of
+// 16 bytes for 32 products.  Tiles of 4 KB a warp leave room for three CTAs an
+// SM: 64 sequences of 1 to 4096 tokens, one token each, 32 heads on 8 of 128,
+// 244 us (4.4 TB/s); with two CTAs 275, with tiles twice as long and one CTA 350.
 template <int DP>
 struct Rows8 {
-  static constexpr int KT = 2048 / DP;  // 32, 16, 8 keys per warp and tile
+  static constexpr int KT = 1024 / DP;  // 16, 8, 4 keys per warp and tile
+  static constexpr int kCtas = DP <= 128 ? 3 : 2;  // of an SM
   static constexpr int ST = 2;
   static constexpr int kTile = kAttnWarps * KT;
   static constexpr int kKeyRow = DP * 4 + 16, kValRow = DP * 4;
@@ -387,7 +398,7 @@ struct Rows8 {
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kAttnThreads, 1) rows8_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, Rows8<DP>::kCtas) rows8_kernel(const __grid_constant__ AttnParams p) {
   using L = Rows8<DP>;
   constexpr int KT = L::KT, ST = L::ST, R = 8;
   extern __shared__ __align__(128) char smem[];
@@ -784,8 +795,9 @@ constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
 
 AttnPlan narrow_plan(int D, int dtype) {
   if (dtype == SPEC_F32) {
-    if (D <= 64) return {kSms, 8, log2_of(Rows8<64>::kTile), 1};
-    return {kSms, 8, log2_of(D <= 128 ? Rows8<128>::kTile : Rows8<256>::kTile), 1};
+    if (D <= 64) return {Rows8<64>::kCtas * kSms, 8, log2_of(Rows8<64>::kTile), 1};
+    if (D <= 128) return {Rows8<128>::kCtas * kSms, 8, log2_of(Rows8<128>::kTile), 1};
+    return {Rows8<256>::kCtas * kSms, 8, log2_of(Rows8<256>::kTile), 1};
   }
   if (D <= 64) return {2 * kSms, 16, log2_of(Rows16<64, 32, 3>::kTile), 1};
   if (D <= 128) return {2 * kSms, 16, log2_of(Rows16<128, 16, 3>::kTile), 1};

@@ -33,6 +33,8 @@
  *   - EAGLE-2 rerank (spec_tree_rerank): the m nodes of highest product of
  *     confidences along the path, shallow nodes first on ties.
  *     zzszmyf.github.io "LLM 推测解码精读笔记 · 04 EAGLE", section 10.3.
+ *   - The paged key-value cache around a verification (spec_paged_attention,
+ *     spec_cache_*): described with those entry points.
  *
  * Readings where the pages are silent (fixed here, identical in the tests):
  *   greedy/argmax ties -> lowest index; top-k keeps every logit >= the k-th
@@ -61,7 +63,7 @@
  *     other strides are accepted and take a scalar-load path.
  *   - The workspace needs no initialisation: each call first clears, with
  *     one cudaMemsetAsync on `stream`, the part of it that must start at zero
- *     (arrival counters and the weight-task queue).  Calls that share one
+ *     (arrival counters and the weight-task queue; none of the cache operators).  Calls that share one
  *     workspace must not overlap on the GPU.
  *
  * Limits: 0 <= gamma <= 4095; 1 <= N <= 4096; V >= 1, and for the verifiers

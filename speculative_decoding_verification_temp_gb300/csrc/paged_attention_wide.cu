@@ -26,8 +26,18 @@
 // group's heads, as many whole tokens as 128 rows hold.
 //
 // One token is bound by HBM: 64 KB of keys and values a tile at head_dim 128
-// arrive in about 3000 cycles of an SM, their products take 850 of them (Q K^T
-// reads both operands from shared memory, 64 cycles a step of 16).
+// arrive in about 3000 cycles of an SM; a stream's tile takes 850 of products (Q K^T
+// reads both operands from shared memory, 65 cycles a step of 16; P V 41) and 600 of
+// softmax in quarters.  256 sequences of 1 to 4096 tokens, one token each, 32 query
+// heads on 8 of 128 bf16: 333 us, 6.48 TB/s, 0.95 of the measured copy rate, DRAM
+// reads 1.004 of the keys' and values' bytes.
+//
+// Many rows are bound by the turns that a stream's softmax (1770 cycles a tile
+// with both streams at it) and products take with one buffer of scores: 256-node
+// trees at B = 16, 64 query heads on 8 of 128 bf16, contexts of 1000 to 8192 tokens:
+// 530 us, 1.16 PFLOP/s.  Measured and not kept: scores in halves of 64 keys with two
+// buffers (710 us: 52 cycles a step of 64 keys make the products the bound) and two
+// warps per row (671 us), when this took 645.
 #include <climits>
 #include <numeric>
 
@@ -1275,6 +1285,9 @@ namespace {
 
 bool wide_pairs(const AttnParams &p) { return p.rows > wide_tile_rows(p.G); }
 int wide_ctas(const AttnParams &p) { return wide_pairs(p) ? p.workers : p.workers / 2; }
+// As many rows as a quarter of the lanes holds.  Split and not: one token at
+// B = 256 325 and 343 us, in windows of 1024 at B = 64 44 and 74, eight tokens at
+// B = 64 (32 rows) 107 and 112.
 bool solo_splits(const AttnParams &p) { return p.S.N * p.G <= 32; }
 
 // cuTensorMapEncodeTiled of the installed driver; the library does not link to it.

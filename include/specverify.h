@@ -441,7 +441,8 @@ spec_status spec_tree_rerank(const int32_t *parent, const float *confidence, int
  * alike.  Any order of the strided dimensions is taken ([page, token, head, d]
  * or [page, head, token, d], keys and values interleaved).
  * dtype: SPEC_F32, SPEC_BF16 or SPEC_F16.  head_dim: a multiple of 16 bytes, at
- * most 256 elements.  page_size: 1..65536, not only powers of two.  k, v and
+ * most 256 elements.  page_size: 1..65536, not only powers of two; the keys of a
+ * page in one layer take at most 16 GB.  k, v and
  * every stride of a dimension larger than one are multiples of 16 bytes, and no
  * such stride is shorter than head_dim; otherwise SPEC_ERR_UNSUPPORTED. */
 typedef struct {
@@ -492,7 +493,7 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  * position (nullable) [B, N], sequence b at b*position_seq_stride; read with a
  *    window only; values are clamped into [0, N).  Required with window and
  *    tree_mask.
- * scale: finite, > 0.  window <= 0: off.  sinks >= 0.
+ * scale: > 0, and finite times log2(e).  window <= 0: off.  sinks >= 0.
  * out [B, N, num_q_heads, head_dim] of the cache's dtype, contiguous, 16-byte
  *    aligned; does not overlap the span of q (SPEC_ERR_INVALID_ARG).  out_lse (nullable) float [B, N, num_q_heads]: ln sum_j w_j.
  * out_flags [B] (nullable): SPEC_FLAG_BAD_LENGTH (num_new outside [0, N], taken
@@ -519,7 +520,10 @@ spec_status spec_paged_attention(
  * k_new, v_new [num_layers, B, N, num_heads, head_dim] of the cache's dtype;
  *    strides in elements, aligned as the cache's.  They do not overlap the cache.
  * Two places on one page slot (sequences that share a page behind their common
- * tokens) leave either token there; spec_cache_fork makes no such pages.
+ * tokens) leave either token there; spec_cache_fork makes no such pages.  A token
+ * on a page that another sequence holds is written for both: a sequence that was
+ * cut to a length inside a shared page goes on from a fork of itself at that
+ * length, which has a page of its own there.
  * out_flags [B] (nullable): SPEC_FLAG_BAD_LENGTH (the sequence's tokens are not
  * written, or num_new is clamped into [0, N]), SPEC_FLAG_BAD_PAGE (the page's
  * tokens are not written).  Costs a launch of its own.

@@ -25,6 +25,20 @@ _KV_DTYPES = {torch.float32: _abi.SPEC_F32, torch.bfloat16: _abi.SPEC_BF16,
               torch.float16: _abi.SPEC_F16}
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _c_int(x):
+    """x for a C int: what lies beyond it would wrap, and is taken as its largest
+    value or as -1."""
+    return max(min(int(x), _INT_MAX), -1)
+
+
+def _sizes(shape):
+    if max(shape) > _INT_MAX:
+        raise ValueError(f"sizes have to fit 32 bits, got {list(shape)}")
+
+
 def _on(x, dev, name):
     if not isinstance(x, torch.Tensor) or x.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
@@ -71,6 +85,7 @@ def _cache(k, v, layers):
     if v.shape != shape or dims != 4 and not (layers and dims == 5):
         raise ValueError("k_cache and v_cache must be [%snum_pages, page_size, num_heads, head_dim]"
                          % ("num_layers, " if layers else ""))
+    _sizes(shape)
     if shape[-1] > 1 and (ks[-1] != 1 or vs[-1] != 1):
         raise ValueError("the last dimension of the caches must be contiguous")
     if dims == 4:
@@ -84,6 +99,7 @@ def _table(page_table, B, dev):
     shape = page_table.shape
     if len(shape) != 2 or shape[0] != B:
         raise ValueError(f"page_table must be [{B}, max_pages]")
+    _sizes(shape)
     if page_table.dtype != torch.int32:
         page_table = _ints(page_table, tuple(shape), dev, "page_table")
     ld, step = page_table.stride()
@@ -180,6 +196,7 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
         out = torch.empty(shape, dtype=q.dtype, device=dev)
     else:
         _on(out, dev, "out")
+        _forward_only(out)
         if out.shape != shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be a contiguous tensor like q")
     lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev) if return_lse else None
@@ -190,8 +207,8 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _run(dev, _abi.load().spec_paged_attention, q.data_ptr(), strides[0], strides[1], strides[2], Hq, cache,
          table, context_len.data_ptr(), _ptr(num_new), B, N, _ptr(tree_mask), mask_stride,
-         _ptr(position), pos_stride, D ** -0.5 if scale is None else float(scale), int(window),
-         int(sinks), out.data_ptr(), _ptr(lse), _ptr(flags), ws.data_ptr(), nbytes)
+         _ptr(position), pos_stride, D ** -0.5 if scale is None else float(scale),
+         _c_int(window), _c_int(sinks), out.data_ptr(), _ptr(lse), _ptr(flags), ws.data_ptr(), nbytes)
     return AttentionResult(out, lse, flags)
 
 
@@ -287,7 +304,7 @@ def cache_resize(pool, length, page_size):
     spec_cache_resize): pages behind them go back to the pool, missing ones are
     taken from it; length 0 frees a sequence.  Returns flags [num_seqs] int32.
     """
-    p = _pool(pool, int(page_size))
+    p = _pool(pool, _c_int(page_size))
     dev = pool.page_table.device
     length = _ints(length, (p.num_seqs,), dev, "length")
     flags = torch.empty(p.num_seqs, dtype=torch.int32, device=dev)

@@ -28,6 +28,7 @@ constexpr int kMaxSeqs = 4096;  // of a pool, and of the forks of a call
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxPageSize = 65536;
 constexpr int kMaxRowsY = 65535;  // blockIdx.y
+constexpr int64_t kMaxPagePieces = 1 << 30;  // of 16 bytes: a page's copy counts them in 32 bits
 
 spec_status map_cuda(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
 
@@ -50,7 +51,8 @@ spec_status check_cache(const spec_kv_cache &c) {
       c.page_size > kMaxPageSize || c.num_heads < 1 || c.head_dim < 1)
     return SPEC_ERR_INVALID_ARG;
   if (c.head_dim > kMaxHeadDim || c.head_dim * esize % 16 != 0 || !aligned16(c.k) ||
-      !aligned16(c.v) || c.num_layers > kMaxRowsY / 2 || c.num_heads > 4096)
+      !aligned16(c.v) || c.num_layers > kMaxRowsY / 2 || c.num_heads > 4096 ||
+      static_cast<int64_t>(c.page_size) * c.num_heads * (c.head_dim * esize / 16) > kMaxPagePieces)
     return SPEC_ERR_UNSUPPORTED;
   const int64_t strides[8] = {c.k_layer_stride, c.k_page_stride, c.k_token_stride, c.k_head_stride,
                               c.v_layer_stride, c.v_page_stride, c.v_token_stride, c.v_head_stride};
@@ -147,7 +149,7 @@ spec_status spec_paged_attention(
     spec_stream_t stream) {
   const int esize = kv_esize(cache.dtype);
   if (esize == 0 || B < 0 || N < 1 || N > kMaxNew || num_q_heads < 1 || !(scale > 0.f) ||
-      scale == INFINITY || sinks < 0)
+      !(scale * sv::kLog2e < INFINITY) || sinks < 0)
     return SPEC_ERR_INVALID_ARG;
   if (B == 0) return SPEC_OK;
   if (const spec_status s = check_cache(cache); s != SPEC_OK) return s;

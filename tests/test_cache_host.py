@@ -173,3 +173,33 @@ def test_the_binding_refuses_tensors_off_the_gpu():
         sv.cache_resize(pool, ints, 16)
     with pytest.raises(ValueError):
         sv.cache_fork(pool, k, k, ints, ints, ints)
+
+
+def test_sizes_beyond_32_bits_are_refused(lib):
+    # 2^34 pieces of 16 bytes in a page: more than the copy of a page counts
+    huge = dict(num_pages=2, page_size=65536, num_heads=4096, head_dim=256, dtype=_abi.SPEC_F32)
+    for x in "kv":
+        huge |= {f"{x}_layer_stride": 1 << 41, f"{x}_page_stride": 1 << 40, f"{x}_token_stride": 1 << 20,
+                 f"{x}_head_stride": 256}
+    assert compact(lib, c=cache(**huge)) == UNS
+    assert lib.spec_cache_fork(pool(num_pages=2, page_size=65536), cache(**huge), P, P, P, 2, None, P, 64,
+                               None) == UNS
+    # finite, but not times log2(e), which the kernels take the scores times
+    assert attention(lib, scale=3e38) == INV
+
+
+@pytest.mark.parametrize("x,want", [(5, 5), (0, 0), (-3, -1), (2 ** 31 - 1, 2 ** 31 - 1),
+                                    (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1), (-2 ** 40, -1)])
+def test_the_bindings_integers_do_not_wrap(x, want):
+    from speculative_decoding_verification_temp_gb300 import cache as binding
+    assert binding._c_int(x) == want
+
+
+def test_the_binding_refuses_shapes_beyond_32_bits():
+    from speculative_decoding_verification_temp_gb300 import cache as binding
+    dev = torch.device("meta")
+    wide = torch.empty(1, 2 ** 31, dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError):
+        binding._table(wide, 1, dev)
+    with pytest.raises(ValueError):
+        binding._sizes((2 ** 32 + 1, 16, 2, 64))

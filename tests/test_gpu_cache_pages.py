@@ -383,3 +383,126 @@ def test_decode_steps_together():
     assert int(ctx[4]) > 0
     assert not sv.cache_resize(pool, torch.zeros_like(ctx), page).any()
     assert int(pool.free_count) == 60 and not pool.ref_count.any()
+
+
+def test_a_captured_step_follows_its_inputs():
+    """Pages, append, attention, compaction and pages given back, captured
+    together and replayed over other lengths and paths, against the same calls
+    outside a graph."""
+    B, N, H, D, page, pages, width = 3, 6, 2, 64, 16, 64, 8
+    gen = torch.Generator("cuda")
+    gen.manual_seed(11)
+    dt = torch.bfloat16
+    new = [torch.randn(2, B, N, H, D, generator=gen, device="cuda").to(dt) for _ in "kv"]
+    q = torch.randn(B, N, 4 * H, D, generator=gen, device="cuda").to(dt)
+    parent = gpu(np.tile(np.array([-1, 0, 0, 1, 2, 4], np.int32), (B, 1)))
+    mask = sv.tree_mask(parent, max_depth=8).mask
+    ctx, path, taken = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((B,), (B, N), (B,)))
+    start = [torch.randn(2, pages, page, H, D, generator=gen, device="cuda").to(dt) for _ in "kv"]
+
+    def state():
+        return sv.page_pool(B, width, pages), [x.clone() for x in start]
+
+    def step(pool, kv):
+        f0 = sv.cache_resize(pool, ctx + N, page)
+        sv.cache_append(*new, *kv, pool.page_table, ctx)
+        outs = [sv.paged_attention(q, kv[0][i], kv[1][i], pool.page_table, ctx, tree_mask=mask).out
+                for i in range(2)]
+        kept = sv.cache_compact(*kv, pool.page_table, ctx, path, taken)
+        f1 = sv.cache_resize(pool, kept.context_len, page)
+        return [*outs, kept.context_len, kept.flags, f0, f1]
+
+    (pool_a, kv_a), (pool_b, kv_b) = state(), state()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = step(pool_a, kv_a)
+    cases = [([0, 0, 0], [[0, 1, 3, -1, -1, -1], [0, 2, 4, 5, -1, -1], [0, -1, -1, -1, -1, -1]], [2, 3, 0]),
+             ([3, 4, 1], [[0, 2, -1, -1, -1, -1], [0, -1, -1, -1, -1, -1], [0, 2, 4, 5, -1, -1]], [1, -1, 3]),
+             ([100, 17, 5], [[0, 2, 4, 5, -1, -1], [0, 1, -1, -1, -1, -1], [0, 1, 3, -1, -1, -1]], [3, 1, 2]),
+             ([90, 0, 122], [[0, 2, 4, -1, -1, -1], [0, 1, 3, -1, -1, -1], [0, 2, 4, 5, -1, -1]], [2, 2, 3])]
+    for lengths, nodes, accepted in cases:
+        ctx.copy_(torch.tensor(lengths, dtype=torch.int32))
+        path.copy_(torch.tensor(nodes, dtype=torch.int32))
+        taken.copy_(torch.tensor(accepted, dtype=torch.int32))
+        graph.replay()
+        want = step(pool_b, kv_b)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        for x, y in zip([*pool_a, *map(bits, kv_a)], [*pool_b, *map(bits, kv_b)]):
+            assert torch.equal(x, y)
+        assert not got[3].any() and not got[4].any() and not got[5].any()
+        for x, y, t in zip(got[2].tolist(), lengths, accepted):
+            assert x == y + t + 1
+
+
+def test_a_shortened_sequence_goes_on_from_a_fork():
+    """Appending behind a length inside a shared page would write the other
+    holder's tokens; a fork at the shorter length has a page of its own there."""
+    B, H, D, page, pages = 4, 2, 64, 16, 32
+    gen = torch.Generator("cuda")
+    gen.manual_seed(12)
+    dt = torch.bfloat16
+    kv = [torch.randn(pages, page, H, D, generator=gen, device="cuda").to(dt) for _ in "kv"]
+    new = [torch.randn(B, 5, H, D, generator=gen, device="cuda").to(dt) for _ in "kv"]
+    pool = sv.page_pool(B, 8, pages)
+    ctx = gpu(np.array([32, 0, 0, 0], np.int32))
+    assert not sv.cache_resize(pool, ctx, page).any()
+
+    def row(b, n):
+        return [x[pool.page_table[b].clamp(min=0).long()].flatten(0, 1)[:n].clone() for x in kv]
+
+    first = row(0, 32)
+    assert not sv.cache_fork(pool, *kv, ctx, gpu(np.array([0], np.int32)), gpu(np.array([1], np.int32))).any()
+    ctx[1] = 20
+    assert not sv.cache_fork(pool, *kv, ctx, gpu(np.array([1], np.int32)), gpu(np.array([2], np.int32))).any()
+    assert ctx.tolist() == [32, 20, 20, 0]
+    ctx[1] = 0
+    assert not sv.cache_resize(pool, ctx, page).any()
+    num = gpu(np.array([0, 0, 5, 0], np.int32))
+    assert not sv.cache_resize(pool, ctx + num, page).any()
+    assert not sv.cache_append(*new, *kv, pool.page_table, ctx, num_new=num, return_flags=True).any()
+    torch.cuda.synchronize()
+    table = pool.page_table.tolist()
+    assert table[0][0] == table[2][0] and table[0][1] != table[2][1]
+    for x, y in zip(row(0, 32), first):
+        assert torch.equal(bits(x), bits(y))
+    for x, y, z in zip(row(2, 25), first, new):
+        assert torch.equal(bits(x[:20]), bits(y[:20])) and torch.equal(bits(x[20:]), bits(z[2]))
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    """Nothing is set up, loaded or told to the driver before the capture."""
+    import os
+    import subprocess
+    import sys
+    script = """
+import torch, speculative_decoding_verification_temp_gb300 as sv
+cases = []
+for dt, N, D in ((torch.bfloat16, 1, 128), (torch.float16, 9, 64), (torch.bfloat16, 70, 128), (torch.float32, 3, 64),
+                 (torch.bfloat16, 2, 96)):
+    g = torch.Generator("cuda"); g.manual_seed(N)
+    k, v = (torch.randn(20, 16, 2, D, generator=g, device="cuda").to(dt) for _ in "kv")
+    q = torch.randn(2, N, 8, D, generator=g, device="cuda").to(dt)
+    cases.append((q, k, v, torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10),
+                  torch.tensor([5, 60], dtype=torch.int32, device="cuda")))
+pool = sv.page_pool(2, 4, 8)
+ctx = torch.tensor([20, 0], dtype=torch.int32, device="cuda")
+kv = [torch.randn(8, 16, 2, 64, device="cuda") for _ in "kv"]
+src, dst = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (0, 1))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = [sv.paged_attention(*c).out for c in cases]
+    flags = sv.cache_resize(pool, ctx, 16), sv.cache_fork(pool, *kv, ctx, src, dst)
+graph.replay()
+torch.cuda.synchronize()
+for x, c in zip(got, cases):
+    assert torch.equal(x, sv.paged_attention(*c).out)
+assert not any(f.any() for f in flags) and ctx.tolist() == [20, 20]
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "captured" in done.stdout, done.stderr[-2000:]

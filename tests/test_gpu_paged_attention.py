@@ -440,3 +440,23 @@ def test_trees_of_several_row_tiles(Hq, Hkv, D):
     again = s.call(tree_mask=s.dev(mask_words(sees)))
     for b, n in enumerate(n_new):
         assert torch.equal(res.out[b, :n], again.out[b, :n])
+
+
+def test_integers_beyond_32_bits_and_outputs_with_gradients():
+    gen = torch.Generator("cuda")
+    gen.manual_seed(5)
+    k, v = (torch.randn(8, 16, 2, 64, generator=gen, device="cuda") for _ in "kv")
+    q = torch.randn(1, 2, 4, 64, generator=gen, device="cuda")
+    args = (q, k, v, torch.arange(8, dtype=torch.int32, device="cuda")[None],
+            torch.tensor([100], dtype=torch.int32, device="cuda"))
+    plain = sv.paged_attention(*args).out
+    assert torch.equal(sv.paged_attention(*args, window=2 ** 32 + 5).out, plain)
+    assert torch.equal(sv.paged_attention(*args, window=8, sinks=2 ** 32 + 1).out, plain)
+    assert torch.equal(sv.paged_attention(*args, window=-2 ** 32 + 5).out, plain)
+    with pytest.raises(Exception):
+        sv.paged_attention(*args, window=8, sinks=-2 ** 32)
+    pool = sv.page_pool(1, 8, 8)
+    with pytest.raises(Exception):
+        sv.cache_resize(pool, args[4], 2 ** 32 + 16)
+    with pytest.raises(ValueError):
+        sv.paged_attention(*args, out=torch.empty_like(q, requires_grad=True))

@@ -505,7 +505,8 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  * weights are rounded to the cache's type before they meet the values.  float32
  * caches are computed in float32.  1 <= N <= 4096.  workspace: 32-byte aligned.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (a head_dim, alignment or
- * stride not listed above) before any launch.  B = 0 is a no-op.  Two launches. */
+ * stride not listed above) before any launch.  B = 0 is a no-op.  Two launches, or
+ * one where the page table or the window keeps the key ranges short. */
 spec_status spec_paged_attention(
     const void *q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
     int num_q_heads, spec_kv_cache cache, spec_page_table pages, const int32_t *context_len,

@@ -789,19 +789,28 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 
 struct AttnPlan {
   int workers, rows, tile_log2, unit_cost;
+  // Units of at most so many tiles are not cut: one launch for two (4.4 us of the
+  // caller's time) and no join (3 to 5 us), against tiles that follow each other on
+  // one worker.  From both forms at B = 1, 16 and 64 over 32 to 8192 keys, contexts of
+  // one length and of 1/16 of it upwards, us cut and whole: one token of 32 heads of
+  // 128 on 8, 512 keys 12.0, 12.4 (B = 1) and 36.2, 30.8 (B = 64), 1024 keys 12.6, 16.7
+  // and 56, 51, ragged 39, 43; trees of 60 nodes, 1024 keys 26, 24 (B = 1) and 40, 27
+  // (B = 16), 2048 keys 36, 37 and 61, 44, 4096 keys 37, 62.  Borders that move to the
+  // ends of longer units did not pay.
+  int few;
 };
 
 constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
 
 AttnPlan narrow_plan(int D, int dtype) {
   if (dtype == SPEC_F32) {
-    if (D <= 64) return {Rows8<64>::kCtas * kSms, 8, log2_of(Rows8<64>::kTile), 1};
-    if (D <= 128) return {Rows8<128>::kCtas * kSms, 8, log2_of(Rows8<128>::kTile), 1};
-    return {Rows8<256>::kCtas * kSms, 8, log2_of(Rows8<256>::kTile), 1};
+    if (D <= 64) return {Rows8<64>::kCtas * kSms, 8, log2_of(Rows8<64>::kTile), 1, 2};
+    if (D <= 128) return {Rows8<128>::kCtas * kSms, 8, log2_of(Rows8<128>::kTile), 1, 2};
+    return {Rows8<256>::kCtas * kSms, 8, log2_of(Rows8<256>::kTile), 1, 2};
   }
-  if (D <= 64) return {2 * kSms, 16, log2_of(Rows16<64, 32, 3>::kTile), 1};
-  if (D <= 128) return {2 * kSms, 16, log2_of(Rows16<128, 16, 3>::kTile), 1};
-  return {kSms, 16, log2_of(Rows16<256, 16, 3>::kTile), 1};
+  if (D <= 64) return {2 * kSms, 16, log2_of(Rows16<64, 32, 3>::kTile), 1, 4};
+  if (D <= 128) return {2 * kSms, 16, log2_of(Rows16<128, 16, 3>::kTile), 1, 4};
+  return {kSms, 16, log2_of(Rows16<256, 16, 3>::kTile), 1, 2};
 }
 
 // Lines of 19 workers each at least; 152 are a multiple of 2, 4 and 8.
@@ -817,8 +826,8 @@ bool wide_sizes(int G, int D, int dtype) {
 // times the median), single ones 1 at head_dim 128, where HBM hides it, and 2 at
 // 64.
 AttnPlan wide_plan(int N, int G, int D) {
-  if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 7, 8};
-  return {2 * kSms, wide_tile_rows(G), 7, D == 64 ? 2 : 1};
+  if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 7, 8, 16};
+  return {2 * kSms, wide_tile_rows(G), 7, D == 64 ? 2 : 1, N * G <= 32 ? 4 : 6};
 }
 
 template <auto kKernel>
@@ -832,6 +841,18 @@ cudaError_t start16(const AttnParams &p, cudaStream_t stream) {
   if (p.D <= 64) return start<rows16_kernel<E, 64, 32, 3>>(Rows16<64, 32, 3>::kSmem, p, stream);
   if (p.D <= 128) return start<rows16_kernel<E, 128, 16, 3>>(Rows16<128, 16, 3>::kSmem, p, stream);
   return start<rows16_kernel<E, 256, 16, 3>>(Rows16<256, 16, 3>::kSmem, p, stream);
+}
+
+// Whether units are not cut: the width of the page table, or the window, bounds
+// their tiles by `few`.  The lengths themselves are known on the device alone.
+bool whole_units(const AttnParams &p, int few) {
+  const int log2 = p.tile_log2, round = (1 << log2) - 1;
+  long long tiles = (static_cast<long long>(p.S.max_pages) * p.C.page_size + round) >> log2;
+  if (p.window) {
+    const long long sinks = std::min((static_cast<long long>(p.sinks) + round) >> log2, tiles);
+    tiles = std::min(tiles, sinks + ((static_cast<long long>(p.window) + p.S.N) >> log2) + 2);
+  }
+  return tiles <= few;
 }
 
 size_t align32(size_t x) { return (x + 31) / 32 * 32; }
@@ -856,6 +877,7 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
     p.rows = plan.rows;
     p.tile_log2 = plan.tile_log2;
     p.unit_cost = plan.unit_cost;
+    p.whole = whole_units(p, plan.few);
     p.row_lines = 1;
   };
   WideMaps maps;
@@ -885,7 +907,7 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
   } else {
     e = dtype == SPEC_BF16 ? start16<Bf16>(p, stream) : start16<F16>(p, stream);
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   const dim3 grid(p.workers, std::min(8, std::min(p.rows, p.S.N * p.G)));
   if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinThreads, 0, stream, p);
   if (dtype == SPEC_BF16)

@@ -15,6 +15,10 @@
 // on the device from the lengths, so a captured launch follows lengths that
 // change.
 //
+// A piece costs beside its keys what a unit does, and the join besides.  Where the
+// page table or the window keeps all units short (`whole`), a worker takes the whole
+// of those that begin in its run, and there is no join.
+//
 // Where a sequence has several row tiles with the same keys (row_lines of them),
 // each has a line and an equal share of the workers of its own: neighbouring
 // workers then go through the same keys at the same time, and HBM is read once
@@ -50,6 +54,7 @@ struct AttnParams {
   int workers, rows, tile_log2;  // at most; R; T as a power of two
   int unit_cost;                 // places on the line behind a unit's key tiles
   int row_lines;                 // 1: all row tiles on one line
+  bool whole;                    // units are not cut, and not joined
 };
 
 // A cut unit, written by the worker that holds its first cut; its pieces are
@@ -251,9 +256,13 @@ struct UnitWalk {
       left -= k.count + p.unit_cost;
     }
     a = L.w0 - left;
-    i0 = static_cast<int>(left);
-    i1 = static_cast<int>(min(static_cast<long long>(k.count), L.w1 - a));
+    i0 = static_cast<int>(p.whole && left > 0 ? k.count : left);
+    i1 = end_of(p, L);
     return i0 < i1 || next(p, L);
+  }
+  // The run's end in the unit.
+  __device__ __forceinline__ int end_of(const AttnParams &p, const Line &L) const {
+    return p.whole ? k.count : static_cast<int>(min(static_cast<long long>(k.count), L.w1 - a));
   }
   // The next unit; false: the run ends before it.
   __device__ __forceinline__ bool next(const AttnParams &p, const Line &L) {
@@ -272,7 +281,7 @@ struct UnitWalk {
     }
     k = key_range(p, k.ctx, k.n_new, fits, r0);
     i0 = 0;
-    i1 = static_cast<int>(min(static_cast<long long>(k.count), L.w1 - a));
+    i1 = end_of(p, L);
     return true;
   }
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == k.count; }

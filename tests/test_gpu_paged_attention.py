@@ -460,3 +460,53 @@ def test_integers_beyond_32_bits_and_outputs_with_gradients():
         sv.cache_resize(pool, args[4], 2 ** 32 + 16)
     with pytest.raises(ValueError):
         sv.paged_attention(*args, out=torch.empty_like(q, requires_grad=True))
+
+
+# Tokens of the widest page table whose units are not cut, for each of KERNELS.
+WHOLE = [512, 512, 768, 768, 2048, 2048, 256, 256, 128, 128, 64, 32]
+
+
+@pytest.mark.parametrize("kernel,tokens", list(zip(KERNELS, WHOLE)))
+def test_units_whole_and_cut(kernel, tokens):
+    """The same call through a page table as wide as whole units allow, a page
+    wider, and one so wide that units are cut: NaN and infinities where no token
+    sees, rows that see nothing, sequences without new tokens."""
+    dtype, N, Hq, Hkv, D, page = kernel
+    rng = np.random.default_rng(31)
+    width = tokens // page
+    room = width * page - N
+    ctx = [room, 0, room - 1, room // 2, 1, room // 3, room]
+    B = len(ctx)
+    n_new = [N, N, N, max(N - 1, 0), N, 0, N]
+    s = Setup(31, ctx, N, Hq, Hkv, D, page, dtype, n_new=n_new, max_pages=width)
+    sees = rng.random((B, N, N)) < 0.7
+    sees[:, :, N // 2] = False
+    for b in range(B):
+        if n_new[b] > N // 2:
+            p, i = s.slot(b, ctx[b] + N // 2)
+            s.k[p, i], s.v[p, i] = math.nan, math.inf
+    position = rng.integers(0, N, (B, N))
+    table = s.table
+    for more in (0, 1, -(-9000 // page)):
+        s.table = np.concatenate([table, np.full((B, more), -1, np.int32)], 1)
+        s.check(s.call(tree_mask=s.dev(mask_words(sees))), sees=sees, label=f"{more} pages more")
+        kw = dict(window=max(tokens // 4, 1), sinks=3, position=position)
+        s.check(s.call(**(kw | {"tree_mask": s.dev(mask_words(sees)), "position": s.dev(position)})),
+                sees=sees, label=f"window, {more} pages more", **kw)
+    # a table of the captured call's width, whatever the lengths: the rows that
+    # see nothing are written too
+    s.ctx[:] = 0
+    none = np.zeros((B, N, N), bool)
+    res = s.call(tree_mask=s.dev(mask_words(none)))
+    s.check(res, sees=none)
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D,page", KERNELS)
+def test_more_whole_units_than_ctas(dtype, N, Hq, Hkv, D, page):
+    rng = np.random.default_rng(32)
+    B = 60 if N >= 40 else 500
+    width = -(-(N + 30) // page)
+    s = Setup(32, rng.integers(0, width * page - N + 1, B), N, Hq, Hkv, D, page, dtype,
+              n_new=rng.integers(0, N + 1, B), max_pages=width)
+    s.check(s.call())
+    s.check(s.call(window=9, sinks=2), window=9, sinks=2)

@@ -1,14 +1,14 @@
 // Attention over a paged cache where the tensor-memory kernels do not apply: 16
 // rows of 16-bit types per unit on warp-level matrix instructions (head_dim other
-// than 64 and 128, pages that are no power of two of 8 to 128 tokens nor a
-// multiple of 128, more than 128 query heads to one), 8 rows of float32 on the FMA
-// pipes; and the join of the pieces of cut units.
+// than 64 and 128, pages that are no multiple of 8 tokens, more than 128 query heads
+// to one), 8 rows of float32 on the FMA pipes; and the join of the pieces of cut
+// units.
 //
 // Each row tile reads its keys and values once.  16-bit, 256 sequences of 1 to
-// 4096 tokens, one token each, 32 query heads on 8 of 128, bound by HBM: 365 us
-// (5.9 TB/s) with pages of 24 tokens, where the tensor-memory kernels take 333 us
-// with pages of 16; many rows are bound by the row tiles' re-reading: 32 trees of
-// 60 nodes 1033 us against 110.
+// 4096 tokens, one token each, 32 query heads on 8 of 128, bound by HBM: 363 us
+// (5.9 TB/s) with pages of 20 tokens, where the tensor-memory kernels take 348 us
+// with pages of 16 (first calls after other work); many rows are bound by the row
+// tiles' re-reading: 32 trees of 60 nodes 1035 us against 115.
 //
 // In both kernels each of the four warps of a CTA streams its own quarter of
 // each key tile through a ring of its own in shared memory (cp.async, 16 bytes
@@ -881,7 +881,7 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
     p.row_lines = 1;
   };
   WideMaps maps;
-  bool wide = wide_sizes(p.G, p.D, dtype) && (P % 128 == 0 || (P >= 8 && 128 % P == 0));
+  bool wide = wide_sizes(p.G, p.D, dtype) && P % 8 == 0;
   if (wide) {
     take(wide_plan(p.S.N, p.G, p.D));
     // row tiles of a tree see the same keys; those of a chain end at their own

@@ -1,5 +1,5 @@
 // Attention over a paged cache on the fifth-generation tensor cores: 16-bit
-// types, head_dim 64 or 128, pages of 8, 16, 32, 64 or a multiple of 128 tokens,
+// types, head_dim 64 or 128, pages of a multiple of 8 tokens,
 // rows in tiles of at most 128 (new tokens times the query heads of a group).
 //
 // For a tile of 128 keys a stream of work computes S = Q K^T into tensor memory
@@ -16,8 +16,8 @@
 //   pair_kernel  units of two row tiles, one per stream, that share the keys and
 //                values
 //
-// Keys and values come by TMA, one box per page, into a ring of entries of 128
-// rows; every hand-over is an mbarrier, every wait is bounded.  Shared rows are
+// Keys and values come by TMA, one box per page or part of one, into a ring of
+// entries of 128 rows; every hand-over is an mbarrier, every wait is bounded.  Shared rows are
 // 128-byte pieces in the 128-byte swizzle.  An entry of keys or values is groups
 // of eight tokens, each with its panels of 64 elements one behind another, so
 // that one box holds a page whole whatever its size; rows of K are K-major for
@@ -37,7 +37,8 @@
 // trees at B = 16, 64 query heads on 8 of 128 bf16, contexts of 1000 to 8192 tokens:
 // 530 us, 1.16 PFLOP/s.  Measured and not kept: scores in halves of 64 keys with two
 // buffers (710 us: 52 cycles a step of 64 keys make the products the bound) and two
-// warps per row (671 us), when this took 645.
+// warps per row (671 us), when this took 645; waits that suspend (566 us) or only
+// poll (566), and ends of units stored by quads in whole lines (554), against 530.
 #include <climits>
 #include <numeric>
 
@@ -704,7 +705,17 @@ __device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk 
   return true;
 }
 
-// The boxes of a tile of keys or values, one per page and lane.
+// Tokens of a box: the largest power of two, up to a tile, that divides the page
+// size.  A tile begins at a multiple of it, so a box never leaves its page.  (32 trees
+// of 60 nodes on pages of 24 tokens, 16 boxes of 8 a tile: 115 us, 110 on pages of 64
+// and 1031 in rows16_kernel; one token within windows there 58 us, 54 in
+// rows16_kernel, on pages of 16 45.)
+__host__ __device__ __forceinline__ int box_tokens(int page_size) {
+  const int two = page_size & -page_size;
+  return two < kTileKeys ? two : kTileKeys;
+}
+
+// The boxes of a tile of keys or values, one per lane.
 struct BoxLoader {
   const CUtensorMap *map;
   int unit_page, unit_head, unit_token;
@@ -715,7 +726,7 @@ struct BoxLoader {
     unit_page = values ? maps.v_page : maps.k_page;
     unit_head = values ? maps.v_head : maps.k_head;
     unit_token = values ? maps.v_token : maps.k_token;
-    box = min(p.C.page_size, kTileKeys);
+    box = box_tokens(p.C.page_size);
     boxes = kTileKeys / box;
     shift = 31 - __clz(box);
   }
@@ -725,7 +736,7 @@ struct BoxLoader {
     if (lane >= boxes || i >= u.i1 - u.i0 || at >= u.k.end) return -1;
     // between the sinks and the window
     if (at >= p.sinks && at + box <= u.k.first) return -1;
-    return page_at(p.S, u.b, p.C.page_size <= kTileKeys ? at >> shift : at / p.C.page_size);
+    return page_at(p.S, u.b, p.C.page_size == box ? at >> shift : at / p.C.page_size);
   }
   // Which of the 32 tokens from 32 * j of the tile at at0 on are copied.
   __device__ __forceinline__ uint32_t valid_word(const UnitWalk &u, uint32_t pages, int at0,
@@ -746,7 +757,7 @@ struct BoxLoader {
     if (lane == 0) bar_expect(full, __popc(pages) * box * W::kRow * W::kPanels);
     __syncwarp();
     if ((pages >> lane) & 1u) {
-      const int token = p.C.page_size <= kTileKeys ? 0 : at0 % p.C.page_size;
+      const int token = p.C.page_size == box ? 0 : (at0 + lane * box) % p.C.page_size;
       box_load(entry + lane * (box >> 3) * W::kGroup, map, full, 0, 0, 0, 0,
                page_id * unit_page + u.h * unit_head + token * unit_token);
     }
@@ -1346,19 +1357,19 @@ bool origin(Origin *o, const long long (&strides)[3], const long long (&sizes)[3
 }
 
 // One layer's keys or values: [64 elements, 8 tokens, panels, groups of 8
-// tokens, origin]; a box is the tokens of a page, at most 128.
+// tokens, origin]; a box is box_tokens() of a page.
 bool cache_map(CUtensorMap *map, Origin *o, int dtype, const KvCache &C, int D, const char *base,
                long long page, long long token, long long head) {
   const long long strides[3] = {page, head, token};
-  const long long sizes[3] = {C.pages, C.heads, C.page_size > kTileKeys ? C.page_size : 1};
+  const int tokens = box_tokens(C.page_size);
+  const long long sizes[3] = {C.pages, C.heads, C.page_size > tokens ? C.page_size : 1};
   if (!origin(o, strides, sizes)) return false;
-  const int box_tokens = C.page_size < kTileKeys ? C.page_size : kTileKeys;
   const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(D / 64),
-                              static_cast<cuuint64_t>(box_tokens / 8),
+                              static_cast<cuuint64_t>(tokens / 8),
                               static_cast<cuuint64_t>(o->count)};
   const long long steps[4] = {token, 128, 8 * token, o->step};
   const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(D / 64),
-                             static_cast<cuuint32_t>(box_tokens / 8), 1};
+                             static_cast<cuuint32_t>(tokens / 8), 1};
   return encode_map(map, dtype, base, dims, steps, box);
 }
 

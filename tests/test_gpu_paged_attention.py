@@ -326,7 +326,7 @@ def test_long_chains_from_an_empty_cache():
     s.check(s.call())
 
 
-# bf16 and f16 at head_dim 64 and 128 with pages of 8..128 tokens take the tensor
+# bf16 and f16 at head_dim 64 and 128 with pages of 8 n tokens take the tensor
 # memory kernels, other sizes the matrix kernel, float32 the FMA kernel; up to 32
 # rows (new tokens times query heads per head) are split over lane quarters, up to
 # 128 are a row tile, more are pairs of row tiles.
@@ -510,3 +510,16 @@ def test_more_whole_units_than_ctas(dtype, N, Hq, Hkv, D, page):
               n_new=rng.integers(0, N + 1, B), max_pages=width)
     s.check(s.call())
     s.check(s.call(window=9, sinks=2), window=9, sinks=2)
+
+
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "pairs"])
+@pytest.mark.parametrize("page", [12, 24, 40, 48, 96, 136, 200, 320])
+@pytest.mark.parametrize("N,D", [(1, 128), (9, 64), (20, 128), (70, 64)])
+def test_pages_of_any_multiple_of_eight(N, D, page, layout):
+    """Pages that end inside tiles; one page of each table is bad."""
+    s = Setup(33, [0, 7, page - 1, page, 3 * page + 5, 1000, 511], N, 8, 2, D, page, "bf16", layout=layout)
+    s.table[4, 1] = -1
+    res = s.call()
+    s.check(res)
+    assert res.flags.tolist() == [0, 0, 0, 0, sv.FLAG_BAD_PAGE, 0, 0]
+    s.check(s.call(window=150, sinks=5), window=150, sinks=5)

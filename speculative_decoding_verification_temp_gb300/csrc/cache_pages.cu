@@ -8,7 +8,9 @@
 // layers of 32 x 60 tokens, 8 heads of 128 bf16: 72.5 us, 503 MB, 6.9 TB/s; copy
 // of 64 partly filled pages of 64 tokens in 32 layers: 71 us).  Resize and the
 // fork's bookkeeping are one CTA each, bound by the latency of their few dependent
-// global accesses (5 to 9 us); they take and give pages in a fixed order, so their
+// global accesses (32 sequences that take and give back 60 tokens on pages of 16: 10
+// us for both, 13 with the claims below made always; 256 sequences 30 and 63); they
+// take and give pages in a fixed order, so their
 // results do not depend on the order in which threads run.
 #include <climits>
 
@@ -261,9 +263,9 @@ cudaError_t launch_compact(const KvSeqs &S, const KvCache &C, const int32_t *pat
 
 // One CTA.  Releases first: a reference less for each released entry; a page
 // left without references is pushed at its first mention in the order of
-// (sequence, entry).  That mention is found with an atomicMin of the mention's
-// number, offset below every count, on the page's own count, so no scratch is
-// needed.  Then the growing sequences pop theirs in ascending order, as long
+// (sequence, entry).  Where a page had several holders, that mention is found with an
+// atomicMin of the mention's number, offset below every count, on the page's own
+// count, so no scratch is needed.  Then the growing sequences pop theirs in ascending order, as long
 // as the pool holds the demand of them and of all before them.
 __global__ void __launch_bounds__(kPool, 1)
     resize_kernel(Pool P, const int32_t *length, uint32_t *flags) {
@@ -302,47 +304,61 @@ __global__ void __launch_bounds__(kPool, 1)
   __syncthreads();
   int filled = top;
   if (released > 0) {  // the same for every thread
+    int *freed_s = reinterpret_cast<int *>(flag_s + P.B);
+    int shared = 0;
     for (int b = warp; b < P.B; b += kPool / 32) {
       const int need = need_s[b], have = have_s[b];
-      int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
+      const int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
       bool bad = false;
-      for (int i = need + lane; i < have; i += 32) {
-        const int page = row[i];
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(P.pages) ||
-            atomicSub(P.refs + page, 1) <= 0)
-          bad = true;
-      }
-      if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) flag_s[b] |= SPEC_FLAG_BAD_PAGE;
-    }
-    __syncthreads();
-    for (int b = warp; b < P.B; b += kPool / 32) {
-      const int need = need_s[b], have = have_s[b], base = at_s[b];
-      const int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
-      for (int i = need + lane; i < have; i += 32) {
-        const int page = row[i];
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(P.pages)) continue;
-        const int refs = __ldcg(P.refs + page);
-        if (refs == 0 || refs < kClaim) atomicMin(P.refs + page, INT_MIN + base + i - need);
-      }
-    }
-    __syncthreads();
-    // pages freed by each sequence, then by those before it
-    auto mine = [&](int page, int mention) {
-      return static_cast<unsigned>(page) < static_cast<unsigned>(P.pages) &&
-             __ldcg(P.refs + page) == INT_MIN + mention;
-    };
-    int *freed_s = reinterpret_cast<int *>(flag_s + P.B);
-    for (int b = warp; b < P.B; b += kPool / 32) {
-      const int need = need_s[b], have = have_s[b], base = at_s[b];
-      const int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
       int n = 0;
       for (int i0 = need; i0 < have; i0 += 32) {
-        const int i = i0 + lane;
-        n += __popc(__ballot_sync(0xFFFFFFFFu, i < have && mine(row[i], base + i - need)));
+        const int i = i0 + lane, page = i < have ? row[i] : -1;
+        const bool good = static_cast<unsigned>(page) < static_cast<unsigned>(P.pages);
+        const int held = good ? atomicSub(P.refs + page, 1) : 0;
+        bad |= i < have && held <= 0;
+        shared |= good && held != 1;
+        n += __popc(__ballot_sync(0xFFFFFFFFu, held == 1));
       }
-      if (lane == 0) freed_s[b] = n;
+      bad = __any_sync(0xFFFFFFFFu, bad);
+      if (lane == 0) {
+        if (bad) flag_s[b] |= SPEC_FLAG_BAD_PAGE;
+        freed_s[b] = n;
+      }
     }
-    __syncthreads();
+    // where every mention found one holder, every page was mentioned once and is
+    // free now: there is nothing to claim
+    const bool claims = __syncthreads_or(shared);
+    // whether this mention frees the page
+    auto mine = [&](int page, int mention) {
+      return static_cast<unsigned>(page) < static_cast<unsigned>(P.pages) &&
+             (!claims || __ldcg(P.refs + page) == INT_MIN + mention);
+    };
+    if (claims) {
+      for (int b = warp; b < P.B; b += kPool / 32) {
+        const int need = need_s[b], have = have_s[b], base = at_s[b];
+        const int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
+        for (int i = need + lane; i < have; i += 32) {
+          const int page = row[i];
+          if (static_cast<unsigned>(page) >= static_cast<unsigned>(P.pages)) continue;
+          const int refs = __ldcg(P.refs + page);
+          if (refs == 0 || refs < kClaim) atomicMin(P.refs + page, INT_MIN + base + i - need);
+        }
+      }
+      __syncthreads();
+      // pages freed by each sequence
+      for (int b = warp; b < P.B; b += kPool / 32) {
+        const int need = need_s[b], have = have_s[b], base = at_s[b];
+        const int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
+        int n = 0;
+        for (int i0 = need; i0 < have; i0 += 32) {
+          const int i = i0 + lane;
+          n += __popc(__ballot_sync(0xFFFFFFFFu, i < have && mine(row[i], base + i - need)));
+        }
+        if (lane == 0) freed_s[b] = n;
+      }
+      __syncthreads();
+    }
+    // ... and by those before it
     int freed = 0;
     for (int b0 = 0; b0 < P.B; b0 += kPool) {
       const int b = b0 + tid, n = b < P.B ? freed_s[b] : 0;
@@ -367,18 +383,21 @@ __global__ void __launch_bounds__(kPool, 1)
           if (p < P.pages) P.free_list[p] = page;
         }
         place += __popc(who);
+        if (!claims && i < have) row[i] = -1;
       }
     }
     __syncthreads();
-    for (int b = warp; b < P.B; b += kPool / 32) {
-      const int need = need_s[b], have = have_s[b];
-      int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
-      for (int i = need + lane; i < have; i += 32) {
-        const int page = row[i];
-        if (static_cast<unsigned>(page) < static_cast<unsigned>(P.pages) &&
-            __ldcg(P.refs + page) < kClaim)
-          P.refs[page] = 0;  // every mention of the page writes the same value
-        row[i] = -1;
+    if (claims) {
+      for (int b = warp; b < P.B; b += kPool / 32) {
+        const int need = need_s[b], have = have_s[b];
+        int32_t *row = P.table + static_cast<long long>(b) * P.ld_table;
+        for (int i = need + lane; i < have; i += 32) {
+          const int page = row[i];
+          if (static_cast<unsigned>(page) < static_cast<unsigned>(P.pages) &&
+              __ldcg(P.refs + page) < kClaim)
+            P.refs[page] = 0;  // every mention of the page writes the same value
+          row[i] = -1;
+        }
       }
     }
     filled = min(top + freed, P.pages);

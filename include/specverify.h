@@ -481,7 +481,9 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  * place(key) < sinks; the place of a context token is its index, that of new
  * token m is context_len[b] + position[b,m] (its depth; without position: m).
  * A token that sees no key has out 0 and out_lse -infinity.  Keys and values
- * that a token does not see do not affect it, whatever they hold.
+ * that a token does not see do not affect it, whatever they hold.  A row with a
+ * score of NaN or +infinity has out and out_lse NaN; a value that is not finite
+ * makes its dimension of the rows that see it an infinity or NaN.
  *
  * q [B, N, num_q_heads, head_dim] of the cache's dtype, strides in elements,
  *    16-byte aligned as the cache.  num_q_heads: a multiple of cache.num_heads.

@@ -66,7 +66,9 @@ __device__ __forceinline__ void mma<F16>(float (&c)[4], const uint32_t (&a)[4], 
 
 // Adds the warps' results of a unit (o_s: each warp's R x DP outputs at
 // warp_floats apart; ml_s: m and l of each warp's rows) and writes the unit's
-// rows, or its piece of them.
+// rows, or its piece of them.  Here and in the other merges a part is empty where
+// its l is zero: the maximum takes no NaN, so a part whose scores are all NaN has m
+// -infinity as an empty one has, and l NaN, which reaches the row.
 template <class TE, int R, int DP, int kSlice>
 __device__ __forceinline__ void write_unit(const AttnParams &p, const UnitWalk &u,
                                            const float *o_s, int warp_floats,
@@ -84,9 +86,8 @@ __device__ __forceinline__ void write_unit(const AttnParams &p, const UnitWalk &
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
-      const float m = ml_s[w][0][row];
-      if (m == -INFINITY) continue;
-      const float f = fast_exp2(m - M);
+      if (ml_s[w][1][row] == 0.f) continue;
+      const float f = fast_exp2(ml_s[w][0][row] - M);
       const float4 x = *reinterpret_cast<const float4 *>(o_s + w * warp_floats + row * DP + d);
       l += f * ml_s[w][1][row];
       o.x += f * x.x;
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (m[j][x] == -INFINITY) continue;
+          if (l[j][x] == 0.f) continue;
           f[x] = fast_exp2(m[j][x] - M);
           sum += f[x] * l[j][x];
           o.x += f[x] * v[j][x].x;
@@ -694,6 +695,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       for (int j = 0; j < 8; ++j) {
         const int i = i0 + j * step;
         m[j] = -INFINITY;
+        lp[j] = 0.f;
         if (i >= count) continue;
         const float *s = slot(i);
         m[j] = s[row];
@@ -715,7 +717,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       M = top;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (m[j] == -INFINITY) continue;
+        if (lp[j] == 0.f) continue;
         const float f = fast_exp2(m[j] - M);
         l += f * lp[j];
 #pragma unroll
@@ -765,7 +767,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (m_s[w] == -INFINITY) continue;
+        if (l_s[w] == 0.f) continue;
         const float f = fast_exp2(m_s[w] - M);
         l += f * l_s[w];
 #pragma unroll

@@ -5,8 +5,9 @@ A cache is a pair of tensors [num_pages, page_size, num_heads, head_dim] (one
 layer) or [num_layers, num_pages, page_size, num_heads, head_dim]; any strides
 whose last is 1 (a transposed [.., num_heads, page_size, head_dim] tensor, keys
 and values interleaved).  The calls run on torch's current stream of the
-cache's device.  They are forward operators: tensors that require gradients are
-refused while autograd records.
+cache's device.  Integer inputs may be of any integer type; values beyond 32 bits
+are flagged as any other bad page or length.  They are forward operators: tensors
+that require gradients are refused while autograd records.
 """
 
 import functools
@@ -51,6 +52,21 @@ def _forward_only(*tensors):
                 "the cache operators have no gradient: call them under torch.no_grad()")
 
 
+def _int32(x):
+    """x as int32.  What lies beyond that would wrap, and is taken as its largest
+    or smallest value: no page, length, node or sequence is that large, so the
+    operators flag it (and clamp num_new and position to their ranges)."""
+    if x.dtype == torch.uint64:
+        # as int64 the upper half is negative
+        x = x.view(torch.int64)
+        x = torch.where(x < 0, _INT_MAX, x)
+    elif x.dtype == torch.uint32:
+        x = x.to(torch.int64)
+    if x.dtype == torch.int64:
+        x = x.clamp(-_INT_MAX - 1, _INT_MAX)
+    return x.to(torch.int32)
+
+
 def _ints(x, shape, dev, name):
     """An int32 tensor of `shape` on dev, contiguous; another integer type is converted."""
     _on(x, dev, name)
@@ -59,7 +75,7 @@ def _ints(x, shape, dev, name):
     if x.dtype != torch.int32:
         if x.is_floating_point() or x.is_complex() or x.dtype == torch.bool:
             raise ValueError(f"{name} must hold integers")
-        x = x.to(torch.int32)
+        x = _int32(x)
     return x if x.is_contiguous() else x.contiguous()
 
 

@@ -203,3 +203,20 @@ def test_the_binding_refuses_shapes_beyond_32_bits():
         binding._table(wide, 1, dev)
     with pytest.raises(ValueError):
         binding._sizes((2 ** 32 + 1, 16, 2, 64))
+
+
+@pytest.mark.parametrize("dtype,values,want", [
+    (torch.int64, [5, -1, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 3, 2 ** 63 - 1, -2 ** 31 - 1, -2 ** 32 + 5],
+     [5, -1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, -2 ** 31, -2 ** 31]),
+    (torch.uint64, [5, 2 ** 32 + 3, 2 ** 63, 2 ** 64 - 1], [5] + 3 * [2 ** 31 - 1]),
+    (torch.uint32, [5, 2 ** 31 + 3, 2 ** 32 - 1], [5] + 2 * [2 ** 31 - 1]),
+    (torch.uint16, [5, 2 ** 16 - 1], [5, 2 ** 16 - 1]), (torch.int16, [5, -7], [5, -7]),
+    (torch.uint8, [5, 255], [5, 255])])
+def test_the_bindings_integer_tensors_do_not_wrap(dtype, values, want):
+    from speculative_decoding_verification_temp_gb300 import cache as binding
+    x = torch.tensor(values, dtype=dtype)
+    dev = torch.device("cpu")
+    got = binding._ints(x, x.shape, dev, "x")
+    assert got.dtype == torch.int32 and got.tolist() == want
+    got, table = binding._table(x[None], 1, dev)
+    assert got.dtype == torch.int32 and got.tolist() == [want] and table.max_pages == len(values)

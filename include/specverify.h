@@ -500,7 +500,9 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  *    aligned; does not overlap the span of q (SPEC_ERR_INVALID_ARG).  out_lse (nullable) float [B, N, num_q_heads]: ln sum_j w_j.
  * out_flags [B] (nullable): SPEC_FLAG_BAD_LENGTH (num_new outside [0, N], taken
  *    as clamped; or a sequence whose tokens do not fit its table row: its
- *    tokens see nothing), SPEC_FLAG_BAD_PAGE (its keys are not seen),
+ *    tokens see nothing), SPEC_FLAG_BAD_PAGE (its keys are not seen; a page whose
+ *    tokens all lie behind the sinks and before context_len[b] - window + 1 is not
+ *    looked at, and may have gone to another sequence),
  *    SPEC_FLAG_TIMEOUT (a bounded on-device wait gave up: the sequence's outputs
  *    are not to be used).  Costs a launch of its own.
  * Products of bf16 and f16 run on the tensor cores with float32 sums; the

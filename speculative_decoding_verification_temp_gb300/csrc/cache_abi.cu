@@ -202,7 +202,7 @@ spec_status spec_paged_attention(
   p.lse = out_lse;
   p.flags = out_flags;
   if (out_flags) {
-    const cudaError_t e = sv::launch_kv_flags(p.S, p.C, false, out_flags, st);
+    const cudaError_t e = sv::launch_kv_flags(p.S, p.C, false, p.window, p.sinks, out_flags, st);
     if (e != cudaSuccess) return map_cuda(e);
   }
   return map_cuda(sv::launch_attention(p, cache.dtype, workspace, st));

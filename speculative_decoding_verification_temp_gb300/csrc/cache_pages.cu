@@ -63,7 +63,7 @@ __device__ __forceinline__ int block_scan(int v, int *warp_s, int &total) {
 // ---------------------------------------------------------------------------
 
 __global__ void __launch_bounds__(kThreads)
-    kv_flags_kernel(KvSeqs S, KvCache C, bool new_only, uint32_t *flags) {
+    kv_flags_kernel(KvSeqs S, KvCache C, bool new_only, int window, int sinks, uint32_t *flags) {
   const int b = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= S.B) return;
   const int ctx = __ldg(S.ctx + b), n = seq_new(S, b);
@@ -74,16 +74,22 @@ __global__ void __launch_bounds__(kThreads)
   } else if (n > 0) {
     const int first = new_only ? ctx / C.page_size : 0;
     const int last = (ctx + n - 1) / C.page_size;
-    for (int i = first + lane; i <= last; i += 32)
+    // the first key that a window shows: no new token stands before ctx
+    const int shown = window ? ctx - window + 1 : 0;
+    for (int i = first + lane; i <= last; i += 32) {
+      const int at = i * C.page_size;
+      if (at >= sinks && at + C.page_size <= shown) continue;
       if (!page_ok(C, page_at(S, b, i))) f |= SPEC_FLAG_BAD_PAGE;
+    }
   }
   f = warp_or(f);
   if (lane == 0) flags[b] = f;
 }
 
-cudaError_t launch_kv_flags(const KvSeqs &S, const KvCache &C, bool new_only, uint32_t *flags,
-                            cudaStream_t stream) {
-  kv_flags_kernel<<<(S.B + kWarps - 1) / kWarps, kThreads, 0, stream>>>(S, C, new_only, flags);
+cudaError_t launch_kv_flags(const KvSeqs &S, const KvCache &C, bool new_only, int window, int sinks,
+                            uint32_t *flags, cudaStream_t stream) {
+  kv_flags_kernel<<<(S.B + kWarps - 1) / kWarps, kThreads, 0, stream>>>(S, C, new_only, window,
+                                                                         sinks, flags);
   return cudaGetLastError();
 }
 
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(KvSeqs S, KvCache C, N
 cudaError_t launch_append(const KvSeqs &S, const KvCache &C, const NewRows &R, uint32_t *flags,
                           cudaStream_t stream) {
   if (flags) {
-    const cudaError_t e = launch_kv_flags(S, C, true, flags, stream);
+    const cudaError_t e = launch_kv_flags(S, C, true, 0, 0, flags, stream);
     if (e != cudaSuccess) return e;
   }
   if (S.N == 0) return cudaSuccess;

@@ -62,10 +62,11 @@ __device__ __forceinline__ bool page_ok(const KvCache &C, int page) {
 
 // Flags of each sequence: SPEC_FLAG_BAD_LENGTH (num_new outside [0, N], or
 // tokens that do not fit the table row) and SPEC_FLAG_BAD_PAGE (a page id
-// outside the cache among the pages from token `first` on: all of them, or
-// those of the new tokens alone).  One launch.
-cudaError_t launch_kv_flags(const KvSeqs &S, const KvCache &C, bool new_only, uint32_t *flags,
-                            cudaStream_t stream);
+// outside the cache among the pages that are looked at: those of the new tokens
+// alone, or all but those behind the sinks that a window (0: none) hides from every
+// new token).  One launch.
+cudaError_t launch_kv_flags(const KvSeqs &S, const KvCache &C, bool new_only, int window, int sinks,
+                            uint32_t *flags, cudaStream_t stream);
 
 // Launch of a kernel with much dynamic shared memory.  It is allowed to use that
 // once per device (done: a bit each), since the call for it costs a good part of

@@ -23,8 +23,8 @@ cudaError_t launch_fork(const Pool &P, const KvCache &C, int32_t *ctx, const int
 
 namespace {
 
-constexpr int kMaxNew = 4096;
-constexpr int kMaxSeqs = 4096;  // of a pool, and of the forks of a call
+using sv::kMaxNew;
+using sv::kMaxSeqs;
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxPageSize = 65536;
 constexpr int kMaxRowsY = 65535;  // blockIdx.y
@@ -246,7 +246,7 @@ spec_status spec_cache_compact(spec_kv_cache cache, spec_page_table pages,
                                const int32_t *context_len, const int32_t *path, int width,
                                const int32_t *num_accepted, int B, int32_t *out_context_len,
                                uint32_t *out_flags, spec_stream_t stream) {
-  if (B < 0 || width < 1 || width > kMaxNew + 1) return SPEC_ERR_INVALID_ARG;
+  if (B < 0 || width < 1 || width > sv::kMaxPath) return SPEC_ERR_INVALID_ARG;
   if (B == 0) return SPEC_OK;
   if (const spec_status s = check_cache(cache); s != SPEC_OK) return s;
   if (!context_len || !path || !num_accepted || !out_context_len ||

@@ -21,6 +21,7 @@ namespace sv {
 namespace {
 
 constexpr int kPool = 1024;  // threads of the bookkeeping CTA
+constexpr int kPlainShared = 40 * 1024;  // dynamic shared memory that any kernel may use
 constexpr int kClaim = -(1 << 30);  // claims on a page are below, counts above
 
 __device__ __forceinline__ uint4 load16(const char *p) {
@@ -252,14 +253,14 @@ cudaError_t launch_compact(const KvSeqs &S, const KvCache &C, const int32_t *pat
   // a CTA no larger than a token's pieces
   const int per_token = C.heads * (C.row_bytes / 16);
   const int threads = per_token >= kThreads ? kThreads : (per_token + 31) / 32 * 32;
-  const size_t smem = static_cast<size_t>(width) * sizeof(Move);
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+  const dim3 grid(S.B, 2 * C.layers);
+  const int smem = width * static_cast<int>(sizeof(Move));
+  if (smem > kPlainShared) {
+    static std::atomic<uint64_t> done{0};
+    return launch_large(compact_kernel, done, kMaxPath * static_cast<int>(sizeof(Move)), grid, threads,
+                        smem, stream, S, C, path, width, accepted, out_len, flags);
   }
-  compact_kernel<<<dim3(S.B, 2 * C.layers), threads, smem, stream>>>(S, C, path, width, accepted,
-                                                                     out_len, flags);
+  compact_kernel<<<grid, threads, smem, stream>>>(S, C, path, width, accepted, out_len, flags);
   return cudaGetLastError();
 }
 
@@ -454,11 +455,12 @@ __global__ void __launch_bounds__(kPool, 1)
 
 cudaError_t launch_resize(const Pool &P, const int32_t *length, uint32_t *flags,
                           cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(P.B) * 5 * sizeof(int);
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+  constexpr int kPerSeq = 5 * static_cast<int>(sizeof(int));
+  const int smem = P.B * kPerSeq;
+  if (smem > kPlainShared) {
+    static std::atomic<uint64_t> done{0};
+    return launch_large(resize_kernel, done, kMaxSeqs * kPerSeq, 1, kPool, smem, stream, P, length,
+                        flags);
   }
   resize_kernel<<<1, kPool, smem, stream>>>(P, length, flags);
   return cudaGetLastError();
@@ -627,14 +629,17 @@ cudaError_t launch_fork(const Pool &P, const KvCache &C, int32_t *ctx, const int
                         const int32_t *dst, int F, void *workspace, uint32_t *flags,
                         cudaStream_t stream) {
   PageCopy *copies = static_cast<PageCopy *>(workspace);
-  const size_t smem = static_cast<size_t>(F) * 3 * sizeof(int);
-  if (smem > 40 * 1024) {
-    const cudaError_t a = cudaFuncSetAttribute(
-        fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (a != cudaSuccess) return a;
+  constexpr int kPerFork = 3 * static_cast<int>(sizeof(int));
+  const int smem = F * kPerFork;
+  cudaError_t e;
+  if (smem > kPlainShared) {
+    static std::atomic<uint64_t> done{0};
+    e = launch_large(fork_plan_kernel, done, kMaxSeqs * kPerFork, 1, kPool, smem, stream, P, ctx, src,
+                     dst, F, copies, flags);
+  } else {
+    fork_plan_kernel<<<1, kPool, smem, stream>>>(P, ctx, src, dst, F, copies, flags);
+    e = cudaGetLastError();
   }
-  fork_plan_kernel<<<1, kPool, smem, stream>>>(P, ctx, src, dst, F, copies, flags);
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_behind(page_copy_kernel, dim3(F, 2 * C.layers), kThreads, 0, stream, C,
                        static_cast<const PageCopy *>(copies));

@@ -8,6 +8,10 @@
 
 namespace sv {
 
+constexpr int kMaxNew = 4096;          // new tokens of a sequence in a call
+constexpr int kMaxPath = kMaxNew + 1;  // entries of an accepted path
+constexpr int kMaxSeqs = 4096;         // of a pool, and of the forks of a call
+
 // One layer's keys and values start at k and v; strides are in bytes.
 struct KvCache {
   char *k, *v;
@@ -68,12 +72,14 @@ __device__ __forceinline__ bool page_ok(const KvCache &C, int page) {
 cudaError_t launch_kv_flags(const KvSeqs &S, const KvCache &C, bool new_only, int window, int sinks,
                             uint32_t *flags, cudaStream_t stream);
 
-// Launch of a kernel with much dynamic shared memory.  It is allowed to use that
-// once per device (done: a bit each), since the call for it costs a good part of
-// a launch's host time; a context that has forgotten it is told again.
+// Launch of a kernel with much dynamic shared memory.  It is allowed the `most`
+// that any call of it uses once per device (done: a bit each): the call for it costs
+// a good part of a launch's host time, and a thread that allowed less for its own
+// call would have another's launch refused.  A context that has forgotten it is told
+// again.
 template <typename... KP, typename... A>
-cudaError_t launch_large(void (*kernel)(KP...), std::atomic<uint64_t> &done, int grid, int threads,
-                         int smem, cudaStream_t stream, const A &...args) {
+cudaError_t launch_large(void (*kernel)(KP...), std::atomic<uint64_t> &done, int most, dim3 grid,
+                         int threads, int smem, cudaStream_t stream, const A &...args) {
   int dev;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -81,7 +87,7 @@ cudaError_t launch_large(void (*kernel)(KP...), std::atomic<uint64_t> &done, int
   for (;;) {
     const bool told = (done.load(std::memory_order_relaxed) & bit) != 0;
     if (!told) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return e;
       done.fetch_or(bit, std::memory_order_relaxed);
     }

@@ -835,7 +835,8 @@ AttnPlan wide_plan(int N, int G, int D) {
 template <auto kKernel>
 cudaError_t start(size_t smem, const AttnParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  return launch_large(kKernel, done, p.workers, kAttnThreads, static_cast<int>(smem), stream, p);
+  return launch_large(kKernel, done, static_cast<int>(smem), p.workers, kAttnThreads,
+                      static_cast<int>(smem), stream, p);
 }
 
 template <class E>

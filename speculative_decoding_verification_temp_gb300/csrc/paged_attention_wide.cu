@@ -1381,7 +1381,7 @@ bool cache_map(CUtensorMap *map, Origin *o, int dtype, const KvCache &C, int D, 
 template <auto kKernel>
 cudaError_t start_wide(int smem, const AttnParams &p, const WideMaps &maps, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  return launch_large(kKernel, done, wide_ctas(p), kWideThreads, smem, stream, p, maps);
+  return launch_large(kKernel, done, smem, wide_ctas(p), kWideThreads, smem, stream, p, maps);
 }
 
 template <class E, int D>

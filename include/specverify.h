@@ -343,7 +343,11 @@ spec_status spec_set_profile_events(void *start_event, void *stop_event);
  * restores the default.  When that wait gives up the kernel flags the call and
  * then waits again with the full bound, so no copy is left in flight and the
  * call completes; every sequence of the call gets SPEC_FLAG_TIMEOUT and the
- * fallback outputs.  Process-wide, read at each call's launch.  Returns SPEC_OK.
+ * fallback outputs.  It also shortens the first wait for keys of
+ * spec_paged_attention's kernels on tensor memory (bf16 and f16, head_dim 64 or
+ * 128, pages of a multiple of 8 tokens): a thread block whose wait gives up waits
+ * for its copies and products in flight and ends, and the sequences of its run get
+ * SPEC_FLAG_TIMEOUT.  Process-wide, read at each call's launch.  Returns SPEC_OK.
  */
 spec_status spec_set_wait_limit(int64_t cycles);
 

@@ -38,8 +38,9 @@ def _stream(device):
 
 def set_wait_limit(cycles=None):
     """spec_set_wait_limit: bound the streaming chain path's first wait on each
-    chunk to `cycles` SM clock cycles (0: one non-blocking test); None restores
-    the default bound.  A wait that gives up turns the call's outputs into the
+    chunk, and the first wait of paged_attention's kernels on tensor memory, to
+    `cycles` SM clock cycles (0: one non-blocking test); None restores the default
+    bound.  A wait that gives up turns the call's outputs into the
     documented fallback with FLAG_TIMEOUT (diagnostics and tests)."""
     _check(_abi.load().spec_set_wait_limit(-1 if cycles is None else int(cycles)))
 

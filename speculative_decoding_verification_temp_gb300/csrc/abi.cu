@@ -268,8 +268,9 @@ const sv::Exp2Table &exp2_table() {
 
 spec_status map_cuda(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA; }
 
-// Cycles the chain rows kernel's first wait on a chunk may take (see
-// spec_set_wait_limit); the full bound unless a caller shortened it.
+// Cycles the chain rows kernel's first wait on a chunk, and a run's first wait in
+// the attention kernels on tensor memory, may take (see spec_set_wait_limit); the
+// full bound unless a caller shortened it.
 std::atomic<long long> g_first_wait{sv::kWaitLimitCycles};
 
 int esize_of(spec_dtype d) { return d == SPEC_BF16 ? 2 : (d == SPEC_F32 ? 4 : 0); }
@@ -451,6 +452,12 @@ spec_status check_chain_args(const void *target_logits, int64_t ld_target,
   if (gamma > 0 && (!draft_logits || ld_draft < V || !draft_tokens)) return SPEC_ERR_INVALID_ARG;
   return SPEC_OK;
 }
+
+}  // namespace sv
+
+namespace sv {
+
+long long first_wait_cycles() { return g_first_wait.load(std::memory_order_relaxed); }
 
 }  // namespace sv
 

@@ -201,6 +201,7 @@ spec_status spec_paged_attention(
   p.out = out;
   p.lse = out_lse;
   p.flags = out_flags;
+  p.first_wait = sv::first_wait_cycles();
   if (out_flags) {
     const cudaError_t e = sv::launch_kv_flags(p.S, p.C, false, p.window, p.sinks, out_flags, st);
     if (e != cudaSuccess) return map_cuda(e);

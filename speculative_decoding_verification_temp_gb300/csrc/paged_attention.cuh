@@ -55,6 +55,7 @@ struct AttnParams {
   int unit_cost;                 // places on the line behind a unit's key tiles
   int row_lines;                 // 1: all row tiles on one line
   bool whole;                    // units are not cut, and not joined
+  long long first_wait;          // cycles of a run's first wait (spec_set_wait_limit)
 };
 
 // A cut unit, written by the worker that holds its first cut; its pieces are
@@ -77,6 +78,8 @@ struct WideMaps {
 // Rows of a tile: whole tokens, at most 128 rows.
 inline int wide_tile_rows(int G) { return 128 / G * G; }
 bool wide_maps(const AttnParams &p, int dtype, WideMaps *maps);
+// Cycles that spec_set_wait_limit allows a first wait.
+long long first_wait_cycles();
 cudaError_t launch_attention_wide(const AttnParams &p, const WideMaps &maps, int dtype,
                                   cudaStream_t stream);
 

@@ -104,6 +104,26 @@ __device__ __forceinline__ bool bar_wait(const void *bar, uint32_t parity, int *
   }
 }
 
+// The first wait of a run, for the keys of its first tile, where a caller has
+// shortened it (limit <= 0: one non-blocking test); by one warp, the others find in
+// their own waits that it gave up.  (In pair_kernel the warp that checks values: before
+// the products' loop it costs 256-node trees 1 % of their time.)
+__device__ __forceinline__ void first_wait(const void *bar, long long limit, int *dead) {
+  if (limit >= kWaitCycles) return;
+  const uint32_t at = smem_u32(bar);
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], 0;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(at)
+      : "memory");
+  for (const long long t0 = clock64(); !done && clock64() - t0 < limit;) done = bar_test(at, 0u);
+  if (!done) *reinterpret_cast<volatile int *>(dead) = 1;
+  __syncwarp();
+}
+
 // A last wait, whether others have given up or not.
 __device__ __forceinline__ void bar_linger(const void *bar, uint32_t parity) {
   const uint32_t at = smem_u32(bar);
@@ -824,6 +844,25 @@ __device__ __forceinline__ void tm_free(uint32_t tmem, int warp) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
+// A wait gave up: the copies into a ring of entries, and of the queries, land before
+// the CTA ends.  The loaders may have made them all without a wait that failed, so
+// this is for when every role has left its loops; by a whole warp.  sent[x]: entries
+// of the numbers x, x + 2, ... below it were asked for.  Entries leave the ring in
+// order, so those before the last kRing have landed.
+struct Sent {
+  uint32_t entries[2], queries;
+};
+template <int kRing>
+__device__ __forceinline__ void land_copies(const unsigned long long (&full)[kRing],
+                                            const unsigned long long *q_full, const Sent &sent) {
+  const uint32_t top = max(sent.entries[0], sent.entries[1]);
+  for (uint32_t i = 0; i < kRing && i < top; ++i) {
+    const uint32_t e = top - 1 - i;
+    if (e < sent.entries[e & 1]) bar_linger(&full[e % kRing], (e / kRing) & 1u);
+  }
+  if (sent.queries > 0) bar_linger(q_full, (sent.queries - 1) & 1u);
+}
+
 // A wait gave up: the outputs of the run's sequences are not to be used.
 __device__ __forceinline__ void flag_run(const AttnParams &p, const Line &line) {
   UnitWalk v;
@@ -845,6 +884,7 @@ struct SoloCtl {
     unsigned long long full[kRing], empty[kRing], s_full, p_full, o_done, q_full, q_empty, meet,
         drain;
     alignas(16) uint32_t valid[kValidRing][4];
+    Sent sent;
   } stream[2];
   RunScratch<kWideThreads, 2> runs;
   uint32_t tmem;
@@ -985,7 +1025,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (warp < 10) {
     // ------------------------------------------------ queries, keys, values
     const BoxLoader keys(p, maps, false), values(p, maps, true);
-    uint32_t tiles = 0, units = 0;
+    uint32_t tiles = 0, units = 0, sent = 0;
     if (busy) do {
         const int n_tiles = u.i1 - u.i0;
         int page = keys.page(p, u, 0, lane), next = keys.page(p, u, 1, lane);
@@ -999,6 +1039,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (lane < 4) st.valid[tiles % kValidRing][lane] = keys.valid_word(u, pages, at0, lane);
           keys.load<D>(p, u, at0, page, pages, ring_at + e % kRing * W::kBytes, &st.full[e % kRing],
                        lane);
+          sent = e + 1;
           if (i == 0) {
             // once the products of the unit before have read theirs
             if (!(ok = warp_wait(&st.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
@@ -1016,20 +1057,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (!(ok = warp_wait(&st.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, &ctl.dead))) break;
           values.load<D>(p, u, at0, page, pages, ring_at + e % kRing * W::kBytes,
                          &st.full[e % kRing], lane);
+          sent = e + 1;
           page = next;
           next = behind;
         }
       } while (ok && u.next(p, line));
-    // the products wait for every copy; where a wait gave up, the copies are
-    // given time to land before the CTA ends
-    if (!ok) {
-      for (uint32_t e = 2 * tiles > kRing ? 2 * tiles - kRing : 0; e < 2 * tiles + 1; ++e)
-        bar_linger(&st.full[e % kRing], (e / kRing) & 1u);
-      if (units > 0) bar_linger(&st.q_full, (units - 1) & 1u);
-    }
+    if (lane == 0) st.sent = Sent{{sent, sent}, units};
     } else {
     // ------------------------------------------------------------- products
     uint32_t tiles = 0, units = 0;
+    if (busy) first_wait(&st.full[0], p.first_wait, &ctl.dead);
     if (busy) do {
         const int n_tiles = u.i1 - u.i0;
         for (int i = 0; i < n_tiles; ++i, ++tiles) {
@@ -1054,7 +1091,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
   }
   tm_free(tmem, warp);
-  if (ctl.dead && tid < 2) flag_run(p, tid ? lines[1] : lines[0]);
+  if (!ctl.dead) return;
+  if (warp == 8 || warp == 9) land_copies(st.full, &st.q_full, st.sent);
+  if (tid < 2) flag_run(p, tid ? lines[1] : lines[0]);
 }
 
 namespace {
@@ -1071,6 +1110,7 @@ struct PairCtl {
       q_full, q_empty, drain;
   alignas(16) uint32_t valid[kValidRing][4];
   RunScratch<kWideThreads, 1> runs;
+  Sent sent;
   uint32_t tmem;
   int dead, bad;
 };
@@ -1183,6 +1223,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // ------------------------------ warp 8: keys and queries, warp 9: values
     const bool values = warp == 9;
     const BoxLoader boxes(p, maps, values);
+    uint32_t sent = 0;
     do {
       const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
       // a tile's pages are looked up two tiles ahead
@@ -1197,6 +1238,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           ctl.valid[tiles % kValidRing][lane] = boxes.valid_word(u, pages, at0, lane);
         boxes.load<D>(p, u, at0, page, pages, ring_at + e % kRing * W::kBytes, &ctl.full[e % kRing],
                       lane);
+        sent = e + 1;
         if (!values && i == 0) {
           // once the products of the unit before have read theirs
           if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
@@ -1214,15 +1256,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         next = behind;
       }
     } while (ok && u.next(p, line));
-    // the products wait for every copy; where a wait gave up, the copies are
-    // given time to land before the CTA ends
-    if (!ok) {
-      for (uint32_t e = 2 * tiles > kRing ? 2 * tiles - kRing : 0; e < 2 * tiles + 2; ++e)
-        bar_linger(&ctl.full[e % kRing], (e / kRing) & 1u);
-      if (units > 0) bar_linger(&ctl.q_full, (units - 1) & 1u);
+    if (lane == 0) {
+      ctl.sent.entries[values] = sent;
+      if (!values) ctl.sent.queries = units;
     }
     } else if (warp == 10) {
     // -------------------------------------------------- values made ready
+    first_wait(&ctl.full[0], p.first_wait, &ctl.dead);
     do {
       const int n_tiles = u.i1 - u.i0;
       for (int i = 0; i < n_tiles; ++i, ++tiles) {
@@ -1294,7 +1334,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
   }
   tm_free(tmem, warp);
-  if (ctl.dead && tid == 0) flag_run(p, line);
+  if (!ctl.dead) return;
+  if (warp == 8) land_copies(ctl.full, &ctl.q_full, ctl.sent);
+  if (tid == 0) flag_run(p, line);
 }
 
 namespace {

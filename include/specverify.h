@@ -346,8 +346,8 @@ spec_status spec_set_profile_events(void *start_event, void *stop_event);
  * fallback outputs.  It also shortens the first wait for keys of
  * spec_paged_attention's kernels on tensor memory (bf16 and f16, head_dim 64 or
  * 128, pages of a multiple of 8 tokens): a thread block whose wait gives up waits
- * for its copies and products in flight and ends, and the sequences of its run get
- * SPEC_FLAG_TIMEOUT.  Process-wide, read at each call's launch.  Returns SPEC_OK.
+ * for its copies and products in flight and ends, the rows of its run are NaN and
+ * their sequences get SPEC_FLAG_TIMEOUT.  Process-wide, read at each call's launch.  Returns SPEC_OK.
  */
 spec_status spec_set_wait_limit(int64_t cycles);
 
@@ -508,7 +508,8 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  *    tokens all lie behind the sinks and before context_len[b] - window + 1 is not
  *    looked at, and may have gone to another sequence),
  *    SPEC_FLAG_TIMEOUT (a bounded on-device wait gave up: the sequence's outputs
- *    are not to be used).  Costs a launch of its own.
+ *    are not to be used; the rows that it left undone are NaN in out and out_lse,
+ *    also where no flags are asked for).  Costs a launch of its own.
  * Products of bf16 and f16 run on the tensor cores with float32 sums; the
  * weights are rounded to the cache's type before they meet the values.  float32
  * caches are computed in float32.  1 <= N <= 4096.  workspace: 32-byte aligned.

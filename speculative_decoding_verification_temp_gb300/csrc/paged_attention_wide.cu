@@ -863,12 +863,32 @@ __device__ __forceinline__ void land_copies(const unsigned long long (&full)[kRi
   if (sent.queries > 0) bar_linger(q_full, (sent.queries - 1) & 1u);
 }
 
-// A wait gave up: the outputs of the run's sequences are not to be used.
-__device__ __forceinline__ void flag_run(const AttnParams &p, const Line &line) {
+// A wait gave up: the rows of the run's units become NaN, whatever was written of
+// them, or the sums of their pieces of cut units, which the join then carries to
+// the rows; and their sequences are flagged.  By the whole CTA.
+template <class E, int D>
+__device__ __noinline__ void void_run(const AttnParams &p, const Line &line) {
+  using TE = typename E::T;
+  const float nan = __int_as_float(0x7FC00000);
   UnitWalk v;
-  if (p.flags && v.start(p, line)) do {
-      atomicOr(p.flags + v.b, SPEC_FLAG_TIMEOUT);
-    } while (v.next(p, line));
+  if (!v.start(p, line)) return;
+  do {
+    const int live = v.live_rows(p);
+    float *slot = p.part + piece_slot(v, line.worker) * slot_floats(p.rows, D);
+    for (int i = threadIdx.x; i < live * (D / 4); i += kWideThreads) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4;
+      const long long at = out_row(p, v.b, v.h, v.r0 + row);
+      if (v.whole()) store4(static_cast<TE *>(p.out) + at * D + d, make_float4(nan, nan, nan, nan));
+      if (d > 0) continue;
+      if (!v.whole()) {
+        slot[row] = -INFINITY;
+        slot[p.rows + row] = nan;
+      } else if (p.lse) {
+        p.lse[at] = nan;
+      }
+    }
+    if (threadIdx.x == 0 && p.flags) atomicOr(p.flags + v.b, SPEC_FLAG_TIMEOUT);
+  } while (v.next(p, line));
 }
 
 // ---------------------------------------------------------------------------
@@ -1093,7 +1113,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   tm_free(tmem, warp);
   if (!ctl.dead) return;
   if (warp == 8 || warp == 9) land_copies(st.full, &st.q_full, st.sent);
-  if (tid < 2) flag_run(p, tid ? lines[1] : lines[0]);
+  void_run<E, D>(p, lines[0]);
+  void_run<E, D>(p, lines[1]);
 }
 
 namespace {
@@ -1336,7 +1357,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   tm_free(tmem, warp);
   if (!ctl.dead) return;
   if (warp == 8) land_copies(ctl.full, &ctl.q_full, ctl.sent);
-  if (tid == 0) flag_run(p, line);
+  void_run<E, D>(p, line);
 }
 
 namespace {

@@ -50,6 +50,24 @@ def test_wait_runs_out_then_recovers(kernel, batch):
         assert torch.equal(after.lse[b, :n], before.lse[b, :n])
 
 
+@pytest.mark.parametrize("batch", list(BATCHES))
+@pytest.mark.parametrize("kernel", WIDE, ids=str)
+def test_no_answer_without_flags(kernel, batch):
+    """Without flags the outputs themselves say that a wait gave up."""
+    (dtype, N, Hq, Hkv, D, page), tokens = kernel
+    ctx = BATCHES[batch]
+    n_new = np.full(len(ctx), N)
+    n_new[1::3] = N // 2
+    s = Setup(73, ctx, N, Hq, Hkv, D, page, dtype, n_new=n_new,
+              max_pages=tokens // page if batch in ("one", "whole") else None)
+    out = torch.full_like(s.q, 3.0)
+    res = short_wait(lambda: sv.paged_attention(s.q, s.k, s.v, s.dev(s.table), s.dev(s.ctx),
+                                                num_new=s.dev(s.n_new), return_lse=True, out=out))
+    for b, n in enumerate(n_new):
+        assert torch.isnan(res.out[b, :n]).all() and torch.isnan(res.lse[b, :n]).all()
+        assert (res.out[b, n:] == 3.0).all()
+
+
 def test_other_kernels_make_no_such_wait():
     for dtype, N, Hq, Hkv, D, page in (k for k in KERNELS if k not in [x for x, _ in WIDE]):
         s = Setup(72, [100, 0], N, Hq, Hkv, D, page, dtype)

@@ -511,8 +511,9 @@ size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int nu
  *    are not to be used; the rows that it left undone are NaN in out and out_lse,
  *    also where no flags are asked for).  Costs a launch of its own.
  * Products of bf16 and f16 run on the tensor cores with float32 sums; the
- * weights are rounded to the cache's type before they meet the values.  float32
- * caches are computed in float32.  1 <= N <= 4096.  workspace: 32-byte aligned.
+ * weights are rounded to the cache's type before they meet the values (float16
+ * weights to zero below 2^-32 of a row's largest).  float32 caches are computed in
+ * float32.  1 <= N <= 4096.  workspace: 32-byte aligned.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (a head_dim, alignment or
  * stride not listed above) before any launch.  B = 0 is a no-op.  Two launches, or
  * one where the page table or the window keeps the key ranges short. */

@@ -17,8 +17,8 @@
 // results meet in shared memory at the end of a unit.
 //
 // A weight is 2^(s c - m) with c = scale log2(e) and m the running maximum of
-// s c, rounded once and then used as it is: the weights of all keys, the sums
-// and the logarithm refer to the same float32 m.
+// s c (less a constant for float16), rounded once and then used as it is: the
+// weights of all keys, the sums and the logarithm refer to the same float32 m.
 #include <algorithm>
 
 #include "paged_attention.cuh"
@@ -290,8 +290,11 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) rows16_kernel
         x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, x));
         x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, x));
       }
-      x0 = fmaxf(m0, x0 * c);
-      x1 = fmaxf(m1, x1 * c);
+      // float16 weights are lifted to 2^15, so that those that it rounds to zero are
+      // below 2^-40 of the row's largest instead of 2^-25
+      constexpr float kLift = E::kNarrow ? 15.f : 0.f;
+      x0 = fmaxf(m0, x0 * c - kLift);
+      x1 = fmaxf(m1, x1 * c - kLift);
       if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
         const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - x0);
         const float f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - x1);

@@ -368,6 +368,7 @@ struct Bf16 {
     return *reinterpret_cast<uint32_t *>(&v);
   }
   static constexpr uint32_t kExp = 0x7F80u;  // all ones: infinity or NaN
+  static constexpr bool kNarrow = false;     // exponents as float32
 };
 struct F16 {
   using T = __half;
@@ -378,6 +379,7 @@ struct F16 {
     return *reinterpret_cast<uint32_t *>(&v);
   }
   static constexpr uint32_t kExp = 0x7C00u;
+  static constexpr bool kNarrow = true;  // 2^-24 to 2^15
 };
 
 // Four outputs of one row: stored as the cache's type.

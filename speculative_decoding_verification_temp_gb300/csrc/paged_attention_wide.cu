@@ -59,6 +59,10 @@ constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 // (in powers of two): until then weights stay below 2^8 and no output is
 // rescaled.  Weights above one have the same relative rounding.
 constexpr float kSlack = 8.f;
+// How far float16 weights are lifted: m lies so far below the maximum that it was
+// raised to, so that weights reach 2^(kLift + kSlack) = 2^15 at most, and those that
+// float16 rounds to zero are below 2^-32 of the row's largest instead of 2^-25.
+constexpr float kLift = 7.f;
 
 // Bytes of an entry of 128 rows.
 template <int D>
@@ -426,7 +430,8 @@ __device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, ui
     for (int e = 0; e < 32; e += 2)
       x[j] = max3(x[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
   }
-  const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
+  float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * c;
+  if constexpr (E::kNarrow) top -= kLift;
   const bool raise = mine && top > m + kSlack;
   if (__any_sync(0xFFFFFFFFu, raise)) {
     const float to = raise ? top : m;
@@ -460,7 +465,8 @@ __device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, ui
       y.y = fast_exp2(y.y);
       sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], y);
       // the product takes the weights in the cache's type: each is off by at
-      // most half a step of that type, as the values themselves are
+      // most half a step of that type, as the values themselves are (float16: or
+      // by 2^-32 of the row's largest, which the sum of weights does not see)
       packed[e / 2] = E::pack(y.x, y.y);
     }
     tm_store16(s_at + j * 16, packed);
@@ -489,7 +495,8 @@ __device__ __forceinline__ void softmax_part(float c, bool mine, bool masked, ui
 #pragma unroll
   for (int e = 0; e < 32; e += 2)
     x[(e >> 1) & 1] = max3(x[(e >> 1) & 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-  const float top = fmaxf(x[0], x[1]) * c;
+  float top = fmaxf(x[0], x[1]) * c;
+  if constexpr (E::kNarrow) top -= kLift;
   const bool raise = mine && top > m + kSlack;
   if (__any_sync(0xFFFFFFFFu, raise)) {
     const float to = raise ? top : m;

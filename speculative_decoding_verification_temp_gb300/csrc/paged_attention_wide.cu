@@ -648,7 +648,6 @@ __device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk 
   x.ml[part][1][lane] = l;
   tc_after();
   float M = -INFINITY, sum = 0.f, f[4];
-  uint32_t some = 0u;  // quarters that are not empty
   for (int pass = 0; pass < (few ? 1 : D / 32); ++pass) {
 #pragma unroll 1
     for (int d = few ? 0 : pass * 32; d < (few ? D : pass * 32 + 32); d += 32) {
@@ -676,17 +675,13 @@ __device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk 
         for (int w = 0; w < 4; ++w) {
           // an empty quarter has l zero; one of NaN scores has m -infinity too
           const float lw = x.ml[w][1][row];
-          f[w] = 0.f;
-          if (lw == 0.f) continue;
-          some |= 1u << w;
-          f[w] = fast_exp2(x.ml[w][0][row] - M);
+          f[w] = lw == 0.f ? 0.f : fast_exp2(x.ml[w][0][row] - M);
           sum += f[w] * lw;
         }
       }
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        if (!((some >> w) & 1u)) continue;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float4 y = *reinterpret_cast<const float4 *>(x.o[w] + row * pitch +

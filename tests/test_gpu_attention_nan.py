@@ -77,3 +77,17 @@ def test_a_context_of_nan_keys(dtype, N, Hq, Hkv, D, page):
     rows = np.zeros(s.q.shape[:3], bool)
     rows[:, :, :Hq // Hkv] = True
     check_rows(s, s.call(), clean, rows)
+
+
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D,page", KERNELS)
+def test_a_score_of_plus_infinity(dtype, N, Hq, Hkv, D, page):
+    """exp(inf - inf): NaN, as in the definition's quotient."""
+    s = Setup(44, [31, 640, 2047], N, Hq, Hkv, D, page, dtype)
+    s.q[:] = s.q.abs() + 0.5
+    clean = s.call()
+    rows = np.zeros(s.q.shape[:3], bool)
+    for b, c in enumerate(s.ctx):
+        p, i = s.slot(b, int(c) + N - 1)
+        s.k[p, i, 0, b] = math.inf
+    rows[:, N - 1, :Hq // Hkv] = True
+    check_rows(s, s.call(), clean, rows)

@@ -826,10 +826,10 @@ bool wide_sizes(int G, int D, int dtype) {
 }
 // What a unit costs beside its tiles (queries, the first products and the last,
 // masked tiles, outputs), in tiles, from runs of one launch fitted by their tiles
-// and units: pairs of row tiles 8 (12 to 16 us; 256-node trees at B=16 take 593 us with
-// 9, 603 with 7, 606 with 5, 665 with 2, where the longest of 152 runs is 1.23
-// times the median), single ones 1 at head_dim 128, where HBM hides it, and 2 at
-// 64.
+// and units: pairs of row tiles 8 (12 to 16 us; 256-node trees at B=16 and 60-node
+// ones at B=32 take 517 and 114 us with 5, 517 and 111 with 7, 523 and 111 with 8, 525
+// and 111 with 9, 529 and 109 with 10), single ones 1 at head_dim 128, where HBM hides
+// it, and 2 at 64.
 AttnPlan wide_plan(int N, int G, int D) {
   if (N * G > wide_tile_rows(G)) return {kSms, 2 * wide_tile_rows(G), 7, 8, 16};
   return {2 * kSms, wide_tile_rows(G), 7, D == 64 ? 2 : 1, N * G <= 32 ? 4 : 6};

@@ -26,19 +26,22 @@
 // group's heads, as many whole tokens as 128 rows hold.
 //
 // One token is bound by HBM: 64 KB of keys and values a tile at head_dim 128
-// arrive in about 3000 cycles of an SM; a stream's tile takes 850 of products (Q K^T
-// reads both operands from shared memory, 65 cycles a step of 16; P V 41) and 600 of
-// softmax in quarters.  256 sequences of 1 to 4096 tokens, one token each, 32 query
+// arrive in about 3000 cycles of an SM; a stream's tile takes 1024 of products (64 a
+// step of 16 in Q K^T and P V alike, the pipe's rate: from the share of the time that
+// the pipe is active) and 600 of softmax in quarters.  256 sequences of 1 to 4096 tokens, one token each, 32 query
 // heads on 8 of 128 bf16: 333 us, 6.48 TB/s, 0.95 of the measured copy rate, DRAM
 // reads 1.004 of the keys' and values' bytes.
 //
 // Many rows are bound by the turns that a stream's softmax (1770 cycles a tile
-// with both streams at it) and products take with one buffer of scores: 256-node
-// trees at B = 16, 64 query heads on 8 of 128 bf16, contexts of 1000 to 8192 tokens:
-// 530 us, 1.16 PFLOP/s.  Measured and not kept: scores in halves of 64 keys with two
-// buffers (710 us: 52 cycles a step of 64 keys make the products the bound) and two
-// warps per row (671 us), when this took 645; waits that suspend (566 us) or only
-// poll (566), and ends of units stored by quads in whole lines (554), against 530.
+// with both streams at it) and products take with one buffer of scores: scores, all
+// their weights, outputs, one after the other.  256-node trees at B = 16, 64 query
+// heads on 8 of 128 bf16, contexts of 1000 to 8192 tokens: 519 to 530 us, 1.16
+// PFLOP/s; a pair of tiles takes about 3900 cycles, of which its products need 2048.
+// Measured and not kept: against 530 us waits that suspend (566 us) or only poll (566)
+// and ends of units stored by quads in whole lines (554); against 645 us, before row
+// tiles had lines of their own, and not measured since: scores in halves of 64 keys
+// with two buffers (710 us, 2520 cycles of products a tile) and two warps per row
+// (671).
 #include <climits>
 #include <numeric>
 

@@ -100,9 +100,10 @@ typedef enum {
   SPEC_ERR_UNSUPPORTED = 3
 } spec_status;
 
-/* SPEC_F16 is a type of key-value caches (spec_paged_attention, spec_cache_*);
- * logits are float32 or bfloat16. */
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
+/* SPEC_F16 is a type of key-value caches (spec_paged_attention, spec_cache_*) and of
+ * rotated rows (spec_rotary); SPEC_Q4 is one of caches alone, whose rows are 4-bit ones
+ * (spec_kv_cache); logits are float32 or bfloat16. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2, SPEC_Q4 = 4 } spec_dtype;
 
 /* Per-sequence (or per-tree) policy arrays, device memory.
  *   temperature [B]: 0 -> greedy; > 0 -> softmax(z / T); NaN, < 0 or inf ->
@@ -449,7 +450,21 @@ spec_status spec_tree_rerank(const int32_t *parent, const float *confidence, int
  * most 256 elements.  page_size: 1..65536, not only powers of two; the keys of a
  * page in one layer take at most 16 GB.  k, v and
  * every stride of a dimension larger than one are multiples of 16 bytes, and no
- * such stride is shorter than head_dim; otherwise SPEC_ERR_UNSUPPORTED. */
+ * such stride is shorter than head_dim; otherwise SPEC_ERR_UNSUPPORTED.
+ *
+ * SPEC_Q4: rows of 4 bits a value, head_dim 64 or 128 (else SPEC_ERR_UNSUPPORTED),
+ * head_dim / 2 + 16 bytes each; strides are in bytes, multiples of 16, and no shorter
+ * than a row.  A row is head_dim / 8 little-endian words of 32 bits, then four pairs of
+ * float16, the scale s and the minimum m of each group of head_dim / 4 values.  Bits 4i
+ * of word w hold the code of value 8w + 2i, bits 16 + 4i that of value 8w + 2i + 1 (i =
+ * 0..3); a code n stands for m + s n.  spec_cache_append_rotary writes them (with or
+ * without a rotation): m = f16(min), s = f16((max - m) / 15), n = round((x - m) / s)
+ * within 0..15, of values taken as +-61440 beyond that; a group that holds an infinity or
+ * a NaN stands for NaNs.  Rows that callers write themselves stand for values below 65504
+ * in magnitude.  Taken by spec_cache_append_rotary, spec_cache_read,
+ * spec_paged_attention_q4, spec_cache_compact and spec_cache_fork; the other entry
+ * points return SPEC_ERR_INVALID_ARG.  Tokens that lie one behind another (token stride
+ * = a row) are read fastest. */
 typedef struct {
   void *k, *v;
   int64_t k_layer_stride, k_page_stride, k_token_stride, k_head_stride;
@@ -612,6 +627,77 @@ size_t spec_cache_fork_workspace_size(int F);
 spec_status spec_cache_fork(spec_page_pool pool, spec_kv_cache cache, int32_t *context_len,
                             const int32_t *src, const int32_t *dst, int F, uint32_t *out_flags,
                             void *workspace, size_t workspace_bytes, spec_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The position rotation of queries and keys, and the cache in 4 bits (SPEC_Q4).  The
+ * pages have no counterpart; a decode loop around the verification needs both: a
+ * tree's tokens stand at context_len + depth, which spec_tree_mask's position ids say.
+ * ------------------------------------------------------------------------- */
+
+/* Rotation of the first dim values of each head: pair i turns by the angle t = position
+ * * frequency[i], (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t); inverse: by
+ * -t.  Pair i is (i, i + dim / 2), interleaved: (2i, 2i + 1).  frequency: dim / 2 values
+ * in device memory (radians per token, float64); the angle is wrapped in 64-bit fixed
+ * point, so that far positions are as exact as near ones; sine, cosine, products and
+ * sums are float32.  A frequency that is not finite makes its pairs NaN.  dim: even, 2..512, at most head_dim (SPEC_ERR_INVALID_ARG
+ * otherwise).  Where dim / 2 values (interleaved: dim) are no multiple of 16 bytes, rows
+ * take a scalar path. */
+typedef struct {
+  const double *frequency;
+  int dim, interleaved, inverse;
+  float amplitude;
+} spec_rotation;
+
+/* Rows [num_layers, B, N, heads, head_dim] in device memory; strides in elements. */
+typedef struct {
+  void *data;
+  int64_t layer_stride, seq_stride, token_stride, head_stride;
+} spec_rows;
+
+/* Rotates the heads of [B, N] tokens: token (b, n) by position[b*position_seq_stride + n].
+ *
+ * x, out: rows of one layer (layer_stride is not looked at); out.data == x.data with
+ * the same strides rotates in place, otherwise the spans of the two do not overlap
+ * (SPEC_ERR_INVALID_ARG).  Strides of dimensions larger than one: at least head_dim
+ * elements.  Values behind rotation.dim are copied.  1 <= head_dim, heads <= 65536, 0 <=
+ * B * N < 2^31 / 2.  16-byte aligned rows take a vectorised path.  One launch. */
+spec_status spec_rotary(spec_rows x, spec_rows out, spec_dtype dtype, int B, int N, int heads,
+                        int head_dim, const int32_t *position, int64_t position_seq_stride,
+                        spec_rotation rotation, spec_stream_t stream);
+
+/* spec_cache_append with the rotation on the way, also into 4-bit rows: token n of
+ * sequence b, n < num_new[b] (NULL: N), has its query rotated from q to out_q, and its
+ * key rotated and its value as it is written to place context_len[b] + n of its pages, all
+ * by the position context_len[b] + position[b, n] (NULL: n; clamped into [0, N) as
+ * spec_paged_attention does).
+ *
+ * q, out_q [num_layers, B, N, num_q_heads, head_dim]: q.data NULL: no queries; in place
+ *    as for spec_rotary.  Rows of out_q behind num_new[b] are left as they were; those of
+ *    sequences and pages that are flagged are rotated all the same.
+ * k_new, v_new [num_layers, B, N, num_heads, head_dim]: of dtype, which is the cache's, or
+ *    any of SPEC_F32, SPEC_BF16 and SPEC_F16 for a SPEC_Q4 cache (keys are rounded to it
+ *    behind the rotation, before they are quantised).
+ * rotation.frequency NULL: nothing is rotated.
+ * Alignments, overlaps, limits, flags and errors as for spec_cache_append.  One launch,
+ * and one for flags. */
+spec_status spec_cache_append_rotary(spec_rows q, spec_rows out_q, int num_q_heads, spec_rows k_new,
+                                     spec_rows v_new, spec_dtype dtype, spec_kv_cache cache,
+                                     spec_page_table pages, const int32_t *context_len,
+                                     const int32_t *num_new, const int32_t *position,
+                                     int64_t position_seq_stride, int B, int N,
+                                     spec_rotation rotation, uint32_t *out_flags,
+                                     spec_stream_t stream);
+
+/* Reads tokens start[b] .. start[b] + num[b] - 1 of each sequence (num NULL: N; clamped
+ * into [0, N]) from their pages: the inverse of an append.  k_out, v_out [num_layers, B, N,
+ * num_heads, head_dim] of dtype, which is the cache's, or any of the three for a SPEC_Q4
+ * cache; 16-byte aligned as the cache; rows of tokens that are not there (behind num,
+ * on bad pages, of sequences that do not fit) are zeros.
+ * out_flags [B] (nullable): as for spec_cache_append; costs a launch of its own.
+ * 0 <= N <= 4096; B * N < 2^28.  One launch. */
+spec_status spec_cache_read(spec_kv_cache cache, spec_page_table pages, const int32_t *start,
+                            const int32_t *num, int B, int N, spec_dtype dtype, spec_rows k_out,
+                            spec_rows v_out, uint32_t *out_flags, spec_stream_t stream);
 
 #ifdef __cplusplus
 }

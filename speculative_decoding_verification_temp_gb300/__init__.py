@@ -21,6 +21,11 @@ and the paged key-value cache around it (``cache``):
   cache_compact    a tree's accepted path moved together
   cache_resize     pages taken for, or given back behind, a length
   cache_fork       sequences that go on from another one's tokens
+  cache_read       tokens of the pages back as rows
+  cache_4bit       a cache of 4-bit rows, which all of these take
+  rotary           queries and keys rotated by their positions (rotary_frequency:
+                   plain or scaled frequencies)
+  cache_append_rotary  new queries and keys rotated, keys and values into the pages
 """
 
 from ._abi import (FLAG_BAD_LENGTH, FLAG_BAD_PAGE, FLAG_BAD_SEQUENCE, FLAG_BAD_TOKEN,  # noqa: F401
@@ -39,7 +44,8 @@ def __getattr__(name):
         api = importlib.import_module(__name__ + ".api")
         return api if name == "api" else getattr(api, name)
     if name in ("paged_attention", "cache_append", "cache_compact", "cache_resize", "cache_fork",
-                "page_pool", "PagePool", "AttentionResult", "CompactResult", "cache"):
+                "cache_read", "cache_4bit", "cache_append_rotary", "rotary", "rotary_frequency",
+                "RotaryAppendResult", "ReadResult", "RotaryFrequency", "page_pool", "PagePool", "AttentionResult", "CompactResult", "cache"):
         import importlib
         cache = importlib.import_module(__name__ + ".cache")
         # importlib binds the module to the name `cache`; the functions are bound

@@ -19,6 +19,7 @@ SPEC_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 SPEC_F32 = 0
 SPEC_BF16 = 1
 SPEC_F16 = 2
+SPEC_Q4 = 4
 
 FLAG_BAD_TOKEN = 1
 FLAG_ZERO_Q = 2
@@ -53,6 +54,9 @@ EXPORTS = (
     "spec_cache_resize",
     "spec_cache_fork_workspace_size",
     "spec_cache_fork",
+    "spec_rotary",
+    "spec_cache_append_rotary",
+    "spec_cache_read",
 )
 
 
@@ -79,6 +83,17 @@ class spec_page_pool(ctypes.Structure):
                 + [(name, ctypes.c_void_p) for name in
                    ("page_count", "ref_count", "free_list", "free_count")]
                 + [(name, ctypes.c_int) for name in ("num_seqs", "num_pages", "page_size")])
+
+
+class spec_rotation(ctypes.Structure):
+    _fields_ = ([("frequency", ctypes.c_void_p)]
+                + [(name, ctypes.c_int) for name in ("dim", "interleaved", "inverse")]
+                + [("amplitude", ctypes.c_float)])
+
+
+class spec_rows(ctypes.Structure):
+    _fields_ = ([("data", ctypes.c_void_p)]
+                + [(f"{dim}_stride", ctypes.c_int64) for dim in ("layer", "seq", "token", "head")])
 
 
 _p = ctypes.c_void_p
@@ -159,6 +174,15 @@ def load():
     lib.spec_cache_fork_workspace_size.restype = _sz
     lib.spec_cache_fork.argtypes = [spec_page_pool, spec_kv_cache, _p, _p, _p, _i, _p, _p, _sz, _p]
     lib.spec_cache_fork.restype = _i
+    lib.spec_rotary.argtypes = [spec_rows, spec_rows, _i, _i, _i, _i, _i, _p, _i64, spec_rotation, _p]
+    lib.spec_rotary.restype = _i
+    lib.spec_cache_append_rotary.argtypes = [
+        spec_rows, spec_rows, _i, spec_rows, spec_rows, _i, spec_kv_cache, spec_page_table, _p, _p, _p,
+        _i64, _i, _i, spec_rotation, _p, _p]
+    lib.spec_cache_append_rotary.restype = _i
+    lib.spec_cache_read.argtypes = [spec_kv_cache, spec_page_table, _p, _p, _i, _i, _i, spec_rows,
+                                    spec_rows, _p, _p]
+    lib.spec_cache_read.restype = _i
     _lib = lib
     return lib
 

@@ -4,13 +4,15 @@ marshalling only, as in ``api``.
 A cache is a pair of tensors [num_pages, page_size, num_heads, head_dim] (one
 layer) or [num_layers, num_pages, page_size, num_heads, head_dim]; any strides
 whose last is 1 (a transposed [.., num_heads, page_size, head_dim] tensor, keys
-and values interleaved).  The calls run on torch's current stream of the
+and values interleaved).  A cache of 4-bit rows is a pair of uint8 tensors whose last
+dimension is head_dim / 2 + 16 (cache_4bit makes one); every operator takes either.  The calls run on torch's current stream of the
 cache's device.  Integer inputs may be of any integer type; values beyond 32 bits
 are flagged as any other bad page or length.  They are forward operators: tensors
 that require gradients are refused while autograd records.
 """
 
 import functools
+import math
 from collections import namedtuple
 
 import torch
@@ -19,6 +21,9 @@ from . import _abi
 from .api import _check
 
 AttentionResult = namedtuple("AttentionResult", "out lse flags")
+RotaryAppendResult = namedtuple("RotaryAppendResult", "q flags")
+ReadResult = namedtuple("ReadResult", "k v flags")
+RotaryFrequency = namedtuple("RotaryFrequency", "frequency amplitude")
 CompactResult = namedtuple("CompactResult", "context_len flags")
 PagePool = namedtuple("PagePool", "page_table page_count ref_count free_list free_count")
 
@@ -95,10 +100,17 @@ def _cache(k, v, layers):
     _on(v, k.device, "v_cache")
     _forward_only(k, v)
     shape, code, ks, vs = k.shape, _KV_DTYPES.get(k.dtype), k.stride(), v.stride()
+    if k.dtype == torch.uint8:
+        # 4-bit rows; their strides count bytes, and are never those of one element
+        code, width = _abi.SPEC_Q4, shape[-1]
+        if width not in (48, 80):
+            raise ValueError("4-bit caches have rows of head_dim / 2 + 16 bytes, head_dim 64 or 128")
+        shape = (*shape[:-1], 2 * (width - 16))
     if code is None or v.dtype != k.dtype:
-        raise ValueError("k_cache and v_cache must both be float32, bfloat16 or float16")
+        raise ValueError("k_cache and v_cache must both be float32, bfloat16 or float16, or 4-bit rows "
+                         "(uint8)")
     dims = len(shape)
-    if v.shape != shape or dims != 4 and not (layers and dims == 5):
+    if v.shape != k.shape or dims != 4 and not (layers and dims == 5):
         raise ValueError("k_cache and v_cache must be [%snum_pages, page_size, num_heads, head_dim]"
                          % ("num_layers, " if layers else ""))
     _sizes(shape)
@@ -161,8 +173,10 @@ def _rows(x):
 
 
 @functools.lru_cache(maxsize=256)
-def _attention_bytes(*sizes):
-    return max(_abi.load().spec_paged_attention_workspace_size(*sizes), 32)
+def _attention_bytes(four, *sizes):
+    lib = _abi.load()
+    size = lib.spec_paged_attention_q4_workspace_size if four else lib.spec_paged_attention_workspace_size
+    return max(size(*sizes), 32)
 
 
 def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, num_new=None,
@@ -171,7 +185,8 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
     """Attention of N new tokens per sequence over the cache's pages (see
     spec_paged_attention); the pages already hold the new tokens (cache_append).
 
-    q [B, N, num_q_heads, head_dim] with the cache's type; k_cache, v_cache
+    q [B, N, num_q_heads, head_dim] with the cache's type (bfloat16 or float16 over
+    4-bit rows, see spec_paged_attention_q4); k_cache, v_cache
     [num_pages, page_size, num_heads, head_dim]; page_table [B, max_pages] and
     context_len [B] integer.  scale: 1/sqrt(head_dim) by default.  num_new [B]:
     new tokens of each sequence (N by default; outputs behind them are not
@@ -187,8 +202,11 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
     dev = k_cache.device
     _on(q, dev, "q")
     _forward_only(q)
-    if q.dim() != 4 or q.shape[3] != k_cache.shape[3] or q.dtype != k_cache.dtype:
-        raise ValueError("q must be [B, N, num_q_heads, head_dim] with the cache's type")
+    four = cache.dtype == _abi.SPEC_Q4
+    if q.dim() != 4 or q.shape[3] != cache.head_dim or \
+            (q.dtype not in (torch.bfloat16, torch.float16) if four else q.dtype != k_cache.dtype):
+        raise ValueError("q must be [B, N, num_q_heads, head_dim] with the cache's type (bfloat16 or "
+                         "float16 over 4-bit rows)")
     B, N, Hq, D = shape = q.shape
     q = _rows(q)
     strides = q.stride()
@@ -217,11 +235,14 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
             raise ValueError("out must be a contiguous tensor like q")
     lse = torch.empty((B, N, Hq), dtype=torch.float32, device=dev) if return_lse else None
     flags = torch.empty(B, dtype=torch.int32, device=dev) if return_flags else None
-    nbytes = _attention_bytes(B, N, Hq, cache.num_heads, D, cache.dtype)
+    dtype = _KV_DTYPES[q.dtype]
+    nbytes = _attention_bytes(four, B, N, Hq, cache.num_heads, D, dtype)
     # of the caching allocator, ordered on this stream and kept by a graph that
     # captures the call: never shared with calls on other streams
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _run(dev, _abi.load().spec_paged_attention, q.data_ptr(), strides[0], strides[1], strides[2], Hq, cache,
+    lib = _abi.load()
+    fn, heads = (lib.spec_paged_attention_q4, (Hq, dtype)) if four else (lib.spec_paged_attention, (Hq,))
+    _run(dev, fn, q.data_ptr(), strides[0], strides[1], strides[2], *heads, cache,
          table, context_len.data_ptr(), _ptr(num_new), B, N, _ptr(tree_mask), mask_stride,
          _ptr(position), pos_stride, D ** -0.5 if scale is None else float(scale),
          _c_int(window), _c_int(sinks), out.data_ptr(), _ptr(lse), _ptr(flags), ws.data_ptr(), nbytes)
@@ -234,9 +255,12 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_ne
 
     k_new, v_new [B, N, num_heads, head_dim] for a cache of one layer, or
     [num_layers, B, N, num_heads, head_dim]; page_table, context_len, num_new as
-    for paged_attention.  Returns flags [B] int32, or None (return_flags False;
+    for paged_attention.  A 4-bit cache takes float32, bfloat16 or float16 rows (see
+    spec_cache_append_rotary).  Returns flags [B] int32, or None (return_flags False;
     asked for, they cost a launch).
     """
+    if isinstance(k_cache, torch.Tensor) and k_cache.dtype == torch.uint8:
+        return _append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_new, None, return_flags)
     cache = _cache(k_cache, v_cache, True)
     dev = k_cache.device
     _on(k_new, dev, "k_new")
@@ -262,6 +286,242 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_ne
     _run(dev, _abi.load().spec_cache_append, k_new.data_ptr(), *ks[:4], v_new.data_ptr(), *vs[:4],
          cache, table, context_len.data_ptr(), _ptr(num_new), B, N, _ptr(flags))
     return flags
+
+
+def _row_view(x, shape):
+    """The spec_rows of rows [(num_layers,) B, N, heads, head_dim] that _rows gave."""
+    strides = x.stride()
+    return _abi.spec_rows(x.data_ptr(), *((0, *strides[:3]) if len(shape) == 4 else strides[:4]))
+
+
+_NO_ROWS = _abi.spec_rows(None, 0, 0, 0, 0)
+_NO_ROTATION = _abi.spec_rotation(None, 0, 0, 0, 1.0)
+
+
+def _rotation(frequency, head_dim, dev, interleaved, inverse, amplitude):
+    _on(frequency, dev, "frequency")
+    if frequency.dtype != torch.float64 or frequency.dim() != 1 or \
+            not 1 <= frequency.shape[0] <= min(256, head_dim // 2):
+        raise ValueError("frequency must be float64 [dim / 2], dim at most head_dim and 512")
+    frequency = frequency.contiguous()
+    return frequency, _abi.spec_rotation(frequency.data_ptr(), 2 * frequency.shape[0], bool(interleaved),
+                                         bool(inverse), float(amplitude))
+
+
+def _append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_new, rotation, return_flags,
+            q=None, out=None, position=None):
+    """spec_cache_append_rotary; rotation: (frequency, interleaved, amplitude) or None."""
+    cache = _cache(k_cache, v_cache, True)
+    dev = k_cache.device
+    _on(k_new, dev, "k_new")
+    _on(v_new, dev, "v_new")
+    _forward_only(k_new, v_new)
+    shape, D, dtype = k_new.shape, cache.head_dim, k_new.dtype
+    if len(shape) != k_cache.dim() or shape[-1] != D or shape[-2] != cache.num_heads or \
+            v_new.shape != shape or (len(shape) == 5 and shape[0] != cache.num_layers):
+        raise ValueError("k_new and v_new must be [%sB, N, num_heads, head_dim] of the cache's sizes"
+                         % ("num_layers, " if k_cache.dim() == 5 else ""))
+    if v_new.dtype != dtype or dtype not in _KV_DTYPES or \
+            (cache.dtype != _abi.SPEC_Q4 and dtype != k_cache.dtype):
+        raise ValueError("k_new and v_new must have the cache's type (float32, bfloat16 or float16 for "
+                         "4-bit rows)")
+    B, N = shape[-4:-2]
+    k_new, v_new = _rows(k_new), _rows(v_new)
+    q_rows = out_rows = _NO_ROWS
+    heads = 0
+    if q is not None:
+        _on(q, dev, "q")
+        _forward_only(q)
+        if q.dtype != dtype or q.dim() != len(shape) or q.shape[:-2] != shape[:-2] or q.shape[-1] != D:
+            raise ValueError("q must be [.., B, N, num_q_heads, head_dim] with the type of k_new")
+        q = _rows(q)
+        if out is None:
+            out = torch.empty(q.shape, dtype=dtype, device=dev)
+        else:
+            _on(out, dev, "out")
+            _forward_only(out)
+            if out.shape != q.shape or out.dtype != dtype or _rows(out) is not out:
+                raise ValueError("out must be like q, with rows on 16 bytes")
+        heads, q_rows, out_rows = q.shape[-2], _row_view(q, shape), _row_view(out, shape)
+    elif out is not None:
+        raise ValueError("out is for the rotated q")
+    frequency, turn = None, _NO_ROTATION
+    if rotation is not None:
+        frequency, turn = _rotation(rotation[0], D, dev, rotation[1], False, rotation[2])
+    pos_stride = 0
+    if position is not None:
+        pos_stride = N if position.dim() == 2 else 0
+        position = _ints(position, (B, N) if position.dim() == 2 else (N,), dev, "position")
+    page_table, table = _table(page_table, B, dev)
+    context_len = _ints(context_len, (B,), dev, "context_len")
+    if num_new is not None:
+        num_new = _ints(num_new, (B,), dev, "num_new")
+    flags = torch.empty(B, dtype=torch.int32, device=dev) if return_flags else None
+    if heads > 0 or q is None:
+        _run(dev, _abi.load().spec_cache_append_rotary, q_rows, out_rows, heads, _row_view(k_new, shape),
+             _row_view(v_new, shape), _KV_DTYPES[dtype], cache, table, context_len.data_ptr(),
+             _ptr(num_new), _ptr(position), pos_stride, B, N, turn, _ptr(flags))
+    return flags if q is None else RotaryAppendResult(out, flags)
+
+
+def cache_append_rotary(k_new, v_new, k_cache, v_cache, page_table, context_len, frequency, q=None,
+                        out=None, position=None, num_new=None, interleaved=False, amplitude=1.0,
+                        return_flags=False):
+    """cache_append with the position rotation on the way (see
+    spec_cache_append_rotary): k_new is rotated and written, v_new written, and q, if
+    given, rotated.
+
+    The rotation is rotary()'s, by position context_len[b] + position[b, n]; position
+    [B, N] or [N], for trees tree_mask()'s position, is 0, 1, .. by default.  q [..,
+    B, N, num_q_heads, head_dim] like k_new but for its heads; out: where the rotated
+    q goes (q itself: in place).  The cache has the type of k_new, or 4-bit rows.
+    Returns RotaryAppendResult with q (None without one) and flags [B] int32 or None.
+    """
+    result = _append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_new,
+                     (frequency, interleaved, amplitude), return_flags, q, out, position)
+    return RotaryAppendResult(None, result) if q is None else result
+
+
+def cache_read(k_cache, v_cache, page_table, start, N, num=None, dtype=None, return_flags=False):
+    """Tokens start[b] .. start[b] + N - 1 of each sequence as rows: the inverse of
+    cache_append (see spec_cache_read).
+
+    num [B]: only the first num[b] of them; rows that are not there are zeros.  dtype: of
+    the rows of a 4-bit cache, bfloat16 by default.  Returns ReadResult with k and v
+    [(num_layers,) B, N, num_heads, head_dim] and flags [B] int32 or None.
+    """
+    cache = _cache(k_cache, v_cache, True)
+    dev = k_cache.device
+    if cache.dtype == _abi.SPEC_Q4:
+        dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype is None:
+        dtype = k_cache.dtype
+    if dtype not in _KV_DTYPES or (cache.dtype != _abi.SPEC_Q4 and dtype != k_cache.dtype):
+        raise ValueError("dtype must be the cache's type (float32, bfloat16 or float16 for 4-bit rows)")
+    _on(start, dev, "start")
+    if start.dim() != 1:
+        raise ValueError("start must be [B]")
+    B, N = start.shape[0], int(N)
+    if not 0 <= N <= 4096:
+        raise ValueError("N must be 0..4096")
+    start = _ints(start, (B,), dev, "start")
+    page_table, table = _table(page_table, B, dev)
+    if num is not None:
+        num = _ints(num, (B,), dev, "num")
+    shape = (B, N, cache.num_heads, cache.head_dim)
+    if k_cache.dim() == 5:
+        shape = (cache.num_layers, *shape)
+    k, v = (torch.empty(shape, dtype=dtype, device=dev) for _ in "kv")
+    flags = torch.empty(B, dtype=torch.int32, device=dev) if return_flags else None
+    _run(dev, _abi.load().spec_cache_read, cache, table, start.data_ptr(), _ptr(num), B, N,
+         _KV_DTYPES[dtype], _row_view(k, shape), _row_view(v, shape), _ptr(flags))
+    return ReadResult(k, v, flags)
+
+
+def cache_4bit(num_pages, page_size, num_heads, head_dim, num_layers=None, device="cuda"):
+    """An empty cache of 4-bit rows: k and v, uint8 [(num_layers,) num_pages, page_size,
+    num_heads, head_dim / 2 + 16], with a head's tokens of a page one behind another."""
+    if head_dim not in (64, 128):
+        raise ValueError("4-bit caches have head_dim 64 or 128")
+    lead = (num_pages,) if num_layers is None else (num_layers, num_pages)
+    shape = (*lead, num_heads, page_size, head_dim // 2 + 16)
+    return tuple(torch.zeros(shape, dtype=torch.uint8, device=device).transpose(-3, -2) for _ in "kv")
+
+
+def rotary_frequency(dim, base=10000.0, scaling=None, factor=1.0, context=4096, low=1.0, high=32.0,
+                     device="cuda"):
+    """Frequencies of a rotation of dim values: RotaryFrequency with frequency float64
+    [dim / 2], base^(-2i/dim) radians per token, and the amplitude that goes with it.
+
+    scaling, for contexts `factor` times longer than the `context` tokens that a model
+    was trained on:
+      None       as they are
+      "linear"   divided by factor
+      "base"     base times factor^(dim / (dim - 2)): the longest wave is factor times
+                 longer, the shortest stays
+      "turns"    pairs that turn less than `low` times over the context are divided by
+                 factor, those that turn more than `high` times kept, the others mixed
+                 in proportion to their turns
+      "index"    the same, mixed in proportion to the pairs' index, with amplitude
+                 0.1 ln(factor) + 1
+    """
+    dim = int(dim)
+    if dim < 2 or dim % 2 or not base > 1.0 or not factor >= 1.0:
+        raise ValueError("dim must be even, base above 1, factor at least 1")
+    if scaling in ("turns", "index") and not (context > 0 and 0 < low < high):
+        raise ValueError("context and 0 < low < high are needed")
+    if scaling == "base" and dim > 2:
+        base = base * factor ** (dim / (dim - 2))
+    i = torch.arange(0, dim, 2, dtype=torch.float64)
+    f = torch.tensor(float(base), dtype=torch.float64) ** (-i / dim)
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "turns":
+        turns = f * (context / (2 * math.pi))
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    elif scaling == "index":
+        # the index of a pair with so many turns over the context
+        at = [dim * math.log(context / (turns * 2 * math.pi)) / (2 * math.log(base)) for turns in (high, low)]
+        first, last = max(math.floor(at[0]), 0), min(math.ceil(at[1]), dim - 1)
+        keep = 1 - ((i / 2 - first) / max(last - first, 1e-3)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError("scaling must be None, 'linear', 'base', 'turns' or 'index'")
+    return RotaryFrequency(f.to(device), amplitude)
+
+
+def _loose_rows(x):
+    """x with the last dimension contiguous and rows apart, a copy where they are not."""
+    strides, shape = x.stride(), x.shape
+    if strides[-1] == 1 and all(n <= 1 or s >= shape[-1] for n, s in zip(shape[:-1], strides[:-1])):
+        return x
+    return x.clone(memory_format=torch.contiguous_format)
+
+
+def rotary(x, position, frequency, interleaved=False, amplitude=1.0, inverse=False, out=None):
+    """Rotates heads by their tokens' positions (see spec_rotary).
+
+    x [B, N, heads, D], [N, heads, D] or [heads, D], float32, bfloat16 or float16;
+    position: integers of x's shape without its last two dimensions, or [N] for all
+    sequences.  frequency float64 [dim / 2], radians per token (rotary_frequency); the
+    values of a head behind the first dim are copied.  Pairs are (i, i + dim / 2), or
+    interleaved (2i, 2i + 1).  amplitude: a factor of the rotated values.  inverse:
+    turns back (with amplitude 1 the inverse, and the gradient).  out: where the
+    result goes (x itself: in place).  Returns the rotated rows.
+    """
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    _forward_only(x)
+    dev, shape = x.device, x.shape
+    if x.dtype not in _KV_DTYPES or not 2 <= x.dim() <= 4:
+        raise ValueError("x must be [B, N, heads, D], [N, heads, D] or [heads, D], float32, bfloat16 or "
+                         "float16")
+    _sizes(shape)
+    frequency, turn = _rotation(frequency, shape[-1], dev, interleaved, inverse, amplitude)
+    _on(position, dev, "position")
+    if x.dim() == 4 and position.dim() == 1:
+        position, pos_stride = _ints(position, shape[1:2], dev, "position"), 0
+    else:
+        position = _ints(position, shape[:-2], dev, "position")
+        pos_stride = shape[1] if x.dim() == 4 else 0
+    x = _loose_rows(x)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=dev)
+    else:
+        _on(out, dev, "out")
+        _forward_only(out)
+        if out.shape != shape or out.dtype != x.dtype or _loose_rows(out) is not out:
+            raise ValueError("out must be like x, its last dimension contiguous")
+    lead = (1,) * (4 - len(shape))
+    view = lambda t: _abi.spec_rows(t.data_ptr(), 0, *(0,) * len(lead), *t.stride()[:-1])  # noqa: E731
+    B, N, H, D = (*lead, *shape)
+    if x.numel():
+        _run(dev, _abi.load().spec_rotary, view(x), view(out), _KV_DTYPES[x.dtype], B, N, H, D,
+             position.data_ptr(), pos_stride, turn)
+    return out
 
 
 def cache_compact(k_cache, v_cache, page_table, context_len, path, num_accepted):

@@ -6,6 +6,8 @@
 #include <cstdint>
 
 #include "paged_attention.cuh"
+#include "q4.cuh"
+#include "rotary.cuh"
 
 namespace sv {
 cudaError_t launch_append(const KvSeqs &S, const KvCache &C, const NewRows &R, uint32_t *flags,
@@ -45,20 +47,24 @@ bool stride_ok(int64_t stride, int64_t n, int head_dim, int esize) {
   return stride >= head_dim && stride * esize % 16 == 0 && stride < (INT64_MAX >> 4) / n;
 }
 
-spec_status check_cache(const spec_kv_cache &c) {
-  const int esize = kv_esize(c.dtype);
+// four: whether 4-bit rows are taken.
+spec_status check_cache(const spec_kv_cache &c, bool four = false) {
+  const bool q4 = four && c.dtype == SPEC_Q4;
+  const int esize = q4 ? 1 : kv_esize(c.dtype);
   if (esize == 0 || !c.k || !c.v || c.num_layers < 1 || c.num_pages < 1 || c.page_size < 1 ||
       c.page_size > kMaxPageSize || c.num_heads < 1 || c.head_dim < 1)
     return SPEC_ERR_INVALID_ARG;
-  if (c.head_dim > kMaxHeadDim || c.head_dim * esize % 16 != 0 || !aligned16(c.k) ||
+  const int row = q4 ? sv::q4_row_bytes(c.head_dim) : c.head_dim;  // elements
+  if (c.head_dim > kMaxHeadDim || (q4 && c.head_dim != 64 && c.head_dim != 128) ||
+      row * esize % 16 != 0 || !aligned16(c.k) ||
       !aligned16(c.v) || c.num_layers > kMaxRowsY / 2 || c.num_heads > 4096 ||
-      static_cast<int64_t>(c.page_size) * c.num_heads * (c.head_dim * esize / 16) > kMaxPagePieces)
+      static_cast<int64_t>(c.page_size) * c.num_heads * (row * esize / 16) > kMaxPagePieces)
     return SPEC_ERR_UNSUPPORTED;
   const int64_t strides[8] = {c.k_layer_stride, c.k_page_stride, c.k_token_stride, c.k_head_stride,
                               c.v_layer_stride, c.v_page_stride, c.v_token_stride, c.v_head_stride};
   const int64_t sizes[4] = {c.num_layers, c.num_pages, c.page_size, c.num_heads};
   for (int i = 0; i < 8; ++i)
-    if (!stride_ok(strides[i], sizes[i & 3], c.head_dim, esize)) return SPEC_ERR_UNSUPPORTED;
+    if (!stride_ok(strides[i], sizes[i & 3], row, esize)) return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }
 
@@ -68,7 +74,8 @@ bool table_ok(const spec_page_table &t, int page_size) {
 }
 
 sv::KvCache view(const spec_kv_cache &c) {
-  const int e = kv_esize(c.dtype);
+  const bool q4 = c.dtype == SPEC_Q4;
+  const int e = q4 ? 1 : kv_esize(c.dtype);
   sv::KvCache v;
   v.k = static_cast<char *>(c.k);
   v.v = static_cast<char *>(c.v);
@@ -84,7 +91,7 @@ sv::KvCache view(const spec_kv_cache &c) {
   v.pages = c.num_pages;
   v.page_size = c.page_size;
   v.heads = c.num_heads;
-  v.row_bytes = c.head_dim * e;
+  v.row_bytes = q4 ? sv::q4_row_bytes(c.head_dim) : c.head_dim * e;
   return v;
 }
 
@@ -98,6 +105,44 @@ sv::KvSeqs view(const spec_page_table &t, const int32_t *ctx, const int32_t *num
   s.B = B;
   s.N = N;
   return s;
+}
+
+sv::TokenRows view(const spec_rows &r, int esize) {
+  return {static_cast<char *>(r.data), r.layer_stride * esize, r.seq_stride * esize,
+          r.token_stride * esize, r.head_stride * esize};
+}
+
+// Rows of whole 16-byte pieces.
+bool rows_ok(const spec_rows &r, int layers, int B, int N, int heads, int D, int esize) {
+  return aligned16(r.data) && stride_ok(r.layer_stride, layers, D, esize) &&
+         stride_ok(r.seq_stride, B, D, esize) && stride_ok(r.token_stride, N, D, esize) &&
+         stride_ok(r.head_stride, heads, D, esize);
+}
+
+// Whether two arrays of rows of the same sizes are the same rows, or lie apart.
+bool same_or_apart(const spec_rows &x, const spec_rows &y, int layers, int B, int N, int heads, int D,
+                   int esize) {
+  const bool same = x.data == y.data && (layers <= 1 || x.layer_stride == y.layer_stride) &&
+                    (B <= 1 || x.seq_stride == y.seq_stride) &&
+                    (N <= 1 || x.token_stride == y.token_stride) &&
+                    (heads <= 1 || x.head_stride == y.head_stride);
+  auto end = [&](const spec_rows &r) {
+    return reinterpret_cast<uintptr_t>(r.data) +
+           (static_cast<uintptr_t>(layers - 1) * (layers > 1 ? r.layer_stride : 0) +
+            static_cast<uintptr_t>(B - 1) * (B > 1 ? r.seq_stride : 0) +
+            static_cast<uintptr_t>(N - 1) * (N > 1 ? r.token_stride : 0) +
+            static_cast<uintptr_t>(heads - 1) * (heads > 1 ? r.head_stride : 0) + D) * esize;
+  };
+  return same || end(x) <= reinterpret_cast<uintptr_t>(y.data) ||
+         end(y) <= reinterpret_cast<uintptr_t>(x.data);
+}
+
+bool rotation_ok(const spec_rotation &r, int head_dim) {
+  return r.frequency && r.dim >= 2 && r.dim % 2 == 0 && r.dim <= 2 * sv::kMaxPairs &&
+         r.dim <= head_dim && (reinterpret_cast<uintptr_t>(r.frequency) & 7u) == 0;
+}
+sv::Rotation view(const spec_rotation &r) {
+  return {r.frequency, r.frequency ? r.dim / 2 : 0, r.interleaved != 0, r.inverse != 0, r.amplitude};
 }
 
 bool pool_ok(const spec_page_pool &p) {
@@ -249,7 +294,7 @@ spec_status spec_cache_compact(spec_kv_cache cache, spec_page_table pages,
                                uint32_t *out_flags, spec_stream_t stream) {
   if (B < 0 || width < 1 || width > sv::kMaxPath) return SPEC_ERR_INVALID_ARG;
   if (B == 0) return SPEC_OK;
-  if (const spec_status s = check_cache(cache); s != SPEC_OK) return s;
+  if (const spec_status s = check_cache(cache, true); s != SPEC_OK) return s;
   if (!context_len || !path || !num_accepted || !out_context_len ||
       out_context_len == context_len || !table_ok(pages, cache.page_size))
     return SPEC_ERR_INVALID_ARG;
@@ -280,11 +325,85 @@ spec_status spec_cache_fork(spec_page_pool pool, spec_kv_cache cache, int32_t *c
       (reinterpret_cast<uintptr_t>(workspace) & 3u) != 0 ||
       workspace_bytes < sv::fork_workspace_bytes(F))
     return SPEC_ERR_INVALID_ARG;
-  if (const spec_status s = check_cache(cache); s != SPEC_OK) return s;
+  if (const spec_status s = check_cache(cache, true); s != SPEC_OK) return s;
   if (cache.num_pages != pool.num_pages || cache.page_size != pool.page_size)
     return SPEC_ERR_INVALID_ARG;
   return map_cuda(sv::launch_fork(view(pool), view(cache), context_len, src, dst, F, workspace,
                                   out_flags, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spec_status spec_rotary(spec_rows x, spec_rows out, spec_dtype dtype, int B, int N, int heads,
+                        int head_dim, const int32_t *position, int64_t position_seq_stride,
+                        spec_rotation rotation, spec_stream_t stream) {
+  const int e = kv_esize(dtype);
+  if (e == 0 || B < 0 || N < 0 || heads < 0 || heads > 65536 || head_dim < 1 || head_dim > 65536 ||
+      static_cast<int64_t>(B) * N >= (1 << 30) || position_seq_stride < 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (B == 0 || N == 0 || heads == 0) return SPEC_OK;
+  if (!x.data || !out.data || !position || !rotation_ok(rotation, head_dim)) return SPEC_ERR_INVALID_ARG;
+  // rows apart, whatever their alignment
+  auto apart = [&](const spec_rows &r) {
+    const int64_t strides[3] = {r.seq_stride, r.token_stride, r.head_stride}, sizes[3] = {B, N, heads};
+    for (int i = 0; i < 3; ++i)
+      if (sizes[i] > 1 && (strides[i] < head_dim || strides[i] >= (INT64_MAX >> 4) / sizes[i])) return false;
+    return (reinterpret_cast<uintptr_t>(r.data) & (e - 1)) == 0;
+  };
+  if (!apart(x) || !apart(out) || !same_or_apart(x, out, 1, B, N, heads, head_dim, e))
+    return SPEC_ERR_INVALID_ARG;
+  return map_cuda(sv::launch_rotary(view(x, e), view(out, e), dtype, B, N, heads, head_dim, position,
+                                    position_seq_stride, view(rotation),
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spec_status spec_cache_append_rotary(spec_rows q, spec_rows out_q, int num_q_heads, spec_rows k_new,
+                                     spec_rows v_new, spec_dtype dtype, spec_kv_cache cache,
+                                     spec_page_table pages, const int32_t *context_len,
+                                     const int32_t *num_new, const int32_t *position,
+                                     int64_t position_seq_stride, int B, int N,
+                                     spec_rotation rotation, uint32_t *out_flags,
+                                     spec_stream_t stream) {
+  const int e = kv_esize(dtype);
+  if (e == 0 || B < 0 || N < 0 || N > kMaxNew || static_cast<int64_t>(B) * N >= (1 << 28))
+    return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (const spec_status s = check_cache(cache, true); s != SPEC_OK) return s;
+  const int D = cache.head_dim, L = cache.num_layers;
+  if ((cache.dtype != SPEC_Q4 && cache.dtype != dtype) || !context_len ||
+      !table_ok(pages, cache.page_size) || (N > 0 && (!k_new.data || !v_new.data)) ||
+      position_seq_stride < 0 || (rotation.frequency && !rotation_ok(rotation, D)))
+    return SPEC_ERR_INVALID_ARG;
+  if (!rows_ok(k_new, L, B, N, cache.num_heads, D, e) || !rows_ok(v_new, L, B, N, cache.num_heads, D, e))
+    return SPEC_ERR_UNSUPPORTED;
+  if (q.data) {
+    if (!out_q.data || num_q_heads < 1 || num_q_heads > 65536) return SPEC_ERR_INVALID_ARG;
+    if (!rows_ok(q, L, B, N, num_q_heads, D, e) || !rows_ok(out_q, L, B, N, num_q_heads, D, e))
+      return SPEC_ERR_UNSUPPORTED;
+    if (N > 0 && !same_or_apart(q, out_q, L, B, N, num_q_heads, D, e)) return SPEC_ERR_INVALID_ARG;
+  }
+  const sv::RotaryRows r = {view(q, e), view(out_q, e), view(k_new, e), view(v_new, e), num_q_heads,
+                            position, position_seq_stride};
+  return map_cuda(sv::launch_append_rotary(view(pages, context_len, num_new, B, N), view(cache), r, D,
+                                           dtype, cache.dtype == SPEC_Q4, view(rotation), out_flags,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spec_status spec_cache_read(spec_kv_cache cache, spec_page_table pages, const int32_t *start,
+                            const int32_t *num, int B, int N, spec_dtype dtype, spec_rows k_out,
+                            spec_rows v_out, uint32_t *out_flags, spec_stream_t stream) {
+  const int e = kv_esize(dtype);
+  if (e == 0 || B < 0 || N < 0 || N > kMaxNew || static_cast<int64_t>(B) * N >= (1 << 28))
+    return SPEC_ERR_INVALID_ARG;
+  if (B == 0) return SPEC_OK;
+  if (const spec_status s = check_cache(cache, true); s != SPEC_OK) return s;
+  const int D = cache.head_dim, L = cache.num_layers;
+  if ((cache.dtype != SPEC_Q4 && cache.dtype != dtype) || !start || !table_ok(pages, cache.page_size) ||
+      (N > 0 && (!k_out.data || !v_out.data)))
+    return SPEC_ERR_INVALID_ARG;
+  if (!rows_ok(k_out, L, B, N, cache.num_heads, D, e) || !rows_ok(v_out, L, B, N, cache.num_heads, D, e))
+    return SPEC_ERR_UNSUPPORTED;
+  return map_cuda(sv::launch_read(view(pages, start, num, B, N), view(cache), view(k_out, e),
+                                  view(v_out, e), D, dtype, cache.dtype == SPEC_Q4, out_flags,
+                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

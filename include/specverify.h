@@ -348,7 +348,8 @@ spec_status spec_set_profile_events(void *start_event, void *stop_event);
  * spec_paged_attention's kernels on tensor memory (bf16 and f16, head_dim 64 or
  * 128, pages of a multiple of 8 tokens): a thread block whose wait gives up waits
  * for its copies and products in flight and ends, the rows of its run are NaN and
- * their sequences get SPEC_FLAG_TIMEOUT.  Process-wide, read at each call's
+ * their sequences get SPEC_FLAG_TIMEOUT (0: always, as if tested at the moment that the
+ * keys are asked for).  Process-wide, read at each call's
  * launch.  Returns SPEC_OK.
  */
 spec_status spec_set_wait_limit(int64_t cycles);

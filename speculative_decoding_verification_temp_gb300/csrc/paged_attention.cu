@@ -792,18 +792,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // plan
 // ---------------------------------------------------------------------------
 
-struct AttnPlan {
-  int workers, rows, tile_log2, unit_cost;
-  // Units of at most so many tiles are not cut: one launch for two (4.4 us of the
-  // caller's time) and no join (3 to 5 us), against tiles that follow each other on
-  // one worker.  From both forms at B = 1, 16 and 64 over 32 to 8192 keys, contexts of
-  // one length and of 1/16 of it upwards, us cut and whole: one token of 32 heads of
-  // 128 on 8, 512 keys 12.0, 12.4 (B = 1) and 36.2, 30.8 (B = 64), 1024 keys 12.6, 16.7
-  // and 56, 51, ragged 39, 43; trees of 60 nodes, 1024 keys 26, 24 (B = 1) and 40, 27
-  // (B = 16), 2048 keys 36, 37 and 61, 44, 4096 keys 37, 62.  Borders that move to the
-  // ends of longer units did not pay.
-  int few;
-};
+// AttnPlan::few.
+// Units of at most so many tiles are not cut: one launch for two (4.4 us of the
+// caller's time) and no join (3 to 5 us), against tiles that follow each other on
+// one worker.  From both forms at B = 1, 16 and 64 over 32 to 8192 keys, contexts of
+// one length and of 1/16 of it upwards, us cut and whole: one token of 32 heads of
+// 128 on 8, 512 keys 12.0, 12.4 (B = 1) and 36.2, 30.8 (B = 64), 1024 keys 12.6, 16.7
+// and 56, 51, ragged 39, 43; trees of 60 nodes, 1024 keys 26, 24 (B = 1) and 40, 27
+// (B = 16), 2048 keys 36, 37 and 61, 44, 4096 keys 37, 62.  Borders that move to the
+// ends of longer units did not pay.
 
 constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
 
@@ -876,29 +873,38 @@ size_t attention_workspace_bytes(int N, int G, int D, int dtype) {
   return narrow > wide ? narrow : wide;
 }
 
+void take_plan(AttnParams &p, const AttnPlan &plan, void *workspace) {
+  p.workers = plan.workers;
+  p.rows = plan.rows;
+  p.tile_log2 = plan.tile_log2;
+  p.unit_cost = plan.unit_cost;
+  p.whole = whole_units(p, plan.few);
+  p.row_lines = 1;
+  p.join = static_cast<JoinDesc *>(workspace);
+  p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                     align32(p.workers * sizeof(JoinDesc)));
+}
+
+cudaError_t launch_join(const AttnParams &p, int dtype, cudaStream_t stream) {
+  const dim3 grid(p.workers, std::min(8, std::min(p.rows, p.S.N * p.G)));
+  if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinThreads, 0, stream, p);
+  if (dtype == SPEC_BF16)
+    return launch_behind(join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, stream, p);
+  return launch_behind(join_kernel<__half>, grid, kJoinThreads, 0, stream, p);
+}
+
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream) {
   const int P = p.C.page_size;
-  auto take = [&](const AttnPlan &plan) {
-    p.workers = plan.workers;
-    p.rows = plan.rows;
-    p.tile_log2 = plan.tile_log2;
-    p.unit_cost = plan.unit_cost;
-    p.whole = whole_units(p, plan.few);
-    p.row_lines = 1;
-  };
   WideMaps maps;
   bool wide = wide_sizes(p.G, p.D, dtype) && P % 8 == 0;
   if (wide) {
-    take(wide_plan(p.S.N, p.G, p.D));
+    take_plan(p, wide_plan(p.S.N, p.G, p.D), workspace);
     // row tiles of a tree see the same keys; those of a chain end at their own
     const int tiles = (p.S.N * p.G + p.rows - 1) / p.rows;
     if (p.mask && tiles <= kMaxRowLines) p.row_lines = tiles;
     wide = wide_maps(p, dtype, &maps);
   }
-  if (!wide) take(narrow_plan(p.D, dtype));
-  p.join = static_cast<JoinDesc *>(workspace);
-  p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                     align32(p.workers * sizeof(JoinDesc)));
+  if (!wide) take_plan(p, narrow_plan(p.D, dtype), workspace);
   cudaError_t e;
   if (dtype == SPEC_F32) {
     if (p.D <= 64) {
@@ -914,11 +920,7 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
     e = dtype == SPEC_BF16 ? start16<Bf16>(p, stream) : start16<F16>(p, stream);
   }
   if (e != cudaSuccess || p.whole) return e;
-  const dim3 grid(p.workers, std::min(8, std::min(p.rows, p.S.N * p.G)));
-  if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinThreads, 0, stream, p);
-  if (dtype == SPEC_BF16)
-    return launch_behind(join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, stream, p);
-  return launch_behind(join_kernel<__half>, grid, kJoinThreads, 0, stream, p);
+  return launch_join(p, dtype, stream);
 }
 
 }  // namespace sv

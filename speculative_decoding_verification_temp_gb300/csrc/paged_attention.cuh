@@ -67,6 +67,19 @@ struct JoinDesc {
 
 size_t attention_workspace_bytes(int N, int G, int D, int dtype);
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream);
+// The same over a cache of 4-bit rows; dtype: of queries and outputs.
+size_t attention_q4_workspace_bytes(int N, int G, int D);
+cudaError_t launch_attention_q4(AttnParams &p, int dtype, void *workspace, cudaStream_t stream);
+
+// What a kernel makes of the rows; few: units of at most so many tiles are not cut.
+struct AttnPlan {
+  int workers, rows, tile_log2, unit_cost, few;
+};
+size_t plan_bytes(const AttnPlan &plan, int D);
+// Takes the plan and lays out the workspace.
+void take_plan(AttnParams &p, const AttnPlan &plan, void *workspace);
+// Joins the pieces of cut units behind their kernel.
+cudaError_t launch_join(const AttnParams &p, int dtype, cudaStream_t stream);
 // The form on tensor memory: one or two tiles of wide_tile_rows(G) rows per unit
 // (p.rows), head_dim 64 or 128, 16-bit types.  wide_maps: false where the
 // tensors cannot be described to TMA.

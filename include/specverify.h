@@ -700,6 +700,22 @@ spec_status spec_cache_read(spec_kv_cache cache, spec_page_table pages, const in
                             const int32_t *num, int B, int N, spec_dtype dtype, spec_rows k_out,
                             spec_rows v_out, uint32_t *out_flags, spec_stream_t stream);
 
+/* spec_paged_attention over a cache of 4-bit rows (cache.dtype SPEC_Q4): keys and values
+ * are what the rows stand for.  dtype: of q and out, SPEC_BF16 or SPEC_F16.  Arguments,
+ * masks, windows, flags, errors and limits as for spec_paged_attention otherwise; a query
+ * that is not finite makes its row NaN.  Values enter the products rounded to float16,
+ * and weights to float16 (to zero below 2^-32 of a row's
+ * largest). */
+size_t spec_paged_attention_q4_workspace_size(int B, int N, int num_q_heads, int num_kv_heads,
+                                              int head_dim, spec_dtype dtype);
+spec_status spec_paged_attention_q4(
+    const void *q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, spec_dtype dtype, spec_kv_cache cache, spec_page_table pages,
+    const int32_t *context_len, const int32_t *num_new, int B, int N, const uint64_t *tree_mask,
+    int64_t mask_seq_stride, const int32_t *position, int64_t position_seq_stride, float scale,
+    int window, int sinks, void *out, float *out_lse, uint32_t *out_flags, void *workspace,
+    size_t workspace_bytes, spec_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

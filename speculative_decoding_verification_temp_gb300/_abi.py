@@ -57,6 +57,8 @@ EXPORTS = (
     "spec_rotary",
     "spec_cache_append_rotary",
     "spec_cache_read",
+    "spec_paged_attention_q4_workspace_size",
+    "spec_paged_attention_q4",
 )
 
 
@@ -183,6 +185,12 @@ def load():
     lib.spec_cache_read.argtypes = [spec_kv_cache, spec_page_table, _p, _p, _i, _i, _i, spec_rows,
                                     spec_rows, _p, _p]
     lib.spec_cache_read.restype = _i
+    lib.spec_paged_attention_q4_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+    lib.spec_paged_attention_q4_workspace_size.restype = _sz
+    lib.spec_paged_attention_q4.argtypes = [
+        _p, _i64, _i64, _i64, _i, _i, spec_kv_cache, spec_page_table, _p, _p, _i, _i, _p, _i64, _p,
+        _i64, _f, _i, _i, _p, _p, _p, _p, _sz, _p]
+    lib.spec_paged_attention_q4.restype = _i
     _lib = lib
     return lib
 

@@ -175,34 +175,30 @@ bool attention_sizes_ok(int B, int N, int Hq, int Hkv, int D, spec_dtype dtype) 
          static_cast<int64_t>(B) * N < (1 << 28);
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int num_kv_heads,
-                                           int head_dim, spec_dtype dtype) {
-  if (!attention_sizes_ok(B, N, num_q_heads, num_kv_heads, head_dim, dtype)) return 0;
-  return sv::attention_workspace_bytes(N, num_q_heads / num_kv_heads, head_dim, dtype);
+size_t workspace_of(int N, int G, int D, spec_dtype dtype, bool four) {
+  return four ? sv::attention_q4_workspace_bytes(N, G, D) : sv::attention_workspace_bytes(N, G, D, dtype);
 }
 
-spec_status spec_paged_attention(
+// dtype: of q and out; four: over 4-bit rows.
+spec_status attention_call(
     const void *q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
-    int num_q_heads, spec_kv_cache cache, spec_page_table pages, const int32_t *context_len,
+    int num_q_heads, spec_dtype dtype, bool four, spec_kv_cache cache, spec_page_table pages, const int32_t *context_len,
     const int32_t *num_new, int B, int N, const uint64_t *tree_mask, int64_t mask_seq_stride,
     const int32_t *position, int64_t position_seq_stride, float scale, int window, int sinks,
     void *out, float *out_lse, uint32_t *out_flags, void *workspace, size_t workspace_bytes,
     spec_stream_t stream) {
-  const int esize = kv_esize(cache.dtype);
+  const int esize = kv_esize(dtype);
   if (esize == 0 || B < 0 || N < 1 || N > kMaxNew || num_q_heads < 1 || !(scale > 0.f) ||
       !(scale * sv::kLog2e < INFINITY) || sinks < 0)
     return SPEC_ERR_INVALID_ARG;
   if (B == 0) return SPEC_OK;
-  if (const spec_status s = check_cache(cache); s != SPEC_OK) return s;
-  if (cache.num_layers != 1 || num_q_heads % cache.num_heads != 0 || !q || !out || !context_len ||
+  if (const spec_status s = check_cache(cache, four); s != SPEC_OK) return s;
+  if ((four ? cache.dtype != SPEC_Q4 || dtype == SPEC_F32 : cache.dtype != dtype) ||
+      cache.num_layers != 1 || num_q_heads % cache.num_heads != 0 || !q || !out || !context_len ||
       !table_ok(pages, cache.page_size) || (window > 0 && tree_mask && !position) ||
       mask_seq_stride < 0 || position_seq_stride < 0)
     return SPEC_ERR_INVALID_ARG;
-  if (!attention_sizes_ok(B, N, num_q_heads, cache.num_heads, cache.head_dim, cache.dtype))
+  if (!attention_sizes_ok(B, N, num_q_heads, cache.num_heads, cache.head_dim, dtype))
     return SPEC_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !stride_ok(q_seq_stride, B, cache.head_dim, esize) ||
       !stride_ok(q_token_stride, N, cache.head_dim, esize) ||
@@ -220,7 +216,7 @@ spec_status spec_paged_attention(
   if (q0 < o1 && o0 < q1) return SPEC_ERR_INVALID_ARG;
   const int group = num_q_heads / cache.num_heads;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 31u) != 0 ||
-      workspace_bytes < sv::attention_workspace_bytes(N, group, cache.head_dim, cache.dtype))
+      workspace_bytes < workspace_of(N, group, cache.head_dim, dtype, four))
     return SPEC_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   sv::AttnParams p = {};
@@ -251,7 +247,52 @@ spec_status spec_paged_attention(
     const cudaError_t e = sv::launch_kv_flags(p.S, p.C, false, p.window, p.sinks, out_flags, st);
     if (e != cudaSuccess) return map_cuda(e);
   }
-  return map_cuda(sv::launch_attention(p, cache.dtype, workspace, st));
+  return map_cuda(four ? sv::launch_attention_q4(p, dtype, workspace, st)
+                       : sv::launch_attention(p, dtype, workspace, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_paged_attention_workspace_size(int B, int N, int num_q_heads, int num_kv_heads,
+                                           int head_dim, spec_dtype dtype) {
+  if (!attention_sizes_ok(B, N, num_q_heads, num_kv_heads, head_dim, dtype)) return 0;
+  return sv::attention_workspace_bytes(N, num_q_heads / num_kv_heads, head_dim, dtype);
+}
+
+spec_status spec_paged_attention(
+    const void *q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, spec_kv_cache cache, spec_page_table pages, const int32_t *context_len,
+    const int32_t *num_new, int B, int N, const uint64_t *tree_mask, int64_t mask_seq_stride,
+    const int32_t *position, int64_t position_seq_stride, float scale, int window, int sinks,
+    void *out, float *out_lse, uint32_t *out_flags, void *workspace, size_t workspace_bytes,
+    spec_stream_t stream) {
+  return attention_call(q, q_seq_stride, q_token_stride, q_head_stride, num_q_heads, cache.dtype, false,
+                        cache, pages, context_len, num_new, B, N, tree_mask, mask_seq_stride, position,
+                        position_seq_stride, scale, window, sinks, out, out_lse, out_flags, workspace,
+                        workspace_bytes, stream);
+}
+
+size_t spec_paged_attention_q4_workspace_size(int B, int N, int num_q_heads, int num_kv_heads,
+                                              int head_dim, spec_dtype dtype) {
+  if (!attention_sizes_ok(B, N, num_q_heads, num_kv_heads, head_dim, dtype) || dtype == SPEC_F32 ||
+      (head_dim != 64 && head_dim != 128))
+    return 0;
+  return workspace_of(N, num_q_heads / num_kv_heads, head_dim, dtype, true);
+}
+
+spec_status spec_paged_attention_q4(
+    const void *q, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, spec_dtype dtype, spec_kv_cache cache, spec_page_table pages,
+    const int32_t *context_len, const int32_t *num_new, int B, int N, const uint64_t *tree_mask,
+    int64_t mask_seq_stride, const int32_t *position, int64_t position_seq_stride, float scale,
+    int window, int sinks, void *out, float *out_lse, uint32_t *out_flags, void *workspace,
+    size_t workspace_bytes, spec_stream_t stream) {
+  return attention_call(q, q_seq_stride, q_token_stride, q_head_stride, num_q_heads, dtype, true, cache,
+                        pages, context_len, num_new, B, N, tree_mask, mask_seq_stride, position,
+                        position_seq_stride, scale, window, sinks, out, out_lse, out_flags, workspace,
+                        workspace_bytes, stream);
 }
 
 spec_status spec_cache_append(

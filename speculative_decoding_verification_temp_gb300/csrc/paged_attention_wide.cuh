@@ -105,6 +105,13 @@ __device__ __forceinline__ void box_load(uint32_t to, const CUtensorMap *map, co
       "l"(map), "r"(smem_u32(bar)), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(x4)
       : "memory");
 }
+// Untiled: both addresses and the size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t to, const void *from, uint32_t bytes, const void *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+      "l"(from), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 template <int kRegs>
 __device__ __forceinline__ void more_regs() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));

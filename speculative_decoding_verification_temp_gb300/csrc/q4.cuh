@@ -35,6 +35,11 @@ __device__ __forceinline__ float2 q4_pair(uint32_t scale_min) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&scale_min));
 }
 
+// Whether every value of a group with this scale and minimum is one of float16's.
+__device__ __forceinline__ bool q4_finite(float2 scale_min) {
+  return fabsf(scale_min.y) + 15.f * fabsf(scale_min.x) < 65520.f;
+}
+
 // Values that are the same float32 operations in a group's every thread: the codes
 // are those of round((x - minimum) (1 / scale)) wherever they are computed.
 struct Q4Scale {

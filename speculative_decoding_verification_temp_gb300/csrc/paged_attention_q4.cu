@@ -41,16 +41,21 @@ constexpr int kSms4 = 152;
 // larger scales lower the weights (see cap).
 constexpr float kLift4 = 6.f;
 
-template <int D, int NT>
+// R: rows of a unit, 4, 8 or 16.
+template <int D, int R>
 struct Rows4 {
   static constexpr int kRow = q4_row_bytes(D);
+  // Four rows leave half of the products' columns free, which take another group.
+  static constexpr bool kQuad = R == 4;
+  static constexpr int kCols = R <= 8 ? 1 : 2;         // times eight columns
   static constexpr int kWarps = 4;                     // of a CTA
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtas = NT == 1 ? 4 : 3;        // of an SM
+  static constexpr int kCtas = kCols == 1 ? 4 : 3;     // of an SM
   static constexpr int kStage = 2 * kQ4Tile * kRow;    // keys, then values
-  // a lane's part of the queries: products' operands, two factors, their sums
-  static constexpr int kQWords = D / 8 + 4;
-  static constexpr int kQBytes = NT * 32 * kQWords * 4;
+  static constexpr int kSteps = D / 16;                // of the scores' products
+  // of the queries: two operands a step, two for the sums, the factors; two steps a piece
+  static constexpr int kQPieces = kCols * (kSteps / 2 + 1);
+  static constexpr int kQBytes = kQPieces * 32 * 16;
   // what 227 KB hold
   static constexpr int kStages = std::min(4, (226 * 1024 / (kCtas * kWarps) - 512 - kQBytes) / kStage);
   static constexpr int kWarp = kStages * kStage + kQBytes;
@@ -78,14 +83,33 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ void mma8_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+// 8x8 matrices of 16-bit halves; with "memory": the ring's contents change under them.
+__device__ __forceinline__ void matrices4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void matrices4_turned(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void matrices2(uint32_t (&r)[2], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void matrices2_turned(uint32_t (&r)[2], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r[0]), "=r"(r[1])
+               : "r"(at)
+               : "memory");
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 __device__ __forceinline__ uint32_t word_at(const char *p) { return *reinterpret_cast<const uint32_t *>(p); }
+__device__ __forceinline__ float scale_at(const char *p) { return __half2float(*reinterpret_cast<const __half *>(p)); }
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // nibbles of two halves
 
 // Two outputs of token n that the keys' values which are not finite (beyond float16
 // too) add, from the parts of tiles that some row does not see whole; see
@@ -120,24 +144,30 @@ static __device__ __noinline__ float2 nonfinite_values_q4(const AttnParams &p, c
   return make_float2(a[0], a[1]);
 }
 
-// A lane's part of eight rows of queries, from row nt * 8 of the unit: for the products
-// with the codes, row g of column g; see Rows4::kQWords.
-template <class E, int D>
-__device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitWalk &u, int nt, int lane,
-                                                uint2 *to) {
+// A lane's operands of the scores' products, of eight columns of queries (four with
+// kQuad) from row `first` of the unit, into pieces of 16 bytes [step / 2][lane]:
+//   kQuad, D 128, step 4 pr + i: nibble i of group 2 pr in columns 0..3, of group 2 pr + 1
+//     in columns 4..7, each with zeros for the other's keys' codes
+//   kQuad, D 64, step 2 pc + i: nibbles 2i, 2i + 1 of words 4 pc + t: columns 0..3 of the
+//     first two (group 2 pc), 4..7 of the others
+//   D 128, step 2 j + i: nibbles 2i, 2i + 1 of group j; D 64, step j: group j
+// then the sums of each group in two float16 terms, against the codes' (scale, minimum)
+// pairs, and the factors of this lane's two rows of scores.
+template <class E, int D, bool kQuad>
+__device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitWalk &u, int first, int lane,
+                                                uint4 *to) {
   using TE = typename E::T;
-  constexpr int kN = D / 16;  // values of each group
-  const int g = lane >> 2, t = lane & 3, live = u.live_rows(p), row = nt * 8 + g;
+  constexpr int kN = D / 16;         // values of each group that this lane has
+  constexpr bool kPieces = D == 128 || kQuad;  // in pieces of eight neighbours
+  constexpr int kParts = kPieces ? D / 32 : 4, kEach = kPieces ? 8 : kN;
+  const int g = lane >> 2, t = lane & 3, live = u.live_rows(p), row = first + (kQuad ? g & 3 : g);
   const int r = u.r0 + min(row, live - 1), n = r / p.G;
   const char *q = p.q + u.b * p.q_seq + n * p.q_token + (u.h * p.G + r - n * p.G) * p.q_head;
-  float x[4][kN];
-  float top = 0.f;
-  bool odd = false;
-  uint32_t v[4][kN / 2];
+  uint32_t v[kParts][kEach / 2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const TE *from = reinterpret_cast<const TE *>(q) + j * (D / 4) + t * kN;
-    if constexpr (D == 128) {
+  for (int j = 0; j < kParts; ++j) {
+    const TE *from = reinterpret_cast<const TE *>(q) + j * (D / kParts) + t * kEach;
+    if constexpr (kEach == 8) {
       const uint4 y = *reinterpret_cast<const uint4 *>(from);
       v[j][0] = y.x, v[j][1] = y.y, v[j][2] = y.z, v[j][3] = y.w;
     } else {
@@ -145,10 +175,13 @@ __device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitW
       v[j][0] = y.x, v[j][1] = y.y;
     }
   }
+  float x[kParts][kEach];
+  float top = 0.f;
+  bool odd = false;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < kParts; ++j)
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
+    for (int e = 0; e < kEach; ++e) {
       x[j][e] = row < live ? E::to(reinterpret_cast<const TE *>(v[j])[e]) : 0.f;
       odd |= !isfinite(x[j][e]);
       top = fmaxf(top, fabsf(x[j][e]));
@@ -164,32 +197,65 @@ __device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitW
   // a query that is not finite makes its row NaN
   const float factor = odd ? __int_as_float(0x7FC00000)
                            : p.scale_log2 * __int_as_float((127 - exponent) << 23);
-  uint32_t sums = 0u;
+  float sum[kParts];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float sum = 0.f;
+  for (int j = 0; j < kParts; ++j) {
+    sum[j] = 0.f;
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
+    for (int e = 0; e < kEach; ++e) {
       // as the products see it
       x[j][e] = odd ? 0.f : __half2float(__float2half_rn(x[j][e] * up));
-      sum += x[j][e];
+      sum[j] += x[j][e];
     }
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-    const __half hi = __float2half_rn(sum);
-    const __half lo = __float2half_rn(sum - __half2float(hi));
-    if (t == j) sums = as_word(__halves2half2(hi, lo));
-#pragma unroll
-    for (int s = 0; s < kN / 4; ++s) {
-      to[(j * (kN / 4) + s) * 32] =
-          make_uint2(F16::pack(x[j][4 * s], x[j][4 * s + 1]),
-                     F16::pack(x[j][4 * s + 2] * 0.0625f, x[j][4 * s + 3] * 0.0625f));
-    }
+    sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 1);
+    if (kEach * 4 == D / 4) sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 2);
   }
-  // of this lane's two columns of the scores
-  to[kN * 32] = make_uint2(__float_as_uint(__shfl_sync(0xFFFFFFFFu, factor, 2 * t * 4)),
-                           __float_as_uint(__shfl_sync(0xFFFFFFFFu, factor, (2 * t + 1) * 4)));
-  to[(kN + 1) * 32] = make_uint2(sums, 0u);
+  // the sum of group t
+  float mine = 0.f;
+  if constexpr (kEach * 4 == D / 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t == j) mine = sum[j];
+  } else {
+    // a piece is two groups: lanes 0, 1 of four have the first, 2, 3 the second
+    const int from = (lane & ~3) | (2 * (t & 1));
+    const float s0 = __shfl_sync(0xFFFFFFFFu, sum[0], from), s1 = __shfl_sync(0xFFFFFFFFu, sum[1], from);
+    mine = t >> 1 ? s1 : s0;
+  }
+  if (kQuad && g >= 4) mine = 0.f;
+  auto pair = [&](int j, int i) {  // nibble i of this lane's word j
+    const float f = i & 1 ? 0.0625f : 1.f;
+    return F16::pack(x[j][2 * i] * f, x[j][2 * i + 1] * f);
+  };
+  uint32_t b[kN * 2];
+  if constexpr (kQuad && D == 128) {
+#pragma unroll
+    for (int pr = 0; pr < 2; ++pr)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        b[(pr * 4 + i) * 2] = g < 4 ? pair(2 * pr, i) : 0u;
+        b[(pr * 4 + i) * 2 + 1] = g < 4 ? 0u : pair(2 * pr + 1, i);
+      }
+  } else if constexpr (kQuad) {
+    const bool here = (g >> 2) == (t >> 1);
+#pragma unroll
+    for (int pc = 0; pc < 2; ++pc)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[pc * 4 + i] = here ? pair(pc, i) : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < kEach / 2; ++i) b[j * (kEach / 2) + i] = pair(j, i);
+  }
+#pragma unroll
+  for (int i = 0; i < kN / 2; ++i) to[i * 32] = make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3]);
+  const __half hi = __float2half_rn(mine), lo = __float2half_rn(mine - __half2float(hi));
+  const int row0 = kQuad ? 2 * (t & 1) : 2 * t;
+  to[kN / 2 * 32] = make_uint4(static_cast<uint32_t>(__half_as_ushort(hi)) << 16,
+                               static_cast<uint32_t>(__half_as_ushort(lo)) << 16,
+                               __float_as_uint(__shfl_sync(0xFFFFFFFFu, factor, row0 * 4)),
+                               __float_as_uint(__shfl_sync(0xFFFFFFFFu, factor, (row0 + 1) * 4)));
 }
 
 // Quotients of numbers below 2^31 by a page size.
@@ -217,12 +283,13 @@ struct Rows4Ctl {
 
 }  // namespace
 
-template <class E, int D, int NT>
-__global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
+template <class E, int D, int R>
+__global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     rows4_kernel(const __grid_constant__ AttnParams p) {
-  using L = Rows4<D, NT>;
+  using L = Rows4<D, R>;
   using TE = typename E::T;
-  constexpr int kRow = L::kRow, kStages = L::kStages;
+  constexpr int kRow = L::kRow, kStages = L::kStages, NT = L::kCols;
+  constexpr bool kQuad = L::kQuad, kPieces = D == 128 || kQuad;
   extern __shared__ __align__(128) char smem4[];
   __shared__ Rows4Ctl<L::kWarps, kStages> ctl;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -247,22 +314,26 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
   if (lane == 0) write_join(p, line, busy ? &u : nullptr);
 
   const int g = lane >> 2, t = lane & 3;
-  constexpr int kSteps = D / 16;   // of the scores' products
   constexpr int kOuts = D / 16;    // 16 dimensions each of the outputs
-  // bytes of two tokens' words: this lane's codes of the even dimensions, the odd ones
-  const int byte = D == 128 ? g & 1 : (g >> 1) & 1;
-  // (the halves' upper bytes are whatever byte 0 is, and masked out below)
-  const uint32_t sel_even = byte | (4 + byte) << 8, sel_odd = (2 + byte) | (6 + byte) << 8;
-  const uint32_t nibble = D == 64 && (g & 1) ? 0x00F000F0u : 0x000F000Fu;
+  constexpr int kKeys = kQuad ? 1 : 2;  // of 16, that this lane weighs
+  auto key_of = [&](int h) { return kQuad ? (t >> 1) * 8 + g : h * 8 + g; };
+  auto row_of = [&](int nt, int e) { return kQuad ? 2 * (t & 1) + e : nt * 8 + 2 * t + e; };
+  // where this lane's row of a matrix of codes begins: keys 0..7 and 8..15 of one piece of
+  // 16 bytes, then of the next
+  const int matrix = ((lane & 7) + ((lane >> 3) & 1) * 8) * kRow + (lane >> 4) * 16;
   char *ring = smem4 + warp * L::kWarp;
-  uint2 *queries = reinterpret_cast<uint2 *>(ring + kStages * L::kStage) + lane;
+  const uint32_t ring_at = smem_u32(ring);
+  uint4 *queries = reinterpret_cast<uint4 *>(ring + kStages * L::kStage) + lane;
   const PageSize P(p.C.page_size);
   const bool packed_k = P.size == 1 || p.C.k_token == kRow, packed_v = P.size == 1 || p.C.v_token == kRow;
+  // pages that are whole parts of a tile, or hold whole tiles
+  const bool even = packed_k && packed_v && (P.size & (P.size - 1)) == 0;
+  const int even_keys = min(P.size, kQ4Tile);  // of a lane's copy there
   uint32_t asked = 0, tiles = 0;  // tiles copied, and weighed
   uint32_t there[kStages];        // which of a tile's keys were copied
 
-  // The page of tile i that this lane looks up: a tile lies on `slots` pages, at most
-  // one per lane.
+  // The page of tile i that this lane looks up: a tile lies on at most 32 pages, one per
+  // lane.
   auto look_up = [&](int i) {
     if (i >= u.i1) return -1;
     const int at0 = key_tile(u.k, i) * kQ4Tile, last = min(at0 + kQ4Tile, u.k.end) - 1;
@@ -275,43 +346,58 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
   };
   // Asks for tile i, whose pages are known; by the whole warp.
   auto ask = [&](int i, int page) {
-    const int at0 = key_tile(u.k, i) * kQ4Tile, index0 = P.index(at0);
-    const int begin = (index0 + lane) * P.size - at0;  // of this lane's page, if it has one
-    // the page's keys that are there: [from, to), and from `again` on, where the window
-    // begins behind the sinks within it
-    const int from = max(0, begin);
-    int end = max(from, min(min(kQ4Tile, begin + P.size), u.k.end - at0));
-    if (!page_ok(p.C, page)) end = from;
-    int to = end, again = end;
-    if (p.sinks < u.k.first) {
-      to = min(max(from, p.sinks - at0), end);
-      again = min(max(to, u.k.first - at0), end);
-    }
-    const uint32_t mine = (low_bits(to) & ~low_bits(from)) | (low_bits(end) & ~low_bits(again));
-    const uint32_t word = __reduce_or_sync(0xFFFFFFFFu, mine);
-    const uint32_t st = asked % kStages;
+    const int at0 = key_tile(u.k, i) * kQ4Tile;
+    const uint32_t st = asked % kStages, stage = ring_at + st * L::kStage;
     const void *full = &ctl.full[warp][st];
-    if (lane == 0) bar_expect(full, 2 * kRow * __popc(word));
-    __syncwarp();
-    if (mine) {
-      const uint32_t stage = smem_u32(ring) + st * L::kStage;
-      const char *k = p.C.k + page * p.C.k_page + u.h * p.C.k_head;
-      const char *v = p.C.v + page * p.C.v_page + u.h * p.C.v_head;
+    const char *k = p.C.k + page * p.C.k_page + u.h * p.C.k_head;
+    const char *v = p.C.v + page * p.C.v_page + u.h * p.C.v_head;
+    uint32_t word;
+    const bool mine = lane * even_keys < kQ4Tile;
+    if (even && at0 + kQ4Tile <= u.k.end && (at0 >= u.k.first || p.sinks >= u.k.first) &&
+        __all_sync(0xFFFFFFFFu, !mine || page_ok(p.C, page))) {
+      // a tile without gaps
+      word = 0xFFFFFFFFu;
+      if (lane == 0) bar_expect(full, L::kStage);
+      __syncwarp();
+      if (mine) {
+        const int offset = (at0 & (P.size - 1)) * kRow, to = lane * even_keys * kRow;
+        bulk_load(stage + to, k + offset, even_keys * kRow, full);
+        bulk_load(stage + kQ4Tile * kRow + to, v + offset, even_keys * kRow, full);
+      }
+    } else {
+      const int begin = (P.index(at0) + lane) * P.size - at0;  // of this lane's page, if it has one
+      // the page's keys that are there: [from, to), and from `again` on, where the window
+      // begins behind the sinks within it
+      const int from = max(0, begin);
+      int end = max(from, min(min(kQ4Tile, begin + P.size), u.k.end - at0));
+      if (!page_ok(p.C, page)) end = from;
+      int to = end, again = end;
+      if (p.sinks < u.k.first) {
+        to = min(max(from, p.sinks - at0), end);
+        again = min(max(to, u.k.first - at0), end);
+      }
+      const uint32_t keys = (low_bits(to) & ~low_bits(from)) | (low_bits(end) & ~low_bits(again));
+      word = __reduce_or_sync(0xFFFFFFFFu, keys);
+      if (lane == 0) bar_expect(full, 2 * kRow * __popc(word));
+      __syncwarp();
       auto copy = [&](bool packed, uint32_t to_s, const char *base, long long token, int a, int b) {
-        if (a >= b) return;
         const int step = packed ? b - a : 1;
         for (int key = a; key < b; key += step)
           bulk_load(to_s + key * kRow, base + (key - begin) * token, step * kRow, full);
       };
-      copy(packed_k, stage, k, p.C.k_token, from, to);
-      copy(packed_v, stage + kQ4Tile * kRow, v, p.C.v_token, from, to);
-      copy(packed_k, stage, k, p.C.k_token, again, end);
-      copy(packed_v, stage + kQ4Tile * kRow, v, p.C.v_token, again, end);
+      if (keys) {
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int a = x ? again : from, b = x ? end : to;
+          copy(packed_k, stage, k, p.C.k_token, a, b);
+          copy(packed_v, stage + kQ4Tile * kRow, v, p.C.v_token, a, b);
+        }
+      }
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kStages; ++i)
-      if (st == i) there[i] = word;
+    for (int x = 0; x < kStages; ++x)
+      if (st == x) there[x] = word;
     if (asked++ == 0) first_wait(full, p.first_wait, &ctl.dead);
   };
 
@@ -325,17 +411,18 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
       page = behind;
     }
     for (int nt = 0; nt < NT; ++nt)
-      prepare_queries<E, D>(p, u, nt, lane, queries + nt * 16 * L::kQWords);
+      prepare_queries<E, D, kQuad>(p, u, nt * 8, lane, queries + nt * (L::kSteps / 2 + 1) * 32);
     __syncwarp();
-    uint32_t qs[NT];
+    uint32_t qs[NT][2];
     float c[NT][2];
     const int live = u.live_rows(p);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint2 x = queries[(nt * (kSteps + 2) + kSteps) * 32];
-      c[nt][0] = __uint_as_float(x.x);
-      c[nt][1] = __uint_as_float(x.y);
-      qs[nt] = queries[(nt * (kSteps + 2) + kSteps + 1) * 32].x;
+      const uint4 x = queries[(nt * (L::kSteps / 2 + 1) + L::kSteps / 2) * 32];
+      qs[nt][0] = x.x;
+      qs[nt][1] = x.y;
+      c[nt][0] = __uint_as_float(x.z);
+      c[nt][1] = __uint_as_float(x.w);
     }
     float m[NT][2], l[NT][2], o[NT][kOuts][4], om[NT][4];
 #pragma unroll
@@ -358,97 +445,149 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
       }
       const uint32_t st = tiles % kStages;
       if (!warp_wait(&ctl.full[warp][st], (tiles / kStages) & 1u, &ctl.dead)) break;
-      const int at0 = key_tile(u.k, i) * kQ4Tile;
       uint32_t valid = there[0];
 #pragma unroll
       for (int x = 1; x < kStages; ++x)
         if (st == x) valid = there[x];
+      if (valid == 0u) continue;
+      const int at0 = key_tile(u.k, i) * kQ4Tile;
       char *k_s = ring + st * L::kStage, *v_s = k_s + kQ4Tile * kRow;
-      if (valid != 0u) {
-        // this lane's key: its values' scales
-        uint4 *scales = reinterpret_cast<uint4 *>(v_s + lane * kRow + D / 2);
-        uint4 s = *scales;
-        const bool masked = valid != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Tile);
-        if (masked) {
-          // rows that were not copied stand for zeros, and so do groups that are not
-          // finite, which nonfinite_values_q4 adds
-          uint32_t *w = reinterpret_cast<uint32_t *>(&s);
-          const bool there = (valid >> lane) & 1u;
+      const uint32_t k_at = ring_at + st * L::kStage, v_at = k_at + kQ4Tile * kRow;
+      // this lane's key: its values' scales
+      uint4 *scales = reinterpret_cast<uint4 *>(v_s + lane * kRow + D / 2);
+      uint4 s = *scales;
+      const bool masked = valid != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Tile);
+      if (masked) {
+        // rows that were not copied stand for zeros, and so do groups that are not
+        // finite, which nonfinite_values_q4 adds
+        uint32_t *w = reinterpret_cast<uint32_t *>(&s);
+        const bool copied = (valid >> lane) & 1u;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!there || !q4_finite(q4_pair(w[j]))) {
-              bad |= there;
-              w[j] = 0u;
+        for (int j = 0; j < 4; ++j)
+          if (!copied || !q4_finite(q4_pair(w[j]))) {
+            bad |= copied;
+            w[j] = 0u;
+          }
+        *scales = s;
+        __syncwarp();
+      }
+      // scales of 2^(cap + 1) and more: the weights are lowered
+      if (__any_sync(0xFFFFFFFFu, ((s.x | s.y) | (s.z | s.w)) & 0x4000u)) {
+        const uint32_t top = max(max(s.x & 0x7FFFu, s.y & 0x7FFFu), max(s.z & 0x7FFFu, s.w & 0x7FFFu));
+        const uint32_t finite = __reduce_max_sync(0xFFFFFFFFu, top < 0x7C00u ? top : 0u);
+        const int more = static_cast<int>(finite >> 10) - 15 - cap;
+        if (more > 0) {
+          cap += more;
+          const float f = __int_as_float((127 - more) << 23);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              m[nt][e] += static_cast<float>(more);
+              l[nt][e] *= f;
             }
-          *scales = s;
-          __syncwarp();
-        }
-        // scales of 2^(cap + 1) and more: the weights are lowered
-        if (__any_sync(0xFFFFFFFFu, ((s.x | s.y) | (s.z | s.w)) & 0x4000u)) {
-          const uint32_t top = max(max(s.x & 0x7FFFu, s.y & 0x7FFFu), max(s.z & 0x7FFFu, s.w & 0x7FFFu));
-          const uint32_t finite = __reduce_max_sync(0xFFFFFFFFu, top < 0x7C00u ? top : 0u);
-          const int more = static_cast<int>(finite >> 10) - 15 - cap;
-          if (more > 0) {
-            cap += more;
-            const float f = __int_as_float((127 - more) << 23);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int e = 0; e < 4; ++e) {
+              om[nt][e] *= f;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                m[nt][e] += static_cast<float>(more);
-                l[nt][e] *= f;
-              }
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                om[nt][e] *= f;
-#pragma unroll
-                for (int j = 0; j < kOuts; ++j) o[nt][j][e] *= f;
-              }
+              for (int j = 0; j < kOuts; ++j) o[nt][j][e] *= f;
             }
           }
         }
+      }
+      // (once in the code: unrolled, its instructions do not stay in the cache, 189 us to
+      // 211)
 #pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-          float y[NT][4];
-          const char *r0 = k_s + (blk * 16 + g) * kRow, *r1 = r0 + 8 * kRow;
-          float a[NT][4][4], am[NT][4];
+      for (int blk = 0; blk < 2; ++blk) {
+        // ------------------------------------------------------------- scores
+        float y[NT][2 * kKeys];
+        const char *r0 = k_s + (blk * 16 + g) * kRow, *r1 = r0 + 8 * kRow;
+        uint32_t pairs[2];
+        matrices2(pairs, k_at + (blk * 16 + (lane & 15)) * kRow + D / 2);
+        if constexpr (kQuad) {
+          float a[2][4], am[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int pr = 0; pr < 2; ++pr) {
+            uint32_t r[4];
             if constexpr (D == 128) {
-              const uint32_t x0 = word_at(r0 + j * 16 + t * 4), x1 = word_at(r1 + j * 16 + t * 4);
-              const uint32_t z0 = x0 >> 8, z1 = x1 >> 8;
+              matrices4(r, k_at + matrix + blk * 16 * kRow + pr * 32);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint2 q0 = queries[(nt * (kSteps + 2) + 2 * j) * 32];
-                const uint2 q1 = queries[(nt * (kSteps + 2) + 2 * j + 1) * 32];
-                mma16_first(a[nt][j], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u,
-                            x1 & 0x00F000F0u, q0.x, q0.y);
-                mma16(a[nt][j], z0 & 0x000F000Fu, z1 & 0x000F000Fu, z0 & 0x00F000F0u,
-                      z1 & 0x00F000F0u, q1.x, q1.y);
+              for (int i = 0; i < 4; i += 2) {
+                const uint4 q = queries[(pr * 2 + i / 2) * 32];
+                if (i == 0) {
+                  mma16_first(a[pr], r[0] & kLow, r[1] & kLow, r[2] & kLow, r[3] & kLow, q.x, q.y);
+                } else {
+                  mma16(a[pr], r[0] & kLow, r[1] & kLow, r[2] & kLow, r[3] & kLow, q.x, q.y);
+                }
+                mma16(a[pr], r[0] & kHigh, r[1] & kHigh, r[2] & kHigh, r[3] & kHigh, q.z, q.w);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) r[x] >>= 8;
               }
             } else {
-              const int shift = (t & 1) * 8;
-              const uint32_t x0 = word_at(r0 + j * 8 + (t >> 1) * 4) >> shift;
-              const uint32_t x1 = word_at(r1 + j * 8 + (t >> 1) * 4) >> shift;
+              // two pieces of 16 bytes: this one's keys 0..7 and 8..15
+              const uint4 q = queries[pr * 32];
+              uint32_t r2[2];
+              matrices2(r2, k_at + (blk * 16 + (lane & 15)) * kRow + pr * 16);
+              mma16_first(a[pr], r2[0] & kLow, r2[1] & kLow, r2[0] & kHigh, r2[1] & kHigh, q.x, q.y);
+              r2[0] >>= 8, r2[1] >>= 8;
+              mma16(a[pr], r2[0] & kLow, r2[1] & kLow, r2[0] & kHigh, r2[1] & kHigh, q.z, q.w);
+            }
+          }
+          mma16_first(am, pairs[0], pairs[1], pairs[0], pairs[1], qs[0][0], qs[0][1]);
+          // columns 0..3 are groups 0 and 2, 4..7 the same rows' groups 1 and 3
+          const char *f0 = r0 + D / 2 + (t >> 1) * 4, *f1 = f0 + 8 * kRow;
+          const float s00 = scale_at(f0), s02 = scale_at(f0 + 8), s10 = scale_at(f1), s12 = scale_at(f1 + 8);
+          float z[4];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint2 q0 = queries[(nt * (kSteps + 2) + j) * 32];
-                mma16_first(a[nt][j], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u,
-                            x1 & 0x00F000F0u, q0.x, q0.y);
+          for (int e = 0; e < 4; ++e)
+            z[e] = fmaf(fmaf(e < 2 ? s02 : s12, a[1][e], (e < 2 ? s00 : s10) * a[0][e]), 16777216.f, am[e]);
+          // lanes 0, 1 of four go on with the first eight keys, 2, 3 with the second
+          const bool second = t >= 2;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? z[e] : z[2 + e], 2);
+            y[0][e] = ((second ? z[2 + e] : z[e]) + other) * c[0][e];
+          }
+        } else {
+          float a[NT][4][4], am[NT][4];
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            if constexpr (D == 128) {
+              uint32_t r[4];
+              matrices4(r, k_at + matrix + blk * 16 * kRow + j * 16);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t x0 = r[2 * x], x1 = r[2 * x + 1], z0 = x0 >> 8, z1 = x1 >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint4 q = queries[(nt * (L::kSteps / 2 + 1) + j + x) * 32];
+                  mma16_first(a[nt][j + x], x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, q.x, q.y);
+                  mma16(a[nt][j + x], z0 & kLow, z1 & kLow, z0 & kHigh, z1 & kHigh, q.z, q.w);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int at = (j + x) * 8 + (t >> 1) * 4, shift = (t & 1) * 8;
+                const uint32_t x0 = word_at(r0 + at) >> shift, x1 = word_at(r1 + at) >> shift;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint4 q = queries[(nt * (L::kSteps / 2 + 1) + j / 2) * 32];
+                  mma16_first(a[nt][j + x], x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, x ? q.z : q.x,
+                              x ? q.w : q.y);
+                }
               }
             }
           }
           const uint4 s0 = *reinterpret_cast<const uint4 *>(r0 + D / 2);
           const uint4 s1 = *reinterpret_cast<const uint4 *>(r1 + D / 2);
-          const uint32_t m0 = __byte_perm(word_at(r0 + D / 2 + t * 4), 0, 0x3232);
-          const uint32_t m1 = __byte_perm(word_at(r1 + D / 2 + t * 4), 0, 0x3232);
           const float f0[4] = {__low2float(as_half2(s0.x)), __low2float(as_half2(s0.y)),
                                __low2float(as_half2(s0.z)), __low2float(as_half2(s0.w))};
           const float f1[4] = {__low2float(as_half2(s1.x)), __low2float(as_half2(s1.y)),
                                __low2float(as_half2(s1.z)), __low2float(as_half2(s1.w))};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma8_first(am[nt], m0, m1, qs[nt]);
+            mma16_first(am[nt], pairs[0], pairs[1], pairs[0], pairs[1], qs[nt][0], qs[nt][1]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float *f = e < 2 ? f0 : f1;
@@ -457,43 +596,44 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
               y[nt][e] = fmaf(z, 16777216.f, am[nt][e]) * c[nt][e & 1];
             }
           }
-          if (masked) {
+        }
+        if (masked) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int n = (u.r0 + min(nt * 8 + 2 * t + e, live - 1)) / p.G;
+            for (int e = 0; e < 2; ++e) {
+              const int n = (u.r0 + min(row_of(nt, e), live - 1)) / p.G;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int key = blk * 16 + h * 8 + g;
-                  if (!((valid >> key) & 1u) || !sees(p, u.k, u.b, n, at0 + key)) y[nt][2 * h + e] = -INFINITY;
-                }
+              for (int h = 0; h < kKeys; ++h) {
+                const int key = blk * 16 + key_of(h);
+                if (!((valid >> key) & 1u) || !sees(p, u.k, u.b, n, at0 + key)) y[nt][2 * h + e] = -INFINITY;
               }
-          }
-        // the running maximum
+            }
+        }
+        // ------------------------------------------------------------ weights
         const float lift = kLift4 - static_cast<float>(cap);
+        auto top_of = [&](int nt, int e) { return kQuad ? y[nt][e] : fmaxf(y[nt][e], y[nt][2 * (kKeys - 1) + e]); };
         bool up = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float top = fmaxf(y[nt][e], y[nt][2 + e]);
-            up |= top - lift > m[nt][e] + kSlack;
-          }
+          for (int e = 0; e < 2; ++e) up |= top_of(nt, e) - lift > m[nt][e] + kSlack;
         if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(y[nt][e], y[nt][2 + e]);
+              float top = top_of(nt, e);
 #pragma unroll
-              for (int s = 4; s <= 16; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+              for (int x = kQuad ? 2 : 4; x <= 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
               top -= lift;
               const float to = top > m[nt][e] + kSlack ? top : m[nt][e];
               const float f = m[nt][e] == -INFINITY ? 0.f : fast_exp2(m[nt][e] - to);
               m[nt][e] = to;
               l[nt][e] *= f;
+              // (with kQuad columns 4..7 are not looked at, or hold the same rows)
               om[nt][e] *= f;
+              om[nt][2 + e] *= f;
 #pragma unroll
               for (int j = 0; j < kOuts; ++j) {
                 o[nt][j][e] *= f;
@@ -507,52 +647,89 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
           // a row that has seen nothing yet keeps weights of zero
           const float u0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], u1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float p0 = fast_exp2(y[nt][2 * h] - u0), p1 = fast_exp2(y[nt][2 * h + 1] - u1);
-              l[nt][0] += p0;
-              l[nt][1] += p1;
-              w[nt][h] = transposed(F16::pack(p0, p1));
-            }
+          for (int h = 0; h < kKeys; ++h) {
+            const float p0 = fast_exp2(y[nt][2 * h] - u0), p1 = fast_exp2(y[nt][2 * h + 1] - u1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            w[nt][h] = transposed(F16::pack(p0, p1));
+          }
         }
-          // tokens 2t, 2t + 1 of the first eight keys (h = 0) and of the second
-          const char *v0 = v_s + (blk * 16 + 2 * t) * kRow;
-          uint32_t sp[2][4], mp[2];
+        if constexpr (kQuad) {
+          // columns 0..3 have the first eight keys' weights here, 4..7 the same rows' of the
+          // second
+          const uint32_t own = w[0][0], other = __shfl_xor_sync(0xFFFFFFFFu, own, 16);
+          w[0][0] = g < 4 ? own : other;
+          w[0][1] = g < 4 ? other : own;
+        }
+        // ------------------------------------------------------------ outputs
+        // tokens 2t, 2t + 1 of the first eight keys (h = 0) and of the second
+        const char *v0 = v_s + (blk * 16 + 2 * t) * kRow;
+        uint32_t low[2];  // row 2j + 1: minima of group j
+        matrices2_turned(low, v_at + (blk * 16 + (lane & 15)) * kRow + D / 2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16(om[nt], low[0], 0u, low[1], 0u, w[nt][0], w[nt][1]);
+        if constexpr (kPieces) {
+          // scales of this column's group: of all four, or (D 64) of two pieces'
+          uint32_t sp[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const char *va = v0 + h * 8 * kRow + D / 2, *vb = va + kRow;
-            const uint4 pa = *reinterpret_cast<const uint4 *>(va), pb = *reinterpret_cast<const uint4 *>(vb);
-            sp[h][0] = __byte_perm(pa.x, pb.x, 0x5410);
-            sp[h][1] = __byte_perm(pa.y, pb.y, 0x5410);
-            sp[h][2] = __byte_perm(pa.z, pb.z, 0x5410);
-            sp[h][3] = __byte_perm(pa.w, pb.w, 0x5410);
-            // of group g mod 4; the products' other rows are not looked at
-            mp[h] = __byte_perm(word_at(va + (g & 3) * 4), word_at(vb + (g & 3) * 4), 0x7632);
+            if constexpr (D == 128) {
+              const uint4 pa = *reinterpret_cast<const uint4 *>(va), pb = *reinterpret_cast<const uint4 *>(vb);
+              sp[h][0] = __byte_perm(pa.x, pb.x, 0x5410);
+              sp[h][1] = __byte_perm(pa.y, pb.y, 0x5410);
+              sp[h][2] = __byte_perm(pa.z, pb.z, 0x5410);
+              sp[h][3] = __byte_perm(pa.w, pb.w, 0x5410);
+            } else {
+              const int x = (g >> 2) * 4;
+              sp[h][0] = __byte_perm(word_at(va + x), word_at(vb + x), 0x5410);
+              sp[h][1] = __byte_perm(word_at(va + x + 8), word_at(vb + x + 8), 0x5410);
+            }
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16(om[nt], mp[0], 0u, mp[1], 0u, w[nt][0], w[nt][1]);
+          for (int j = 0; j < D / 32; j += 2) {
+            uint32_t r[4];
+            matrices4_turned(r, v_at + matrix + blk * 16 * kRow + j * 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t a[4];
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t x0 = r[2 * x], x1 = r[2 * x + 1], z0 = x0 >> 8, z1 = x1 >> 8;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const char *at = v0 + h * 8 * kRow + j * (D / 8) + (D == 128 ? g >> 1 : g >> 2) * 4;
-              const uint32_t xa = word_at(at), xb = word_at(at + kRow);
-              a[2 * h] = __byte_perm(xa, xb, sel_even);
-              a[2 * h + 1] = __byte_perm(xa, xb, sel_odd);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = as_word(__hmul2(as_half2(w[nt][0]), as_half2(sp[0][j])));
-              const uint32_t b1 = as_word(__hmul2(as_half2(w[nt][1]), as_half2(sp[1][j])));
-              if constexpr (D == 128) {
-                mma16(o[nt][2 * j], a[0] & 0x000F000Fu, a[1] & 0x000F000Fu, a[2] & 0x000F000Fu,
-                      a[3] & 0x000F000Fu, b0, b1);
-                mma16(o[nt][2 * j + 1], a[0] & 0x00F000F0u, a[1] & 0x00F000F0u, a[2] & 0x00F000F0u,
-                      a[3] & 0x00F000F0u, b0, b1);
-              } else {
-                mma16(o[nt][j], a[0] & nibble, a[1] & nibble, a[2] & nibble, a[3] & nibble, b0, b1);
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t b0 = as_word(__hmul2(as_half2(w[nt][0]), as_half2(sp[0][j + x])));
+                const uint32_t b1 = as_word(__hmul2(as_half2(w[nt][1]), as_half2(sp[1][j + x])));
+                mma16(o[nt][2 * (j + x)], x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh, b0, b1);
+                mma16(o[nt][2 * (j + x) + 1], z0 & kLow, z0 & kHigh, z1 & kLow, z1 & kHigh, b0, b1);
               }
             }
+          }
+        } else {
+          // a group is two words: this lane's nibble of both dimensions
+          const uint32_t nibble = g & 1 ? kHigh : kLow;
+          const int byte = (g >> 1) & 1;
+          // (the halves' upper bytes are whatever byte 0 is, and masked out)
+          const uint32_t sel_even = byte | (4 + byte) << 8, sel_odd = (2 + byte) | (6 + byte) << 8;
+          uint4 pa[2], pb[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            pa[h] = *reinterpret_cast<const uint4 *>(v0 + h * 8 * kRow + D / 2);
+            pb[h] = *reinterpret_cast<const uint4 *>(v0 + (h * 8 + 1) * kRow + D / 2);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a[4], sp[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const char *at = v0 + h * 8 * kRow + j * 8 + (g >> 2) * 4;
+              const uint32_t xa = word_at(at), xb = word_at(at + kRow);
+              a[2 * h] = __byte_perm(xa, xb, sel_even) & nibble;
+              a[2 * h + 1] = __byte_perm(xa, xb, sel_odd) & nibble;
+              sp[h] = __byte_perm(reinterpret_cast<const uint32_t *>(&pa[h])[j],
+                                  reinterpret_cast<const uint32_t *>(&pb[h])[j], 0x5410);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16(o[nt][j], a[0], a[1], a[2], a[3], as_word(__hmul2(as_half2(w[nt][0]), as_half2(sp[0]))),
+                    as_word(__hmul2(as_half2(w[nt][1]), as_half2(sp[1]))));
           }
         }
       }
@@ -560,8 +737,8 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
     }
     if (*reinterpret_cast<volatile int *>(&ctl.dead)) break;
 
-    // the unit's end.  A lane has 16 bytes of outputs in a row: of row nt * 8 + 2t + e,
-    // D 128: dimensions 32 j + 4 g .. + 3, D 64: 32 j + 2 g, + 1 and the same + 16
+    // the unit's end.  A lane has 16 bytes of float32 outputs at a time, of row
+    // row_of(nt, e): dimensions d0, d0 + 1, d1, d1 + 1
     const bool whole = u.whole();
     bad = __any_sync(0xFFFFFFFFu, bad);
     float *slot = p.part + piece_slot(u, line.worker) * slot_floats(p.rows, D);
@@ -569,50 +746,65 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float low[4], sum = l[nt][e];
+        float sum = l[nt][e];
 #pragma unroll
-        for (int s = 4; s <= 16; s <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) low[j] = __shfl_sync(0xFFFFFFFFu, om[nt][e], j * 4 + t);
-        const int row = nt * 8 + 2 * t + e;
-        if (row >= live) continue;
-        const long long at = out_row(p, u.b, u.h, u.r0 + row);
+        for (int x = kQuad ? 2 : 4; x <= 16; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        const int row = row_of(nt, e);
+        // with kQuad half of the columns are another group's, or not looked at
+        const bool mine = row < live && (!kQuad || (t >> 1) == (D == 128 ? 0 : g >> 2));
+        const long long at = mine ? out_row(p, u.b, u.h, u.r0 + row) : 0;
         const float n = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<TE *>(p.out) + at * D);
         float *to = slot + slot_stats(p.rows) + static_cast<size_t>(row) * D;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           float4 y;
-          if constexpr (D == 128) {
-            y = make_float4(fmaf(o[nt][2 * j][e], 16777216.f, low[j]), fmaf(o[nt][2 * j][2 + e], 16777216.f, low[j]),
-                            fmaf(o[nt][2 * j + 1][e], 1048576.f, low[j]),
-                            fmaf(o[nt][2 * j + 1][2 + e], 1048576.f, low[j]));
+          int d0, d1;
+          if constexpr (kPieces) {
+            // codes 2i (+ 1 in odd g) of a word: neighbours swap, so that each has four
+            // dimensions of it
+            const int group = D == 128 ? j : 2 * j + (g >> 2);
+            const float lo = __shfl_sync(0xFFFFFFFFu, om[nt][e], (2 * group + 1) * 4 + t);
+            const float x0 = fmaf(o[nt][2 * j][e], 16777216.f, lo), x1 = fmaf(o[nt][2 * j][2 + e], 1048576.f, lo);
+            const float x2 = fmaf(o[nt][2 * j + 1][e], 16777216.f, lo);
+            const float x3 = fmaf(o[nt][2 * j + 1][2 + e], 1048576.f, lo);
+            const bool odd = g & 1;
+            const float z0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x2, 4);
+            const float z1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? x1 : x3, 4);
+            y = odd ? make_float4(z0, x2, z1, x3) : make_float4(x0, z0, x1, z1);
+            d0 = 32 * j + 4 * g;
+            d1 = d0 + 2;
           } else {
+            const float lo = __shfl_sync(0xFFFFFFFFu, om[nt][e], (4 * j + 1) * 4 + t);
+            const float hi = __shfl_sync(0xFFFFFFFFu, om[nt][e], (4 * j + 3) * 4 + t);
             const float f = g & 1 ? 1048576.f : 16777216.f;
-            y = make_float4(fmaf(o[nt][2 * j][e], f, low[2 * j]), fmaf(o[nt][2 * j][2 + e], f, low[2 * j]),
-                            fmaf(o[nt][2 * j + 1][e], f, low[2 * j + 1]),
-                            fmaf(o[nt][2 * j + 1][2 + e], f, low[2 * j + 1]));
+            y = make_float4(fmaf(o[nt][2 * j][e], f, lo), fmaf(o[nt][2 * j][2 + e], f, lo),
+                            fmaf(o[nt][2 * j + 1][e], f, hi), fmaf(o[nt][2 * j + 1][2 + e], f, hi));
+            d0 = 32 * j + 2 * g;
+            d1 = d0 + 16;
           }
-          const int d0 = D == 128 ? 32 * j + 4 * g : 32 * j + 2 * g, d1 = d0 + (D == 128 ? 2 : 16);
+          if (!mine) continue;
           if (bad) {
             const int token = (u.r0 + row) / p.G;
             const float2 z0 = nonfinite_values_q4<D>(p, u, token, d0), z1 = nonfinite_values_q4<D>(p, u, token, d1);
             y.x += z0.x, y.y += z0.y, y.z += z1.x, y.w += z1.y;
           }
-          if (whole) {
-            const uint32_t a = E::pack(y.x * n, y.y * n), b = E::pack(y.z * n, y.w * n);
-            if constexpr (D == 128) {
-              *reinterpret_cast<uint2 *>(out + d0 / 2) = make_uint2(a, b);
+          const uint2 packed = make_uint2(E::pack(y.x * n, y.y * n), E::pack(y.z * n, y.w * n));
+          if constexpr (kPieces) {
+            if (whole) {
+              *reinterpret_cast<uint2 *>(out + d0 / 2) = packed;
             } else {
-              out[d0 / 2] = a;
-              out[d1 / 2] = b;
+              *reinterpret_cast<float4 *>(to + d0) = y;
             }
+          } else if (whole) {
+            out[d0 / 2] = packed.x;
+            out[d1 / 2] = packed.y;
           } else {
             *reinterpret_cast<float2 *>(to + d0) = make_float2(y.x, y.y);
             *reinterpret_cast<float2 *>(to + d1) = make_float2(y.z, y.w);
           }
         }
-        if (g == 0) {
+        if (mine && (g & 3) == 0 && (kQuad || g == 0)) {
           if (!whole) {
             slot[row] = m[nt][e];
             slot[p.rows + row] = sum;
@@ -632,23 +824,26 @@ __global__ void __launch_bounds__(Rows4<D, NT>::kThreads, Rows4<D, NT>::kCtas)
 
 namespace {
 
-template <class E, int D, int NT>
+template <class E, int D, int R>
 cudaError_t start4(const AttnParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  using L = Rows4<D, NT>;
-  return launch_large(rows4_kernel<E, D, NT>, done, L::kSmem, p.workers / L::kWarps, L::kThreads, L::kSmem,
+  using L = Rows4<D, R>;
+  return launch_large(rows4_kernel<E, D, R>, done, L::kSmem, p.workers / L::kWarps, L::kThreads, L::kSmem,
                       stream, p);
 }
-template <int NT>
+template <int R>
 cudaError_t start4(const AttnParams &p, int dtype, cudaStream_t stream) {
   if (dtype == SPEC_BF16)
-    return p.D == 64 ? start4<Bf16, 64, NT>(p, stream) : start4<Bf16, 128, NT>(p, stream);
-  return p.D == 64 ? start4<F16, 64, NT>(p, stream) : start4<F16, 128, NT>(p, stream);
+    return p.D == 64 ? start4<Bf16, 64, R>(p, stream) : start4<Bf16, 128, R>(p, stream);
+  return p.D == 64 ? start4<F16, 64, R>(p, stream) : start4<F16, 128, R>(p, stream);
 }
 
+template <int R>
+AttnPlan q4_plan_of() {
+  return {Rows4<128, R>::kCtas * Rows4<128, R>::kWarps * kSms4, R, 5, 2, 8};
+}
 AttnPlan q4_plan(int N, int G) {
-  if (N * G <= 8) return {Rows4<128, 1>::kCtas * Rows4<128, 1>::kWarps * kSms4, 8, 5, 2, 8};
-  return {Rows4<128, 2>::kCtas * Rows4<128, 2>::kWarps * kSms4, 16, 5, 2, 8};
+  return N * G <= 4 ? q4_plan_of<4>() : N * G <= 8 ? q4_plan_of<8>() : q4_plan_of<16>();
 }
 
 }  // namespace
@@ -660,7 +855,9 @@ cudaError_t launch_attention_q4(AttnParams &p, int dtype, void *workspace, cudaS
   const int tiles = (p.S.N * p.G + p.rows - 1) / p.rows;
   // a CTA's workers are on one line
   if (p.mask && tiles <= 8 && p.workers / 4 % tiles == 0) p.row_lines = tiles;
-  const cudaError_t e = p.rows == 8 ? start4<1>(p, dtype, stream) : start4<2>(p, dtype, stream);
+  const cudaError_t e = p.rows == 4   ? start4<4>(p, dtype, stream)
+                        : p.rows == 8 ? start4<8>(p, dtype, stream)
+                                      : start4<16>(p, dtype, stream);
   if (e != cudaSuccess || p.whole) return e;
   return launch_join(p, dtype, stream);
 }

@@ -50,17 +50,15 @@ struct Rows4 {
   static constexpr int kCols = R <= 8 ? 1 : 2;         // times eight columns
   static constexpr int kWarps = 4;                     // of a CTA
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtas = kCols == 1 ? 4 : 3;     // of an SM
+  static constexpr int kCtas = 3;                      // of an SM (four: 179 us for 157)
   static constexpr int kStage = 2 * kQ4Tile * kRow;    // keys, then values
   static constexpr int kSteps = D / 16;                // of the scores' products
   // of the queries: two operands a step, two for the sums, the factors; two steps a piece
   static constexpr int kQPieces = kCols * (kSteps / 2 + 1);
   static constexpr int kQBytes = kQPieces * 32 * 16;
-  // what 227 KB hold
-  static constexpr int kStages = std::min(4, (226 * 1024 / (kCtas * kWarps) - 512 - kQBytes) / kStage);
-  static constexpr int kWarp = kStages * kStage + kQBytes;
+  static constexpr int kWarp = 2 * kStage + kQBytes;
   static constexpr int kSmem = kWarps * kWarp;
-  static_assert(kStages >= 2, "a copy ahead");
+  static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -82,6 +80,9 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
       "{%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void copy16(uint32_t to, const char *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 // 8x8 matrices of 16-bit halves; with "memory": the ring's contents change under them.
 __device__ __forceinline__ void matrices4(uint32_t (&r)[4], uint32_t at) {
@@ -258,29 +259,6 @@ __device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitW
                                __float_as_uint(__shfl_sync(0xFFFFFFFFu, factor, (row0 + 1) * 4)));
 }
 
-// Quotients of numbers below 2^31 by a page size.
-struct PageSize {
-  uint32_t factor;
-  int size, shift;
-  __device__ __forceinline__ PageSize(int P) {
-    size = P;
-    shift = 32 - __clz(P - 1);
-    // 2^(31 + shift) / P, rounded up, is off by less than P <= 2^shift
-    factor = static_cast<uint32_t>(((1ull << (31 + shift)) + P - 1) / P);
-  }
-  __device__ __forceinline__ int index(int at) const {
-    return size == 1 ? at : static_cast<int>(__umulhi(at, factor) >> (shift - 1));
-  }
-};
-
-template <int kWarps, int kStages>
-struct Rows4Ctl {
-  unsigned long long full[kWarps][kStages];
-  RunScratch<32 * kWarps, kWarps> runs;
-  Line lines[kWarps];
-  int dead;
-};
-
 }  // namespace
 
 template <class E, int D, int R>
@@ -288,27 +266,23 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     rows4_kernel(const __grid_constant__ AttnParams p) {
   using L = Rows4<D, R>;
   using TE = typename E::T;
-  constexpr int kRow = L::kRow, kStages = L::kStages, NT = L::kCols;
+  constexpr int kRow = L::kRow, kPieces16 = kRow / 16, NT = L::kCols;
   constexpr bool kQuad = L::kQuad, kPieces = D == 128 || kQuad;
   extern __shared__ __align__(128) char smem4[];
-  __shared__ Rows4Ctl<L::kWarps, kStages> ctl;
+  __shared__ RunScratch<L::kThreads, L::kWarps> runs;
+  __shared__ Line lines_s[L::kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) bar_init(&ctl.full[warp][i], 1);
-    ctl.dead = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   {
     Line lines[L::kWarps];
-    // barriers as well; consecutive workers on different CTAs
-    find_runs(p, ctl.runs, blockIdx.x, gridDim.x, lines);
+    // consecutive workers on different CTAs
+    find_runs(p, runs, blockIdx.x, gridDim.x, lines);
 #pragma unroll
     for (int w = 0; w < L::kWarps; ++w)
-      if (tid == w * 32) ctl.lines[w] = lines[w];
+      if (tid == w * 32) lines_s[w] = lines[w];
   }
   __syncwarp();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Line &line = ctl.lines[warp];
+  const Line &line = lines_s[warp];
   UnitWalk u;
   bool busy = u.start(p, line);
   if (lane == 0) write_join(p, line, busy ? &u : nullptr);
@@ -323,93 +297,87 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
   const int matrix = ((lane & 7) + ((lane >> 3) & 1) * 8) * kRow + (lane >> 4) * 16;
   char *ring = smem4 + warp * L::kWarp;
   const uint32_t ring_at = smem_u32(ring);
-  uint4 *queries = reinterpret_cast<uint4 *>(ring + kStages * L::kStage) + lane;
-  const PageSize P(p.C.page_size);
-  const bool packed_k = P.size == 1 || p.C.k_token == kRow, packed_v = P.size == 1 || p.C.v_token == kRow;
-  // pages that are whole parts of a tile, or hold whole tiles
-  const bool even = packed_k && packed_v && (P.size & (P.size - 1)) == 0;
-  const int even_keys = min(P.size, kQ4Tile);  // of a lane's copy there
+  uint4 *queries = reinterpret_cast<uint4 *>(ring + 2 * L::kStage) + lane;
+  // Pages that are whole parts of a tile, or hold whole tiles, their tokens one behind
+  // another: a page's pieces of 16 bytes within a tile are `per_slot`, and of the tile's
+  // pieces this lane copies every 32nd, from the pages (5 bits each) in slot_of.
+  const int P = p.C.page_size, log2 = 31 - __clz(P);
+  const bool even = (P & (P - 1)) == 0 && (P == 1 || (p.C.k_token == kRow && p.C.v_token == kRow));
+  const int slots = max(kQ4Tile >> log2, 1), per_slot = min(P, kQ4Tile) * kPieces16;
+  uint32_t slot_of = 0;
+#pragma unroll
+  for (int x = 0; x < kPieces16; ++x) slot_of |= static_cast<uint32_t>((x * 32 + lane) / per_slot) << (5 * x);
   uint32_t asked = 0, tiles = 0;  // tiles copied, and weighed
-  uint32_t there[kStages];        // which of a tile's keys were copied
-
-  // The page of tile i that this lane looks up: a tile lies on at most 32 pages, one per
-  // lane.
-  auto look_up = [&](int i) {
-    if (i >= u.i1) return -1;
-    const int at0 = key_tile(u.k, i) * kQ4Tile, last = min(at0 + kQ4Tile, u.k.end) - 1;
-    const int index = P.index(at0) + lane;
-    // not behind the last key, nor between the sinks and the window
-    if (last < at0 || index > P.index(last)) return -1;
-    const int begin = index * P.size;
-    if (max(at0, begin) >= p.sinks && begin + P.size <= u.k.first) return -1;
-    return page_at(p.S, u.b, index);
+  uint32_t there[2] = {0u, 0u};   // which of a tile's keys were copied
+  const char *k_head = nullptr, *v_head = nullptr;
+  // The page table's entries from pages_from on, one per lane, and those behind them.
+  int pages_from = 0, pages = -1, pages_behind = -1;
+  bool pages_fine = false;
+  auto fetch = [&](int from) {
+    return from + lane <= (u.k.end - 1) >> log2 ? page_at(p.S, u.b, from + lane) : 0;
   };
-  // Asks for tile i, whose pages are known; by the whole warp.
-  auto ask = [&](int i, int page) {
-    const int at0 = key_tile(u.k, i) * kQ4Tile;
-    const uint32_t st = asked % kStages, stage = ring_at + st * L::kStage;
-    const void *full = &ctl.full[warp][st];
-    const char *k = p.C.k + page * p.C.k_page + u.h * p.C.k_head;
-    const char *v = p.C.v + page * p.C.v_page + u.h * p.C.v_head;
-    uint32_t word;
-    const bool mine = lane * even_keys < kQ4Tile;
-    if (even && at0 + kQ4Tile <= u.k.end && (at0 >= u.k.first || p.sinks >= u.k.first) &&
-        __all_sync(0xFFFFFFFFu, !mine || page_ok(p.C, page))) {
-      // a tile without gaps
-      word = 0xFFFFFFFFu;
-      if (lane == 0) bar_expect(full, L::kStage);
-      __syncwarp();
-      if (mine) {
-        const int offset = (at0 & (P.size - 1)) * kRow, to = lane * even_keys * kRow;
-        bulk_load(stage + to, k + offset, even_keys * kRow, full);
-        bulk_load(stage + kQ4Tile * kRow + to, v + offset, even_keys * kRow, full);
+  // A unit's first pages, on their way.
+  auto begin_unit = [&] {
+    k_head = p.C.k + u.h * p.C.k_head;
+    v_head = p.C.v + u.h * p.C.v_head;
+    pages_from = (key_tile(u.k, u.i0) * kQ4Tile >> log2) - 32;
+    pages_fine = false;
+    if (even && u.k.end > 0) pages_behind = fetch(pages_from + 32);
+  };
+  // Asks for tile i; by the whole warp.
+  auto ask = [&](int i) {
+    const int at0 = key_tile(u.k, i) * kQ4Tile, st = asked++ & 1u;
+    const uint32_t k_to = ring_at + st * L::kStage + lane * 16, v_to = k_to + kQ4Tile * kRow;
+    uint32_t word = 0xFFFFFFFFu;
+    // without gaps
+    bool plain = even && at0 + kQ4Tile <= u.k.end && (at0 >= u.k.first || at0 + kQ4Tile <= p.sinks);
+    const int index = at0 >> log2;
+    if (plain && (index < pages_from || index + slots > pages_from + 32)) {
+      // (those behind were asked for when these were)
+      pages = index == pages_from + 32 ? pages_behind : fetch(index);
+      pages_from = index;
+      pages_fine = __all_sync(0xFFFFFFFFu, page_ok(p.C, pages));
+      pages_behind = fetch(index + 32);
+    }
+    if (plain && pages_fine) {
+      const int in_page = (at0 & (P - 1)) * kRow + lane * 16;
+#pragma unroll
+      for (int x = 0; x < kPieces16; ++x) {
+        const int slot = (slot_of >> (5 * x)) & 31;
+        const int page = __shfl_sync(0xFFFFFFFFu, pages, index - pages_from + slot);
+        const int at = in_page + x * 512 - slot * per_slot * 16;
+        copy16(k_to + x * 512, k_head + page * p.C.k_page + at);
+        copy16(v_to + x * 512, v_head + page * p.C.v_page + at);
       }
     } else {
-      const int begin = (P.index(at0) + lane) * P.size - at0;  // of this lane's page, if it has one
-      // the page's keys that are there: [from, to), and from `again` on, where the window
-      // begins behind the sinks within it
-      const int from = max(0, begin);
-      int end = max(from, min(min(kQ4Tile, begin + P.size), u.k.end - at0));
-      if (!page_ok(p.C, page)) end = from;
-      int to = end, again = end;
-      if (p.sinks < u.k.first) {
-        to = min(max(from, p.sinks - at0), end);
-        again = min(max(to, u.k.first - at0), end);
+      // a key a lane finds its place, then a piece a lane
+      const int at = at0 + lane;
+      int page = -1;
+      long long ko = 0, vo = 0;
+      // not behind the last key, nor between the sinks and the window
+      if (at < u.k.end && (at < p.sinks || at >= u.k.first)) {
+        const int in = at / P;
+        page = page_at(p.S, u.b, in);
+        ko = page * p.C.k_page + (at - in * P) * p.C.k_token;
+        vo = page * p.C.v_page + (at - in * P) * p.C.v_token;
       }
-      const uint32_t keys = (low_bits(to) & ~low_bits(from)) | (low_bits(end) & ~low_bits(again));
-      word = __reduce_or_sync(0xFFFFFFFFu, keys);
-      if (lane == 0) bar_expect(full, 2 * kRow * __popc(word));
-      __syncwarp();
-      auto copy = [&](bool packed, uint32_t to_s, const char *base, long long token, int a, int b) {
-        const int step = packed ? b - a : 1;
-        for (int key = a; key < b; key += step)
-          bulk_load(to_s + key * kRow, base + (key - begin) * token, step * kRow, full);
-      };
-      if (keys) {
+      word = __ballot_sync(0xFFFFFFFFu, page_ok(p.C, page));
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const int a = x ? again : from, b = x ? end : to;
-          copy(packed_k, stage, k, p.C.k_token, a, b);
-          copy(packed_v, stage + kQ4Tile * kRow, v, p.C.v_token, a, b);
+      for (int x = 0; x < kPieces16; ++x) {
+        const int key = (x * 32 + lane) / kPieces16, piece = x * 32 + lane - key * kPieces16;
+        const long long kr = __shfl_sync(0xFFFFFFFFu, ko, key), vr = __shfl_sync(0xFFFFFFFFu, vo, key);
+        if ((word >> key) & 1u) {
+          copy16(k_to + x * 512, k_head + kr + piece * 16);
+          copy16(v_to + x * 512, v_head + vr + piece * 16);
         }
       }
     }
-    __syncwarp();
-#pragma unroll
-    for (int x = 0; x < kStages; ++x)
-      if (st == x) there[x] = word;
-    if (asked++ == 0) first_wait(full, p.first_wait, &ctl.dead);
+    there[0] = st ? there[0] : word;
+    there[1] = st ? word : there[1];
   };
 
+  if (busy) begin_unit();
   while (busy) {
-    int page = look_up(u.i0);
-    // the ring's stages but one, which the loop fills
-    int next = u.i0;
-    for (; next < u.i0 + kStages - 1 && next < u.i1; ++next) {
-      const int behind = look_up(next + 1);
-      ask(next, page);
-      page = behind;
-    }
     for (int nt = 0; nt < NT; ++nt)
       prepare_queries<E, D, kQuad>(p, u, nt * 8, lane, queries + nt * (L::kSteps / 2 + 1) * 32);
     __syncwarp();
@@ -437,19 +405,17 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     int cap = 0;
     bool bad = false;
 
-    for (int i = u.i0; i < u.i1; ++i, ++tiles) {
-      if (next < u.i1) {
-        const int behind = look_up(next + 1);
-        ask(next++, page);
-        page = behind;
+    // two tiles are on their way while one is weighed
+    for (int i = u.i0 - 2; i < u.i1; ++i) {
+      uint32_t valid = 0u;
+      const uint32_t st = tiles & 1u;
+      if (i >= u.i0) {
+        copy_wait<1>();
+        __syncwarp();
+        ++tiles;
+        valid = st ? there[1] : there[0];
       }
-      const uint32_t st = tiles % kStages;
-      if (!warp_wait(&ctl.full[warp][st], (tiles / kStages) & 1u, &ctl.dead)) break;
-      uint32_t valid = there[0];
-#pragma unroll
-      for (int x = 1; x < kStages; ++x)
-        if (st == x) valid = there[x];
-      if (valid == 0u) continue;
+      if (valid != 0u) {
       const int at0 = key_tile(u.k, i) * kQ4Tile;
       char *k_s = ring + st * L::kStage, *v_s = k_s + kQ4Tile * kRow;
       const uint32_t k_at = ring_at + st * L::kStage, v_at = k_at + kQ4Tile * kRow;
@@ -733,15 +699,26 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
           }
         }
       }
+      }
       __syncwarp();
+      if (i + 2 < u.i1) ask(i + 2);
+      copy_commit();
     }
-    if (*reinterpret_cast<volatile int *>(&ctl.dead)) break;
+    // the next unit's pages and queries are on their way while this one ends
+    const UnitWalk v = u;
+    busy = u.next(p, line);
+    if (busy) {
+      begin_unit();
+      const int r = u.r0 + min(lane / 2, u.live_rows(p) - 1), n = r / p.G;
+      const char *q = p.q + u.b * p.q_seq + n * p.q_token + (u.h * p.G + r - n * p.G) * p.q_head;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (lane & 1) * D) : "memory");
+    }
 
     // the unit's end.  A lane has 16 bytes of float32 outputs at a time, of row
     // row_of(nt, e): dimensions d0, d0 + 1, d1, d1 + 1
-    const bool whole = u.whole();
+    const bool whole = v.whole();
     bad = __any_sync(0xFFFFFFFFu, bad);
-    float *slot = p.part + piece_slot(u, line.worker) * slot_floats(p.rows, D);
+    float *slot = p.part + piece_slot(v, line.worker) * slot_floats(p.rows, D);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -752,7 +729,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
         const int row = row_of(nt, e);
         // with kQuad half of the columns are another group's, or not looked at
         const bool mine = row < live && (!kQuad || (t >> 1) == (D == 128 ? 0 : g >> 2));
-        const long long at = mine ? out_row(p, u.b, u.h, u.r0 + row) : 0;
+        const long long at = mine ? out_row(p, v.b, v.h, v.r0 + row) : 0;
         const float n = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<TE *>(p.out) + at * D);
         float *to = slot + slot_stats(p.rows) + static_cast<size_t>(row) * D;
@@ -785,8 +762,8 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
           }
           if (!mine) continue;
           if (bad) {
-            const int token = (u.r0 + row) / p.G;
-            const float2 z0 = nonfinite_values_q4<D>(p, u, token, d0), z1 = nonfinite_values_q4<D>(p, u, token, d1);
+            const int token = (v.r0 + row) / p.G;
+            const float2 z0 = nonfinite_values_q4<D>(p, v, token, d0), z1 = nonfinite_values_q4<D>(p, v, token, d1);
             y.x += z0.x, y.y += z0.y, y.z += z1.x, y.w += z1.y;
           }
           const uint2 packed = make_uint2(E::pack(y.x * n, y.y * n), E::pack(y.z * n, y.w * n));
@@ -813,13 +790,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
           }
         }
       }
-    busy = u.next(p, line);
   }
-  // a wait gave up: no copy is in flight when the CTA ends
-  for (uint32_t i = tiles; i < asked; ++i) bar_linger(&ctl.full[warp][i % kStages], (i / kStages) & 1u);
-  __syncthreads();
-  if (!ctl.dead) return;
-  for (int w = 0; w < L::kWarps; ++w) void_run<E, D, L::kThreads>(p, ctl.lines[w]);
 }
 
 namespace {

@@ -338,7 +338,7 @@ def test_many_sequences(N, Hq, Hkv, D):
     s.check(out)
 
 
-@pytest.mark.parametrize("N", [1, 5, 40])
+@pytest.mark.parametrize("N", [16, 40])
 def test_a_wait_that_gives_up(N):
     s = Setup(16, [300, 20, 5000], N, 8, 2, 128, 16, "bf16")
     before = s.call()

@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["abi.cu", "verify_units.cu", "verify_stream.cu", "tree_mask.cu", "static_scratch.cu",
            "refine.cu", "chain_rows.cu", "verify_chain.cu", "overlap.cu", "typical.cu", "tree_rerank.cu",
            "cache_abi.cu", "cache_pages.cu", "cache_rows.cu", "paged_attention.cu",
-           "paged_attention_wide.cu", "paged_attention_q4.cu"]
+           "paged_attention_wide.cu", "paged_attention_q4.cu",
+           "paged_attention_q4_wide.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -70,6 +70,8 @@ cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStre
 // The same over a cache of 4-bit rows; dtype: of queries and outputs.
 size_t attention_q4_workspace_bytes(int N, int G, int D);
 cudaError_t launch_attention_q4(AttnParams &p, int dtype, void *workspace, cudaStream_t stream);
+// Its form on tensor memory, for units of two tiles of wide_tile_rows(G) rows.
+cudaError_t launch_attention_q4_wide(const AttnParams &p, int dtype, cudaStream_t stream);
 
 // What a kernel makes of the rows; few: units of at most so many tiles are not cut.
 struct AttnPlan {

@@ -108,42 +108,8 @@ __device__ __forceinline__ void matrices2_turned(uint32_t (&r)[2], uint32_t at) 
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
-__device__ __forceinline__ uint32_t word_at(const char *p) { return *reinterpret_cast<const uint32_t *>(p); }
 __device__ __forceinline__ float scale_at(const char *p) { return __half2float(*reinterpret_cast<const __half *>(p)); }
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // nibbles of two halves
-
-// Two outputs of token n that the keys' values which are not finite (beyond float16
-// too) add, from the parts of tiles that some row does not see whole; see
-// nonfinite_values.
-template <int D>
-static __device__ __noinline__ float2 nonfinite_values_q4(const AttnParams &p, const UnitWalk u, int n,
-                                                          int d) {
-  float a[2] = {0.f, 0.f};
-  for (int i = u.i0; i < u.i1; ++i) {
-    const int t0 = key_tile(u.k, i) << p.tile_log2;
-    for (int at0 = t0; at0 < t0 + (1 << p.tile_log2) && at0 < u.k.end; at0 += kQ4Tile) {
-      bool whole = all_seen(p, u.k, at0, kQ4Tile);
-      for (int at = at0; at < at0 + kQ4Tile && whole; ++at)
-        whole = at < u.k.end && page_ok(p.C, page_at(p.S, u.b, at / p.C.page_size));
-      if (whole) continue;
-      for (int at = at0; at < min(at0 + kQ4Tile, u.k.end); ++at) {
-        const int index = at / p.C.page_size, page = page_at(p.S, u.b, index);
-        if (!page_ok(p.C, page) || !sees(p, u.k, u.b, n, at)) continue;
-        const char *row = p.C.v + page * p.C.v_page + (at - index * p.C.page_size) * p.C.v_token +
-                          u.h * p.C.v_head;
-        const float2 s = q4_pair(word_at(row + D / 2 + d / (D / 4) * 4));
-        if (q4_finite(s)) continue;
-        float x[8];
-        q4_codes(word_at(row + d / 8 * 4), x);
-        for (int j = 0; j < 2; ++j) {
-          const float v = fmaf(s.x, x[d % 8 + j], s.y);
-          a[j] += fabsf(v) < 65520.f ? 0.f : (isnan(v) ? v : copysignf(INFINITY, v));
-        }
-      }
-    }
-  }
-  return make_float2(a[0], a[1]);
-}
 
 // A lane's operands of the scores' products, of eight columns of queries (four with
 // kQuad) from row `first` of the unit, into pieces of 16 bytes [step / 2][lane]:
@@ -763,7 +729,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
           if (!mine) continue;
           if (bad) {
             const int token = (v.r0 + row) / p.G;
-            const float2 z0 = nonfinite_values_q4<D>(p, v, token, d0), z1 = nonfinite_values_q4<D>(p, v, token, d1);
+            const float2 z0 = nonfinite_values_q4<D, kQ4Tile>(p, v, token, d0), z1 = nonfinite_values_q4<D, kQ4Tile>(p, v, token, d1);
             y.x += z0.x, y.y += z0.y, y.z += z1.x, y.w += z1.y;
           }
           const uint2 packed = make_uint2(E::pack(y.x * n, y.y * n), E::pack(y.z * n, y.w * n));
@@ -813,7 +779,10 @@ template <int R>
 AttnPlan q4_plan_of() {
   return {Rows4<128, R>::kCtas * Rows4<128, R>::kWarps * kSms4, R, 5, 2, 8};
 }
+// More rows go to tensor memory.
+bool q4_wide(int N, int G) { return N * G > 16 && G <= 128; }
 AttnPlan q4_plan(int N, int G) {
+  if (q4_wide(N, G)) return {kSms4, 2 * wide_tile_rows(G), 7, 8, 16};
   return N * G <= 4 ? q4_plan_of<4>() : N * G <= 8 ? q4_plan_of<8>() : q4_plan_of<16>();
 }
 
@@ -822,11 +791,14 @@ AttnPlan q4_plan(int N, int G) {
 size_t attention_q4_workspace_bytes(int N, int G, int D) { return plan_bytes(q4_plan(N, G), D); }
 
 cudaError_t launch_attention_q4(AttnParams &p, int dtype, void *workspace, cudaStream_t stream) {
+  const bool wide = q4_wide(p.S.N, p.G);
   take_plan(p, q4_plan(p.S.N, p.G), workspace);
+  // row tiles of a tree see the same keys, those of a chain end at their own; a CTA's
+  // workers are on one line
   const int tiles = (p.S.N * p.G + p.rows - 1) / p.rows;
-  // a CTA's workers are on one line
-  if (p.mask && tiles <= 8 && p.workers / 4 % tiles == 0) p.row_lines = tiles;
-  const cudaError_t e = p.rows == 4   ? start4<4>(p, dtype, stream)
+  if (p.mask && tiles <= 8 && (wide || p.workers / 4 % tiles == 0)) p.row_lines = tiles;
+  const cudaError_t e = wide          ? launch_attention_q4_wide(p, dtype, stream)
+                        : p.rows == 4 ? start4<4>(p, dtype, stream)
                         : p.rows == 8 ? start4<8>(p, dtype, stream)
                                       : start4<16>(p, dtype, stream);
   if (e != cudaSuccess || p.whole) return e;

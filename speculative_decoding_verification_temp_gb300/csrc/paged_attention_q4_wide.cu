@@ -1,0 +1,376 @@
+// Attention over a paged cache of 4-bit rows (q4.cuh) for many rows of queries, on the
+// fifth-generation tensor cores: pairs of row tiles of at most 128 rows (new tokens
+// times the group's heads), as pair_kernel of the 16-bit caches.
+//
+// Three warps make the products' operands: they read the rows' codes into registers,
+// write the values m + s n as float16 into the entries of a ring (half a step of 2^-11,
+// against quantisation by half a step of 1/15 of a group's spread), and bring the
+// queries, as float16 scaled by a power of two where a row's largest leaves 2^14.  One
+// warp issues the products, two warpgroups turn scores into weights, a thread a row.
+// Every hand-over is an mbarrier, every wait is bounded.
+//
+// Bound by the turns that a stream's softmax and products take with one buffer of
+// scores, as there; a tile's 32768 codes take the three warps about MEASURE cycles.
+#include "paged_attention_wide.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int kMakers = 3;  // warps that make operands
+
+template <int D>
+struct PairCtl4 {
+  static constexpr int kRing = D == 128 ? 4 : 8;
+  unsigned long long full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
+  alignas(16) uint32_t valid[kValidRing][4];
+  RunScratch<kWideThreads, 1> runs;
+  float factor[2][256];                // of the scores of a unit's rows, two units
+  int2 place[kMakers][2][kTileKeys];   // of a tile's keys, two tiles: page (-1: not there), token in it
+  uint32_t tmem;
+  int dead, bad;
+};
+template <int D>
+struct PairShape4 {
+  static constexpr int kQPanel = 128 * 128, kQ = Entry<D>::kPanels * kQPanel;  // of a row tile
+  static constexpr int kRing = PairCtl4<D>::kRing;
+  static constexpr int kEntries = 2 * kQ;
+  static constexpr int kCtl = kEntries + kRing * Entry<D>::kBytes;
+  static constexpr int kSmem = kCtl + static_cast<int>(sizeof(PairCtl4<D>));
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t word_of(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+
+// The eight values of a word as float16: a nibble becomes 1024 + n or 64 + n by its mask,
+// n by a subtraction, both exactly.
+__device__ __forceinline__ uint4 word_values(uint32_t w, __half2 scale, __half2 low) {
+  auto value = [&](uint32_t x, bool high) {
+    const __half2 n = high ? __hsub2(half2_of((x & 0x00F000F0u) | 0x54005400u), half2_of(0x54005400u))
+                           : __hsub2(half2_of((x & 0x000F000Fu) | 0x64006400u), half2_of(0x64006400u));
+    return word_of(__hfma2(n, scale, low));
+  };
+  const uint32_t x = w >> 8;
+  return make_uint4(value(w, false), value(w, true), value(x, false), value(x, true));
+}
+
+// A row of queries as float16, by D / 8 lanes with eight values each; returns the factor
+// that the row's scores take.  Rows stay as they are up to 2^14: float16's absolute step
+// 2^-24 below its normal values is far below what scores notice.
+template <class E, int D>
+__device__ __forceinline__ float query_values(const char *from, float scale, uint4 &to) {
+  using TE = typename E::T;
+  const uint4 v = *reinterpret_cast<const uint4 *>(from);
+  float x[8], top = 0.f;
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = E::to(reinterpret_cast<const TE *>(&v)[e]);
+    odd |= !isfinite(x[e]);
+    top = fmaxf(top, fabsf(x[e]));
+  }
+#pragma unroll
+  for (int o = 1; o < D / 8; o <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    odd |= __shfl_xor_sync(0xFFFFFFFFu, static_cast<int>(odd), o) != 0;
+  }
+  // tiny rows up as well, for scales that bring them back
+  const int exponent = top > 16384.f || (top > 1e-30f && top < 0.0625f) ? min(max(8 - ilogbf(top), -126), 126) : 0;
+  const float up = __int_as_float((127 + exponent) << 23);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = odd ? 0.f : x[e] * up;
+  to = make_uint4(F16::pack(x[0], x[1]), F16::pack(x[2], x[3]), F16::pack(x[4], x[5]), F16::pack(x[6], x[7]));
+  return odd ? __int_as_float(0x7FC00000) : scale * __int_as_float((127 - exponent) << 23);
+}
+
+}  // namespace
+
+template <class E, int D>
+__global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_constant__ AttnParams p) {
+  using W = Entry<D>;
+  using Shape = PairShape4<D>;
+  using Ctl = PairCtl4<D>;
+  constexpr int kRing = Shape::kRing, kRow = q4_row_bytes(D);
+  extern __shared__ __align__(1024) char wide4_s[];
+  char *ring = wide4_s + Shape::kEntries;
+  Ctl &ctl = *reinterpret_cast<Ctl *>(wide4_s + Shape::kCtl);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const int tile_rows = p.rows / 2;
+
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      bar_init(&ctl.full[i], kMakers);
+      bar_init(&ctl.empty[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      bar_init(&ctl.s_full[g], 1);
+      bar_init(&ctl.p_full[g], 4);
+      bar_init(&ctl.o_done[g], 1);
+    }
+    bar_init(&ctl.q_full, kMakers);
+    bar_init(&ctl.q_empty, 1);
+    bar_init(&ctl.drain, 1);
+    ctl.dead = 0;
+    ctl.bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 11) tm_alloc(&ctl.tmem);
+  __syncwarp();
+  Line lines[1];
+  find_runs(p, ctl.runs, blockIdx.x, 0, lines);  // barriers as well
+  const Line &line = lines[0];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  UnitWalk u;
+  const bool busy = u.start(p, line);
+  if (tid == 0) write_join(p, line, busy ? &u : nullptr);
+  tc_after();
+  const uint32_t tmem = ctl.tmem;
+  if (!busy) {  // the same for every thread
+    tm_free(tmem, warp);
+    return;
+  }
+  const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(wide4_s);
+  uint32_t tiles = 0, units = 0;
+  bool ok = true;
+
+  if (warp < 8) {
+    // -------------------------------------------------------------- softmax
+    more_regs<kSoftRegs>();
+    const int g = warp >> 2, part = warp & 3, tile_row = tid & 127, row = g * tile_rows + tile_row;
+    const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
+    const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * 128;
+    uint32_t turns = 0, ended = 0;  // tiles and units of this stream
+    do {
+      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+      const int rows = min(tile_rows, live - g * tile_rows);  // of this stream
+      const bool mine = tile_row < rows, works = part * 32 < rows;
+      const int n = (u.r0 + min(row, live - 1)) / p.G;
+      float m = -INFINITY, l = 0.f, c = 0.f;
+      for (int i = 0; rows > 0 && i < n_tiles; ++i) {
+        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+        uint4 seen = make_uint4(0, 0, 0, 0);
+        if (works) seen = seen_tile(p, u, n, at0);
+        if (!(ok = warp_wait(&ctl.s_full[g], turns++ & 1u, &ctl.dead))) break;
+        if (works) {
+          if (i == 0 && mine) c = ctl.factor[units & 1u][row];
+          const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.valid[(tiles + i) % kValidRing]);
+          softmax_tile<F16, D>(c, mine, tile_masked(p, u, at0, valid), both(seen, valid), s_at, o_at,
+                               i == 0, m, l);
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&ctl.p_full[g]);
+      }
+      if (!ok) break;
+      tiles += n_tiles;
+      ++units;
+      if (rows > 0) {
+        if (!(ok = warp_wait(&ctl.o_done[g], ended++ & 1u, &ctl.dead))) break;
+        if (works)
+          write_row<E, D, true>(p, u, line.worker, row, n, mine, o_at, m, l,
+                                *reinterpret_cast<volatile int *>(&ctl.bad) != 0);
+      }
+    } while (u.next(p, line));
+  } else {
+    fewer_regs<kRestRegs>();
+    if (warp < 8 + kMakers) {
+      // ------------------------------------------------- operands of the products
+      const int maker = warp - 8;
+      // A step is 8 (D 64: 16) keys, a lane's part 16 bytes of codes: of key `own` of the
+      // step the piece-th 32 values.  Eight neighbouring lanes write eight rows' places
+      // of the swizzle.
+      constexpr int kStepKeys = D == 128 ? 8 : 16, kSteps = kTileKeys / kStepKeys;
+      const int own = D == 128 ? lane & 7 : (lane & 7) + (lane >> 4) * 8;
+      const int piece = D == 128 ? lane >> 3 : (lane >> 3) & 1;
+      auto find_places = [&](int i, int2 (&at)[4]) {
+        // this lane's keys of tile i: lane + 32 w
+        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int key = at0 + w * 32 + lane;
+          at[w] = make_int2(-1, 0);
+          // not behind the last key, nor between the sinks and the window
+          if (i < u.i1 - u.i0 && key < u.k.end && (key < p.sinks || key >= u.k.first)) {
+            const int index = key / p.C.page_size;
+            at[w] = make_int2(page_at(p.S, u.b, index), key - index * p.C.page_size);
+          }
+        }
+      };
+      do {
+        const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+        int2 next[4];
+        find_places(0, next);
+        for (int i = 0; ok && i < n_tiles; ++i, ++tiles) {
+          int2 *place = ctl.place[maker][tiles & 1u];
+          const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+          uint4 valid;
+          uint32_t *words = reinterpret_cast<uint32_t *>(&valid);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const bool there = page_ok(p.C, next[w].x);
+            words[w] = __ballot_sync(0xFFFFFFFFu, there);
+            place[w * 32 + lane] = there ? next[w] : make_int2(-1, 0);
+          }
+          __syncwarp();
+          // a tile's pages are looked up a tile ahead
+          find_places(i + 1, next);
+          const bool masked = tile_masked(p, u, at0, valid);
+#pragma unroll 1
+          for (int values = 0; values < 2; ++values) {
+            const uint32_t e = 2 * tiles + values;
+            const char *base = values ? p.C.v + u.h * p.C.v_head : p.C.k + u.h * p.C.k_head;
+            const long long page_step = values ? p.C.v_page : p.C.k_page;
+            const long long token_step = values ? p.C.v_token : p.C.k_token;
+            struct Part {
+              uint4 codes;
+              uint32_t pair[D == 128 ? 1 : 2];
+            };
+            auto load = [&](int step, Part &x) {
+              const int2 at = place[min(step, kSteps - 1) * kStepKeys + own];
+              x.codes = make_uint4(0, 0, 0, 0);
+              x.pair[0] = 0u;
+              if constexpr (D == 64) x.pair[1] = 0u;
+              if (at.x < 0 || step >= kSteps) return;
+              const char *row = base + at.x * page_step + at.y * token_step;
+              x.codes = *reinterpret_cast<const uint4 *>(row + piece * 16);
+              if constexpr (D == 128) {
+                x.pair[0] = *reinterpret_cast<const uint32_t *>(row + D / 2 + piece * 4);
+              } else {
+                const uint2 y = *reinterpret_cast<const uint2 *>(row + D / 2 + piece * 8);
+                x.pair[0] = y.x, x.pair[1] = y.y;
+              }
+            };
+            // the steps of this warp: every third, three of them on their way
+            const int first = (maker + values) % kMakers;
+            Part ahead[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) load(first + x * kMakers, ahead[x]);
+            if (!(ok = warp_wait(&ctl.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, &ctl.dead))) break;
+            if (!values && maker == 0 && lane < 4)
+              ctl.valid[tiles % kValidRing][lane] = lane == 0 ? valid.x : lane == 1 ? valid.y : lane == 2 ? valid.z : valid.w;
+            char *entry = ring + e % kRing * W::kBytes;
+#pragma unroll 1
+            for (int step = first; step < kSteps; step += kMakers) {
+              Part x = ahead[0];
+              ahead[0] = ahead[1];
+              ahead[1] = ahead[2];
+              load(step + 3 * kMakers, ahead[2]);
+              if (values && masked) {
+                // groups that are not finite stand for zeros here, see nonfinite_values_q4
+#pragma unroll
+                for (int j = 0; j < (D == 128 ? 1 : 2); ++j)
+                  if (!q4_finite(q4_pair(x.pair[j]))) {
+                    x.pair[j] = 0u;
+                    *reinterpret_cast<volatile int *>(&ctl.bad) = 1;
+                  }
+              }
+              const int key = step * kStepKeys + own, r = key & 7;
+              // 32 values are half of a panel's row
+              char *to = entry + key / 8 * W::kGroup + piece / 2 * W::kPanel + r * W::kRow;
+              const uint32_t w[4] = {x.codes.x, x.codes.y, x.codes.z, x.codes.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t pair = x.pair[D == 128 ? 0 : j >> 1];
+                *reinterpret_cast<uint4 *>(to + ((((piece & 1) * 4 + j) ^ r) << 4)) =
+                    word_values(w[j], half2_of(__byte_perm(pair, 0, 0x1010)), half2_of(__byte_perm(pair, 0, 0x3232)));
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ctl.full[e % kRing]);
+            if (!values && maker == 0 && tiles == 0) first_wait(&ctl.full[0], p.first_wait, &ctl.dead);
+            if (!values && i == 0) {
+              // the queries, once the products of the unit before have read theirs
+              if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
+              constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+              for (int r0 = maker * kAtOnce; r0 < live; r0 += kMakers * kAtOnce) {
+                const int row = r0 + lane / kLanes, chunk = lane % kLanes;
+                const int r = u.r0 + min(row, live - 1), n = r / p.G;
+                uint4 x;
+                const float f = query_values<E, D>(p.q + u.b * p.q_seq + n * p.q_token +
+                                                       (u.h * p.G + r - n * p.G) * p.q_head + chunk * 16,
+                                                   p.scale_log2, x);
+                if (row < live) {
+                  const int t = row >= tile_rows, tr = row - t * tile_rows;
+                  *reinterpret_cast<uint4 *>(wide4_s + t * Shape::kQ + chunk / 8 * Shape::kQPanel + tr * 128 +
+                                             (((chunk & 7) ^ (tr & 7)) << 4)) = x;
+                  if (chunk == 0) ctl.factor[units & 1u][row] = f;
+                }
+              }
+              ++units;
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) bar_arrive(&ctl.q_full);
+            }
+          }
+        }
+      } while (ok && u.next(p, line));
+    } else {
+      // ------------------------------------------------------------- products
+      uint32_t made[2] = {0, 0};  // tiles of each stream
+      auto take = [&](uint32_t e) {  // an entry that is ready
+        ok = warp_wait(&ctl.full[e % kRing], (e / kRing) & 1u, &ctl.dead);
+        return ring_at + e % kRing * W::kBytes;
+      };
+      auto scores = [&](int g, uint32_t k_at) {
+        issue_scores<F16, D>(tmem + g * 128, q_at + g * Shape::kQ, Shape::kQPanel, k_at);
+        issue_commit(&ctl.s_full[g]);
+      };
+      do {
+        const int n_tiles = u.i1 - u.i0, streams = u.live_rows(p) > tile_rows ? 2 : 1;
+        uint32_t k_at = take(2 * tiles);
+        if (!ok || !(ok = warp_wait(&ctl.q_full, units++ & 1u, &ctl.dead))) break;
+        for (int g = 0; g < streams; ++g) scores(g, k_at);
+        issue_commit(&ctl.empty[2 * tiles % kRing]);
+        if (n_tiles == 1) issue_commit(&ctl.q_empty);
+        for (int i = 0; ok && i < n_tiles; ++i, ++tiles) {
+          const uint32_t e = 2 * tiles + 1;
+          const bool more = i + 1 < n_tiles;
+          const uint32_t v_at = take(e);
+          if (!ok) break;
+          for (int g = 0; ok && g < streams; ++g) {
+            if (!(ok = warp_wait(&ctl.p_full[g], made[g]++ & 1u, &ctl.dead))) break;
+            issue_outputs<F16, D>(tmem + 256 + g * 128, tmem + g * 128, v_at, i == 0);
+            if (!more) issue_commit(&ctl.o_done[g]);
+            if (g == streams - 1) issue_commit(&ctl.empty[e % kRing]);
+            if (more) {
+              if (g == 0) k_at = take(e + 1);
+              if (!ok) break;
+              scores(g, k_at);
+              if (g == streams - 1) {
+                issue_commit(&ctl.empty[(e + 1) % kRing]);
+                if (i + 2 == n_tiles) issue_commit(&ctl.q_empty);
+              }
+            }
+          }
+        }
+      } while (ok && u.next(p, line));
+      // nothing is in flight when the tensor memory goes back
+      issue_commit(&ctl.drain);
+      bar_linger(&ctl.drain, 0u);
+    }
+  }
+  tm_free(tmem, warp);
+  if (!ctl.dead) return;
+  void_run<E, D>(p, line);
+}
+
+namespace {
+
+template <class E, int D>
+cudaError_t start_pair4(const AttnParams &p, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  constexpr int smem = PairShape4<D>::kSmem;
+  return launch_large(pair4_kernel<E, D>, done, smem, p.workers, kWideThreads, smem, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_q4_wide(const AttnParams &p, int dtype, cudaStream_t stream) {
+  if (dtype == SPEC_BF16)
+    return p.D == 64 ? start_pair4<Bf16, 64>(p, stream) : start_pair4<Bf16, 128>(p, stream);
+  return p.D == 64 ? start_pair4<F16, 64>(p, stream) : start_pair4<F16, 128>(p, stream);
+}
+
+}  // namespace sv

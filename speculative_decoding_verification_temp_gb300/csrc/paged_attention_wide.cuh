@@ -4,6 +4,7 @@
 #pragma once
 
 #include "paged_attention.cuh"
+#include "q4.cuh"
 
 namespace sv {
 
@@ -503,9 +504,44 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t word_at(const char *p) { return *reinterpret_cast<const uint32_t *>(p); }
+
+// Two outputs of token n that the keys' values which are not finite (beyond float16
+// too) add, from the parts of tiles that some row does not see whole; see
+// nonfinite_values.
+template <int D, int kSlice>
+static __device__ __noinline__ float2 nonfinite_values_q4(const AttnParams &p, const UnitWalk u, int n,
+                                                          int d) {
+  float a[2] = {0.f, 0.f};
+  for (int i = u.i0; i < u.i1; ++i) {
+    const int t0 = key_tile(u.k, i) << p.tile_log2;
+    for (int at0 = t0; at0 < t0 + (1 << p.tile_log2) && at0 < u.k.end; at0 += kSlice) {
+      bool whole = all_seen(p, u.k, at0, kSlice);
+      for (int at = at0; at < at0 + kSlice && whole; ++at)
+        whole = at < u.k.end && page_ok(p.C, page_at(p.S, u.b, at / p.C.page_size));
+      if (whole) continue;
+      for (int at = at0; at < min(at0 + kSlice, u.k.end); ++at) {
+        const int index = at / p.C.page_size, page = page_at(p.S, u.b, index);
+        if (!page_ok(p.C, page) || !sees(p, u.k, u.b, n, at)) continue;
+        const char *row = p.C.v + page * p.C.v_page + (at - index * p.C.page_size) * p.C.v_token +
+                          u.h * p.C.v_head;
+        const float2 s = q4_pair(word_at(row + D / 2 + d / (D / 4) * 4));
+        if (q4_finite(s)) continue;
+        float x[8];
+        q4_codes(word_at(row + d / 8 * 4), x);
+        for (int j = 0; j < 2; ++j) {
+          const float v = fmaf(s.x, x[d % 8 + j], s.y);
+          a[j] += fabsf(v) < 65520.f ? 0.f : (isnan(v) ? v : copysignf(INFINITY, v));
+        }
+      }
+    }
+  }
+  return make_float2(a[0], a[1]);
+}
+
 // A row's end: its outputs from tensor memory, divided by the sum, or its piece
-// of a cut unit.  By whole warps; `mine`: the row exists.
-template <class E, int D>
+// of a cut unit.  By whole warps; `mine`: the row exists; kFour: of a 4-bit cache.
+template <class E, int D, bool kFour = false>
 __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u, int worker, int row,
                                           int n, bool mine, uint32_t o_at, float m, float l,
                                           bool bad) {
@@ -554,8 +590,14 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
   }
   if (bad && mine && l != 0.f) {
     for (int d = 0; d < D; d += 4) {
-      const float4 v =
-          nonfinite_values<TE, kTileKeys>(p, u, n, d, make_float4(0.f, 0.f, 0.f, 0.f));
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if constexpr (kFour) {
+        const float2 a = nonfinite_values_q4<D, kTileKeys>(p, u, n, d);
+        const float2 b = nonfinite_values_q4<D, kTileKeys>(p, u, n, d + 2);
+        v = make_float4(a.x, a.y, b.x, b.y);
+      } else {
+        v = nonfinite_values<TE, kTileKeys>(p, u, n, d, v);
+      }
       const float x[4] = {v.x, v.y, v.z, v.w};
       for (int e = 0; e < 4; ++e) {
         if (x[e] == 0.f) continue;

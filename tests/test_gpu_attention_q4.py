@@ -109,7 +109,7 @@ class Setup:
         q, k_cache, v_cache = self.q.cpu(), self.k.cpu(), self.v.cpu()
         out, lse = res.out.cpu().double(), res.lse.cpu().double()
         B, N, Hq, D = q.shape
-        wide = N * (Hq // k_cache.shape[2]) > 32
+        wide = N * (Hq // k_cache.shape[2]) > 16  # rows on tensor memory
         for b in range(B):
             n = N if self.n_new is None else int(self.n_new[b])
             if n == 0:

@@ -28,14 +28,13 @@
 // another, one per row elsewhere) and writes their outputs, without a barrier.
 #include <algorithm>
 
-#include "paged_attention_wide.cuh"
-#include "q4.cuh"
+#include "q4_copies.cuh"
 
 namespace sv {
 
 namespace {
 
-constexpr int kQ4Tile = 32;  // keys
+constexpr int kQ4Tile = kQ4Keys;  // of a tile
 constexpr int kSms4 = 152;
 // Weights reach 2^(kLift4 + kSlack) = 2^14, and times scales below 2 stay in float16;
 // larger scales lower the weights (see cap).
@@ -80,9 +79,6 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
       "{%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void copy16(uint32_t to, const char *from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 // 8x8 matrices of 16-bit halves; with "memory": the ring's contents change under them.
 __device__ __forceinline__ void matrices4(uint32_t (&r)[4], uint32_t at) {
@@ -232,7 +228,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     rows4_kernel(const __grid_constant__ AttnParams p) {
   using L = Rows4<D, R>;
   using TE = typename E::T;
-  constexpr int kRow = L::kRow, kPieces16 = kRow / 16, NT = L::kCols;
+  constexpr int kRow = L::kRow, NT = L::kCols;
   constexpr bool kQuad = L::kQuad, kPieces = D == 128 || kQuad;
   extern __shared__ __align__(128) char smem4[];
   __shared__ RunScratch<L::kThreads, L::kWarps> runs;
@@ -264,85 +260,17 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
   char *ring = smem4 + warp * L::kWarp;
   const uint32_t ring_at = smem_u32(ring);
   uint4 *queries = reinterpret_cast<uint4 *>(ring + 2 * L::kStage) + lane;
-  // Pages that are whole parts of a tile, or hold whole tiles, their tokens one behind
-  // another: a page's pieces of 16 bytes within a tile are `per_slot`, and of the tile's
-  // pieces this lane copies every 32nd, from the pages (5 bits each) in slot_of.
-  const int P = p.C.page_size, log2 = 31 - __clz(P);
-  const bool even = (P & (P - 1)) == 0 && (P == 1 || (p.C.k_token == kRow && p.C.v_token == kRow));
-  const int slots = max(kQ4Tile >> log2, 1), per_slot = min(P, kQ4Tile) * kPieces16;
-  uint32_t slot_of = 0;
-#pragma unroll
-  for (int x = 0; x < kPieces16; ++x) slot_of |= static_cast<uint32_t>((x * 32 + lane) / per_slot) << (5 * x);
+  Q4Copies<kRow> copies(p, lane);
   uint32_t asked = 0, tiles = 0;  // tiles copied, and weighed
   uint32_t there[2] = {0u, 0u};   // which of a tile's keys were copied
-  const char *k_head = nullptr, *v_head = nullptr;
-  // The page table's entries from pages_from on, one per lane, and those behind them.
-  int pages_from = 0, pages = -1, pages_behind = -1;
-  bool pages_fine = false;
-  auto fetch = [&](int from) {
-    return from + lane <= (u.k.end - 1) >> log2 ? page_at(p.S, u.b, from + lane) : 0;
-  };
-  // A unit's first pages, on their way.
-  auto begin_unit = [&] {
-    k_head = p.C.k + u.h * p.C.k_head;
-    v_head = p.C.v + u.h * p.C.v_head;
-    pages_from = (key_tile(u.k, u.i0) * kQ4Tile >> log2) - 32;
-    pages_fine = false;
-    if (even && u.k.end > 0) pages_behind = fetch(pages_from + 32);
-  };
-  // Asks for tile i; by the whole warp.
   auto ask = [&](int i) {
-    const int at0 = key_tile(u.k, i) * kQ4Tile, st = asked++ & 1u;
-    const uint32_t k_to = ring_at + st * L::kStage + lane * 16, v_to = k_to + kQ4Tile * kRow;
-    uint32_t word = 0xFFFFFFFFu;
-    // without gaps
-    bool plain = even && at0 + kQ4Tile <= u.k.end && (at0 >= u.k.first || at0 + kQ4Tile <= p.sinks);
-    const int index = at0 >> log2;
-    if (plain && (index < pages_from || index + slots > pages_from + 32)) {
-      // (those behind were asked for when these were)
-      pages = index == pages_from + 32 ? pages_behind : fetch(index);
-      pages_from = index;
-      pages_fine = __all_sync(0xFFFFFFFFu, page_ok(p.C, pages));
-      pages_behind = fetch(index + 32);
-    }
-    if (plain && pages_fine) {
-      const int in_page = (at0 & (P - 1)) * kRow + lane * 16;
-#pragma unroll
-      for (int x = 0; x < kPieces16; ++x) {
-        const int slot = (slot_of >> (5 * x)) & 31;
-        const int page = __shfl_sync(0xFFFFFFFFu, pages, index - pages_from + slot);
-        const int at = in_page + x * 512 - slot * per_slot * 16;
-        copy16(k_to + x * 512, k_head + page * p.C.k_page + at);
-        copy16(v_to + x * 512, v_head + page * p.C.v_page + at);
-      }
-    } else {
-      // a key a lane finds its place, then a piece a lane
-      const int at = at0 + lane;
-      int page = -1;
-      long long ko = 0, vo = 0;
-      // not behind the last key, nor between the sinks and the window
-      if (at < u.k.end && (at < p.sinks || at >= u.k.first)) {
-        const int in = at / P;
-        page = page_at(p.S, u.b, in);
-        ko = page * p.C.k_page + (at - in * P) * p.C.k_token;
-        vo = page * p.C.v_page + (at - in * P) * p.C.v_token;
-      }
-      word = __ballot_sync(0xFFFFFFFFu, page_ok(p.C, page));
-#pragma unroll 1
-      for (int x = 0; x < kPieces16; ++x) {
-        const int key = (x * 32 + lane) / kPieces16, piece = x * 32 + lane - key * kPieces16;
-        const long long kr = __shfl_sync(0xFFFFFFFFu, ko, key), vr = __shfl_sync(0xFFFFFFFFu, vo, key);
-        if ((word >> key) & 1u) {
-          copy16(k_to + x * 512, k_head + kr + piece * 16);
-          copy16(v_to + x * 512, v_head + vr + piece * 16);
-        }
-      }
-    }
+    const uint32_t st = asked++ & 1u;
+    const uint32_t word = copies.ask(p, u, key_tile(u.k, i) * kQ4Tile, ring_at + st * L::kStage, lane);
     there[0] = st ? there[0] : word;
     there[1] = st ? word : there[1];
   };
 
-  if (busy) begin_unit();
+  if (busy) copies.begin(p, u, key_tile(u.k, u.i0) * kQ4Tile, lane);
   while (busy) {
     for (int nt = 0; nt < NT; ++nt)
       prepare_queries<E, D, kQuad>(p, u, nt * 8, lane, queries + nt * (L::kSteps / 2 + 1) * 32);
@@ -674,7 +602,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     const UnitWalk v = u;
     busy = u.next(p, line);
     if (busy) {
-      begin_unit();
+      copies.begin(p, u, key_tile(u.k, u.i0) * kQ4Tile, lane);
       const int r = u.r0 + min(lane / 2, u.live_rows(p) - 1), n = r / p.G;
       const char *q = p.q + u.b * p.q_seq + n * p.q_token + (u.h * p.G + r - n * p.G) * p.q_head;
       asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (lane & 1) * D) : "memory");

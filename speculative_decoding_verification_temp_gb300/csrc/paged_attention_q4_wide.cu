@@ -11,7 +11,7 @@
 //
 // Bound by the turns that a stream's softmax and products take with one buffer of
 // scores, as there; a tile's 32768 codes take the three warps about MEASURE cycles.
-#include "paged_attention_wide.cuh"
+#include "q4_copies.cuh"
 
 namespace sv {
 
@@ -21,12 +21,11 @@ constexpr int kMakers = 3;  // warps that make operands
 
 template <int D>
 struct PairCtl4 {
-  static constexpr int kRing = D == 128 ? 4 : 8;
+  static constexpr int kRing = D == 128 ? 3 : 8;
   unsigned long long full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
   alignas(16) uint32_t valid[kValidRing][4];
   RunScratch<kWideThreads, 1> runs;
   float factor[2][256];                // of the scores of a unit's rows, two units
-  int2 place[kMakers][2][kTileKeys];   // of a tile's keys, two tiles: page (-1: not there), token in it
   uint32_t tmem;
   int dead, bad;
 };
@@ -35,7 +34,10 @@ struct PairShape4 {
   static constexpr int kQPanel = 128 * 128, kQ = Entry<D>::kPanels * kQPanel;  // of a row tile
   static constexpr int kRing = PairCtl4<D>::kRing;
   static constexpr int kEntries = 2 * kQ;
-  static constexpr int kCtl = kEntries + kRing * Entry<D>::kBytes;
+  // rows as they are, copied by a warp for itself
+  static constexpr int kRaw = kEntries + kRing * Entry<D>::kBytes;
+  static constexpr int kRawSlots = 2, kRawWarp = kRawSlots * Q4Copies<q4_row_bytes(D)>::kBytes;
+  static constexpr int kCtl = kRaw + kMakers * kRawWarp;
   static constexpr int kSmem = kCtl + static_cast<int>(sizeof(PairCtl4<D>));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
-      bar_init(&ctl.full[i], kMakers);
+      bar_init(&ctl.full[i], kTileKeys / kQ4Keys);
       bar_init(&ctl.empty[i], 1);
     }
     for (int g = 0; g < 2; ++g) {
@@ -176,136 +178,130 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
     fewer_regs<kRestRegs>();
     if (warp < 8 + kMakers) {
       // ------------------------------------------------- operands of the products
+      // In turn they take 32 keys and their values: copied into the warp's own slots
+      // while those before are made, keys into an entry, then values into the next.
       const int maker = warp - 8;
-      // A step is 8 (D 64: 16) keys, a lane's part 16 bytes of codes: of key `own` of the
-      // step the piece-th 32 values.  Eight neighbouring lanes write eight rows' places
-      // of the swizzle.
-      constexpr int kStepKeys = D == 128 ? 8 : 16, kSteps = kTileKeys / kStepKeys;
+      constexpr int kParts = kTileKeys / kQ4Keys, kSlots = Shape::kRawSlots;
+      using Copies = Q4Copies<kRow>;
+      Copies copies(p, lane);
+      char *raw = wide4_s + Shape::kRaw + maker * Shape::kRawWarp;
+      const uint32_t raw_at = smem_u32(raw);
+      // a pass makes 32 16-byte pieces of codes, of eight neighbouring rows each (which
+      // meet eight banks, in the rows as in the swizzle)
+      constexpr int kPieces = D / 32, kPasses = kPieces, kOwn = 32 / kPieces;
       const int own = D == 128 ? lane & 7 : (lane & 7) + (lane >> 4) * 8;
       const int piece = D == 128 ? lane >> 3 : (lane >> 3) & 1;
-      auto find_places = [&](int i, int2 (&at)[4]) {
-        // this lane's keys of tile i: lane + 32 w
-        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+      uint32_t done = 0;  // parts before the unit, of all makers
+      do {
+        const int n_tiles = u.i1 - u.i0, live = u.live_rows(p), parts = n_tiles * kParts;
+        auto at_of = [&](int part) {
+          return key_tile(u.k, u.i0 + part / kParts) * kTileKeys + part % kParts * kQ4Keys;
+        };
+        // this warp's parts: first, first + kMakers, ...
+        const int first = (maker + kMakers - static_cast<int>(done % kMakers)) % kMakers;
+        copies.begin(p, u, at_of(first), lane);
+        uint32_t there[kSlots];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int key = at0 + w * 32 + lane;
-          at[w] = make_int2(-1, 0);
-          // not behind the last key, nor between the sinks and the window
-          if (i < u.i1 - u.i0 && key < u.k.end && (key < p.sinks || key >= u.k.first)) {
-            const int index = key / p.C.page_size;
-            at[w] = make_int2(page_at(p.S, u.b, index), key - index * p.C.page_size);
+        for (int x = 0; x < kSlots; ++x) {
+          there[x] = 0u;
+          if (first + x * kMakers < parts)
+            there[x] = copies.ask(p, u, at_of(first + x * kMakers), raw_at + x * Copies::kBytes, lane);
+          copy_commit();
+        }
+        // the queries, once the products of the unit before have read theirs
+        if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+#pragma unroll 2
+        for (int r0 = maker * kAtOnce; r0 < live; r0 += kMakers * kAtOnce) {
+          const int row = r0 + lane / kLanes, chunk = lane % kLanes;
+          const int r = u.r0 + min(row, live - 1), n = r / p.G;
+          uint4 x;
+          const float f = query_values<E, D>(p.q + u.b * p.q_seq + n * p.q_token +
+                                                 (u.h * p.G + r - n * p.G) * p.q_head + chunk * 16,
+                                             p.scale_log2, x);
+          if (row < live) {
+            const int t = row >= tile_rows, tr = row - t * tile_rows;
+            *reinterpret_cast<uint4 *>(wide4_s + t * Shape::kQ + chunk / 8 * Shape::kQPanel + tr * 128 +
+                                       (((chunk & 7) ^ (tr & 7)) << 4)) = x;
+            if (chunk == 0) ctl.factor[units & 1u][row] = f;
           }
         }
-      };
-      do {
-        const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
-        int2 next[4];
-        find_places(0, next);
-        for (int i = 0; ok && i < n_tiles; ++i, ++tiles) {
-          int2 *place = ctl.place[maker][tiles & 1u];
-          const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
-          uint4 valid;
-          uint32_t *words = reinterpret_cast<uint32_t *>(&valid);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const bool there = page_ok(p.C, next[w].x);
-            words[w] = __ballot_sync(0xFFFFFFFFu, there);
-            place[w * 32 + lane] = there ? next[w] : make_int2(-1, 0);
-          }
+        ++units;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(&ctl.q_full);
+
+        int slot = 0;
+        for (int part = first; ok && part < parts; part += kMakers) {
+          copy_wait<kSlots - 1>();
           __syncwarp();
-          // a tile's pages are looked up a tile ahead
-          find_places(i + 1, next);
-          const bool masked = tile_masked(p, u, at0, valid);
-#pragma unroll 1
-          for (int values = 0; values < 2; ++values) {
-            const uint32_t e = 2 * tiles + values;
-            const char *base = values ? p.C.v + u.h * p.C.v_head : p.C.k + u.h * p.C.k_head;
-            const long long page_step = values ? p.C.v_page : p.C.k_page;
-            const long long token_step = values ? p.C.v_token : p.C.k_token;
-            struct Part {
-              uint4 codes;
-              uint32_t pair[D == 128 ? 1 : 2];
-            };
-            auto load = [&](int step, Part &x) {
-              const int2 at = place[min(step, kSteps - 1) * kStepKeys + own];
-              x.codes = make_uint4(0, 0, 0, 0);
-              x.pair[0] = 0u;
-              if constexpr (D == 64) x.pair[1] = 0u;
-              if (at.x < 0 || step >= kSteps) return;
-              const char *row = base + at.x * page_step + at.y * token_step;
-              x.codes = *reinterpret_cast<const uint4 *>(row + piece * 16);
-              if constexpr (D == 128) {
-                x.pair[0] = *reinterpret_cast<const uint32_t *>(row + D / 2 + piece * 4);
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2 *>(row + D / 2 + piece * 8);
-                x.pair[0] = y.x, x.pair[1] = y.y;
-              }
-            };
-            // the steps of this warp: every third, three of them on their way
-            const int first = (maker + values) % kMakers;
-            Part ahead[3];
+          const uint32_t tile = tiles + part / kParts;
+          const int quarter = part % kParts, at0 = at_of(part);
+          uint32_t word = there[0];
 #pragma unroll
-            for (int x = 0; x < 3; ++x) load(first + x * kMakers, ahead[x]);
+          for (int x = 1; x < kSlots; ++x)
+            if (slot == x) word = there[x];
+          const bool masked = word != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Keys);
+          char *rows = raw + slot * Copies::kBytes;
+#pragma unroll 1
+          for (int values = 0; values < 2; ++values, rows += kQ4Keys * kRow) {
+            const uint32_t e = 2 * tile + values;
             if (!(ok = warp_wait(&ctl.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, &ctl.dead))) break;
-            if (!values && maker == 0 && lane < 4)
-              ctl.valid[tiles % kValidRing][lane] = lane == 0 ? valid.x : lane == 1 ? valid.y : lane == 2 ? valid.z : valid.w;
-            char *entry = ring + e % kRing * W::kBytes;
-#pragma unroll 1
-            for (int step = first; step < kSteps; step += kMakers) {
-              Part x = ahead[0];
-              ahead[0] = ahead[1];
-              ahead[1] = ahead[2];
-              load(step + 3 * kMakers, ahead[2]);
-              if (values && masked) {
-                // groups that are not finite stand for zeros here, see nonfinite_values_q4
+            if (!values && lane == 0) ctl.valid[tile % kValidRing][quarter] = word;
+            // 32 values are half of a panel's row
+            char *entry = ring + e % kRing * W::kBytes + quarter * (kQ4Keys / 8) * W::kGroup + piece / 2 * W::kPanel;
+#pragma unroll 2
+            for (int x = 0; x < kPasses; ++x) {
+              const int key = x * kOwn + own, r = key & 7;
+              const char *row = rows + key * kRow;
+              const uint4 codes = *reinterpret_cast<const uint4 *>(row + piece * 16);
+              uint32_t pair[2];
+              if constexpr (D == 128) {
+                pair[0] = word_at(row + D / 2 + piece * 4);
+                pair[1] = pair[0];
+              } else {
+                pair[0] = word_at(row + D / 2 + piece * 8);
+                pair[1] = word_at(row + D / 2 + piece * 8 + 4);
+              }
+              if (masked) {
+                // rows that were not copied stand for zeros, and so do groups that are not
+                // finite, which nonfinite_values_q4 adds
+                const bool copied = (word >> key) & 1u;
 #pragma unroll
-                for (int j = 0; j < (D == 128 ? 1 : 2); ++j)
-                  if (!q4_finite(q4_pair(x.pair[j]))) {
-                    x.pair[j] = 0u;
-                    *reinterpret_cast<volatile int *>(&ctl.bad) = 1;
+                for (int j = 0; j < 2; ++j)
+                  if (!copied || (values && !q4_finite(q4_pair(pair[j])))) {
+                    if (copied) *reinterpret_cast<volatile int *>(&ctl.bad) = 1;
+                    pair[j] = 0u;
                   }
               }
-              const int key = step * kStepKeys + own, r = key & 7;
-              // 32 values are half of a panel's row
-              char *to = entry + key / 8 * W::kGroup + piece / 2 * W::kPanel + r * W::kRow;
-              const uint32_t w[4] = {x.codes.x, x.codes.y, x.codes.z, x.codes.w};
+              char *to = entry + key / 8 * W::kGroup + r * W::kRow;
+              const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t pair = x.pair[D == 128 ? 0 : j >> 1];
+              for (int j = 0; j < 4; ++j)
                 *reinterpret_cast<uint4 *>(to + ((((piece & 1) * 4 + j) ^ r) << 4)) =
-                    word_values(w[j], half2_of(__byte_perm(pair, 0, 0x1010)), half2_of(__byte_perm(pair, 0, 0x3232)));
-              }
+                    word_values(w[j], half2_of(__byte_perm(pair[j >> 1], 0, 0x1010)),
+                                half2_of(__byte_perm(pair[j >> 1], 0, 0x3232)));
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) bar_arrive(&ctl.full[e % kRing]);
-            if (!values && maker == 0 && tiles == 0) first_wait(&ctl.full[0], p.first_wait, &ctl.dead);
-            if (!values && i == 0) {
-              // the queries, once the products of the unit before have read theirs
-              if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
-              constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-              for (int r0 = maker * kAtOnce; r0 < live; r0 += kMakers * kAtOnce) {
-                const int row = r0 + lane / kLanes, chunk = lane % kLanes;
-                const int r = u.r0 + min(row, live - 1), n = r / p.G;
-                uint4 x;
-                const float f = query_values<E, D>(p.q + u.b * p.q_seq + n * p.q_token +
-                                                       (u.h * p.G + r - n * p.G) * p.q_head + chunk * 16,
-                                                   p.scale_log2, x);
-                if (row < live) {
-                  const int t = row >= tile_rows, tr = row - t * tile_rows;
-                  *reinterpret_cast<uint4 *>(wide4_s + t * Shape::kQ + chunk / 8 * Shape::kQPanel + tr * 128 +
-                                             (((chunk & 7) ^ (tr & 7)) << 4)) = x;
-                  if (chunk == 0) ctl.factor[units & 1u][row] = f;
-                }
-              }
-              ++units;
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) bar_arrive(&ctl.q_full);
-            }
           }
+          if (!ok) break;
+          if (done == 0 && part == 0) first_wait(&ctl.full[0], p.first_wait, &ctl.dead);
+          const int ahead = part + kSlots * kMakers;
+          if (ahead < parts) {
+            const uint32_t next = copies.ask(p, u, at_of(ahead), raw_at + slot * Copies::kBytes, lane);
+#pragma unroll
+            for (int x = 0; x < kSlots; ++x)
+              if (slot == x) there[x] = next;
+          }
+          copy_commit();
+          slot = slot + 1 == kSlots ? 0 : slot + 1;
         }
+        tiles += n_tiles;
+        done += parts;
       } while (ok && u.next(p, line));
+      copy_wait<0>();
     } else {
       // ------------------------------------------------------------- products
       uint32_t made[2] = {0, 0};  // tiles of each stream

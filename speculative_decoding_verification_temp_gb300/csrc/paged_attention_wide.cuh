@@ -592,8 +592,8 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
     for (int d = 0; d < D; d += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if constexpr (kFour) {
-        const float2 a = nonfinite_values_q4<D, kTileKeys>(p, u, n, d);
-        const float2 b = nonfinite_values_q4<D, kTileKeys>(p, u, n, d + 2);
+        const float2 a = nonfinite_values_q4<D, 32>(p, u, n, d);
+        const float2 b = nonfinite_values_q4<D, 32>(p, u, n, d + 2);
         v = make_float4(a.x, a.y, b.x, b.y);
       } else {
         v = nonfinite_values<TE, kTileKeys>(p, u, n, d, v);

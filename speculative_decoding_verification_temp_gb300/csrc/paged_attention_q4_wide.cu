@@ -17,14 +17,18 @@ namespace sv {
 
 namespace {
 
-constexpr int kMakers = 3;  // warps that make operands
+// Two warpgroups of softmax, six warps that make operands, one that issues products.
+constexpr int kThreads4 = 512, kMakers = 6, kIssuer = 8 + kMakers;
+// Registers of a softmax thread and of the others: 256 * 184 + 256 * 72 are the 512 * 128
+// that the CTA is launched with.
+constexpr int kSoftRegs4 = 184, kRestRegs4 = 72;
 
 template <int D>
 struct PairCtl4 {
   static constexpr int kRing = D == 128 ? 3 : 8;
   unsigned long long full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
   alignas(16) uint32_t valid[kValidRing][4];
-  RunScratch<kWideThreads, 1> runs;
+  RunScratch<kThreads4, 1> runs;
   float factor[2][256];                // of the scores of a unit's rows, two units
   uint32_t tmem;
   int dead, bad;
@@ -89,7 +93,7 @@ __device__ __forceinline__ float query_values(const char *from, float scale, uin
 }  // namespace
 
 template <class E, int D>
-__global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_constant__ AttnParams p) {
   using W = Entry<D>;
   using Shape = PairShape4<D>;
   using Ctl = PairCtl4<D>;
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
     ctl.bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 11) tm_alloc(&ctl.tmem);
+  if (warp == kIssuer) tm_alloc(&ctl.tmem);
   __syncwarp();
   Line lines[1];
   find_runs(p, ctl.runs, blockIdx.x, 0, lines);  // barriers as well
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
   tc_after();
   const uint32_t tmem = ctl.tmem;
   if (!busy) {  // the same for every thread
-    tm_free(tmem, warp);
+    tm_free<kIssuer>(tmem, warp);
     return;
   }
   const uint32_t ring_at = smem_u32(ring), q_at = smem_u32(wide4_s);
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
 
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
-    more_regs<kSoftRegs>();
+    more_regs<kSoftRegs4>();
     const int g = warp >> 2, part = warp & 3, tile_row = tid & 127, row = g * tile_rows + tile_row;
     const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
     const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * 128;
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
       }
     } while (u.next(p, line));
   } else {
-    fewer_regs<kRestRegs>();
+    fewer_regs<kRestRegs4>();
     if (warp < 8 + kMakers) {
       // ------------------------------------------------- operands of the products
       // In turn they take 32 keys and their values: copied into the warp's own slots
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
         done += parts;
       } while (ok && u.next(p, line));
       copy_wait<0>();
-    } else {
+    } else if (warp == kIssuer) {
       // ------------------------------------------------------------- products
       uint32_t made[2] = {0, 0};  // tiles of each stream
       auto take = [&](uint32_t e) {  // an entry that is ready
@@ -347,9 +351,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) pair4_kernel(const __grid_con
       bar_linger(&ctl.drain, 0u);
     }
   }
-  tm_free(tmem, warp);
+  tm_free<kIssuer>(tmem, warp);
   if (!ctl.dead) return;
-  void_run<E, D>(p, line);
+  void_run<E, D, kThreads4>(p, line);
 }
 
 namespace {
@@ -358,7 +362,7 @@ template <class E, int D>
 cudaError_t start_pair4(const AttnParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   constexpr int smem = PairShape4<D>::kSmem;
-  return launch_large(pair4_kernel<E, D>, done, smem, p.workers, kWideThreads, smem, stream, p);
+  return launch_large(pair4_kernel<E, D>, done, smem, p.workers, kThreads4, smem, stream, p);
 }
 
 }  // namespace

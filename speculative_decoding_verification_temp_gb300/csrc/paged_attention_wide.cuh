@@ -839,12 +839,13 @@ __device__ __forceinline__ void tm_alloc(void *slot) {
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+template <int kWarp = 11>
 __device__ __forceinline__ void tm_free(uint32_t tmem, int warp) {
   __syncwarp();
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 11)
+  if (warp == kWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 

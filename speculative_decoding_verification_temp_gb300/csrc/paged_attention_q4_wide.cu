@@ -25,11 +25,10 @@ constexpr int kSoftRegs4 = 184, kRestRegs4 = 72;
 
 template <int D>
 struct PairCtl4 {
-  static constexpr int kRing = D == 128 ? 3 : 8;
+  static constexpr int kRing = D == 128 ? 4 : 8;
   unsigned long long full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
   alignas(16) uint32_t valid[kValidRing][4];
   RunScratch<kThreads4, 1> runs;
-  float factor[2][256];                // of the scores of a unit's rows, two units
   uint32_t tmem;
   int dead, bad;
 };
@@ -40,7 +39,7 @@ struct PairShape4 {
   static constexpr int kEntries = 2 * kQ;
   // rows as they are, copied by a warp for itself
   static constexpr int kRaw = kEntries + kRing * Entry<D>::kBytes;
-  static constexpr int kRawSlots = 2, kRawWarp = kRawSlots * Q4Copies<q4_row_bytes(D)>::kBytes;
+  static constexpr int kRawSlots = 1, kRawWarp = kRawSlots * Q4Copies<q4_row_bytes(D)>::kBytes;
   static constexpr int kCtl = kRaw + kMakers * kRawWarp;
   static constexpr int kSmem = kCtl + static_cast<int>(sizeof(PairCtl4<D>));
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -61,32 +60,40 @@ __device__ __forceinline__ uint4 word_values(uint32_t w, __half2 scale, __half2 
   return make_uint4(value(w, false), value(w, true), value(x, false), value(x, true));
 }
 
-// A row of queries as float16, by D / 8 lanes with eight values each; returns the factor
-// that the row's scores take.  Rows stay as they are up to 2^14: float16's absolute step
-// 2^-24 below its normal values is far below what scores notice.
+// A row of queries as float16 into its place of a tile (panels of 64 values, the
+// 128-byte swizzle), by one thread; returns the factor that the row's scores take.  Rows
+// whose largest lies within 2^-4 .. 2^14 stay as they are, others are brought there by a
+// power of two: float16's step below its normal values, 2^-24, is then 2^-20 of the largest.
 template <class E, int D>
-__device__ __forceinline__ float query_values(const char *from, float scale, uint4 &to) {
+__device__ __forceinline__ float put_query(const char *from, float scale, char *tile, int panel_bytes, int row) {
   using TE = typename E::T;
-  const uint4 v = *reinterpret_cast<const uint4 *>(from);
-  float x[8], top = 0.f;
+  uint4 v[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) v[i] = *reinterpret_cast<const uint4 *>(from + i * 16);
+  float top = 0.f;
   bool odd = false;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = E::to(reinterpret_cast<const TE *>(&v)[e]);
-    odd |= !isfinite(x[e]);
-    top = fmaxf(top, fabsf(x[e]));
-  }
+  for (int i = 0; i < D / 8; ++i)
 #pragma unroll
-  for (int o = 1; o < D / 8; o <<= 1) {
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    odd |= __shfl_xor_sync(0xFFFFFFFFu, static_cast<int>(odd), o) != 0;
-  }
-  // tiny rows up as well, for scales that bring them back
+    for (int e = 0; e < 8; ++e) {
+      const float x = fabsf(E::to(reinterpret_cast<const TE *>(&v[i])[e]));
+      odd |= !(x < INFINITY);
+      top = fmaxf(top, x);
+    }
   const int exponent = top > 16384.f || (top > 1e-30f && top < 0.0625f) ? min(max(8 - ilogbf(top), -126), 126) : 0;
-  const float up = __int_as_float((127 + exponent) << 23);
+  // a query that is not finite makes its row NaN
+  const float up = odd ? 0.f : __int_as_float((127 + exponent) << 23);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = odd ? 0.f : x[e] * up;
-  to = make_uint4(F16::pack(x[0], x[1]), F16::pack(x[2], x[3]), F16::pack(x[4], x[5]), F16::pack(x[6], x[7]));
+  for (int i = 0; i < D / 8; ++i) {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const TE *x = reinterpret_cast<const TE *>(&v[i]) + 2 * e;
+      h[e] = odd ? 0u : F16::pack(E::to(x[0]) * up, E::to(x[1]) * up);
+    }
+    *reinterpret_cast<uint4 *>(tile + i / 8 * panel_bytes + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+        make_uint4(h[0], h[1], h[2], h[3]);
+  }
   return odd ? __int_as_float(0x7FC00000) : scale * __int_as_float((127 - exponent) << 23);
 }
 
@@ -114,7 +121,7 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
       bar_init(&ctl.p_full[g], 4);
       bar_init(&ctl.o_done[g], 1);
     }
-    bar_init(&ctl.q_full, kMakers);
+    bar_init(&ctl.q_full, 8);
     bar_init(&ctl.q_empty, 1);
     bar_init(&ctl.drain, 1);
     ctl.dead = 0;
@@ -147,19 +154,37 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
     const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
     const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * 128;
     uint32_t turns = 0, ended = 0;  // tiles and units of this stream
-    do {
+    char *q_tile = wide4_s + g * Shape::kQ;
+    float c = 0.f;
+    // This thread's row of the next unit's queries, once the products of the unit before
+    // have read theirs.  Its outputs are written behind that, while the next unit's first
+    // products run.
+    auto bring_queries = [&](const UnitWalk &w) {
+      const int live = w.live_rows(p);
+      if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) return;
+      ++units;
+      if (row < live && tile_row < tile_rows) {
+        const int r = w.r0 + row, n = r / p.G;
+        c = put_query<E, D>(p.q + w.b * p.q_seq + n * p.q_token + (w.h * p.G + r - n * p.G) * p.q_head,
+                            p.scale_log2, q_tile, Shape::kQPanel, tile_row);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(&ctl.q_full);
+    };
+    bring_queries(u);
+    for (bool more = true; ok && more;) {
       const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
       const int rows = min(tile_rows, live - g * tile_rows);  // of this stream
       const bool mine = tile_row < rows, works = part * 32 < rows;
       const int n = (u.r0 + min(row, live - 1)) / p.G;
-      float m = -INFINITY, l = 0.f, c = 0.f;
+      float m = -INFINITY, l = 0.f;
       for (int i = 0; rows > 0 && i < n_tiles; ++i) {
         const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
         uint4 seen = make_uint4(0, 0, 0, 0);
         if (works) seen = seen_tile(p, u, n, at0);
         if (!(ok = warp_wait(&ctl.s_full[g], turns++ & 1u, &ctl.dead))) break;
         if (works) {
-          if (i == 0 && mine) c = ctl.factor[units & 1u][row];
           const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.valid[(tiles + i) % kValidRing]);
           softmax_tile<F16, D>(c, mine, tile_masked(p, u, at0, valid), both(seen, valid), s_at, o_at,
                                i == 0, m, l);
@@ -170,14 +195,16 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
       }
       if (!ok) break;
       tiles += n_tiles;
-      ++units;
+      const UnitWalk v = u;
+      more = u.next(p, line);
+      if (more) bring_queries(u);
       if (rows > 0) {
-        if (!(ok = warp_wait(&ctl.o_done[g], ended++ & 1u, &ctl.dead))) break;
+        if (!ok || !(ok = warp_wait(&ctl.o_done[g], ended++ & 1u, &ctl.dead))) break;
         if (works)
-          write_row<E, D, true>(p, u, line.worker, row, n, mine, o_at, m, l,
+          write_row<E, D, true>(p, v, line.worker, row, n, mine, o_at, m, l,
                                 *reinterpret_cast<volatile int *>(&ctl.bad) != 0);
       }
-    } while (u.next(p, line));
+    }
   } else {
     fewer_regs<kRestRegs4>();
     if (warp < 8 + kMakers) {
@@ -212,29 +239,6 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
             there[x] = copies.ask(p, u, at_of(first + x * kMakers), raw_at + x * Copies::kBytes, lane);
           copy_commit();
         }
-        // the queries, once the products of the unit before have read theirs
-        if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) break;
-        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-#pragma unroll 2
-        for (int r0 = maker * kAtOnce; r0 < live; r0 += kMakers * kAtOnce) {
-          const int row = r0 + lane / kLanes, chunk = lane % kLanes;
-          const int r = u.r0 + min(row, live - 1), n = r / p.G;
-          uint4 x;
-          const float f = query_values<E, D>(p.q + u.b * p.q_seq + n * p.q_token +
-                                                 (u.h * p.G + r - n * p.G) * p.q_head + chunk * 16,
-                                             p.scale_log2, x);
-          if (row < live) {
-            const int t = row >= tile_rows, tr = row - t * tile_rows;
-            *reinterpret_cast<uint4 *>(wide4_s + t * Shape::kQ + chunk / 8 * Shape::kQPanel + tr * 128 +
-                                       (((chunk & 7) ^ (tr & 7)) << 4)) = x;
-            if (chunk == 0) ctl.factor[units & 1u][row] = f;
-          }
-        }
-        ++units;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(&ctl.q_full);
-
         int slot = 0;
         for (int part = first; ok && part < parts; part += kMakers) {
           copy_wait<kSlots - 1>();
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
             if (!values && lane == 0) ctl.valid[tile % kValidRing][quarter] = word;
             // 32 values are half of a panel's row
             char *entry = ring + e % kRing * W::kBytes + quarter * (kQ4Keys / 8) * W::kGroup + piece / 2 * W::kPanel;
-#pragma unroll 2
+#pragma unroll 1
             for (int x = 0; x < kPasses; ++x) {
               const int key = x * kOwn + own, r = key & 7;
               const char *row = rows + key * kRow;

@@ -17,32 +17,68 @@ namespace sv {
 
 namespace {
 
-// Two warpgroups of softmax, six warps that make operands, one that issues products.
+// Two warpgroups of softmax, six warps that make operands, two that issue products.
 constexpr int kThreads4 = 512, kMakers = 6, kIssuer = 8 + kMakers;
 // Registers of a softmax thread and of the others: 256 * 184 + 256 * 72 are the 512 * 128
 // that the CTA is launched with.
 constexpr int kSoftRegs4 = 184, kRestRegs4 = 72;
 
+// Hand-overs of a ring of entries.
+template <int kSize>
+struct Ring4 {
+  static constexpr int kRing = kSize;
+  unsigned long long full[kRing], empty[kRing];
+  alignas(16) uint32_t valid[kValidRing][4];
+  __device__ __forceinline__ void init() {
+    for (int i = 0; i < kRing; ++i) {
+      bar_init(&full[i], kTileKeys / kQ4Keys);
+      bar_init(&empty[i], 1);
+    }
+  }
+};
+// Hand-overs of a stream.
+struct Stream4 {
+  unsigned long long s_full, p_full, o_done;
+  __device__ __forceinline__ void init() {
+    bar_init(&s_full, 1);
+    bar_init(&p_full, 4);
+    bar_init(&o_done, 1);
+  }
+};
+// Rows as they are, copied by a maker for itself.
+template <int D>
+struct Raw4 {
+  static constexpr int kSlots = 1, kWarp = kSlots * Q4Copies<q4_row_bytes(D)>::kBytes;
+};
+
 template <int D>
 struct PairCtl4 {
-  static constexpr int kRing = D == 128 ? 4 : 8;
-  unsigned long long full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2], q_full, q_empty, drain;
-  alignas(16) uint32_t valid[kValidRing][4];
+  Ring4<D == 128 ? 4 : 8> ring;
+  Stream4 stream[2];
+  unsigned long long q_full, q_empty, drain;
   RunScratch<kThreads4, 1> runs;
   uint32_t tmem;
   int dead, bad;
 };
 template <int D>
-struct PairShape4 {
+struct SoloCtl4 {
+  Ring4<D == 128 ? 2 : 4> ring[2];
+  Stream4 stream[2];
+  unsigned long long q_full[2], q_empty[2], drain[2];
+  RunScratch<kThreads4, 2> runs;
+  uint32_t tmem;
+  int dead, bad;
+};
+template <int D>
+struct Shape4 {
   static constexpr int kQPanel = 128 * 128, kQ = Entry<D>::kPanels * kQPanel;  // of a row tile
-  static constexpr int kRing = PairCtl4<D>::kRing;
   static constexpr int kEntries = 2 * kQ;
-  // rows as they are, copied by a warp for itself
+  static constexpr int kRing = D == 128 ? 4 : 8;  // entries, of both streams together
   static constexpr int kRaw = kEntries + kRing * Entry<D>::kBytes;
-  static constexpr int kRawSlots = 1, kRawWarp = kRawSlots * Q4Copies<q4_row_bytes(D)>::kBytes;
-  static constexpr int kCtl = kRaw + kMakers * kRawWarp;
-  static constexpr int kSmem = kCtl + static_cast<int>(sizeof(PairCtl4<D>));
-  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static constexpr int kCtl = kRaw + kMakers * Raw4<D>::kWarp;
+  static constexpr int kPair = kCtl + static_cast<int>(sizeof(PairCtl4<D>));
+  static constexpr int kSolo = kCtl + static_cast<int>(sizeof(SoloCtl4<D>));
+  static_assert(kPair <= 227 * 1024 && kSolo <= 227 * 1024, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
@@ -97,14 +133,189 @@ __device__ __forceinline__ float put_query(const char *from, float scale, char *
   return odd ? __int_as_float(0x7FC00000) : scale * __int_as_float((127 - exponent) << 23);
 }
 
+// The rows of a stream, a thread each: their queries, their weights and their outputs.
+// first_row: of the stream in a unit; by the stream's four warps.
+template <class E, int D, int kRing>
+__device__ __forceinline__ void weigh_rows(const AttnParams &p, const Line &line, UnitWalk u, int part, int lane,
+                                           int first_row, int tile_rows, uint32_t s_at, uint32_t o_at,
+                                           char *q_tile, Stream4 &st, const void *q_full, const void *q_empty,
+                                           Ring4<kRing> &ring, int *dead, int *bad) {
+  const int tile_row = part * 32 + lane, row = first_row + tile_row;
+  s_at += static_cast<uint32_t>(part * 32) << 16;
+  o_at += static_cast<uint32_t>(part * 32) << 16;
+  uint32_t tiles = 0, units = 0;
+  bool ok = true;
+  uint32_t turns = 0, ended = 0;  // tiles and units of this stream
+  float c = 0.f;
+  // This thread's row of the next unit's queries, once the products of the unit before
+  // have read theirs.  Its outputs are written behind that, while the next unit's first
+  // products run.
+  auto bring_queries = [&](const UnitWalk &w) {
+    const int live = w.live_rows(p);
+    if (!(ok = warp_wait(q_empty, (units & 1u) ^ 1u, dead))) return;
+    ++units;
+    if (row < live && tile_row < tile_rows) {
+      const int r = w.r0 + row, n = r / p.G;
+      c = put_query<E, D>(p.q + w.b * p.q_seq + n * p.q_token + (w.h * p.G + r - n * p.G) * p.q_head,
+                          p.scale_log2, q_tile, Shape4<D>::kQPanel, tile_row);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) bar_arrive(q_full);
+  };
+  bring_queries(u);
+  for (bool more = true; ok && more;) {
+    const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+    const int rows = min(tile_rows, live - first_row);  // of this stream
+    const bool mine = tile_row < rows, works = part * 32 < rows;
+    const int n = (u.r0 + min(row, live - 1)) / p.G;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; rows > 0 && i < n_tiles; ++i) {
+      const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+      uint4 seen = make_uint4(0, 0, 0, 0);
+      if (works) seen = seen_tile(p, u, n, at0);
+      if (!(ok = warp_wait(&st.s_full, turns++ & 1u, dead))) break;
+      if (works) {
+        const uint4 valid = *reinterpret_cast<const uint4 *>(ring.valid[(tiles + i) % kValidRing]);
+        softmax_tile<F16, D>(c, mine, tile_masked(p, u, at0, valid), both(seen, valid), s_at, o_at,
+                             i == 0, m, l);
+      }
+      tc_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&st.p_full);
+    }
+    if (!ok) break;
+    tiles += n_tiles;
+    const UnitWalk v = u;
+    more = u.next(p, line);
+    if (more) bring_queries(u);
+    if (rows > 0) {
+      if (!ok || !(ok = warp_wait(&st.o_done, ended++ & 1u, dead))) break;
+      if (works)
+        write_row<E, D, true>(p, v, line.worker, row, n, mine, o_at, m, l,
+                              *reinterpret_cast<volatile int *>(bad) != 0);
+    }
+  }
+}
+
+// A stream's or a pair's operands, by kCount warps of which this is the maker-th: they
+// take 32 keys and their values in turn, copied into the warp's own slots while those
+// before are made, keys into an entry, then values into the next.
+template <int D, int kCount, int kRing>
+__device__ __forceinline__ void make_operands(const AttnParams &p, const Line &line, UnitWalk u, int maker,
+                                              int lane, char *raw, char *entries, Ring4<kRing> &ring,
+                                              int *dead, int *bad) {
+  using W = Entry<D>;
+  constexpr int kRow = q4_row_bytes(D);
+  uint32_t tiles = 0;
+  bool ok = true;
+  constexpr int kParts = kTileKeys / kQ4Keys, kSlots = Raw4<D>::kSlots;
+  using Copies = Q4Copies<kRow>;
+  Copies copies(p, lane);
+  const uint32_t raw_at = smem_u32(raw);
+  // a pass makes 32 16-byte pieces of codes, of eight neighbouring rows each (which
+  // meet eight banks, in the rows as in the swizzle)
+  constexpr int kPieces = D / 32, kPasses = kPieces, kOwn = 32 / kPieces;
+  const int own = D == 128 ? lane & 7 : (lane & 7) + (lane >> 4) * 8;
+  const int piece = D == 128 ? lane >> 3 : (lane >> 3) & 1;
+  uint32_t done = 0;  // parts before the unit, of all makers
+  do {
+    const int n_tiles = u.i1 - u.i0, parts = n_tiles * kParts;
+    auto at_of = [&](int part) {
+      return key_tile(u.k, u.i0 + part / kParts) * kTileKeys + part % kParts * kQ4Keys;
+    };
+    // this warp's parts: first, first + kCount, ...
+    const int first = (maker + kCount - static_cast<int>(done % kCount)) % kCount;
+    copies.begin(p, u, at_of(first), lane);
+    uint32_t there[kSlots];
+#pragma unroll
+    for (int x = 0; x < kSlots; ++x) {
+      there[x] = 0u;
+      if (first + x * kCount < parts)
+        there[x] = copies.ask(p, u, at_of(first + x * kCount), raw_at + x * Copies::kBytes, lane);
+      copy_commit();
+    }
+    int slot = 0;
+    for (int part = first; ok && part < parts; part += kCount) {
+      copy_wait<kSlots - 1>();
+      __syncwarp();
+      const uint32_t tile = tiles + part / kParts;
+      const int quarter = part % kParts, at0 = at_of(part);
+      uint32_t word = there[0];
+#pragma unroll
+      for (int x = 1; x < kSlots; ++x)
+        if (slot == x) word = there[x];
+      const bool masked = word != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Keys);
+      char *rows = raw + slot * Copies::kBytes;
+#pragma unroll 1
+      for (int values = 0; values < 2; ++values, rows += kQ4Keys * kRow) {
+        const uint32_t e = 2 * tile + values;
+        if (!(ok = warp_wait(&ring.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, dead))) break;
+        if (!values && lane == 0) ring.valid[tile % kValidRing][quarter] = word;
+        // 32 values are half of a panel's row
+        char *entry = entries + e % kRing * W::kBytes + quarter * (kQ4Keys / 8) * W::kGroup + piece / 2 * W::kPanel;
+#pragma unroll 1
+        for (int x = 0; x < kPasses; ++x) {
+          const int key = x * kOwn + own, r = key & 7;
+          const char *row = rows + key * kRow;
+          const uint4 codes = *reinterpret_cast<const uint4 *>(row + piece * 16);
+          uint32_t pair[2];
+          if constexpr (D == 128) {
+            pair[0] = word_at(row + D / 2 + piece * 4);
+            pair[1] = pair[0];
+          } else {
+            pair[0] = word_at(row + D / 2 + piece * 8);
+            pair[1] = word_at(row + D / 2 + piece * 8 + 4);
+          }
+          if (masked) {
+            // rows that were not copied stand for zeros, and so do groups that are not
+            // finite, which nonfinite_values_q4 adds
+            const bool copied = (word >> key) & 1u;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (!copied || (values && !q4_finite(q4_pair(pair[j])))) {
+                if (copied) *reinterpret_cast<volatile int *>(bad) = 1;
+                pair[j] = 0u;
+              }
+          }
+          char *to = entry + key / 8 * W::kGroup + r * W::kRow;
+          const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(to + ((((piece & 1) * 4 + j) ^ r) << 4)) =
+                word_values(w[j], half2_of(__byte_perm(pair[j >> 1], 0, 0x1010)),
+                            half2_of(__byte_perm(pair[j >> 1], 0, 0x3232)));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(&ring.full[e % kRing]);
+      }
+      if (!ok) break;
+      if (done == 0 && part == 0) first_wait(&ring.full[0], p.first_wait, dead);
+      const int ahead = part + kSlots * kCount;
+      if (ahead < parts) {
+        const uint32_t next = copies.ask(p, u, at_of(ahead), raw_at + slot * Copies::kBytes, lane);
+#pragma unroll
+        for (int x = 0; x < kSlots; ++x)
+          if (slot == x) there[x] = next;
+      }
+      copy_commit();
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+    }
+    tiles += n_tiles;
+    done += parts;
+  } while (ok && u.next(p, line));
+  copy_wait<0>();
+}
+
 }  // namespace
 
 template <class E, int D>
 __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_constant__ AttnParams p) {
   using W = Entry<D>;
-  using Shape = PairShape4<D>;
+  using Shape = Shape4<D>;
   using Ctl = PairCtl4<D>;
-  constexpr int kRing = Shape::kRing, kRow = q4_row_bytes(D);
+  constexpr int kRing = Shape::kRing;
   extern __shared__ __align__(1024) char wide4_s[];
   char *ring = wide4_s + Shape::kEntries;
   Ctl &ctl = *reinterpret_cast<Ctl *>(wide4_s + Shape::kCtl);
@@ -112,15 +323,9 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
   const int tile_rows = p.rows / 2;
 
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      bar_init(&ctl.full[i], kTileKeys / kQ4Keys);
-      bar_init(&ctl.empty[i], 1);
-    }
-    for (int g = 0; g < 2; ++g) {
-      bar_init(&ctl.s_full[g], 1);
-      bar_init(&ctl.p_full[g], 4);
-      bar_init(&ctl.o_done[g], 1);
-    }
+    ctl.ring.init();
+    ctl.stream[0].init();
+    ctl.stream[1].init();
     bar_init(&ctl.q_full, 8);
     bar_init(&ctl.q_empty, 1);
     bar_init(&ctl.drain, 1);
@@ -150,183 +355,33 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
     more_regs<kSoftRegs4>();
-    const int g = warp >> 2, part = warp & 3, tile_row = tid & 127, row = g * tile_rows + tile_row;
-    const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
-    const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * 128;
-    uint32_t turns = 0, ended = 0;  // tiles and units of this stream
-    char *q_tile = wide4_s + g * Shape::kQ;
-    float c = 0.f;
-    // This thread's row of the next unit's queries, once the products of the unit before
-    // have read theirs.  Its outputs are written behind that, while the next unit's first
-    // products run.
-    auto bring_queries = [&](const UnitWalk &w) {
-      const int live = w.live_rows(p);
-      if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) return;
-      ++units;
-      if (row < live && tile_row < tile_rows) {
-        const int r = w.r0 + row, n = r / p.G;
-        c = put_query<E, D>(p.q + w.b * p.q_seq + n * p.q_token + (w.h * p.G + r - n * p.G) * p.q_head,
-                            p.scale_log2, q_tile, Shape::kQPanel, tile_row);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) bar_arrive(&ctl.q_full);
-    };
-    bring_queries(u);
-    for (bool more = true; ok && more;) {
-      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
-      const int rows = min(tile_rows, live - g * tile_rows);  // of this stream
-      const bool mine = tile_row < rows, works = part * 32 < rows;
-      const int n = (u.r0 + min(row, live - 1)) / p.G;
-      float m = -INFINITY, l = 0.f;
-      for (int i = 0; rows > 0 && i < n_tiles; ++i) {
-        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
-        uint4 seen = make_uint4(0, 0, 0, 0);
-        if (works) seen = seen_tile(p, u, n, at0);
-        if (!(ok = warp_wait(&ctl.s_full[g], turns++ & 1u, &ctl.dead))) break;
-        if (works) {
-          const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.valid[(tiles + i) % kValidRing]);
-          softmax_tile<F16, D>(c, mine, tile_masked(p, u, at0, valid), both(seen, valid), s_at, o_at,
-                               i == 0, m, l);
-        }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&ctl.p_full[g]);
-      }
-      if (!ok) break;
-      tiles += n_tiles;
-      const UnitWalk v = u;
-      more = u.next(p, line);
-      if (more) bring_queries(u);
-      if (rows > 0) {
-        if (!ok || !(ok = warp_wait(&ctl.o_done[g], ended++ & 1u, &ctl.dead))) break;
-        if (works)
-          write_row<E, D, true>(p, v, line.worker, row, n, mine, o_at, m, l,
-                                *reinterpret_cast<volatile int *>(&ctl.bad) != 0);
-      }
-    }
+    const int g = warp >> 2;
+    weigh_rows<E, D>(p, line, u, warp & 3, lane, g * tile_rows, tile_rows, tmem + g * 128, tmem + 256 + g * 128,
+                     wide4_s + g * Shape::kQ, ctl.stream[g], &ctl.q_full, &ctl.q_empty, ctl.ring, &ctl.dead,
+                     &ctl.bad);
   } else {
     fewer_regs<kRestRegs4>();
     if (warp < 8 + kMakers) {
       // ------------------------------------------------- operands of the products
-      // In turn they take 32 keys and their values: copied into the warp's own slots
-      // while those before are made, keys into an entry, then values into the next.
-      const int maker = warp - 8;
-      constexpr int kParts = kTileKeys / kQ4Keys, kSlots = Shape::kRawSlots;
-      using Copies = Q4Copies<kRow>;
-      Copies copies(p, lane);
-      char *raw = wide4_s + Shape::kRaw + maker * Shape::kRawWarp;
-      const uint32_t raw_at = smem_u32(raw);
-      // a pass makes 32 16-byte pieces of codes, of eight neighbouring rows each (which
-      // meet eight banks, in the rows as in the swizzle)
-      constexpr int kPieces = D / 32, kPasses = kPieces, kOwn = 32 / kPieces;
-      const int own = D == 128 ? lane & 7 : (lane & 7) + (lane >> 4) * 8;
-      const int piece = D == 128 ? lane >> 3 : (lane >> 3) & 1;
-      uint32_t done = 0;  // parts before the unit, of all makers
-      do {
-        const int n_tiles = u.i1 - u.i0, live = u.live_rows(p), parts = n_tiles * kParts;
-        auto at_of = [&](int part) {
-          return key_tile(u.k, u.i0 + part / kParts) * kTileKeys + part % kParts * kQ4Keys;
-        };
-        // this warp's parts: first, first + kMakers, ...
-        const int first = (maker + kMakers - static_cast<int>(done % kMakers)) % kMakers;
-        copies.begin(p, u, at_of(first), lane);
-        uint32_t there[kSlots];
-#pragma unroll
-        for (int x = 0; x < kSlots; ++x) {
-          there[x] = 0u;
-          if (first + x * kMakers < parts)
-            there[x] = copies.ask(p, u, at_of(first + x * kMakers), raw_at + x * Copies::kBytes, lane);
-          copy_commit();
-        }
-        int slot = 0;
-        for (int part = first; ok && part < parts; part += kMakers) {
-          copy_wait<kSlots - 1>();
-          __syncwarp();
-          const uint32_t tile = tiles + part / kParts;
-          const int quarter = part % kParts, at0 = at_of(part);
-          uint32_t word = there[0];
-#pragma unroll
-          for (int x = 1; x < kSlots; ++x)
-            if (slot == x) word = there[x];
-          const bool masked = word != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Keys);
-          char *rows = raw + slot * Copies::kBytes;
-#pragma unroll 1
-          for (int values = 0; values < 2; ++values, rows += kQ4Keys * kRow) {
-            const uint32_t e = 2 * tile + values;
-            if (!(ok = warp_wait(&ctl.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, &ctl.dead))) break;
-            if (!values && lane == 0) ctl.valid[tile % kValidRing][quarter] = word;
-            // 32 values are half of a panel's row
-            char *entry = ring + e % kRing * W::kBytes + quarter * (kQ4Keys / 8) * W::kGroup + piece / 2 * W::kPanel;
-#pragma unroll 1
-            for (int x = 0; x < kPasses; ++x) {
-              const int key = x * kOwn + own, r = key & 7;
-              const char *row = rows + key * kRow;
-              const uint4 codes = *reinterpret_cast<const uint4 *>(row + piece * 16);
-              uint32_t pair[2];
-              if constexpr (D == 128) {
-                pair[0] = word_at(row + D / 2 + piece * 4);
-                pair[1] = pair[0];
-              } else {
-                pair[0] = word_at(row + D / 2 + piece * 8);
-                pair[1] = word_at(row + D / 2 + piece * 8 + 4);
-              }
-              if (masked) {
-                // rows that were not copied stand for zeros, and so do groups that are not
-                // finite, which nonfinite_values_q4 adds
-                const bool copied = (word >> key) & 1u;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  if (!copied || (values && !q4_finite(q4_pair(pair[j])))) {
-                    if (copied) *reinterpret_cast<volatile int *>(&ctl.bad) = 1;
-                    pair[j] = 0u;
-                  }
-              }
-              char *to = entry + key / 8 * W::kGroup + r * W::kRow;
-              const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4 *>(to + ((((piece & 1) * 4 + j) ^ r) << 4)) =
-                    word_values(w[j], half2_of(__byte_perm(pair[j >> 1], 0, 0x1010)),
-                                half2_of(__byte_perm(pair[j >> 1], 0, 0x3232)));
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) bar_arrive(&ctl.full[e % kRing]);
-          }
-          if (!ok) break;
-          if (done == 0 && part == 0) first_wait(&ctl.full[0], p.first_wait, &ctl.dead);
-          const int ahead = part + kSlots * kMakers;
-          if (ahead < parts) {
-            const uint32_t next = copies.ask(p, u, at_of(ahead), raw_at + slot * Copies::kBytes, lane);
-#pragma unroll
-            for (int x = 0; x < kSlots; ++x)
-              if (slot == x) there[x] = next;
-          }
-          copy_commit();
-          slot = slot + 1 == kSlots ? 0 : slot + 1;
-        }
-        tiles += n_tiles;
-        done += parts;
-      } while (ok && u.next(p, line));
-      copy_wait<0>();
+      make_operands<D, kMakers>(p, line, u, warp - 8, lane, wide4_s + Shape::kRaw + (warp - 8) * Raw4<D>::kWarp,
+                                ring, ctl.ring, &ctl.dead, &ctl.bad);
     } else if (warp == kIssuer) {
       // ------------------------------------------------------------- products
       uint32_t made[2] = {0, 0};  // tiles of each stream
       auto take = [&](uint32_t e) {  // an entry that is ready
-        ok = warp_wait(&ctl.full[e % kRing], (e / kRing) & 1u, &ctl.dead);
+        ok = warp_wait(&ctl.ring.full[e % kRing], (e / kRing) & 1u, &ctl.dead);
         return ring_at + e % kRing * W::kBytes;
       };
       auto scores = [&](int g, uint32_t k_at) {
         issue_scores<F16, D>(tmem + g * 128, q_at + g * Shape::kQ, Shape::kQPanel, k_at);
-        issue_commit(&ctl.s_full[g]);
+        issue_commit(&ctl.stream[g].s_full);
       };
       do {
         const int n_tiles = u.i1 - u.i0, streams = u.live_rows(p) > tile_rows ? 2 : 1;
         uint32_t k_at = take(2 * tiles);
         if (!ok || !(ok = warp_wait(&ctl.q_full, units++ & 1u, &ctl.dead))) break;
         for (int g = 0; g < streams; ++g) scores(g, k_at);
-        issue_commit(&ctl.empty[2 * tiles % kRing]);
+        issue_commit(&ctl.ring.empty[2 * tiles % kRing]);
         if (n_tiles == 1) issue_commit(&ctl.q_empty);
         for (int i = 0; ok && i < n_tiles; ++i, ++tiles) {
           const uint32_t e = 2 * tiles + 1;
@@ -334,16 +389,16 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
           const uint32_t v_at = take(e);
           if (!ok) break;
           for (int g = 0; ok && g < streams; ++g) {
-            if (!(ok = warp_wait(&ctl.p_full[g], made[g]++ & 1u, &ctl.dead))) break;
+            if (!(ok = warp_wait(&ctl.stream[g].p_full, made[g]++ & 1u, &ctl.dead))) break;
             issue_outputs<F16, D>(tmem + 256 + g * 128, tmem + g * 128, v_at, i == 0);
-            if (!more) issue_commit(&ctl.o_done[g]);
-            if (g == streams - 1) issue_commit(&ctl.empty[e % kRing]);
+            if (!more) issue_commit(&ctl.stream[g].o_done);
+            if (g == streams - 1) issue_commit(&ctl.ring.empty[e % kRing]);
             if (more) {
               if (g == 0) k_at = take(e + 1);
               if (!ok) break;
               scores(g, k_at);
               if (g == streams - 1) {
-                issue_commit(&ctl.empty[(e + 1) % kRing]);
+                issue_commit(&ctl.ring.empty[(e + 1) % kRing]);
                 if (i + 2 == n_tiles) issue_commit(&ctl.q_empty);
               }
             }
@@ -360,21 +415,117 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
   void_run<E, D, kThreads4>(p, line);
 }
 
+// Units of one row tile: two streams with units, keys and values of their own, three
+// makers and an issuer each, so that the products of one run while the other is in its
+// softmax.
+template <class E, int D>
+__global__ void __launch_bounds__(kThreads4, 1) solo4_kernel(const __grid_constant__ AttnParams p) {
+  using W = Entry<D>;
+  using Shape = Shape4<D>;
+  using Ctl = SoloCtl4<D>;
+  constexpr int kRing = Shape::kRing / 2;
+  extern __shared__ __align__(1024) char wide4_s[];
+  Ctl &ctl = *reinterpret_cast<Ctl *>(wide4_s + Shape::kCtl);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  if (tid < 2) {
+    ctl.ring[tid].init();
+    ctl.stream[tid].init();
+    bar_init(&ctl.q_full[tid], 4);
+    bar_init(&ctl.q_empty[tid], 1);
+    bar_init(&ctl.drain[tid], 1);
+    ctl.dead = 0;
+    ctl.bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kIssuer) tm_alloc(&ctl.tmem);
+  __syncwarp();
+  Line lines[2];
+  // barriers as well; consecutive workers on different CTAs
+  find_runs(p, ctl.runs, blockIdx.x, gridDim.x, lines);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // of this warp's stream
+  const int g = warp < 8 ? warp >> 2 : (warp < kIssuer ? (warp - 8) / (kMakers / 2) : warp - kIssuer);
+  const Line line = g ? lines[1] : lines[0];
+  UnitWalk u;
+  const bool busy = u.start(p, line);
+  if (lane == 0 && warp >= kIssuer) write_join(p, line, busy ? &u : nullptr);
+  tc_after();
+  const uint32_t tmem = ctl.tmem;
+  if (lines[0].w0 == lines[0].w1 && lines[1].w0 == lines[1].w1) {
+    tm_free<kIssuer>(tmem, warp);
+    return;
+  }
+  char *entries = wide4_s + Shape::kEntries + g * kRing * W::kBytes, *q_tile = wide4_s + g * Shape::kQ;
+  auto &ring = ctl.ring[g];
+  Stream4 &st = ctl.stream[g];
+  const uint32_t s_at = tmem + g * 128, o_at = tmem + 256 + g * 128;
+
+  if (warp < 8) {
+    more_regs<kSoftRegs4>();
+    if (busy)
+      weigh_rows<E, D>(p, line, u, warp & 3, lane, 0, p.rows, s_at, o_at, q_tile, st, &ctl.q_full[g],
+                       &ctl.q_empty[g], ring, &ctl.dead, &ctl.bad);
+  } else {
+    fewer_regs<kRestRegs4>();
+    if (warp < kIssuer) {
+      const int maker = warp - 8;
+      if (busy)
+        make_operands<D, kMakers / 2>(p, line, u, maker % (kMakers / 2), lane,
+                                      wide4_s + Shape::kRaw + maker * Raw4<D>::kWarp, entries, ring, &ctl.dead,
+                                      &ctl.bad);
+    } else {
+      // ------------------------------------------------------------- products
+      uint32_t tiles = 0, units = 0;
+      bool ok = true;
+      const uint32_t entries_at = smem_u32(entries), q_at = smem_u32(q_tile);
+      if (busy) do {
+          const int n_tiles = u.i1 - u.i0;
+          for (int i = 0; i < n_tiles; ++i, ++tiles) {
+            uint32_t e = 2 * tiles;
+            if (!(ok = warp_wait(&ring.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+            if (i == 0 && !(ok = warp_wait(&ctl.q_full[g], units++ & 1u, &ctl.dead))) break;
+            issue_scores<F16, D>(s_at, q_at, Shape::kQPanel, entries_at + e % kRing * W::kBytes);
+            issue_commit(&st.s_full);
+            issue_commit(&ring.empty[e % kRing]);
+            if (i + 1 == n_tiles) issue_commit(&ctl.q_empty[g]);
+            ++e;
+            if (!(ok = warp_wait(&ring.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
+            if (!(ok = warp_wait(&st.p_full, tiles & 1u, &ctl.dead))) break;
+            issue_outputs<F16, D>(o_at, s_at, entries_at + e % kRing * W::kBytes, i == 0);
+            if (i + 1 == n_tiles) issue_commit(&st.o_done);
+            issue_commit(&ring.empty[e % kRing]);
+          }
+        } while (ok && u.next(p, line));
+      // nothing is in flight when the tensor memory goes back
+      issue_commit(&ctl.drain[g]);
+      bar_linger(&ctl.drain[g], 0u);
+    }
+  }
+  tm_free<kIssuer>(tmem, warp);
+  if (!ctl.dead) return;
+  void_run<E, D, kThreads4>(p, lines[0]);
+  void_run<E, D, kThreads4>(p, lines[1]);
+}
+
 namespace {
 
-template <class E, int D>
-cudaError_t start_pair4(const AttnParams &p, cudaStream_t stream) {
+template <auto kKernel>
+cudaError_t start_wide4(int smem, int ctas, const AttnParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  constexpr int smem = PairShape4<D>::kSmem;
-  return launch_large(pair4_kernel<E, D>, done, smem, p.workers, kThreads4, smem, stream, p);
+  return launch_large(kKernel, done, smem, ctas, kThreads4, smem, stream, p);
+}
+template <class E, int D>
+cudaError_t start_wide4(const AttnParams &p, cudaStream_t stream) {
+  if (p.rows > wide_tile_rows(p.G)) return start_wide4<pair4_kernel<E, D>>(Shape4<D>::kPair, p.workers, p, stream);
+  return start_wide4<solo4_kernel<E, D>>(Shape4<D>::kSolo, p.workers / 2, p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_q4_wide(const AttnParams &p, int dtype, cudaStream_t stream) {
   if (dtype == SPEC_BF16)
-    return p.D == 64 ? start_pair4<Bf16, 64>(p, stream) : start_pair4<Bf16, 128>(p, stream);
-  return p.D == 64 ? start_pair4<F16, 64>(p, stream) : start_pair4<F16, 128>(p, stream);
+    return p.D == 64 ? start_wide4<Bf16, 64>(p, stream) : start_wide4<Bf16, 128>(p, stream);
+  return p.D == 64 ? start_wide4<F16, 64>(p, stream) : start_wide4<F16, 128>(p, stream);
 }
 
 }  // namespace sv

@@ -712,8 +712,7 @@ bool q4_wide(int N, int G) { return N * G > 16 && G <= 128; }
 AttnPlan q4_plan(int N, int G) {
   if (q4_wide(N, G)) {
     const int rows = wide_tile_rows(G);
-    if (N * G > rows) return {kSms4, 2 * rows, 7, 8, 16};
-    return {2 * kSms4, rows, 7, 2, 6};
+    return N * G > 32 ? AttnPlan{kSms4, 2 * rows, 7, 8, 16} : AttnPlan{kSms4, 32, 7, 4, 8};
   }
   return N * G <= 4 ? q4_plan_of<4>() : N * G <= 8 ? q4_plan_of<8>() : q4_plan_of<16>();
 }

@@ -23,6 +23,10 @@ constexpr int kThreads4 = 512, kMakers = 6, kIssuer = 8 + kMakers;
 // that the CTA is launched with.
 constexpr int kSoftRegs4 = 184, kRestRegs4 = 72;
 
+// For at most 32 rows: one warpgroup of softmax, eight warps that make operands, one that
+// issues products.
+constexpr int kSplitMakers = 8, kSplitIssuer = 4 + kSplitMakers, kSplitThreads = 32 * (kSplitIssuer + 1);
+
 // Hand-overs of a ring of entries.
 template <int kSize>
 struct Ring4 {
@@ -61,11 +65,12 @@ struct PairCtl4 {
   int dead, bad;
 };
 template <int D>
-struct SoloCtl4 {
-  Ring4<D == 128 ? 2 : 4> ring[2];
-  Stream4 stream[2];
-  unsigned long long q_full[2], q_empty[2], drain[2];
-  RunScratch<kThreads4, 2> runs;
+struct SplitCtl4 {
+  Ring4<D == 128 ? 4 : 8> ring;
+  // of even and odd tiles, in turn: outputs of a tile that is not the last one are waited
+  // for only where they are scaled, and its phase is not mistaken for the one before
+  unsigned long long s_full[2], p_full[2], o_done[2], q_full, q_empty, drain, meet;
+  RunScratch<kSplitThreads, 1> runs;
   uint32_t tmem;
   int dead, bad;
 };
@@ -77,8 +82,11 @@ struct Shape4 {
   static constexpr int kRaw = kEntries + kRing * Entry<D>::kBytes;
   static constexpr int kCtl = kRaw + kMakers * Raw4<D>::kWarp;
   static constexpr int kPair = kCtl + static_cast<int>(sizeof(PairCtl4<D>));
-  static constexpr int kSolo = kCtl + static_cast<int>(sizeof(SoloCtl4<D>));
-  static_assert(kPair <= 227 * 1024 && kSolo <= 227 * 1024, "shared memory of a CTA");
+  static constexpr int kSplitEntries = kQ, kSplitRaw = kSplitEntries + kRing * Entry<D>::kBytes;
+  static constexpr int kMeet = kSplitRaw + kSplitMakers * Raw4<D>::kWarp;
+  static constexpr int kSplitCtl = kMeet + static_cast<int>(sizeof(Quarters));
+  static constexpr int kSplit = kSplitCtl + static_cast<int>(sizeof(SplitCtl4<D>));
+  static_assert(kPair <= 227 * 1024 && kSplit <= 227 * 1024, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
@@ -415,109 +423,162 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
   void_run<E, D, kThreads4>(p, line);
 }
 
-// Units of one row tile: two streams with units, keys and values of their own, three
-// makers and an issuer each, so that the products of one run while the other is in its
-// softmax.
+// Units of at most 32 rows: each quarter of the lanes holds them all and weighs a quarter
+// of a tile's keys, and the quarters are added at the unit's end.  Scores have two places:
+// a tile's products with the keys run while the tile before is in its softmax.
 template <class E, int D>
-__global__ void __launch_bounds__(kThreads4, 1) solo4_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_constant__ AttnParams p) {
   using W = Entry<D>;
   using Shape = Shape4<D>;
-  using Ctl = SoloCtl4<D>;
-  constexpr int kRing = Shape::kRing / 2;
+  using Ctl = SplitCtl4<D>;
+  constexpr int kRing = Shape::kRing;
   extern __shared__ __align__(1024) char wide4_s[];
-  Ctl &ctl = *reinterpret_cast<Ctl *>(wide4_s + Shape::kCtl);
+  Ctl &ctl = *reinterpret_cast<Ctl *>(wide4_s + Shape::kSplitCtl);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  if (tid < 2) {
-    ctl.ring[tid].init();
-    ctl.stream[tid].init();
-    bar_init(&ctl.q_full[tid], 4);
-    bar_init(&ctl.q_empty[tid], 1);
-    bar_init(&ctl.drain[tid], 1);
+  if (tid == 0) {
+    ctl.ring.init();
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&ctl.s_full[i], 1);
+      bar_init(&ctl.p_full[i], 4);
+      bar_init(&ctl.o_done[i], 1);
+    }
+    bar_init(&ctl.q_full, 4);
+    bar_init(&ctl.q_empty, 1);
+    bar_init(&ctl.drain, 1);
+    bar_init(&ctl.meet, 4);
     ctl.dead = 0;
     ctl.bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kIssuer) tm_alloc(&ctl.tmem);
+  if (warp == kSplitIssuer) tm_alloc(&ctl.tmem);
   __syncwarp();
-  Line lines[2];
-  // barriers as well; consecutive workers on different CTAs
-  find_runs(p, ctl.runs, blockIdx.x, gridDim.x, lines);
+  Line lines[1];
+  find_runs(p, ctl.runs, blockIdx.x, 0, lines);  // barriers as well
+  const Line &line = lines[0];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // of this warp's stream
-  const int g = warp < 8 ? warp >> 2 : (warp < kIssuer ? (warp - 8) / (kMakers / 2) : warp - kIssuer);
-  const Line line = g ? lines[1] : lines[0];
   UnitWalk u;
   const bool busy = u.start(p, line);
-  if (lane == 0 && warp >= kIssuer) write_join(p, line, busy ? &u : nullptr);
+  if (tid == 0) write_join(p, line, busy ? &u : nullptr);
   tc_after();
   const uint32_t tmem = ctl.tmem;
-  if (lines[0].w0 == lines[0].w1 && lines[1].w0 == lines[1].w1) {
-    tm_free<kIssuer>(tmem, warp);
+  if (!busy) {  // the same for every thread
+    tm_free<kSplitIssuer>(tmem, warp);
     return;
   }
-  char *entries = wide4_s + Shape::kEntries + g * kRing * W::kBytes, *q_tile = wide4_s + g * Shape::kQ;
-  auto &ring = ctl.ring[g];
-  Stream4 &st = ctl.stream[g];
-  const uint32_t s_at = tmem + g * 128, o_at = tmem + 256 + g * 128;
+  char *entries = wide4_s + Shape::kSplitEntries;
+  bool ok = true;
 
-  if (warp < 8) {
-    more_regs<kSoftRegs4>();
-    if (busy)
-      weigh_rows<E, D>(p, line, u, warp & 3, lane, 0, p.rows, s_at, o_at, q_tile, st, &ctl.q_full[g],
-                       &ctl.q_empty[g], ring, &ctl.dead, &ctl.bad);
-  } else {
-    fewer_regs<kRestRegs4>();
-    if (warp < kIssuer) {
-      const int maker = warp - 8;
-      if (busy)
-        make_operands<D, kMakers / 2>(p, line, u, maker % (kMakers / 2), lane,
-                                      wide4_s + Shape::kRaw + maker * Raw4<D>::kWarp, entries, ring, &ctl.dead,
-                                      &ctl.bad);
-    } else {
-      // ------------------------------------------------------------- products
-      uint32_t tiles = 0, units = 0;
-      bool ok = true;
-      const uint32_t entries_at = smem_u32(entries), q_at = smem_u32(q_tile);
-      if (busy) do {
-          const int n_tiles = u.i1 - u.i0;
-          for (int i = 0; i < n_tiles; ++i, ++tiles) {
-            uint32_t e = 2 * tiles;
-            if (!(ok = warp_wait(&ring.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
-            if (i == 0 && !(ok = warp_wait(&ctl.q_full[g], units++ & 1u, &ctl.dead))) break;
-            issue_scores<F16, D>(s_at, q_at, Shape::kQPanel, entries_at + e % kRing * W::kBytes);
-            issue_commit(&st.s_full);
-            issue_commit(&ring.empty[e % kRing]);
-            if (i + 1 == n_tiles) issue_commit(&ctl.q_empty[g]);
-            ++e;
-            if (!(ok = warp_wait(&ring.full[e % kRing], (e / kRing) & 1u, &ctl.dead))) break;
-            if (!(ok = warp_wait(&st.p_full, tiles & 1u, &ctl.dead))) break;
-            issue_outputs<F16, D>(o_at, s_at, entries_at + e % kRing * W::kBytes, i == 0);
-            if (i + 1 == n_tiles) issue_commit(&st.o_done);
-            issue_commit(&ring.empty[e % kRing]);
-          }
-        } while (ok && u.next(p, line));
-      // nothing is in flight when the tensor memory goes back
-      issue_commit(&ctl.drain[g]);
-      bar_linger(&ctl.drain[g], 0u);
+  if (warp < 4) {
+    // -------------------------------------------------------------- softmax
+    const uint32_t s_at = tmem + (static_cast<uint32_t>(warp * 32) << 16), o_at = s_at + 256;
+    Quarters &quarters = *reinterpret_cast<Quarters *>(wide4_s + Shape::kMeet);
+    uint32_t t = 0, units = 0, met = 0;
+    float c = 0.f;
+    auto outputs_done = [&](uint32_t of) {
+      return ok = warp_wait(&ctl.o_done[of & 1], (of >> 1) & 1u, &ctl.dead);
+    };
+    // as in weigh_rows, four times
+    auto bring_queries = [&](const UnitWalk &w) {
+      if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) return;
+      ++units;
+      if (lane < w.live_rows(p)) {
+        const int r = w.r0 + lane, n = r / p.G;
+        c = put_query<E, D>(p.q + w.b * p.q_seq + n * p.q_token + (w.h * p.G + r - n * p.G) * p.q_head,
+                            p.scale_log2, wide4_s, Shape::kQPanel, tid);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(&ctl.q_full);
+    };
+    bring_queries(u);
+    for (bool more = true; ok && more;) {
+      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+      const bool mine = lane < live;
+      const int n = (u.r0 + min(lane, live - 1)) / p.G;
+      const float unit_c = c;
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < n_tiles; ++i, ++t) {
+        const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
+        const uint32_t seen =
+            all_seen(p, u.k, at0, kTileKeys) ? 0xFFFFFFFFu : seen_word(p, u.k, u.b, n, at0 + warp * 32);
+        if (!(ok = warp_wait(&ctl.s_full[t & 1], (t >> 1) & 1u, &ctl.dead))) break;
+        const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.ring.valid[t % kValidRing]);
+        const uint32_t word = ctl.ring.valid[t % kValidRing][warp];
+        softmax_part<F16, D>(unit_c, mine, tile_masked(p, u, at0, valid), seen & word, warp, s_at + (t & 1) * 128,
+                             o_at, i == 0, m, l,
+                             [&] {
+                               outputs_done(t - 1);
+                               tc_after();
+                               return ok;
+                             });
+        if (!ok) break;
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&ctl.p_full[t & 1]);
+      }
+      if (!ok) break;
+      const UnitWalk v = u;
+      more = u.next(p, line);
+      if (more) bring_queries(u);
+      if (!ok || !outputs_done(t - 1)) break;
+      if (!(ok = write_split<E, D, true>(p, v, line.worker, warp, lane, o_at, m, l, quarters, &ctl.meet, met,
+                                         &ctl.dead, &ctl.bad)))
+        break;
     }
+  } else if (warp < kSplitIssuer) {
+    // ------------------------------------------------- operands of the products
+    const int maker = warp - 4;
+    make_operands<D, kSplitMakers>(p, line, u, maker, lane, wide4_s + Shape::kSplitRaw + maker * Raw4<D>::kWarp,
+                                   entries, ctl.ring, &ctl.dead, &ctl.bad);
+  } else {
+    // ------------------------------------------------------------- products
+    uint32_t t = 0, units = 0;
+    const uint32_t entries_at = smem_u32(entries), q_at = smem_u32(wide4_s);
+    auto take = [&](uint32_t e) {  // an entry that is ready
+      ok = warp_wait(&ctl.ring.full[e % kRing], (e / kRing) & 1u, &ctl.dead);
+      return entries_at + e % kRing * W::kBytes;
+    };
+    do {
+      const int n_tiles = u.i1 - u.i0;
+      for (int i = 0; i <= n_tiles; ++i) {
+        if (i < n_tiles) {  // scores of tile i
+          const uint32_t e = 2 * (t + i), k_at = take(e);
+          if (!ok || (i == 0 && !(ok = warp_wait(&ctl.q_full, units++ & 1u, &ctl.dead)))) break;
+          issue_scores<F16, D>(tmem + ((t + i) & 1) * 128, q_at, Shape::kQPanel, k_at);
+          issue_commit(&ctl.s_full[(t + i) & 1]);
+          issue_commit(&ctl.ring.empty[e % kRing]);
+          if (i + 1 == n_tiles) issue_commit(&ctl.q_empty);
+        }
+        if (i > 0) {  // outputs of the tile before
+          const uint32_t b = t + i - 1, e = 2 * b + 1, v_at = take(e);
+          if (!ok || !(ok = warp_wait(&ctl.p_full[b & 1], (b >> 1) & 1u, &ctl.dead))) break;
+          issue_outputs<F16, D>(tmem + 256, tmem + (b & 1) * 128, v_at, i == 1);
+          issue_commit(&ctl.o_done[b & 1]);
+          issue_commit(&ctl.ring.empty[e % kRing]);
+        }
+      }
+      t += n_tiles;
+    } while (ok && u.next(p, line));
+    // nothing is in flight when the tensor memory goes back
+    issue_commit(&ctl.drain);
+    bar_linger(&ctl.drain, 0u);
   }
-  tm_free<kIssuer>(tmem, warp);
+  tm_free<kSplitIssuer>(tmem, warp);
   if (!ctl.dead) return;
-  void_run<E, D, kThreads4>(p, lines[0]);
-  void_run<E, D, kThreads4>(p, lines[1]);
+  void_run<E, D, kSplitThreads>(p, line);
 }
 
 namespace {
 
 template <auto kKernel>
-cudaError_t start_wide4(int smem, int ctas, const AttnParams &p, cudaStream_t stream) {
+cudaError_t start_wide4(int smem, int threads, const AttnParams &p, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  return launch_large(kKernel, done, smem, ctas, kThreads4, smem, stream, p);
+  return launch_large(kKernel, done, smem, p.workers, threads, smem, stream, p);
 }
 template <class E, int D>
 cudaError_t start_wide4(const AttnParams &p, cudaStream_t stream) {
-  if (p.rows > wide_tile_rows(p.G)) return start_wide4<pair4_kernel<E, D>>(Shape4<D>::kPair, p.workers, p, stream);
-  return start_wide4<solo4_kernel<E, D>>(Shape4<D>::kSolo, p.workers / 2, p, stream);
+  return p.rows <= 32 ? start_wide4<split4_kernel<E, D>>(Shape4<D>::kSplit, kSplitThreads, p, stream)
+                      : start_wide4<pair4_kernel<E, D>>(Shape4<D>::kPair, kThreads4, p, stream);
 }
 
 }  // namespace

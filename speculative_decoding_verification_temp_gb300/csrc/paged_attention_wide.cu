@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const uint32_t word = part < 2 ? (part == 0 ? valid.x : valid.y)
                                            : (part == 2 ? valid.z : valid.w);
             softmax_part<E, D>(p.scale_log2, mine, masked, seen.x & word, part, s_at + lanes,
-                               o_at + lanes, i == 0, m, l);
+                               o_at + lanes, i == 0, m, l, [] { return true; });
           } else if (works) {
             softmax_tile<E, D>(p.scale_log2, mine, masked, both(seen, valid), s_at + lanes,
                                o_at + lanes, i == 0, m, l);

@@ -106,13 +106,6 @@ __device__ __forceinline__ void box_load(uint32_t to, const CUtensorMap *map, co
       "l"(map), "r"(smem_u32(bar)), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(x4)
       : "memory");
 }
-// Untiled: both addresses and the size are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t to, const void *from, uint32_t bytes, const void *bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
-      "l"(from), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
 template <int kRegs>
 __device__ __forceinline__ void more_regs() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -438,11 +431,12 @@ __device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, ui
 }
 
 // The same for a quarter of the tile's keys, those of the warp's part: weights of
-// zero for the other quarters' keys.  seen: of the 32 keys.
-template <class E, int D>
+// zero for the other quarters' keys.  seen: of the 32 keys; outputs_whole: called by
+// whole warps before the outputs so far are scaled, false where a wait gave up.
+template <class E, int D, class F>
 __device__ __forceinline__ void softmax_part(float c, bool mine, bool masked, uint32_t seen,
                                              int part, uint32_t s_at, uint32_t o_at, bool first,
-                                             float &m, float &l) {
+                                             float &m, float &l, const F &outputs_whole) {
   tc_after();
   uint32_t s[32];
   tm_load32(s, s_at + part * 32);
@@ -464,7 +458,7 @@ __device__ __forceinline__ void softmax_part(float c, bool mine, bool masked, ui
     const float f = m == -INFINITY ? 0.f : fast_exp2(m - to);
     l *= f;
     m = to;
-    if (!first) {
+    if (!first && outputs_whole()) {
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
         uint32_t o[16];
@@ -539,6 +533,18 @@ static __device__ __noinline__ float2 nonfinite_values_q4(const AttnParams &p, c
   return make_float2(a[0], a[1]);
 }
 
+// What values that are not finite add to outputs d to d + 3 of token n's rows.
+template <class E, int D, bool kFour>
+__device__ __forceinline__ float4 nonfinite_row(const AttnParams &p, const UnitWalk &u, int n, int d) {
+  if constexpr (kFour) {
+    const float2 a = nonfinite_values_q4<D, 32>(p, u, n, d);
+    const float2 b = nonfinite_values_q4<D, 32>(p, u, n, d + 2);
+    return make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    return nonfinite_values<typename E::T, kTileKeys>(p, u, n, d, make_float4(0.f, 0.f, 0.f, 0.f));
+  }
+}
+
 // A row's end: its outputs from tensor memory, divided by the sum, or its piece
 // of a cut unit.  By whole warps; `mine`: the row exists; kFour: of a 4-bit cache.
 template <class E, int D, bool kFour = false>
@@ -590,14 +596,7 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
   }
   if (bad && mine && l != 0.f) {
     for (int d = 0; d < D; d += 4) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if constexpr (kFour) {
-        const float2 a = nonfinite_values_q4<D, 32>(p, u, n, d);
-        const float2 b = nonfinite_values_q4<D, 32>(p, u, n, d + 2);
-        v = make_float4(a.x, a.y, b.x, b.y);
-      } else {
-        v = nonfinite_values<TE, kTileKeys>(p, u, n, d, v);
-      }
+      const float4 v = nonfinite_row<E, D, kFour>(p, u, n, d);
       const float x[4] = {v.x, v.y, v.z, v.w};
       for (int e = 0; e < 4; ++e) {
         if (x[e] == 0.f) continue;
@@ -632,7 +631,7 @@ struct Quarters {
 // four warps.  Few rows meet at once (8 of 128 outputs, 16 of 64), more rows 32
 // outputs at a time, a row's 16-byte pieces permuted so that eight rows meet
 // eight banks.  False: a wait gave up.
-template <class E, int D>
+template <class E, int D, bool kFour = false>
 __device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk &u, int worker,
                                             int part, int lane, uint32_t o_at, float m, float l,
                                             Quarters &x, const void *meet, uint32_t &met, int *dead,
@@ -698,8 +697,7 @@ __device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk 
       if (*reinterpret_cast<const volatile int *>(bad)) {
 #pragma unroll 1
         for (int e = 0; e < 8; e += 4) {
-          const float4 y = nonfinite_values<TE, kTileKeys>(p, u, (u.r0 + row) / p.G, d + e,
-                                                           make_float4(0.f, 0.f, 0.f, 0.f));
+          const float4 y = nonfinite_row<E, D, kFour>(p, u, (u.r0 + row) / p.G, d + e);
           if (e == 0) {
             v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
           } else {

@@ -23,9 +23,9 @@ constexpr int kThreads4 = 512, kMakers = 6, kIssuer = 8 + kMakers;
 // that the CTA is launched with.
 constexpr int kSoftRegs4 = 184, kRestRegs4 = 72;
 
-// For at most 32 rows: one warpgroup of softmax, eight warps that make operands, one that
+// For at most 32 rows: two warpgroups of softmax, six warps that make operands, one that
 // issues products.
-constexpr int kSplitMakers = 8, kSplitIssuer = 4 + kSplitMakers, kSplitThreads = 32 * (kSplitIssuer + 1);
+constexpr int kSplitMakers = 6, kSplitIssuer = 8 + kSplitMakers, kSplitThreads = 32 * (kSplitIssuer + 1);
 
 // Hand-overs of a ring of entries.
 template <int kSize>
@@ -67,9 +67,13 @@ struct PairCtl4 {
 template <int D>
 struct SplitCtl4 {
   Ring4<D == 128 ? 4 : 8> ring;
-  // of even and odd tiles, in turn: outputs of a tile that is not the last one are waited
-  // for only where they are scaled, and its phase is not mistaken for the one before
-  unsigned long long s_full[2], p_full[2], o_done[2], q_full, q_empty, drain, meet;
+  // of a group's even and odd tiles, in turn: outputs of a tile that is not the last one
+  // are waited for only where they are scaled, and its phase is not mistaken for the one
+  // before
+  struct {
+    unsigned long long s_full[2], p_full[2], o_done[2], q_full, q_empty, meet;
+  } group[2];
+  unsigned long long drain;
   RunScratch<kSplitThreads, 1> runs;
   uint32_t tmem;
   int dead, bad;
@@ -84,7 +88,7 @@ struct Shape4 {
   static constexpr int kPair = kCtl + static_cast<int>(sizeof(PairCtl4<D>));
   static constexpr int kSplitEntries = kQ, kSplitRaw = kSplitEntries + kRing * Entry<D>::kBytes;
   static constexpr int kMeet = kSplitRaw + kSplitMakers * Raw4<D>::kWarp;
-  static constexpr int kSplitCtl = kMeet + static_cast<int>(sizeof(Quarters));
+  static constexpr int kSplitCtl = kMeet + 2 * static_cast<int>(sizeof(Quarters));
   static constexpr int kSplit = kSplitCtl + static_cast<int>(sizeof(SplitCtl4<D>));
   static_assert(kPair <= 227 * 1024 && kSplit <= 227 * 1024, "shared memory of a CTA");
 };
@@ -108,12 +112,15 @@ __device__ __forceinline__ uint4 word_values(uint32_t w, __half2 scale, __half2 
 // 128-byte swizzle), by one thread; returns the factor that the row's scores take.  Rows
 // whose largest lies within 2^-4 .. 2^14 stay as they are, others are brought there by a
 // power of two: float16's step below its normal values, 2^-24, is then 2^-20 of the largest.
-template <class E, int D>
-__device__ __forceinline__ float put_query(const char *from, float scale, char *tile, int panel_bytes, int row) {
+// By whole warps: `mine`: there is such a row; ready: the place may be written, false where
+// a wait gave up.
+template <class E, int D, class F>
+__device__ __forceinline__ float put_query(const char *from, bool mine, float scale, char *tile, int panel_bytes,
+                                           int row, const F &ready) {
   using TE = typename E::T;
   uint4 v[D / 8];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) v[i] = *reinterpret_cast<const uint4 *>(from + i * 16);
+  for (int i = 0; i < D / 8; ++i) v[i] = mine ? *reinterpret_cast<const uint4 *>(from + i * 16) : make_uint4(0, 0, 0, 0);
   float top = 0.f;
   bool odd = false;
 #pragma unroll
@@ -127,8 +134,9 @@ __device__ __forceinline__ float put_query(const char *from, float scale, char *
   const int exponent = top > 16384.f || (top > 1e-30f && top < 0.0625f) ? min(max(8 - ilogbf(top), -126), 126) : 0;
   // a query that is not finite makes its row NaN
   const float up = odd ? 0.f : __int_as_float((127 + exponent) << 23);
+  if (!ready()) return 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
+  for (int i = 0; mine && i < D / 8; ++i) {
     uint32_t h[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -159,14 +167,13 @@ __device__ __forceinline__ void weigh_rows(const AttnParams &p, const Line &line
   // have read theirs.  Its outputs are written behind that, while the next unit's first
   // products run.
   auto bring_queries = [&](const UnitWalk &w) {
-    const int live = w.live_rows(p);
-    if (!(ok = warp_wait(q_empty, (units & 1u) ^ 1u, dead))) return;
+    const bool has = row < w.live_rows(p) && tile_row < tile_rows;
+    const int r = w.r0 + (has ? row : 0), n = r / p.G;
+    c = put_query<E, D>(p.q + w.b * p.q_seq + n * p.q_token + (w.h * p.G + r - n * p.G) * p.q_head, has,
+                        p.scale_log2, q_tile, Shape4<D>::kQPanel, tile_row,
+                        [&] { return ok = warp_wait(q_empty, (units & 1u) ^ 1u, dead); });
+    if (!ok) return;
     ++units;
-    if (row < live && tile_row < tile_rows) {
-      const int r = w.r0 + row, n = r / p.G;
-      c = put_query<E, D>(p.q + w.b * p.q_seq + n * p.q_token + (w.h * p.G + r - n * p.G) * p.q_head,
-                          p.scale_log2, q_tile, Shape4<D>::kQPanel, tile_row);
-    }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) bar_arrive(q_full);
@@ -425,7 +432,8 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
 
 // Units of at most 32 rows: each quarter of the lanes holds them all and weighs a quarter
 // of a tile's keys, and the quarters are added at the unit's end.  Scores have two places:
-// a tile's products with the keys run while the tile before is in its softmax.
+// a tile's products with the keys run while the tile before is in its softmax.  Two
+// warpgroups take the units in turn: one writes a unit while the other has the next.
 template <class E, int D>
 __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_constant__ AttnParams p) {
   using W = Entry<D>;
@@ -437,15 +445,17 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   if (tid == 0) {
     ctl.ring.init();
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&ctl.s_full[i], 1);
-      bar_init(&ctl.p_full[i], 4);
-      bar_init(&ctl.o_done[i], 1);
+    for (auto &x : ctl.group) {
+      for (int i = 0; i < 2; ++i) {
+        bar_init(&x.s_full[i], 1);
+        bar_init(&x.p_full[i], 4);
+        bar_init(&x.o_done[i], 1);
+      }
+      bar_init(&x.q_full, 4);
+      bar_init(&x.q_empty, 1);
+      bar_init(&x.meet, 4);
     }
-    bar_init(&ctl.q_full, 4);
-    bar_init(&ctl.q_empty, 1);
     bar_init(&ctl.drain, 1);
-    bar_init(&ctl.meet, 4);
     ctl.dead = 0;
     ctl.bad = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -468,96 +478,97 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_c
   char *entries = wide4_s + Shape::kSplitEntries;
   bool ok = true;
 
-  if (warp < 4) {
+  if (warp < 8) {
     // -------------------------------------------------------------- softmax
-    const uint32_t s_at = tmem + (static_cast<uint32_t>(warp * 32) << 16), o_at = s_at + 256;
-    Quarters &quarters = *reinterpret_cast<Quarters *>(wide4_s + Shape::kMeet);
-    uint32_t t = 0, units = 0, met = 0;
-    float c = 0.f;
-    auto outputs_done = [&](uint32_t of) {
-      return ok = warp_wait(&ctl.o_done[of & 1], (of >> 1) & 1u, &ctl.dead);
-    };
-    // as in weigh_rows, four times
-    auto bring_queries = [&](const UnitWalk &w) {
-      if (!(ok = warp_wait(&ctl.q_empty, (units & 1u) ^ 1u, &ctl.dead))) return;
-      ++units;
-      if (lane < w.live_rows(p)) {
-        const int r = w.r0 + lane, n = r / p.G;
-        c = put_query<E, D>(p.q + w.b * p.q_seq + n * p.q_token + (w.h * p.G + r - n * p.G) * p.q_head,
-                            p.scale_log2, wide4_s, Shape::kQPanel, tid);
+    const int g = warp >> 2, part = warp & 3;
+    auto &x = ctl.group[g];
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(part * 32) << 16), o_at = lanes + 256 + g * 128;
+    Quarters &quarters = reinterpret_cast<Quarters *>(wide4_s + Shape::kMeet)[g];
+    uint32_t t = 0, own = 0, units = 0, met = 0;  // tiles, of this group, units of this group
+    int unit = 0;
+    auto outputs_done = [&](uint32_t of) { return ok = warp_wait(&x.o_done[of & 1], (of >> 1) & 1u, &ctl.dead); };
+    do {
+      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
+      if ((unit++ & 1) != g) {
+        t += n_tiles;
+        continue;
       }
+      const bool mine = lane < live;
+      const int r = u.r0 + min(lane, live - 1), n = r / p.G;
+      // once the products of the unit before, the other group's, have read theirs
+      const float c = put_query<E, D>(
+          p.q + u.b * p.q_seq + n * p.q_token + (u.h * p.G + r - n * p.G) * p.q_head, mine, p.scale_log2, wide4_s,
+          Shape::kQPanel, part * 32 + lane, [&] {
+            if (unit > 1) ok = warp_wait(&ctl.group[g ^ 1].q_empty, (units + g - 1) & 1u, &ctl.dead);
+            return ok;
+          });
+      if (!ok) break;
+      ++units;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) bar_arrive(&ctl.q_full);
-    };
-    bring_queries(u);
-    for (bool more = true; ok && more;) {
-      const int n_tiles = u.i1 - u.i0, live = u.live_rows(p);
-      const bool mine = lane < live;
-      const int n = (u.r0 + min(lane, live - 1)) / p.G;
-      const float unit_c = c;
+      if (lane == 0) bar_arrive(&x.q_full);
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < n_tiles; ++i, ++t) {
+      for (int i = 0; i < n_tiles; ++i, ++t, ++own) {
         const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
         const uint32_t seen =
-            all_seen(p, u.k, at0, kTileKeys) ? 0xFFFFFFFFu : seen_word(p, u.k, u.b, n, at0 + warp * 32);
-        if (!(ok = warp_wait(&ctl.s_full[t & 1], (t >> 1) & 1u, &ctl.dead))) break;
+            all_seen(p, u.k, at0, kTileKeys) ? 0xFFFFFFFFu : seen_word(p, u.k, u.b, n, at0 + part * 32);
+        if (!(ok = warp_wait(&x.s_full[own & 1], (own >> 1) & 1u, &ctl.dead))) break;
         const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.ring.valid[t % kValidRing]);
-        const uint32_t word = ctl.ring.valid[t % kValidRing][warp];
-        softmax_part<F16, D>(unit_c, mine, tile_masked(p, u, at0, valid), seen & word, warp, s_at + (t & 1) * 128,
-                             o_at, i == 0, m, l,
-                             [&] {
-                               outputs_done(t - 1);
+        const uint32_t word = ctl.ring.valid[t % kValidRing][part];
+        softmax_part<F16, D>(c, mine, tile_masked(p, u, at0, valid), seen & word, part, lanes + (t & 1) * 128,
+                             o_at, i == 0, m, l, [&] {
+                               outputs_done(own - 1);
                                tc_after();
                                return ok;
                              });
         if (!ok) break;
         tc_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(&ctl.p_full[t & 1]);
+        if (lane == 0) bar_arrive(&x.p_full[own & 1]);
       }
-      if (!ok) break;
-      const UnitWalk v = u;
-      more = u.next(p, line);
-      if (more) bring_queries(u);
-      if (!ok || !outputs_done(t - 1)) break;
-      if (!(ok = write_split<E, D, true>(p, v, line.worker, warp, lane, o_at, m, l, quarters, &ctl.meet, met,
+      // the other group goes on with the next unit meanwhile
+      if (!ok || !outputs_done(own - 1)) break;
+      if (!(ok = write_split<E, D, true>(p, u, line.worker, part, lane, o_at, m, l, quarters, &x.meet, met,
                                          &ctl.dead, &ctl.bad)))
         break;
-    }
+    } while (u.next(p, line));
   } else if (warp < kSplitIssuer) {
     // ------------------------------------------------- operands of the products
-    const int maker = warp - 4;
+    const int maker = warp - 8;
     make_operands<D, kSplitMakers>(p, line, u, maker, lane, wide4_s + Shape::kSplitRaw + maker * Raw4<D>::kWarp,
                                    entries, ctl.ring, &ctl.dead, &ctl.bad);
   } else {
     // ------------------------------------------------------------- products
-    uint32_t t = 0, units = 0;
+    uint32_t t = 0, own[2] = {0, 0}, units = 0;  // tiles, of each group
     const uint32_t entries_at = smem_u32(entries), q_at = smem_u32(wide4_s);
     auto take = [&](uint32_t e) {  // an entry that is ready
       ok = warp_wait(&ctl.ring.full[e % kRing], (e / kRing) & 1u, &ctl.dead);
       return entries_at + e % kRing * W::kBytes;
     };
     do {
-      const int n_tiles = u.i1 - u.i0;
+      const int n_tiles = u.i1 - u.i0, g = units & 1;
+      auto &x = ctl.group[g];
+      const uint32_t base = g ? own[1] : own[0];
       for (int i = 0; i <= n_tiles; ++i) {
         if (i < n_tiles) {  // scores of tile i
           const uint32_t e = 2 * (t + i), k_at = take(e);
-          if (!ok || (i == 0 && !(ok = warp_wait(&ctl.q_full, units++ & 1u, &ctl.dead)))) break;
+          if (!ok || (i == 0 && !(ok = warp_wait(&x.q_full, (units >> 1) & 1u, &ctl.dead)))) break;
           issue_scores<F16, D>(tmem + ((t + i) & 1) * 128, q_at, Shape::kQPanel, k_at);
-          issue_commit(&ctl.s_full[(t + i) & 1]);
+          issue_commit(&x.s_full[(base + i) & 1]);
           issue_commit(&ctl.ring.empty[e % kRing]);
-          if (i + 1 == n_tiles) issue_commit(&ctl.q_empty);
+          if (i + 1 == n_tiles) issue_commit(&x.q_empty);
         }
         if (i > 0) {  // outputs of the tile before
-          const uint32_t b = t + i - 1, e = 2 * b + 1, v_at = take(e);
-          if (!ok || !(ok = warp_wait(&ctl.p_full[b & 1], (b >> 1) & 1u, &ctl.dead))) break;
-          issue_outputs<F16, D>(tmem + 256, tmem + (b & 1) * 128, v_at, i == 1);
-          issue_commit(&ctl.o_done[b & 1]);
+          const uint32_t b = t + i - 1, of = base + i - 1, e = 2 * b + 1, v_at = take(e);
+          if (!ok || !(ok = warp_wait(&x.p_full[of & 1], (of >> 1) & 1u, &ctl.dead))) break;
+          issue_outputs<F16, D>(tmem + 256 + g * 128, tmem + (b & 1) * 128, v_at, i == 1);
+          issue_commit(&x.o_done[of & 1]);
           issue_commit(&ctl.ring.empty[e % kRing]);
         }
       }
       t += n_tiles;
+      (g ? own[1] : own[0]) += n_tiles;
+      ++units;
     } while (ok && u.next(p, line));
     // nothing is in flight when the tensor memory goes back
     issue_commit(&ctl.drain);

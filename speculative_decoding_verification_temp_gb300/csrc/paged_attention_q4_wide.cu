@@ -52,7 +52,7 @@ struct Stream4 {
 // Rows as they are, copied by a maker for itself.
 template <int D>
 struct Raw4 {
-  static constexpr int kSlots = 1, kWarp = kSlots * Q4Copies<q4_row_bytes(D)>::kBytes;
+  static constexpr int kWarp = Q4Copies<q4_row_bytes(D)>::kBytes;
 };
 
 template <int D>
@@ -96,16 +96,24 @@ struct Shape4 {
 __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t word_of(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 
-// The eight values of a word as float16: a nibble becomes 1024 + n or 64 + n by its mask,
-// n by a subtraction, both exactly.
+// The operands are values times kFourth (paged_attention_wide.cuh), 2^-4.  A nibble at
+// bits 6 to 9 is a float16 below its normal ones, n 2^-18, exactly: with a scale of s 2^14,
+// for s below 4 (a group that spans less than 60), a value takes a shift, a mask and half
+// of a fused multiply and add.  (The nibble as 1024 + n, less 1024, before that: twice the
+// instructions of float16, which run at a quarter of the rate.)
 __device__ __forceinline__ uint4 word_values(uint32_t w, __half2 scale, __half2 low) {
-  auto value = [&](uint32_t x, bool high) {
-    const __half2 n = high ? __hsub2(half2_of((x & 0x00F000F0u) | 0x54005400u), half2_of(0x54005400u))
-                           : __hsub2(half2_of((x & 0x000F000Fu) | 0x64006400u), half2_of(0x64006400u));
-    return word_of(__hfma2(n, scale, low));
-  };
-  const uint32_t x = w >> 8;
-  return make_uint4(value(w, false), value(w, true), value(x, false), value(x, true));
+  auto value = [&](uint32_t x) { return word_of(__hfma2(half2_of(x & 0x03C003C0u), scale, low)); };
+  return make_uint4(value(w << 6), value(w << 2), value(w >> 2), value(w >> 6));
+}
+// For any scale.
+__device__ __forceinline__ uint4 word_values_any(uint32_t w, uint32_t pair) {
+  const __half2 x = half2_of(pair), part = __float2half2_rn(kFourth);
+  const __half2 scale = __hmul2(__low2half2(x), part), low = __hmul2(__high2half2(x), part);
+  uint32_t v[4];
+  for (int i = 0; i < 4; ++i)
+    v[i] = word_of(__hfma2(__hsub2(half2_of((w >> 4 * i & 0x000F000Fu) | 0x64006400u), half2_of(0x64006400u)),
+                           scale, low));
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // A row of queries as float16 into its place of a tile (panels of 64 values, the
@@ -146,7 +154,7 @@ __device__ __forceinline__ float put_query(const char *from, bool mine, float sc
     *reinterpret_cast<uint4 *>(tile + i / 8 * panel_bytes + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
         make_uint4(h[0], h[1], h[2], h[3]);
   }
-  return odd ? __int_as_float(0x7FC00000) : scale * __int_as_float((127 - exponent) << 23);
+  return odd ? __int_as_float(0x7FC00000) : scale * (1.f / kFourth) * __int_as_float((127 - exponent) << 23);
 }
 
 // The rows of a stream, a thread each: their queries, their weights and their outputs.
@@ -214,8 +222,9 @@ __device__ __forceinline__ void weigh_rows(const AttnParams &p, const Line &line
 }
 
 // A stream's or a pair's operands, by kCount warps of which this is the maker-th: they
-// take 32 keys and their values in turn, copied into the warp's own slots while those
-// before are made, keys into an entry, then values into the next.
+// take 32 keys and their values in turn, keys into an entry, then values into the next.
+// The warp copies keys behind those that it has made while it makes the values, and the
+// other way round.
 template <int D, int kCount, int kRing>
 __device__ __forceinline__ void make_operands(const AttnParams &p, const Line &line, UnitWalk u, int maker,
                                               int lane, char *raw, char *entries, Ring4<kRing> &ring,
@@ -224,8 +233,8 @@ __device__ __forceinline__ void make_operands(const AttnParams &p, const Line &l
   constexpr int kRow = q4_row_bytes(D);
   uint32_t tiles = 0;
   bool ok = true;
-  constexpr int kParts = kTileKeys / kQ4Keys, kSlots = Raw4<D>::kSlots;
-  using Copies = Q4Copies<kRow>;
+  constexpr int kParts = kTileKeys / kQ4Keys;
+  using Copies = Q4Copies<kRow, kCount * kQ4Keys>;
   Copies copies(p, lane);
   const uint32_t raw_at = smem_u32(raw);
   // a pass makes 32 16-byte pieces of codes, of eight neighbouring rows each (which
@@ -242,31 +251,22 @@ __device__ __forceinline__ void make_operands(const AttnParams &p, const Line &l
     // this warp's parts: first, first + kCount, ...
     const int first = (maker + kCount - static_cast<int>(done % kCount)) % kCount;
     copies.begin(p, u, at_of(first), lane);
-    uint32_t there[kSlots];
-#pragma unroll
-    for (int x = 0; x < kSlots; ++x) {
-      there[x] = 0u;
-      if (first + x * kCount < parts)
-        there[x] = copies.ask(p, u, at_of(first + x * kCount), raw_at + x * Copies::kBytes, lane);
-      copy_commit();
-    }
-    int slot = 0;
-    for (int part = first; ok && part < parts; part += kCount) {
-      copy_wait<kSlots - 1>();
-      __syncwarp();
-      const uint32_t tile = tiles + part / kParts;
-      const int quarter = part % kParts, at0 = at_of(part);
-      uint32_t word = there[0];
-#pragma unroll
-      for (int x = 1; x < kSlots; ++x)
-        if (slot == x) word = there[x];
-      const bool masked = word != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Keys);
-      char *rows = raw + slot * Copies::kBytes;
+    uint32_t word = 0u;  // of the next part
+    // (the first turn makes none)
+#pragma unroll 1
+    for (int part = first - kCount; ok && part < parts; part += kCount) {
+      const uint32_t tile = tiles + part / kParts, there = word;
+      const int quarter = part % kParts, at0 = at_of(part), ahead = part + kCount;
+      const bool masked = there != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Keys);
+      const char *rows = raw;
 #pragma unroll 1
       for (int values = 0; values < 2; ++values, rows += kQ4Keys * kRow) {
+       if (part >= 0) {
+        copy_wait<1>();
         const uint32_t e = 2 * tile + values;
         if (!(ok = warp_wait(&ring.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, dead))) break;
-        if (!values && lane == 0) ring.valid[tile % kValidRing][quarter] = word;
+        __syncwarp();
+        if (!values && lane == 0) ring.valid[tile % kValidRing][quarter] = there;
         // 32 values are half of a panel's row
         char *entry = entries + e % kRing * W::kBytes + quarter * (kQ4Keys / 8) * W::kGroup + piece / 2 * W::kPanel;
 #pragma unroll 1
@@ -285,7 +285,7 @@ __device__ __forceinline__ void make_operands(const AttnParams &p, const Line &l
           if (masked) {
             // rows that were not copied stand for zeros, and so do groups that are not
             // finite, which nonfinite_values_q4 adds
-            const bool copied = (word >> key) & 1u;
+            const bool copied = (there >> key) & 1u;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               if (!copied || (values && !q4_finite(q4_pair(pair[j])))) {
@@ -295,27 +295,36 @@ __device__ __forceinline__ void make_operands(const AttnParams &p, const Line &l
           }
           char *to = entry + key / 8 * W::kGroup + r * W::kRow;
           const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+          auto put = [&](int j, uint4 v) {
+            *reinterpret_cast<uint4 *>(to + ((((piece & 1) * 4 + j) ^ r) << 4)) = v;
+          };
+          // (as integers: scales are not below zero; not-a-number counts as large)
+          const uint32_t large = max(pair[0] & 0xFFFFu, pair[1] & 0xFFFFu);
+          if (__any_sync(0xFFFFFFFFu, large >= 0x4400u)) {
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j)
+              put(j, word_values_any(word_at(row + piece * 16 + j * 4), j < 2 ? pair[0] : pair[1]));
+          } else {
+            uint32_t f[2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(to + ((((piece & 1) * 4 + j) ^ r) << 4)) =
-                word_values(w[j], half2_of(__byte_perm(pair[j >> 1], 0, 0x1010)),
-                            half2_of(__byte_perm(pair[j >> 1], 0, 0x3232)));
+            for (int j = 0; j < 2; ++j)
+              f[j] = word_of(__hmul2(half2_of(pair[j]), __floats2half2_rn(kFourth * 262144.f, kFourth)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              put(j, word_values(w[j], half2_of(__byte_perm(f[j >> 1], 0, 0x1010)),
+                                 half2_of(__byte_perm(f[j >> 1], 0, 0x3232))));
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) bar_arrive(&ring.full[e % kRing]);
+       }
+        // the rows are read: those ahead may take their place, while the others are made
+        if (ahead < parts) word = copies.template ask<false>(p, u, at_of(ahead), raw_at, lane, values);
+        copy_commit();
       }
       if (!ok) break;
       if (done == 0 && part == 0) first_wait(&ring.full[0], p.first_wait, dead);
-      const int ahead = part + kSlots * kCount;
-      if (ahead < parts) {
-        const uint32_t next = copies.ask(p, u, at_of(ahead), raw_at + slot * Copies::kBytes, lane);
-#pragma unroll
-        for (int x = 0; x < kSlots; ++x)
-          if (slot == x) there[x] = next;
-      }
-      copy_commit();
-      slot = slot + 1 == kSlots ? 0 : slot + 1;
     }
     tiles += n_tiles;
     done += parts;

@@ -23,6 +23,9 @@ constexpr float kSlack = 8.f;
 // raised to, so that weights reach 2^(kLift + kSlack) = 2^15 at most, and those that
 // float16 rounds to zero are below 2^-32 of the row's largest instead of 2^-25.
 constexpr float kLift = 7.f;
+// What the operands made of a 4-bit cache are multiplied by; scores and outputs take the
+// factor back.  Values of 2^-10 and more keep all of float16's bits.
+constexpr float kFourth = 1.f / 16.f;
 
 // Bytes of an entry of 128 rows.
 template <int D>
@@ -558,7 +561,7 @@ __device__ __forceinline__ void write_row(const AttnParams &p, const UnitWalk &u
   const bool wide_out = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
   const long long at = mine ? out_row(p, u.b, u.h, u.r0 + row) : 0;
   TE *out = static_cast<TE *>(p.out) + at * D;
-  const float norm = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f);
+  const float norm = l == 0.f ? 0.f : (whole ? 1.f / l : 1.f) * (kFour ? 1.f / kFourth : 1.f);
   tc_after();
 #pragma unroll 1
   for (int d = 0; d < D; d += 32) {
@@ -678,6 +681,7 @@ __device__ __forceinline__ bool write_split(const AttnParams &p, const UnitWalk 
           const float lw = x.ml[w][1][row];
           f[w] = lw == 0.f ? 0.f : fast_exp2(x.ml[w][0][row] - M);
           sum += f[w] * lw;
+          if constexpr (kFour) f[w] *= 1.f / kFourth;
         }
       }
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};

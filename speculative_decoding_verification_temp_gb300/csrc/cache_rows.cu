@@ -59,15 +59,24 @@ __device__ __forceinline__ unsigned long long turn_of(double frequency) {
       static_cast<long long>(__double2ull_rd((r - floor(r)) * 18446744073709551616.0)));
 }
 
+// Where a pair's angle is: neighbouring lanes take neighbouring pieces of kEach pairs, and
+// of a piece one pair at a time, so that the first pairs of all pieces come first, then the
+// second ones (pairs in order: four lanes meet a bank; prompts' rows 84 us, 69 so).
+template <int kEach>
+__device__ __forceinline__ int angle_at(int pairs, int pair) {
+  return pair % kEach * (pairs / kEach) + pair / kEach;
+}
+
 // cos and sin of every (token of the batch, pair), by the whole CTA; place(i): the
-// position of token i of the batch.  Ends with a barrier.
+// position of token i of the batch; each: of angle_at.  Ends with a barrier.
 template <class Place>
-__device__ __forceinline__ void find_angles(const Rotation &r, int tokens, Place place, float2 *cs) {
+__device__ __forceinline__ void find_angles(const Rotation &r, int tokens, Place place, float2 *cs, int each) {
   // pairs <= kRotThreads: a thread keeps its pair
   const int per = kRotThreads / r.pairs, pair = threadIdx.x % r.pairs;
   const int first = threadIdx.x / r.pairs;
   if (first < per && first < tokens) {
     const double f = __ldg(r.frequency + pair);
+    const int to = pair % each * (r.pairs / each) + pair / each;
     const unsigned long long turn = turn_of(f);
     for (int i = first; i < tokens; i += per) {
       const long long at = place(i);
@@ -77,7 +86,7 @@ __device__ __forceinline__ void find_angles(const Rotation &r, int tokens, Place
       // fraction * 2^-64 turns are fraction * 2^-63 half turns
       sincospif(static_cast<float>(fraction) * 1.0842021724855044e-19f, &s, &c);
       if (!isfinite(f)) s = c = __int_as_float(0x7FC00000);
-      cs[i * r.pairs + pair] = make_float2(c * r.amplitude, (r.inverse ? -s : s) * r.amplitude);
+      cs[i * r.pairs + to] = make_float2(c * r.amplitude, (r.inverse ? -s : s) * r.amplitude);
     }
   }
   __syncthreads();
@@ -89,110 +98,183 @@ __device__ __forceinline__ void turn(float &a, float &b, float2 cs) {
   a = x;
 }
 
-// One row rotated, by the `lanes` threads of which this is the lane-th.  kVector:
-// the pairs' halves begin at 16-byte pieces.
+// Pairs of a piece (angle_at); pairs that do not fall on whole pieces stay in order.
 template <class E, bool kVector>
-__device__ __forceinline__ void rotate_row(const char *from, char *to, int D, const Rotation &r,
-                                           const float2 *cs, int lane, int lanes) {
+__device__ __forceinline__ int each_of(const Rotation &r) {
+  constexpr int kN = Piece<E>::kN;
+  return !kVector || r.pairs == 0 ? 1 : (r.interleaved ? kN / 2 : kN);
+}
+
+// A row to rotate: angles NULL: there is none.
+struct RowJob {
+  const char *from;
+  char *to;
+  const float2 *angles;
+};
+
+constexpr int kAtOnce = 2, kFourAtOnce = 1;
+
+// Walks the (token, head) rows of a batch, every groups-th of them.
+struct RowWalk {
+  int token, h, heads, step_token, step_h;
+  __device__ __forceinline__ RowWalk(int heads, int group, int groups)
+      : token(group / heads), h(group - token * heads), heads(heads), step_token(groups / heads),
+        step_h(groups - step_token * heads) {}
+  __device__ __forceinline__ void next() {
+    token += step_token;
+    h += step_h;
+    if (h >= heads) {
+      h -= heads;
+      ++token;
+    }
+  }
+};
+
+// The heads' rows of `count` tokens rotated, the first of them this thread's group's, then
+// every groups-th, by the `lanes` threads of which this is the lane-th.  kVector: the
+// pairs' halves begin at 16-byte pieces; of kAtOnce rows all pieces are asked for before
+// the first is written.
+template <class E, bool kVector, class Job>
+__device__ __forceinline__ void rotate_rows(int count, int heads, int group, int groups, int D, const Rotation &r,
+                                            int lane, int lanes, Job job) {
   using T = typename E::T;
   constexpr int kN = Piece<E>::kN;
   if constexpr (kVector) {
-    const int pieces = D / kN;
-    if (r.interleaved) {
-      const int turned = 2 * r.pairs / kN;
-      for (int i = lane; i < pieces; i += lanes) {
-        uint4 v = *reinterpret_cast<const uint4 *>(from + i * 16);
-        if (i < turned) {
-          Piece<E> p;
-          p.set(v);
+    // a lane has a piece, or one of each half
+    const int pieces = D / kN, half = r.interleaved ? 0 : r.pairs / kN;
+    const int turned = r.interleaved ? 2 * r.pairs / kN : half;
+    for (int i = lane; i < pieces - half; i += lanes) {
+      const bool turns = i < turned, two = turns && !r.interleaved;
+      const int first = turns ? i : i + half;
+      for (RowWalk w(heads, group, groups); w.token < count;) {
+        uint4 a[kAtOnce], b[kAtOnce];
+        RowJob jobs[kAtOnce];
 #pragma unroll
-          for (int e = 0; e < kN; e += 2) turn(p.x[e], p.x[e + 1], cs[(i * kN + e) / 2]);
-          v = p.get();
+        for (int x = 0; x < kAtOnce; ++x, w.next()) {
+          jobs[x].angles = nullptr;
+          if (w.token >= count) continue;
+          jobs[x] = job(w.token, w.h);
+          if (!jobs[x].angles) continue;
+          a[x] = *reinterpret_cast<const uint4 *>(jobs[x].from + first * 16);
+          if (two) b[x] = *reinterpret_cast<const uint4 *>(jobs[x].from + (i + half) * 16);
         }
-        *reinterpret_cast<uint4 *>(to + i * 16) = v;
-      }
-    } else {
-      const int half = r.pairs / kN;
-      for (int i = lane; i < pieces - half; i += lanes) {
-        if (i < half) {
-          Piece<E> a, b;
-          a.load(from + i * 16);
-          b.load(from + (i + half) * 16);
 #pragma unroll
-          for (int e = 0; e < kN; ++e) turn(a.x[e], b.x[e], cs[i * kN + e]);
-          *reinterpret_cast<uint4 *>(to + i * 16) = a.get();
-          *reinterpret_cast<uint4 *>(to + (i + half) * 16) = b.get();
-        } else if (from != to) {
-          *reinterpret_cast<uint4 *>(to + (i + half) * 16) =
-              *reinterpret_cast<const uint4 *>(from + (i + half) * 16);
+        for (int x = 0; x < kAtOnce; ++x) {
+          if (!jobs[x].angles) continue;
+          if (two) {
+            Piece<E> y, z;
+            y.set(a[x]);
+            z.set(b[x]);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) turn(y.x[e], z.x[e], jobs[x].angles[e * half + i]);
+            a[x] = y.get();
+            *reinterpret_cast<uint4 *>(jobs[x].to + (i + half) * 16) = z.get();
+          } else if (turns) {
+            Piece<E> y;
+            y.set(a[x]);
+#pragma unroll
+            for (int e = 0; e < kN; e += 2) turn(y.x[e], y.x[e + 1], jobs[x].angles[e / 2 * turned + i]);
+            a[x] = y.get();
+          }
+          *reinterpret_cast<uint4 *>(jobs[x].to + first * 16) = a[x];
         }
       }
     }
   } else {
-    const T *x = reinterpret_cast<const T *>(from);
-    T *y = reinterpret_cast<T *>(to);
-    for (int i = lane; i < D - r.pairs; i += lanes) {
-      if (i < r.pairs) {
-        const int i0 = r.interleaved ? 2 * i : i, i1 = r.interleaved ? 2 * i + 1 : i + r.pairs;
-        float a = E::to(x[i0]), b = E::to(x[i1]);
-        turn(a, b, cs[i]);
-        y[i0] = E::from(a);
-        y[i1] = E::from(b);
-      } else if (from != to) {
-        y[i + r.pairs] = x[i + r.pairs];
+    for (RowWalk w(heads, group, groups); w.token < count; w.next()) {
+      const RowJob j = job(w.token, w.h);
+      if (!j.angles) continue;
+      const T *x = reinterpret_cast<const T *>(j.from);
+      T *y = reinterpret_cast<T *>(j.to);
+      for (int i = lane; i < D - r.pairs; i += lanes) {
+        if (i < r.pairs) {
+          const int i0 = r.interleaved ? 2 * i : i, i1 = r.interleaved ? 2 * i + 1 : i + r.pairs;
+          float a = E::to(x[i0]), b = E::to(x[i1]);
+          turn(a, b, j.angles[i]);
+          y[i0] = E::from(a);
+          y[i1] = E::from(b);
+        } else if (j.from != j.to) {
+          y[i + r.pairs] = x[i + r.pairs];
+        }
       }
     }
   }
 }
 
-// Eight values of a row from element 8 * i on, rotated.
-template <class E, bool kVector>
-__device__ __forceinline__ void rotated8(const char *row, int i, const Rotation &r, const float2 *cs,
-                                         float (&x)[8]) {
-  using T = typename E::T;
-  constexpr int kN = Piece<E>::kN;
-  auto load8 = [&](int e0, float (&y)[8]) {
+// Eight values of a row.
+template <class E>
+struct Eight {
+  static constexpr int kN = Piece<E>::kN;
+  uint4 v[8 / kN];
+  __device__ __forceinline__ void load(const char *row, int e0) {
 #pragma unroll
-    for (int e = 0; e < 8; e += kN) {
+    for (int i = 0; i < 8 / kN; ++i)
+      v[i] = *reinterpret_cast<const uint4 *>(row + e0 * sizeof(typename E::T) + i * 16);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8 / kN; ++i) {
       Piece<E> p;
-      p.load(row + (e0 + e) * sizeof(T));
+      p.set(v[i]);
 #pragma unroll
-      for (int j = 0; j < kN; ++j) y[e + j] = p.x[j];
-    }
-  };
-  load8(8 * i, x);
-  if (8 * i >= 2 * r.pairs) return;
-  if (kVector && r.interleaved) {
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) turn(x[e], x[e + 1], cs[4 * i + e / 2]);
-  } else if (kVector) {
-    const bool second = 8 * i >= r.pairs;
-    const int pair0 = second ? 8 * i - r.pairs : 8 * i;
-    float y[8];
-    load8(second ? pair0 : pair0 + r.pairs, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float a = second ? y[e] : x[e], b = second ? x[e] : y[e];
-      turn(a, b, cs[pair0 + e]);
-      x[e] = second ? b : a;
-    }
-  } else {
-    const T *t = reinterpret_cast<const T *>(row);
-    for (int e = 0; e < 8; ++e) {
-      const int at = 8 * i + e;
-      if (at >= 2 * r.pairs) break;
-      const bool second = r.interleaved ? at & 1 : at >= r.pairs;
-      const int pair = r.interleaved ? at / 2 : (second ? at - r.pairs : at);
-      float a = E::to(t[r.interleaved ? 2 * pair : pair]);
-      float b = E::to(t[r.interleaved ? 2 * pair + 1 : pair + r.pairs]);
-      turn(a, b, cs[pair]);
-      x[e] = second ? b : a;
+      for (int j = 0; j < kN; ++j) x[i * kN + j] = p.x[j];
     }
   }
-  // the rows are made of keys in the type that they come in
+};
+
+// A lane's part of a row that becomes a 4-bit one: eight values from element 8 * i on, and
+// with kVector the other values of their pairs.
+template <class E, bool kVector>
+struct RowPart {
+  Eight<E> own, other;
+  // 0: as they are, 1: neighbours are pairs, 2, 3: first, second values of pairs
+  __device__ __forceinline__ static int how(int i, const Rotation &r) {
+    return 8 * i >= 2 * r.pairs ? 0 : (r.interleaved ? 1 : (8 * i >= r.pairs ? 3 : 2));
+  }
+  __device__ __forceinline__ void load(const char *row, int i, const Rotation &r) {
+    own.load(row, 8 * i);
+    if (kVector && how(i, r) >= 2) other.load(row, how(i, r) == 3 ? 8 * i - r.pairs : 8 * i + r.pairs);
+  }
+  __device__ __forceinline__ void rotated(const char *row, int i, const Rotation &r, const float2 *cs,
+                                          float (&x)[8]) const {
+    using T = typename E::T;
+    constexpr int kN = Piece<E>::kN;
+    own.get(x);
+    const int kind = how(i, r);
+    if (kind == 0) return;
+    if (kVector && kind == 1) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = E::to(E::from(x[e]));
-}
+      for (int e = 0; e < 8; e += 2) turn(x[e], x[e + 1], cs[angle_at<kN / 2>(r.pairs, 4 * i + e / 2)]);
+    } else if (kVector) {
+      const bool second = kind == 3;
+      const int pair0 = second ? 8 * i - r.pairs : 8 * i;
+      float y[8];
+      other.get(y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float2 t = cs[angle_at<kN>(r.pairs, pair0 + e)];
+        // b cos + a sin, a cos - b sin
+        if (!second) t.y = -t.y;
+        x[e] = second ? fmaf(y[e], t.y, x[e] * t.x) : fmaf(x[e], t.x, y[e] * t.y);
+      }
+    } else {
+      const T *t = reinterpret_cast<const T *>(row);
+      for (int e = 0; e < 8; ++e) {
+        const int at = 8 * i + e;
+        if (at >= 2 * r.pairs) break;
+        const bool second = r.interleaved ? at & 1 : at >= r.pairs;
+        const int pair = r.interleaved ? at / 2 : (second ? at - r.pairs : at);
+        float a = E::to(t[r.interleaved ? 2 * pair : pair]);
+        float b = E::to(t[r.interleaved ? 2 * pair + 1 : pair + r.pairs]);
+        turn(a, b, cs[pair]);
+        x[e] = second ? b : a;
+      }
+    }
+    // the rows are made of keys in the type that they come in
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = E::to(E::from(x[e]));
+  }
+};
 
 // One row as a 4-bit row, by the D / 8 neighbouring lanes of which this is the
 // lane-th (whole warps call it); x: its values.
@@ -223,11 +305,13 @@ __device__ __forceinline__ char *at_row(const TokenRows &t, long long layer, int
   return t.data + layer * t.layer + b * t.seq + n * t.token;
 }
 
-// A token of a batch: what find_token looks up once.
+constexpr int kMaxBatch = 16;
+
+// A token of a batch: byte offsets of its first heads' rows.
 struct Token {
-  int b, n;          // n < 0: none, or behind the sequence's new tokens
-  long long k, v;    // byte offsets of its slot's first head; -1: not written
-  long long place;   // position
+  long long q, out_q, k, v, to_k, to_v;  // to_k < 0: not written
+  long long place;                       // position
+  bool there;                            // not behind the sequence's new tokens
 };
 
 // ---------------------------------------------------------------------------
@@ -243,87 +327,107 @@ struct AppendArgs {
 };
 
 template <class E, bool kFour, bool kVector>
-__global__ void __launch_bounds__(kRotThreads) append_rotary_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 5) append_rotary_kernel(const __grid_constant__ AppendArgs a) {
   extern __shared__ float2 cs[];  // batch x pairs
-  __shared__ Token tokens[kRotThreads];
+  __shared__ Token tokens[kMaxBatch];
   const int tid = threadIdx.x, layer = blockIdx.y;
   const long long total = static_cast<long long>(a.S.B) * a.S.N, t0 = static_cast<long long>(blockIdx.x) * a.batch;
   const int count = static_cast<int>(min(static_cast<long long>(a.batch), total - t0));
   if (tid < count) {
     Token t;
-    t.b = static_cast<int>((t0 + tid) / a.S.N);
-    t.n = static_cast<int>(t0 + tid - static_cast<long long>(t.b) * a.S.N);
-    t.k = t.v = -1;
-    const int ctx = __ldg(a.S.ctx + t.b), m = seq_new(a.S, t.b);
-    int behind = t.n;
-    if (a.R.position)
-      behind = min(max(__ldg(a.R.position + t.b * a.R.position_seq + t.n), 0), a.S.N - 1);
+    const int b = static_cast<int>((t0 + tid) / a.S.N);
+    const int n = static_cast<int>(t0 + tid - static_cast<long long>(b) * a.S.N);
+    auto offset = [&](const TokenRows &x) { return layer * x.layer + b * x.seq + n * x.token; };
+    t.q = offset(a.R.q);
+    t.out_q = offset(a.R.out_q);
+    t.k = offset(a.R.k);
+    t.v = offset(a.R.v);
+    t.to_k = t.to_v = -1;
+    const int ctx = __ldg(a.S.ctx + b), m = seq_new(a.S, b);
+    int behind = n;
+    if (a.R.position) behind = min(max(__ldg(a.R.position + b * a.R.position_seq + n), 0), a.S.N - 1);
     t.place = static_cast<long long>(ctx) + behind;
-    if (t.n >= m) {
-      t.n = -1;
-    } else if (seq_fits(a.S, a.C, ctx, m)) {
-      const int at = ctx + t.n, index = at / a.C.page_size, page = page_at(a.S, t.b, index);
+    t.there = n < m;
+    if (t.there && seq_fits(a.S, a.C, ctx, m)) {
+      const int at = ctx + n, index = at / a.C.page_size, page = page_at(a.S, b, index);
       if (page_ok(a.C, page)) {
         const int in_page = at - index * a.C.page_size;
-        t.k = layer * a.C.k_layer + page * a.C.k_page + in_page * a.C.k_token;
-        t.v = layer * a.C.v_layer + page * a.C.v_page + in_page * a.C.v_token;
+        t.to_k = layer * a.C.k_layer + page * a.C.k_page + in_page * a.C.k_token;
+        t.to_v = layer * a.C.v_layer + page * a.C.v_page + in_page * a.C.v_token;
       }
     }
     tokens[tid] = t;
   }
   __syncthreads();
   if (a.rotation.pairs > 0)
-    find_angles(a.rotation, count, [&](int i) { return tokens[i].place; }, cs);
+    find_angles(a.rotation, count, [&](int i) { return tokens[i].place; }, cs, each_of<E, kVector>(a.rotation));
   const int lane = tid % a.row_lanes, group = tid / a.row_lanes, groups = kRotThreads / a.row_lanes;
-  if (a.R.q.data) {
-    const int heads = a.R.q_heads;
-    for (int i = group; i < count * heads; i += groups) {
-      const int token = i / heads, h = i - token * heads;
-      const Token &t = tokens[token];
-      if (t.n < 0) continue;
-      rotate_row<E, kVector>(at_row(a.R.q, layer, t.b, t.n) + h * a.R.q.head,
-                             at_row(a.R.out_q, layer, t.b, t.n) + h * a.R.out_q.head, a.D, a.rotation,
-                             cs + token * a.rotation.pairs, lane, a.row_lanes);
-    }
-  }
+  if (a.R.q.data)
+    rotate_rows<E, kVector>(
+        count, a.R.q_heads, group, groups, a.D, a.rotation, lane, a.row_lanes, [&](int token, int h) {
+          const Token &t = tokens[token];
+          return RowJob{a.R.q.data + t.q + h * a.R.q.head, a.R.out_q.data + t.out_q + h * a.R.out_q.head,
+                        t.there ? cs + token * a.rotation.pairs : nullptr};
+        });
   const int heads = a.C.heads, rows = 2 * heads;
   if constexpr (!kFour) {
-    for (int i = group; i < count * rows; i += groups) {
-      const int token = i / rows, r = i - token * rows;
-      const Token &t = tokens[token];
-      if (t.n < 0) continue;
-      if (r < heads) {
-        if (t.k >= 0)
-          rotate_row<E, kVector>(at_row(a.R.k, layer, t.b, t.n) + r * a.R.k.head,
-                                 a.C.k + t.k + r * a.C.k_head, a.D, a.rotation,
-                                 cs + token * a.rotation.pairs, lane, a.row_lanes);
-      } else if (t.v >= 0) {
-        const char *from = at_row(a.R.v, layer, t.b, t.n) + (r - heads) * a.R.v.head;
-        char *to = a.C.v + t.v + (r - heads) * a.C.v_head;
-        for (int p = lane; p < a.C.row_bytes / 16; p += a.row_lanes)
-          *reinterpret_cast<uint4 *>(to + p * 16) = *reinterpret_cast<const uint4 *>(from + p * 16);
+    rotate_rows<E, kVector>(
+        count, heads, group, groups, a.D, a.rotation, lane, a.row_lanes, [&](int token, int h) {
+          const Token &t = tokens[token];
+          return RowJob{a.R.k.data + t.k + h * a.R.k.head, a.C.k + t.to_k + h * a.C.k_head,
+                        t.to_k >= 0 ? cs + token * a.rotation.pairs : nullptr};
+        });
+    for (int piece = lane; piece < a.C.row_bytes / 16; piece += a.row_lanes)
+      for (RowWalk w(heads, group, groups); w.token < count;) {
+        uint4 x[kAtOnce];
+        char *to[kAtOnce];
+#pragma unroll
+        for (int y = 0; y < kAtOnce; ++y, w.next()) {
+          to[y] = nullptr;
+          if (w.token >= count) continue;
+          const Token &t = tokens[w.token];
+          if (t.to_k < 0) continue;
+          to[y] = a.C.v + t.to_v + w.h * a.C.v_head + piece * 16;
+          x[y] = *reinterpret_cast<const uint4 *>(a.R.v.data + t.v + w.h * a.R.v.head + piece * 16);
+        }
+#pragma unroll
+        for (int y = 0; y < kAtOnce; ++y)
+          if (to[y]) *reinterpret_cast<uint4 *>(to[y]) = x[y];
       }
-    }
   } else {
     const int words = a.D / 8, word = tid % words, each = kRotThreads / words;
+    const Rotation none = {};
     // whole warps stay together for the groups' shuffles
-    for (int i0 = 0; i0 < count * rows; i0 += each) {
-      const int i = i0 + tid / words, token = min(i / rows, count - 1), r = i % rows;
-      const Token &t = tokens[token];
-      const bool is_k = r < heads;
-      const bool there = i < count * rows && t.n >= 0 && (is_k ? t.k : t.v) >= 0;
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (there) {
-        if (is_k) {
-          rotated8<E, kVector>(at_row(a.R.k, layer, t.b, t.n) + r * a.R.k.head, word, a.rotation,
-                               cs + token * a.rotation.pairs, x);
-        } else {
-          Rotation none = {};
-          rotated8<E, true>(at_row(a.R.v, layer, t.b, t.n) + (r - heads) * a.R.v.head, word, none, cs, x);
-        }
+    RowWalk w(rows, tid / words, each);
+    for (int i0 = 0; i0 < count * rows; i0 += kFourAtOnce * each) {
+      RowPart<E, kVector> part[kFourAtOnce];
+      const char *from[kFourAtOnce];
+      char *to[kFourAtOnce];
+      int of[kFourAtOnce];  // token; negative: of a value
+#pragma unroll
+      for (int y = 0; y < kFourAtOnce; ++y, w.next()) {
+        from[y] = nullptr;
+        if (w.token >= count) continue;
+        const Token &t = tokens[w.token];
+        if (t.to_k < 0) continue;
+        const bool is_k = w.h < heads;
+        from[y] = is_k ? a.R.k.data + t.k + w.h * a.R.k.head : a.R.v.data + t.v + (w.h - heads) * a.R.v.head;
+        to[y] = is_k ? a.C.k + t.to_k + w.h * a.C.k_head : a.C.v + t.to_v + (w.h - heads) * a.C.v_head;
+        of[y] = is_k ? w.token : -1;
+        part[y].load(from[y], word, is_k ? a.rotation : none);
       }
-      write_q4(is_k ? a.C.k + t.k + r * a.C.k_head : a.C.v + t.v + (r - heads) * a.C.v_head, a.D, word,
-               x, there);
+#pragma unroll
+      for (int y = 0; y < kFourAtOnce; ++y) {
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (from[y]) {
+          if (of[y] < 0) {
+            part[y].own.get(x);
+          } else {
+            part[y].rotated(from[y], word, a.rotation, cs + of[y] * a.rotation.pairs, x);
+          }
+        }
+        write_q4(to[y], a.D, word, x, from[y] != nullptr);
+      }
     }
   }
 }
@@ -341,9 +445,9 @@ struct RotateArgs {
 };
 
 template <class E, bool kVector>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotateArgs a) {
+__global__ void __launch_bounds__(kRotThreads, 6) rotary_kernel(const __grid_constant__ RotateArgs a) {
   extern __shared__ float2 cs[];
-  __shared__ long long from[kRotThreads], to[kRotThreads];
+  __shared__ long long from[kMaxBatch], to[kMaxBatch];
   const int tid = threadIdx.x;
   const long long total = static_cast<long long>(a.B) * a.N, t0 = static_cast<long long>(blockIdx.x) * a.batch;
   const int count = static_cast<int>(min(static_cast<long long>(a.batch), total - t0));
@@ -356,13 +460,13 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
   find_angles(a.rotation, count, [&](int i) {
     const long long t = t0 + i, b = t / a.N;
     return static_cast<long long>(__ldg(a.position + b * a.position_seq + (t - b * a.N)));
-  }, cs);
+  }, cs, each_of<E, kVector>(a.rotation));
   const int lane = tid % a.row_lanes, group = tid / a.row_lanes, groups = kRotThreads / a.row_lanes;
-  for (int i = group; i < count * a.heads; i += groups) {
-    const int token = i / a.heads, h = i - token * a.heads;
-    rotate_row<E, kVector>(a.x.data + from[token] + h * a.x.head, a.out.data + to[token] + h * a.out.head,
-                           a.D, a.rotation, cs + token * a.rotation.pairs, lane, a.row_lanes);
-  }
+  rotate_rows<E, kVector>(
+      count, a.heads, group, groups, a.D, a.rotation, lane, a.row_lanes, [&](int token, int h) {
+        return RowJob{a.x.data + from[token] + h * a.x.head, a.out.data + to[token] + h * a.out.head,
+                      cs + token * a.rotation.pairs};
+      });
 }
 
 // ---------------------------------------------------------------------------
@@ -448,7 +552,7 @@ int lanes_of(int D, int n, const Rotation &r, bool vector) {
 int batch_of(long long tokens, int layers, int pairs) {
   const int most = pairs > 0 ? std::max(1, kRotThreads / pairs) : 4;
   const long long spread = tokens * layers / (4 * 152);
-  return static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(most, 16), spread)));
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(most, kMaxBatch), spread)));
 }
 
 template <class F>

@@ -622,71 +622,21 @@ __global__ void __launch_bounds__(kAttnThreads, Rows8<DP>::kCtas) rows8_kernel(c
 // the join
 // ---------------------------------------------------------------------------
 
-// The rows of a cut unit, dealt over gridDim.y CTAs.  Units of two pieces, the
-// most there are in a full batch: a warp takes four rows at once, since a row
-// alone is one round trip to L2 whatever its size.  Units of few pieces: a warp
-// per row.  Units of many: the CTA's warps share the pieces of one row after the
-// other, and their sums are added in order.  A warp has eight pieces in flight.
-template <class TE>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kWarps = kJoinThreads / 32;
-  __shared__ float m_s[kWarps], l_s[kWarps];
-  __shared__ float4 o_s[kWarps][64];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const JoinDesc d = p.join[blockIdx.x];
-  if (d.pieces_end < 0) return;
-  const int rows = d.rows, Y = gridDim.y;
-  const int step = p.row_lines, first = static_cast<int>(blockIdx.x) - step;
-  const int count = (d.pieces_end - first) / step + 1;
-  const size_t per_slot = slot_floats(p.rows, p.D);
-  auto slot = [&](int i) { return p.part + (2 * (first + i * step) + (i == 0 ? 1 : 0)) * per_slot; };
-  if (count == 2 && p.D <= 128) {
-    const float *s[2] = {slot(0), slot(1)};
-    const int at = lane * 4;
-    for (int r = (blockIdx.y * kWarps + warp) * 4; r < rows; r += 4 * Y * kWarps) {
-      float m[4][2], l[4][2];
-      float4 v[4][2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int row = min(r + j, rows - 1);
-          m[j][x] = s[x][row];
-          l[j][x] = s[x][p.rows + row];
-          if (at < p.D)
-            v[j][x] = *reinterpret_cast<const float4 *>(s[x] + slot_stats(p.rows) +
-                                                        static_cast<size_t>(row) * p.D + at);
-        }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = r + j;
-        if (row >= rows) break;
-        const float M = fmaxf(m[j][0], m[j][1]);
-        float f[2], sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (l[j][x] == 0.f) continue;
-          f[x] = fast_exp2(m[j][x] - M);
-          sum += f[x] * l[j][x];
-          o.x += f[x] * v[j][x].x;
-          o.y += f[x] * v[j][x].y;
-          o.z += f[x] * v[j][x].z;
-          o.w += f[x] * v[j][x].w;
-        }
-        const long long to = out_row(p, d.b, d.h, d.r0 + row);
-        const float n = sum == 0.f ? 0.f : 1.f / sum;
-        if (at < p.D)
-          store4(static_cast<TE *>(p.out) + to * p.D + at,
-                 make_float4(o.x * n, o.y * n, o.z * n, o.w * n));
-        if (lane == 0 && p.lse) p.lse[to] = row_lse(M, sum);
-      }
-    }
-    return;
+// The pieces of a cut unit, of which the worker holds the first; by whole warps.
+template <typename TE>
+struct Pieces {
+  const AttnParams &p;
+  const JoinDesc &d;
+  int lane, first, lines, count;
+  size_t per_slot;
+  __device__ __forceinline__ Pieces(const AttnParams &p, const JoinDesc &d, int worker, int lane)
+      : p(p), d(d), lane(lane), first(worker - p.row_lines), lines(p.row_lines),
+        count((d.pieces_end - first) / lines + 1), per_slot(slot_floats(p.rows, p.D)) {}
+  __device__ __forceinline__ const float *slot(int i) const {
+    return p.part + (2 * (first + i * lines) + (i == 0 ? 1 : 0)) * per_slot;
   }
   // pieces from, from + step, ... of a row
-  auto gather = [&](int row, int from, int step, float &M, float &l, float4 (&o)[2]) {
+  __device__ __forceinline__ void gather(int row, int from, int step, float &M, float &l, float4 (&o)[2]) const {
     M = -INFINITY;
     l = 0.f;
     o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -733,8 +683,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         }
       }
     }
-  };
-  auto finish = [&](int row, float M, float l, const float4 (&o)[2]) {
+  }
+  __device__ __forceinline__ void finish(int row, float M, float l, const float4 (&o)[2]) const {
     const long long at = out_row(p, d.b, d.h, d.r0 + row);
     const float r = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -745,18 +695,81 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
                make_float4(o[x].x * r, o[x].y * r, o[x].z * r, o[x].w * r));
     }
     if (lane == 0 && p.lse) p.lse[at] = row_lse(M, l);
-  };
+  }
+};
+
+// The rows of a cut unit, dealt over gridDim.y CTAs.  Units of two pieces, the
+// most there are in a full batch: a warp takes four rows at once, since a row
+// alone is one round trip to L2 whatever its size.  Units of few pieces: a warp
+// per row.  Units of many: the CTA's warps share the pieces of one row after the
+// other, and their sums are added in order.  A warp has eight pieces in flight.
+template <class TE>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kWarps = kJoinThreads / 32;
+  __shared__ float m_s[kWarps], l_s[kWarps];
+  __shared__ float4 o_s[kWarps][64];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const JoinDesc d = p.join[blockIdx.x];
+  if (d.pieces_end < 0) return;
+  const int rows = d.rows, Y = gridDim.y;
+  const Pieces<TE> u(p, d, blockIdx.x, lane);
+  const int count = u.count;
+  if (count == 2 && p.D <= 128) {
+    const float *s[2] = {u.slot(0), u.slot(1)};
+    const int at = lane * 4;
+    for (int r = (blockIdx.y * kWarps + warp) * 4; r < rows; r += 4 * Y * kWarps) {
+      float m[4][2], l[4][2];
+      float4 v[4][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = min(r + j, rows - 1);
+          m[j][x] = s[x][row];
+          l[j][x] = s[x][p.rows + row];
+          if (at < p.D)
+            v[j][x] = *reinterpret_cast<const float4 *>(s[x] + slot_stats(p.rows) +
+                                                        static_cast<size_t>(row) * p.D + at);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = r + j;
+        if (row >= rows) break;
+        const float M = fmaxf(m[j][0], m[j][1]);
+        float f[2], sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (l[j][x] == 0.f) continue;
+          f[x] = fast_exp2(m[j][x] - M);
+          sum += f[x] * l[j][x];
+          o.x += f[x] * v[j][x].x;
+          o.y += f[x] * v[j][x].y;
+          o.z += f[x] * v[j][x].z;
+          o.w += f[x] * v[j][x].w;
+        }
+        const long long to = out_row(p, d.b, d.h, d.r0 + row);
+        const float n = sum == 0.f ? 0.f : 1.f / sum;
+        if (at < p.D)
+          store4(static_cast<TE *>(p.out) + to * p.D + at,
+                 make_float4(o.x * n, o.y * n, o.z * n, o.w * n));
+        if (lane == 0 && p.lse) p.lse[to] = row_lse(M, sum);
+      }
+    }
+    return;
+  }
   float M, l;
   float4 o[2];
   if (count <= 16) {
     for (int row = blockIdx.y * kWarps + warp; row < rows; row += Y * kWarps) {
-      gather(row, 0, 1, M, l, o);
-      finish(row, M, l, o);
+      u.gather(row, 0, 1, M, l, o);
+      u.finish(row, M, l, o);
     }
     return;
   }
   for (int row = blockIdx.y; row < rows; row += Y) {
-    gather(row, warp, kWarps, M, l, o);
+    u.gather(row, warp, kWarps, M, l, o);
     if (lane == 0) {
       m_s[warp] = M;
       l_s[warp] = l;
@@ -782,9 +795,79 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
           o[x].w += f * v.w;
         }
       }
-      finish(row, M, l, o);
+      u.finish(row, M, l, o);
     }
     __syncthreads();
+  }
+}
+
+// For few units cut into many pieces by many workers, most of which have no unit to join:
+// a CTA looks at 32 of them.  Their units of few pieces are dealt over its warps row by row;
+// the pieces of larger ones are shared by all warps, a row after the other.  (1824 workers,
+// both kernels of a call together, a CTA a worker and 32: 8 units of 32 tiles 16.4 us and
+// 13.2, 8 of 3072 tiles, 7 rows 58.7 and 45.2, but 2048 units 158 and 166.)
+constexpr int kManyThreads = 512, kManyWorkers = 32, kFewPieces = 16;
+template <typename TE>
+__global__ void __launch_bounds__(kManyThreads) join_many_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kWarps = kManyThreads / 32;
+  __shared__ float m_s[kWarps], l_s[kWarps];
+  __shared__ float4 o_s[kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Y = gridDim.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int worker0 = blockIdx.x * kManyWorkers;
+  // a worker's unit a lane
+  JoinDesc mine = {0, 0, 0, 0, -1};
+  if (worker0 + lane < p.workers) mine = p.join[worker0 + lane];
+  const int count = mine.pieces_end < 0 ? 0 : Pieces<TE>(p, mine, worker0 + lane, lane).count;
+  auto unit_of = [&](int of) {
+    return JoinDesc{__shfl_sync(0xFFFFFFFFu, mine.b, of), __shfl_sync(0xFFFFFFFFu, mine.h, of),
+                    __shfl_sync(0xFFFFFFFFu, mine.r0, of), __shfl_sync(0xFFFFFFFFu, mine.rows, of),
+                    __shfl_sync(0xFFFFFFFFu, mine.pieces_end, of)};
+  };
+  float M, l;
+  float4 o[2];
+  int turn = 0;
+  for (uint32_t left = __ballot_sync(0xFFFFFFFFu, count > 0 && count <= kFewPieces); left; left &= left - 1) {
+    const int worker = worker0 + __ffs(left) - 1;
+    const JoinDesc d = unit_of(worker - worker0);
+    const Pieces<TE> u(p, d, worker, lane);
+    for (int row = blockIdx.y; row < d.rows; row += Y) {
+      if (turn++ % kWarps != warp) continue;
+      u.gather(row, 0, 1, M, l, o);
+      u.finish(row, M, l, o);
+    }
+  }
+  for (uint32_t left = __ballot_sync(0xFFFFFFFFu, count > kFewPieces); left; left &= left - 1) {
+    const int worker = worker0 + __ffs(left) - 1;
+    const JoinDesc d = unit_of(worker - worker0);
+    const Pieces<TE> u(p, d, worker, lane);
+    for (int row = blockIdx.y; row < d.rows; row += Y) {
+      u.gather(row, warp, kWarps, M, l, o);
+      if (lane == 0) {
+        m_s[warp] = M;
+        l_s[warp] = l;
+      }
+      o_s[warp][lane] = o[0];  // head dimensions up to 128
+      __syncthreads();
+      if (warp == 0) {
+        M = -INFINITY;
+        l = 0.f;
+        o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, m_s[w]);
+        for (int w = 0; w < kWarps; ++w) {
+          if (l_s[w] == 0.f) continue;
+          const float f = fast_exp2(m_s[w] - M);
+          l += f * l_s[w];
+          const float4 v = o_s[w][lane];
+          o[0].x += f * v.x;
+          o[0].y += f * v.y;
+          o[0].z += f * v.z;
+          o[0].w += f * v.w;
+        }
+        u.finish(row, M, l, o);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -885,12 +968,18 @@ void take_plan(AttnParams &p, const AttnPlan &plan, void *workspace) {
                                      align32(p.workers * sizeof(JoinDesc)));
 }
 
+template <typename TE>
+cudaError_t start_join(const AttnParams &p, cudaStream_t stream) {
+  const int rows = std::min(8, std::min(p.rows, p.S.N * p.G));
+  const int tiles = (p.S.N * p.G + p.rows - 1) / p.rows;
+  if constexpr (sizeof(TE) == 2)
+    if (p.workers > 8 * kSms && p.workers > 4ll * p.S.B * p.C.heads * tiles && p.D <= 128) return launch_behind(
+        join_many_kernel<TE>, dim3((p.workers + kManyWorkers - 1) / kManyWorkers, rows), kManyThreads, 0, stream, p);
+  return launch_behind(join_kernel<TE>, dim3(p.workers, rows), kJoinThreads, 0, stream, p);
+}
 cudaError_t launch_join(const AttnParams &p, int dtype, cudaStream_t stream) {
-  const dim3 grid(p.workers, std::min(8, std::min(p.rows, p.S.N * p.G)));
-  if (dtype == SPEC_F32) return launch_behind(join_kernel<float>, grid, kJoinThreads, 0, stream, p);
-  if (dtype == SPEC_BF16)
-    return launch_behind(join_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, stream, p);
-  return launch_behind(join_kernel<__half>, grid, kJoinThreads, 0, stream, p);
+  if (dtype == SPEC_F32) return start_join<float>(p, stream);
+  return dtype == SPEC_BF16 ? start_join<__nv_bfloat16>(p, stream) : start_join<__half>(p, stream);
 }
 
 cudaError_t launch_attention(AttnParams &p, int dtype, void *workspace, cudaStream_t stream) {

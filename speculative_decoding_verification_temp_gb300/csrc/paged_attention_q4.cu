@@ -1,31 +1,34 @@
 // Attention over a paged cache of 4-bit rows (q4.cuh): head_dim 64 or 128, queries and
-// outputs of 16 bits, 8 or 16 rows of queries per unit (new tokens times the group's
-// heads).
+// outputs of 16 bits, 4 or 8 rows of queries per unit (new tokens times the group's heads).
 //
-// A warp takes 32 keys of a tile of 128.  Scores: the keys are the rows of the matrix
-// instruction and the queries its columns, so that up to eight rows of queries cost
-// what one does.  A code n, masked out of its word and taken as float16, is the
-// subnormal n 2^-24 (16 n 2^-24 for the odd nibbles, whose queries are divided by 16): the
-// products are exact, and cost a mask each.  Each of the four groups of a row has sums
-// of its own; a key's score is
+// A warp is a worker: it has units of its own, copies 32 keys and their values at a time
+// into a ring of its own, two ahead, and writes its units' outputs, without a barrier.
+//
+// Scores: the keys are the rows of the matrix instruction and the queries its columns.  A
+// code n, masked out of its word and taken as float16, is the subnormal n 2^-24 (16 n
+// 2^-24 for the odd nibbles, whose queries are divided by 16): the products are exact, and
+// cost a mask each.  Each of the four groups of a row has sums of its own; a key's score is
 //   sum over groups g of s_g (q . n)_g + m_g (sum of q)_g
 // with the scales applied to the sums in float32 and the minima as one more step of
 // the instruction, against the queries' sums in two float16 terms.  So scores are as
 // exact as those of rows in float16 without any value being made.  Queries enter as
 // float16, each row scaled by a power of two to 2^9 at most: exact but for what lies
-// 2^-24 below a row's largest.
+// 2^-24 below a row's largest.  Four rows leave half of the eight columns free: those take
+// another group's codes, with zeros against the first's.
 //
-// Outputs: the values are the rows, the keys the inner dimension.  Two tokens' words are
-// swapped into pairs of tokens, a nibble becomes 1024 + n or 64 + n by its mask, n by
-// a subtraction and m + s n by one more instruction, rounded to float16 once (half a
-// step of 2^-11, against quantisation by half a step of 1/15 of the spread).  The weights
-// of 8 keys and 8 rows cross from the scores' layout to the products' by one
-// transposing move.  Weights are float16 as in the tensor-memory kernels: lifted, so
-// that those rounded to zero are below 2^-32 of the row's largest.
+// Outputs: the values are the rows, the keys the inner dimension, the codes the same
+// subnormals.  The scales go into the weights, one product of float16 per key, row and
+// group instead of one per key and value; sums of the weights times the minima are two
+// more columns.  Weights are float16 as in the tensor-memory kernels: lifted, so that
+// those rounded to zero are below 2^-32 of the row's largest; the product with a scale
+// rounds once more (half a step of 2^-11, against quantisation by half a step of 1/15 of
+// the spread).  The weights of 8 keys and 8 rows cross from the scores' layout to the
+// products' by one transposing move.
 //
-// A warp is a worker: it has units of its own, copies their keys and values into a ring
-// of its own (a bulk copy per page and head where a head's tokens lie one behind
-// another, one per row elsewhere) and writes their outputs, without a barrier.
+// Bound by instructions and the latencies of a warp's turn, about 430 instructions for 32
+// keys and values, of which half go to units that issue every other cycle: 256 sequences of
+// 1 to 4096 tokens, one token each, 32/8 heads of 128: 158 us, 4.28 TB/s; the copies alone
+// take 115.  Twelve warps an SM (three thread blocks; sixteen with fewer registers 179 us).
 #include <algorithm>
 
 #include "q4_copies.cuh"
@@ -40,20 +43,19 @@ constexpr int kSms4 = 152;
 // larger scales lower the weights (see cap).
 constexpr float kLift4 = 6.f;
 
-// R: rows of a unit, 4, 8 or 16.
+// R: rows of a unit, 4 or 8.
 template <int D, int R>
 struct Rows4 {
   static constexpr int kRow = q4_row_bytes(D);
   // Four rows leave half of the products' columns free, which take another group.
   static constexpr bool kQuad = R == 4;
-  static constexpr int kCols = R <= 8 ? 1 : 2;         // times eight columns
   static constexpr int kWarps = 4;                     // of a CTA
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kCtas = 3;                      // of an SM (four: 179 us for 157)
   static constexpr int kStage = 2 * kQ4Tile * kRow;    // keys, then values
   static constexpr int kSteps = D / 16;                // of the scores' products
   // of the queries: two operands a step, two for the sums, the factors; two steps a piece
-  static constexpr int kQPieces = kCols * (kSteps / 2 + 1);
+  static constexpr int kQPieces = kSteps / 2 + 1;
   static constexpr int kQBytes = kQPieces * 32 * 16;
   static constexpr int kWarp = 2 * kStage + kQBytes;
   static constexpr int kSmem = kWarps * kWarp;
@@ -107,8 +109,8 @@ __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cas
 __device__ __forceinline__ float scale_at(const char *p) { return __half2float(*reinterpret_cast<const __half *>(p)); }
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // nibbles of two halves
 
-// A lane's operands of the scores' products, of eight columns of queries (four with
-// kQuad) from row `first` of the unit, into pieces of 16 bytes [step / 2][lane]:
+// A lane's operands of the scores' products, of the unit's queries as eight columns
+// (four with kQuad), into pieces of 16 bytes [step / 2][lane]:
 //   kQuad, D 128, step 4 pr + i: nibble i of group 2 pr in columns 0..3, of group 2 pr + 1
 //     in columns 4..7, each with zeros for the other's keys' codes
 //   kQuad, D 64, step 2 pc + i: nibbles 2i, 2i + 1 of words 4 pc + t: columns 0..3 of the
@@ -117,13 +119,12 @@ constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // nibbles of two h
 // then the sums of each group in two float16 terms, against the codes' (scale, minimum)
 // pairs, and the factors of this lane's two rows of scores.
 template <class E, int D, bool kQuad>
-__device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitWalk &u, int first, int lane,
-                                                uint4 *to) {
+__device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitWalk &u, int lane, uint4 *to) {
   using TE = typename E::T;
   constexpr int kN = D / 16;         // values of each group that this lane has
   constexpr bool kPieces = D == 128 || kQuad;  // in pieces of eight neighbours
   constexpr int kParts = kPieces ? D / 32 : 4, kEach = kPieces ? 8 : kN;
-  const int g = lane >> 2, t = lane & 3, live = u.live_rows(p), row = first + (kQuad ? g & 3 : g);
+  const int g = lane >> 2, t = lane & 3, live = u.live_rows(p), row = kQuad ? g & 3 : g;
   const int r = u.r0 + min(row, live - 1), n = r / p.G;
   const char *q = p.q + u.b * p.q_seq + n * p.q_token + (u.h * p.G + r - n * p.G) * p.q_head;
   uint32_t v[kParts][kEach / 2];
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     rows4_kernel(const __grid_constant__ AttnParams p) {
   using L = Rows4<D, R>;
   using TE = typename E::T;
-  constexpr int kRow = L::kRow, NT = L::kCols;
+  constexpr int kRow = L::kRow;
   constexpr bool kQuad = L::kQuad, kPieces = D == 128 || kQuad;
   extern __shared__ __align__(128) char smem4[];
   __shared__ RunScratch<L::kThreads, L::kWarps> runs;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
   constexpr int kOuts = D / 16;    // 16 dimensions each of the outputs
   constexpr int kKeys = kQuad ? 1 : 2;  // of 16, that this lane weighs
   auto key_of = [&](int h) { return kQuad ? (t >> 1) * 8 + g : h * 8 + g; };
-  auto row_of = [&](int nt, int e) { return kQuad ? 2 * (t & 1) + e : nt * 8 + 2 * t + e; };
+  auto row_of = [&](int e) { return kQuad ? 2 * (t & 1) + e : 2 * t + e; };
   // where this lane's row of a matrix of codes begins: keys 0..7 and 8..15 of one piece of
   // 16 bytes, then of the next
   const int matrix = ((lane & 7) + ((lane >> 3) & 1) * 8) * kRow + (lane >> 4) * 16;
@@ -272,28 +273,25 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
 
   if (busy) copies.begin(p, u, key_tile(u.k, u.i0) * kQ4Tile, lane);
   while (busy) {
-    for (int nt = 0; nt < NT; ++nt)
-      prepare_queries<E, D, kQuad>(p, u, nt * 8, lane, queries + nt * (L::kSteps / 2 + 1) * 32);
+      prepare_queries<E, D, kQuad>(p, u, lane, queries);
     __syncwarp();
-    uint32_t qs[NT][2];
-    float c[NT][2];
+    uint32_t qs[2];
+    float c[2];
     const int live = u.live_rows(p);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const uint4 x = queries[(nt * (L::kSteps / 2 + 1) + L::kSteps / 2) * 32];
-      qs[nt][0] = x.x;
-      qs[nt][1] = x.y;
-      c[nt][0] = __uint_as_float(x.z);
-      c[nt][1] = __uint_as_float(x.w);
+    {
+      const uint4 x = queries[(L::kSteps / 2) * 32];
+      qs[0] = x.x;
+      qs[1] = x.y;
+      c[0] = __uint_as_float(x.z);
+      c[1] = __uint_as_float(x.w);
     }
-    float m[NT][2], l[NT][2], o[NT][kOuts][4], om[NT][4];
+    float m[2], l[2], o[kOuts][4], om[4];
+    {
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+      om[0] = om[1] = om[2] = om[3] = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-      om[nt][0] = om[nt][1] = om[nt][2] = om[nt][3] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kOuts; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      for (int i = 0; i < kOuts; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }
     // scales are below 2^(cap + 1)
     int cap = 0;
@@ -340,27 +338,23 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
           cap += more;
           const float f = __int_as_float((127 - more) << 23);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+          for (int e = 0; e < 2; ++e) {
+            m[e] += static_cast<float>(more);
+            l[e] *= f;
+          }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              m[nt][e] += static_cast<float>(more);
-              l[nt][e] *= f;
-            }
+          for (int e = 0; e < 4; ++e) {
+            om[e] *= f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              om[nt][e] *= f;
-#pragma unroll
-              for (int j = 0; j < kOuts; ++j) o[nt][j][e] *= f;
-            }
+            for (int j = 0; j < kOuts; ++j) o[j][e] *= f;
           }
         }
       }
-      // (once in the code: unrolled, its instructions do not stay in the cache, 189 us to
-      // 211)
+      // (once in the code: unrolled, its instructions do not stay in the cache, 12 % slower)
 #pragma unroll 1
       for (int blk = 0; blk < 2; ++blk) {
         // ------------------------------------------------------------- scores
-        float y[NT][2 * kKeys];
+        float y[2 * kKeys];
         const char *r0 = k_s + (blk * 16 + g) * kRow, *r1 = r0 + 8 * kRow;
         uint32_t pairs[2];
         matrices2(pairs, k_at + (blk * 16 + (lane & 15)) * kRow + D / 2);
@@ -393,7 +387,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
               mma16(a[pr], r2[0] & kLow, r2[1] & kLow, r2[0] & kHigh, r2[1] & kHigh, q.z, q.w);
             }
           }
-          mma16_first(am, pairs[0], pairs[1], pairs[0], pairs[1], qs[0][0], qs[0][1]);
+          mma16_first(am, pairs[0], pairs[1], pairs[0], pairs[1], qs[0], qs[1]);
           // columns 0..3 are groups 0 and 2, 4..7 the same rows' groups 1 and 3
           const char *f0 = r0 + D / 2 + (t >> 1) * 4, *f1 = f0 + 8 * kRow;
           const float s00 = scale_at(f0), s02 = scale_at(f0 + 8), s10 = scale_at(f1), s12 = scale_at(f1 + 8);
@@ -406,10 +400,10 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float other = __shfl_xor_sync(0xFFFFFFFFu, second ? z[e] : z[2 + e], 2);
-            y[0][e] = ((second ? z[2 + e] : z[e]) + other) * c[0][e];
+            y[e] = ((second ? z[2 + e] : z[e]) + other) * c[e];
           }
         } else {
-          float a[NT][4][4], am[NT][4];
+          float a[4][4], am[4];
 #pragma unroll
           for (int j = 0; j < 4; j += 2) {
             if constexpr (D == 128) {
@@ -418,24 +412,18 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const uint32_t x0 = r[2 * x], x1 = r[2 * x + 1], z0 = x0 >> 8, z1 = x1 >> 8;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint4 q = queries[(nt * (L::kSteps / 2 + 1) + j + x) * 32];
-                  mma16_first(a[nt][j + x], x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, q.x, q.y);
-                  mma16(a[nt][j + x], z0 & kLow, z1 & kLow, z0 & kHigh, z1 & kHigh, q.z, q.w);
-                }
+                const uint4 q = queries[(j + x) * 32];
+                mma16_first(a[j + x], x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, q.x, q.y);
+                mma16(a[j + x], z0 & kLow, z1 & kLow, z0 & kHigh, z1 & kHigh, q.z, q.w);
               }
             } else {
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const int at = (j + x) * 8 + (t >> 1) * 4, shift = (t & 1) * 8;
                 const uint32_t x0 = word_at(r0 + at) >> shift, x1 = word_at(r1 + at) >> shift;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint4 q = queries[(nt * (L::kSteps / 2 + 1) + j / 2) * 32];
-                  mma16_first(a[nt][j + x], x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, x ? q.z : q.x,
-                              x ? q.w : q.y);
-                }
+                const uint4 q = queries[(j / 2) * 32];
+                mma16_first(a[j + x], x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh, x ? q.z : q.x,
+                            x ? q.w : q.y);
               }
             }
           }
@@ -445,89 +433,76 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
                                __low2float(as_half2(s0.z)), __low2float(as_half2(s0.w))};
           const float f1[4] = {__low2float(as_half2(s1.x)), __low2float(as_half2(s1.y)),
                                __low2float(as_half2(s1.z)), __low2float(as_half2(s1.w))};
+          mma16_first(am, pairs[0], pairs[1], pairs[0], pairs[1], qs[0], qs[1]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16_first(am[nt], pairs[0], pairs[1], pairs[0], pairs[1], qs[nt][0], qs[nt][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float *f = e < 2 ? f0 : f1;
-              const float z = fmaf(f[3], a[nt][3][e],
-                                   fmaf(f[2], a[nt][2][e], fmaf(f[1], a[nt][1][e], f[0] * a[nt][0][e])));
-              y[nt][e] = fmaf(z, 16777216.f, am[nt][e]) * c[nt][e & 1];
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float *f = e < 2 ? f0 : f1;
+            const float z = fmaf(f[3], a[3][e],
+                                 fmaf(f[2], a[2][e], fmaf(f[1], a[1][e], f[0] * a[0][e])));
+            y[e] = fmaf(z, 16777216.f, am[e]) * c[e & 1];
           }
         }
         if (masked) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int n = (u.r0 + min(row_of(nt, e), live - 1)) / p.G;
+              const int n = (u.r0 + min(row_of(e), live - 1)) / p.G;
 #pragma unroll
               for (int h = 0; h < kKeys; ++h) {
                 const int key = blk * 16 + key_of(h);
-                if (!((valid >> key) & 1u) || !sees(p, u.k, u.b, n, at0 + key)) y[nt][2 * h + e] = -INFINITY;
+                if (!((valid >> key) & 1u) || !sees(p, u.k, u.b, n, at0 + key)) y[2 * h + e] = -INFINITY;
               }
             }
         }
         // ------------------------------------------------------------ weights
         const float lift = kLift4 - static_cast<float>(cap);
-        auto top_of = [&](int nt, int e) { return kQuad ? y[nt][e] : fmaxf(y[nt][e], y[nt][2 * (kKeys - 1) + e]); };
+        auto top_of = [&](int e) { return kQuad ? y[e] : fmaxf(y[e], y[2 * (kKeys - 1) + e]); };
         bool up = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) up |= top_of(nt, e) - lift > m[nt][e] + kSlack;
+          for (int e = 0; e < 2; ++e) up |= top_of(e) - lift > m[e] + kSlack;
         if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = top_of(nt, e);
+              float top = top_of(e);
 #pragma unroll
               for (int x = kQuad ? 2 : 4; x <= 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
               top -= lift;
-              const float to = top > m[nt][e] + kSlack ? top : m[nt][e];
-              const float f = m[nt][e] == -INFINITY ? 0.f : fast_exp2(m[nt][e] - to);
-              m[nt][e] = to;
-              l[nt][e] *= f;
+              const float to = top > m[e] + kSlack ? top : m[e];
+              const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - to);
+              m[e] = to;
+              l[e] *= f;
               // (with kQuad columns 4..7 are not looked at, or hold the same rows)
-              om[nt][e] *= f;
-              om[nt][2 + e] *= f;
+              om[e] *= f;
+              om[2 + e] *= f;
 #pragma unroll
               for (int j = 0; j < kOuts; ++j) {
-                o[nt][j][e] *= f;
-                o[nt][j][2 + e] *= f;
+                o[j][e] *= f;
+                o[j][2 + e] *= f;
               }
             }
         }
-        uint32_t w[NT][2];
+        uint32_t w[2];
+        // a row that has seen nothing yet keeps weights of zero
+        const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // a row that has seen nothing yet keeps weights of zero
-          const float u0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], u1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-#pragma unroll
-          for (int h = 0; h < kKeys; ++h) {
-            const float p0 = fast_exp2(y[nt][2 * h] - u0), p1 = fast_exp2(y[nt][2 * h + 1] - u1);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            w[nt][h] = transposed(F16::pack(p0, p1));
-          }
+        for (int h = 0; h < kKeys; ++h) {
+          const float p0 = fast_exp2(y[2 * h] - u0), p1 = fast_exp2(y[2 * h + 1] - u1);
+          l[0] += p0;
+          l[1] += p1;
+          w[h] = transposed(F16::pack(p0, p1));
         }
         if constexpr (kQuad) {
           // columns 0..3 have the first eight keys' weights here, 4..7 the same rows' of the
           // second
-          const uint32_t own = w[0][0], other = __shfl_xor_sync(0xFFFFFFFFu, own, 16);
-          w[0][0] = g < 4 ? own : other;
-          w[0][1] = g < 4 ? other : own;
+          const uint32_t own = w[0], other = __shfl_xor_sync(0xFFFFFFFFu, own, 16);
+          w[0] = g < 4 ? own : other;
+          w[1] = g < 4 ? other : own;
         }
         // ------------------------------------------------------------ outputs
         // tokens 2t, 2t + 1 of the first eight keys (h = 0) and of the second
         const char *v0 = v_s + (blk * 16 + 2 * t) * kRow;
         uint32_t low[2];  // row 2j + 1: minima of group j
         matrices2_turned(low, v_at + (blk * 16 + (lane & 15)) * kRow + D / 2);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16(om[nt], low[0], 0u, low[1], 0u, w[nt][0], w[nt][1]);
+        mma16(om, low[0], 0u, low[1], 0u, w[0], w[1]);
         if constexpr (kPieces) {
           // scales of this column's group: of all four, or (D 64) of two pieces'
           uint32_t sp[2][4];
@@ -553,13 +528,10 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const uint32_t x0 = r[2 * x], x1 = r[2 * x + 1], z0 = x0 >> 8, z1 = x1 >> 8;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t b0 = as_word(__hmul2(as_half2(w[nt][0]), as_half2(sp[0][j + x])));
-                const uint32_t b1 = as_word(__hmul2(as_half2(w[nt][1]), as_half2(sp[1][j + x])));
-                mma16(o[nt][2 * (j + x)], x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh, b0, b1);
-                mma16(o[nt][2 * (j + x) + 1], z0 & kLow, z0 & kHigh, z1 & kLow, z1 & kHigh, b0, b1);
-              }
+              const uint32_t b0 = as_word(__hmul2(as_half2(w[0]), as_half2(sp[0][j + x])));
+              const uint32_t b1 = as_word(__hmul2(as_half2(w[1]), as_half2(sp[1][j + x])));
+              mma16(o[2 * (j + x)], x0 & kLow, x0 & kHigh, x1 & kLow, x1 & kHigh, b0, b1);
+              mma16(o[2 * (j + x) + 1], z0 & kLow, z0 & kHigh, z1 & kLow, z1 & kHigh, b0, b1);
             }
           }
         } else {
@@ -586,10 +558,8 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
               sp[h] = __byte_perm(reinterpret_cast<const uint32_t *>(&pa[h])[j],
                                   reinterpret_cast<const uint32_t *>(&pb[h])[j], 0x5410);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16(o[nt][j], a[0], a[1], a[2], a[3], as_word(__hmul2(as_half2(w[nt][0]), as_half2(sp[0]))),
-                    as_word(__hmul2(as_half2(w[nt][1]), as_half2(sp[1]))));
+              mma16(o[j], a[0], a[1], a[2], a[3], as_word(__hmul2(as_half2(w[0]), as_half2(sp[0]))),
+                    as_word(__hmul2(as_half2(w[1]), as_half2(sp[1]))));
           }
         }
       }
@@ -609,18 +579,16 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     }
 
     // the unit's end.  A lane has 16 bytes of float32 outputs at a time, of row
-    // row_of(nt, e): dimensions d0, d0 + 1, d1, d1 + 1
+    // row_of(e): dimensions d0, d0 + 1, d1, d1 + 1
     const bool whole = v.whole();
     bad = __any_sync(0xFFFFFFFFu, bad);
     float *slot = p.part + piece_slot(v, line.worker) * slot_floats(p.rows, D);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float sum = l[nt][e];
+        float sum = l[e];
 #pragma unroll
         for (int x = kQuad ? 2 : 4; x <= 16; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-        const int row = row_of(nt, e);
+        const int row = row_of(e);
         // with kQuad half of the columns are another group's, or not looked at
         const bool mine = row < live && (!kQuad || (t >> 1) == (D == 128 ? 0 : g >> 2));
         const long long at = mine ? out_row(p, v.b, v.h, v.r0 + row) : 0;
@@ -635,10 +603,10 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
             // codes 2i (+ 1 in odd g) of a word: neighbours swap, so that each has four
             // dimensions of it
             const int group = D == 128 ? j : 2 * j + (g >> 2);
-            const float lo = __shfl_sync(0xFFFFFFFFu, om[nt][e], (2 * group + 1) * 4 + t);
-            const float x0 = fmaf(o[nt][2 * j][e], 16777216.f, lo), x1 = fmaf(o[nt][2 * j][2 + e], 1048576.f, lo);
-            const float x2 = fmaf(o[nt][2 * j + 1][e], 16777216.f, lo);
-            const float x3 = fmaf(o[nt][2 * j + 1][2 + e], 1048576.f, lo);
+            const float lo = __shfl_sync(0xFFFFFFFFu, om[e], (2 * group + 1) * 4 + t);
+            const float x0 = fmaf(o[2 * j][e], 16777216.f, lo), x1 = fmaf(o[2 * j][2 + e], 1048576.f, lo);
+            const float x2 = fmaf(o[2 * j + 1][e], 16777216.f, lo);
+            const float x3 = fmaf(o[2 * j + 1][2 + e], 1048576.f, lo);
             const bool odd = g & 1;
             const float z0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x2, 4);
             const float z1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? x1 : x3, 4);
@@ -646,11 +614,11 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
             d0 = 32 * j + 4 * g;
             d1 = d0 + 2;
           } else {
-            const float lo = __shfl_sync(0xFFFFFFFFu, om[nt][e], (4 * j + 1) * 4 + t);
-            const float hi = __shfl_sync(0xFFFFFFFFu, om[nt][e], (4 * j + 3) * 4 + t);
+            const float lo = __shfl_sync(0xFFFFFFFFu, om[e], (4 * j + 1) * 4 + t);
+            const float hi = __shfl_sync(0xFFFFFFFFu, om[e], (4 * j + 3) * 4 + t);
             const float f = g & 1 ? 1048576.f : 16777216.f;
-            y = make_float4(fmaf(o[nt][2 * j][e], f, lo), fmaf(o[nt][2 * j][2 + e], f, lo),
-                            fmaf(o[nt][2 * j + 1][e], f, hi), fmaf(o[nt][2 * j + 1][2 + e], f, hi));
+            y = make_float4(fmaf(o[2 * j][e], f, lo), fmaf(o[2 * j][2 + e], f, lo),
+                            fmaf(o[2 * j + 1][e], f, hi), fmaf(o[2 * j + 1][2 + e], f, hi));
             d0 = 32 * j + 2 * g;
             d1 = d0 + 16;
           }
@@ -677,10 +645,10 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
         }
         if (mine && (g & 3) == 0 && (kQuad || g == 0)) {
           if (!whole) {
-            slot[row] = m[nt][e];
+            slot[row] = m[e];
             slot[p.rows + row] = sum;
           } else if (p.lse) {
-            p.lse[at] = row_lse(m[nt][e], sum);
+            p.lse[at] = row_lse(m[e], sum);
           }
         }
       }
@@ -707,14 +675,14 @@ template <int R>
 AttnPlan q4_plan_of() {
   return {Rows4<128, R>::kCtas * Rows4<128, R>::kWarps * kSms4, R, 5, 2, 8};
 }
-// More rows go to tensor memory.
-bool q4_wide(int N, int G) { return N * G > 16 && G <= 128; }
+// More rows go to tensor memory.  (As units of 16 rows here, whose outputs alone are 128
+// registers a thread: four tokens of 32/8 heads of 128 at B = 64 119 us, 117 there, at B = 4
+// 33 us and 22.  Eight rows there: 116 us, 68 here.)
+bool q4_wide(int N, int G) { return N * G > 8 && G <= 128; }
 AttnPlan q4_plan(int N, int G) {
-  if (q4_wide(N, G)) {
-    const int rows = wide_tile_rows(G);
-    return N * G > 32 ? AttnPlan{kSms4, 2 * rows, 7, 8, 16} : AttnPlan{kSms4, 32, 7, 4, 8};
-  }
-  return N * G <= 4 ? q4_plan_of<4>() : N * G <= 8 ? q4_plan_of<8>() : q4_plan_of<16>();
+  if (q4_wide(N, G))
+    return N * G > 32 ? AttnPlan{kSms4, 2 * wide_tile_rows(G), 7, 8, 16} : AttnPlan{kSms4, 32, 7, 4, 8};
+  return N * G <= 4 ? q4_plan_of<4>() : q4_plan_of<8>();
 }
 
 }  // namespace
@@ -730,8 +698,7 @@ cudaError_t launch_attention_q4(AttnParams &p, int dtype, void *workspace, cudaS
   if (p.mask && tiles <= 8 && (wide || p.workers / 4 % tiles == 0)) p.row_lines = tiles;
   const cudaError_t e = wide          ? launch_attention_q4_wide(p, dtype, stream)
                         : p.rows == 4 ? start4<4>(p, dtype, stream)
-                        : p.rows == 8 ? start4<8>(p, dtype, stream)
-                                      : start4<16>(p, dtype, stream);
+                                      : start4<8>(p, dtype, stream);
   if (e != cudaSuccess || p.whole) return e;
   return launch_join(p, dtype, stream);
 }

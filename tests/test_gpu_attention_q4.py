@@ -27,7 +27,9 @@ def tolerance(out, lse, mean, reach, vmax, T, D, dtype, wide):
     group's whole span, of which each end is within a step of some value: vmax is taken
     over the row's seen values of all dimensions).  Scores: on the exact codes the
     queries' float16 (2^-24 of a row's largest), two terms of their sums (2^-22), the
-    sums' float32; in the wide kernel keys are float16 as the values are, each product
+    sums' float32; in the kernels on tensor memory keys are float16 as the values are (both
+    a sixteenth, so that magnitudes below 2^-10 are off by 2^-21, which the 1 % that reach
+    is taken larger covers for keys of 2^-4 on average), each product
     off by 2^-11 of |q| times a key's magnitude: reach 2^-11.
     """
     d = (D + 16) * 2.0 ** -22 * reach + 2.0 ** -20 + T * 2.0 ** -23
@@ -109,7 +111,7 @@ class Setup:
         q, k_cache, v_cache = self.q.cpu(), self.k.cpu(), self.v.cpu()
         out, lse = res.out.cpu().double(), res.lse.cpu().double()
         B, N, Hq, D = q.shape
-        wide = N * (Hq // k_cache.shape[2]) > 16  # rows on tensor memory
+        wide = N * (Hq // k_cache.shape[2]) > 8  # rows on tensor memory
         for b in range(B):
             n = N if self.n_new is None else int(self.n_new[b])
             if n == 0:
@@ -336,6 +338,61 @@ def test_many_sequences(N, Hq, Hkv, D):
     out = type(res)(res.out[sub], res.lse[sub], None)
     s.q, s.table, s.ctx = s.q[sub], s.table[sub], s.ctx[sub]
     s.check(out)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 4, 2, 64), (1, 8, 1, 128), (6, 4, 2, 128), (9, 4, 2, 64), (40, 4, 2, 64)])
+def test_scales_of_every_size(N, Hq, Hkv, D):
+    """Groups that span next to nothing, 60 and more, and thousands, in one cache; the
+    queries are as small as the largest keys are large."""
+    s = Setup(20, [50, 0, 700], N, Hq, Hkv, D, 16, "bf16")
+    gen = torch.Generator("cuda")
+    gen.manual_seed(20)
+    for x in (s.k, s.v):
+        pair = x[..., D // 2:].contiguous().view(torch.float16).reshape(*x.shape[:3], 4, 2)
+        up = torch.randint(0, 4, pair.shape[:-1], generator=gen, device="cuda")
+        by = torch.tensor([2.0 ** -9, 1.0, 16.0, 1024.0], device="cuda")[up]
+        pair = (pair.float() * by[..., None]).half()
+        x[..., D // 2:] = pair.flatten(-2).view(torch.uint8)
+    s.q = (s.q.float() / 512).to(s.q.dtype)
+    s.check(s.call())
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 130, 1, 64), (3, 256, 1, 128), (1, 128, 1, 128), (5, 96, 2, 64)])
+def test_groups_of_many_heads(N, Hq, Hkv, D):
+    s = Setup(21, [33, 0, 900], N, Hq, Hkv, D, 16, "bf16")
+    s.check(s.call(), only=sorted({0, N - 1}))
+
+
+@pytest.mark.parametrize("N,G", [(2, 8), (3, 3), (32, 1), (11, 3), (8, 4), (9, 1), (16, 2)])
+def test_rows_spread_over_the_quarters(N, G):
+    """Between nine and 33 rows: many short sequences, so that a thread block has units of
+    one tile and of several behind one another, and long ones cut between blocks."""
+    ctx = np.random.default_rng(22).integers(0, 90, 700)
+    ctx[::97] = 3000 + np.arange(len(ctx[::97])) * 31
+    s = Setup(22, ctx, N, 2 * G, 2, 64, 16, "f16", max_pages=3300 // 16)
+    res = s.call()
+    again = s.call()
+    assert torch.equal(res.out, again.out) and torch.equal(res.lse, again.lse)
+    sub = [0, 1, 2, 96, 97, 98, 194, 291, 500, 679, 680, 698, 699]
+    out = type(res)(res.out[sub], res.lse[sub], None)
+    s.q, s.table, s.ctx = s.q[sub], s.table[sub], s.ctx[sub]
+    s.check(out, only=sorted({0, N // 2, N - 1}))
+
+
+def test_two_calls_at_once_on_two_streams():
+    a, b = (Setup(23 + i, [4000, 20, 900], n, 8, 2, 128, 16, "bf16") for i, n in enumerate((1, 8)))
+    want = a.call(), b.call()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    args = [(x.q, x.k, x.v, x.dev(x.table), x.dev(x.ctx)) for x in (a, b)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for st, x in zip(streams, args):
+            with torch.cuda.stream(st):
+                got.append(sv.paged_attention(*x, return_lse=True))
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        assert torch.equal(x.out, want[i % 2].out) and torch.equal(x.lse, want[i % 2].lse)
 
 
 @pytest.mark.parametrize("N", [16, 40])

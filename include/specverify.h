@@ -640,9 +640,9 @@ spec_status spec_cache_fork(spec_page_pool pool, spec_kv_cache cache, int32_t *c
  * -t.  Pair i is (i, i + dim / 2), interleaved: (2i, 2i + 1).  frequency: dim / 2 values
  * in device memory (radians per token, float64); the angle is wrapped in 64-bit fixed
  * point, so that far positions are as exact as near ones; sine, cosine, products and
- * sums are float32.  A frequency that is not finite makes its pairs NaN.  dim: even, 2..512, at most head_dim (SPEC_ERR_INVALID_ARG
- * otherwise).  Where dim / 2 values (interleaved: dim) are no multiple of 16 bytes, rows
- * take a scalar path. */
+ * sums are float32.  A frequency that is not finite makes its pairs NaN.  dim: even,
+ * 2..512, at most head_dim (SPEC_ERR_INVALID_ARG otherwise).  Where dim / 2 values
+ * (interleaved: dim) are no multiple of 16 bytes, rows take a scalar path. */
 typedef struct {
   const double *frequency;
   int dim, interleaved, inverse;
@@ -703,9 +703,10 @@ spec_status spec_cache_read(spec_kv_cache cache, spec_page_table pages, const in
 /* spec_paged_attention over a cache of 4-bit rows (cache.dtype SPEC_Q4): keys and values
  * are what the rows stand for.  dtype: of q and out, SPEC_BF16 or SPEC_F16.  Arguments,
  * masks, windows, flags, errors and limits as for spec_paged_attention otherwise; a query
- * that is not finite makes its row NaN.  Values enter the products rounded to float16,
- * and weights to float16 (to zero below 2^-32 of a row's
- * largest). */
+ * that is not finite makes its row NaN.  Up to 8 rows (N times the group's query heads)
+ * take the codes as they are: weights are float16 (zero below 2^-32 of a row's largest),
+ * and so are their products with the scales.  More rows take keys and values rounded to
+ * float16 (those below 2^-10 to multiples of 2^-20) and such weights. */
 size_t spec_paged_attention_q4_workspace_size(int B, int N, int num_q_heads, int num_kv_heads,
                                               int head_dim, spec_dtype dtype);
 spec_status spec_paged_attention_q4(

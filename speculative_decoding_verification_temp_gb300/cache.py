@@ -342,7 +342,9 @@ def _append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_new, ro
             _forward_only(out)
             if out.shape != q.shape or out.dtype != dtype or _rows(out) is not out:
                 raise ValueError("out must be like q, with rows on 16 bytes")
-        heads, q_rows, out_rows = q.shape[-2], _row_view(q, shape), _row_view(out, shape)
+        heads = q.shape[-2]
+        if heads:
+            q_rows, out_rows = _row_view(q, shape), _row_view(out, shape)
     elif out is not None:
         raise ValueError("out is for the rotated q")
     frequency, turn = None, _NO_ROTATION
@@ -357,10 +359,9 @@ def _append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_new, ro
     if num_new is not None:
         num_new = _ints(num_new, (B,), dev, "num_new")
     flags = torch.empty(B, dtype=torch.int32, device=dev) if return_flags else None
-    if heads > 0 or q is None:
-        _run(dev, _abi.load().spec_cache_append_rotary, q_rows, out_rows, heads, _row_view(k_new, shape),
-             _row_view(v_new, shape), _KV_DTYPES[dtype], cache, table, context_len.data_ptr(),
-             _ptr(num_new), _ptr(position), pos_stride, B, N, turn, _ptr(flags))
+    _run(dev, _abi.load().spec_cache_append_rotary, q_rows, out_rows, heads, _row_view(k_new, shape),
+         _row_view(v_new, shape), _KV_DTYPES[dtype], cache, table, context_len.data_ptr(),
+         _ptr(num_new), _ptr(position), pos_stride, B, N, turn, _ptr(flags))
     return flags if q is None else RotaryAppendResult(out, flags)
 
 

@@ -1,16 +1,20 @@
-// Attention over a paged cache of 4-bit rows (q4.cuh) for many rows of queries, on the
-// fifth-generation tensor cores: pairs of row tiles of at most 128 rows (new tokens
-// times the group's heads), as pair_kernel of the 16-bit caches.
+// Attention over a paged cache of 4-bit rows (q4.cuh) for more than 8 rows of queries, on
+// the fifth-generation tensor cores: units of at most 32 rows, which the four quarters of
+// the lanes hold each, or pairs of row tiles of at most 128 rows (new tokens times the
+// group's heads), as solo_kernel and pair_kernel of the 16-bit caches.
 //
-// Three warps make the products' operands: they read the rows' codes into registers,
-// write the values m + s n as float16 into the entries of a ring (half a step of 2^-11,
-// against quantisation by half a step of 1/15 of a group's spread), and bring the
-// queries, as float16 scaled by a power of two where a row's largest leaves 2^14.  One
-// warp issues the products, two warpgroups turn scores into weights, a thread a row.
-// Every hand-over is an mbarrier, every wait is bounded.
+// Six warps make the products' operands: each copies 32 keys and then their values for
+// itself, reads the codes into registers and writes the values m + s n as float16 into the
+// entries of a ring (half a step of 2^-11, against quantisation by half a step of 1/15 of a
+// group's spread).  The softmax threads bring the queries, as float16 scaled by a power of
+// two where a row's largest leaves 2^14.  One warp issues the products, two warpgroups turn
+// scores into weights, a thread a row.  Every hand-over is an mbarrier, every wait is
+// bounded.
 //
-// Bound by the turns that a stream's softmax and products take with one buffer of
-// scores, as there; a tile's 32768 codes take the three warps about MEASURE cycles.
+// Bound by the turns of making, scores, softmax and outputs, not by a unit of the SM
+// (issue slots 0.33, tensor pipe 0.23 active).  A tile of 128 keys of one unit of eight
+// tokens (32/8 heads of 128, B = 64, 1..4096 tokens: 118 us) takes about 3200 cycles, without
+// its making 2700; of a pair (60-node trees, B = 32: 121 us) 4900, without it 4700.
 #include "q4_copies.cuh"
 
 namespace sv {

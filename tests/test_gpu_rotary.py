@@ -394,3 +394,19 @@ def test_compaction_and_forks_move_four_bit_rows():
     assert torch.equal(got.k[:, 0], got.k[:, 2]) and torch.equal(got.v[:, 0], got.v[:, 2])
     # values of normal rows lie within half a step of what came in: 4.5 / 15 / 2 and roundings
     assert (got.k[:, 0] - new[:, 0]).abs().max() < 0.4 and (got.k[:, 1] == 0).all()
+
+
+def test_no_query_heads():
+    """Queries without heads: the rows are appended all the same."""
+    k, v = sv.cache_4bit(4, 16, 2, 64)
+    new = torch.randn(1, 3, 2, 64, device="cuda", dtype=torch.float16)
+    f, _ = sv.rotary_frequency(64)
+    table = torch.arange(4, device="cuda", dtype=torch.int32)[None]
+    ctx = torch.tensor([5], device="cuda", dtype=torch.int32)
+    res = sv.cache_append_rotary(new, new, k, v, table, ctx, f, q=new[:, :, :0])
+    assert res.q.shape == (1, 3, 0, 64)
+    want = sv.rotary(new, ctx[:, None] + torch.arange(3, device="cuda"), f)
+    got = sv.cache_read(k, v, table, ctx, 3, dtype=torch.float16)
+    for x, y in ((got.k, want), (got.v, new)):
+        span = (y.float().amax() - y.float().amin()).item()
+        assert ((x.float() - y.float()).abs() <= span / 30 * 1.1 + 1e-2).all() and x.abs().sum() > 0

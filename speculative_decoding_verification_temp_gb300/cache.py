@@ -92,6 +92,33 @@ def _inplace(x, shape, dev, name):
     return x
 
 
+@functools.lru_cache(maxsize=512)
+def _cache_layout(dtype, v_dtype, shape, v_shape, ks, vs, layers):
+    """The spec_kv_cache of caches of these sizes and strides (2.7 us a call to check and
+    fill it in, 1.4 to copy it)."""
+    code = _KV_DTYPES.get(dtype)
+    sizes = shape
+    if dtype == torch.uint8:
+        # 4-bit rows; their strides count bytes, and are never those of one element
+        code, width = _abi.SPEC_Q4, shape[-1] if shape else 0
+        if width not in (48, 80):
+            raise ValueError("4-bit caches have rows of head_dim / 2 + 16 bytes, head_dim 64 or 128")
+        sizes = (*shape[:-1], 2 * (width - 16))
+    if code is None or v_dtype != dtype:
+        raise ValueError("k_cache and v_cache must both be float32, bfloat16 or float16, or 4-bit rows "
+                         "(uint8)")
+    dims = len(shape)
+    if v_shape != shape or dims != 4 and not (layers and dims == 5):
+        raise ValueError("k_cache and v_cache must be [%snum_pages, page_size, num_heads, head_dim]"
+                         % ("num_layers, " if layers else ""))
+    _sizes(sizes)
+    if sizes[-1] > 1 and (ks[-1] != 1 or vs[-1] != 1):
+        raise ValueError("the last dimension of the caches must be contiguous")
+    if dims == 4:
+        return _abi.spec_kv_cache(None, None, 0, ks[0], ks[1], ks[2], 0, vs[0], vs[1], vs[2], code, 1, *sizes)
+    return _abi.spec_kv_cache(None, None, *ks[:4], *vs[:4], code, *sizes)
+
+
 def _cache(k, v, layers):
     """The spec_kv_cache of a pair of cache tensors.  layers: whether a layer
     dimension is allowed."""
@@ -99,27 +126,10 @@ def _cache(k, v, layers):
         raise ValueError("k_cache must be a CUDA tensor")
     _on(v, k.device, "v_cache")
     _forward_only(k, v)
-    shape, code, ks, vs = k.shape, _KV_DTYPES.get(k.dtype), k.stride(), v.stride()
-    if k.dtype == torch.uint8:
-        # 4-bit rows; their strides count bytes, and are never those of one element
-        code, width = _abi.SPEC_Q4, shape[-1]
-        if width not in (48, 80):
-            raise ValueError("4-bit caches have rows of head_dim / 2 + 16 bytes, head_dim 64 or 128")
-        shape = (*shape[:-1], 2 * (width - 16))
-    if code is None or v.dtype != k.dtype:
-        raise ValueError("k_cache and v_cache must both be float32, bfloat16 or float16, or 4-bit rows "
-                         "(uint8)")
-    dims = len(shape)
-    if v.shape != k.shape or dims != 4 and not (layers and dims == 5):
-        raise ValueError("k_cache and v_cache must be [%snum_pages, page_size, num_heads, head_dim]"
-                         % ("num_layers, " if layers else ""))
-    _sizes(shape)
-    if shape[-1] > 1 and (ks[-1] != 1 or vs[-1] != 1):
-        raise ValueError("the last dimension of the caches must be contiguous")
-    if dims == 4:
-        return _abi.spec_kv_cache(k.data_ptr(), v.data_ptr(), 0, ks[0], ks[1], ks[2], 0, vs[0],
-                                  vs[1], vs[2], code, 1, *shape)
-    return _abi.spec_kv_cache(k.data_ptr(), v.data_ptr(), *ks[:4], *vs[:4], code, *shape)
+    cache = _abi.spec_kv_cache.from_buffer_copy(
+        _cache_layout(k.dtype, v.dtype, k.shape, v.shape, k.stride(), v.stride(), layers))
+    cache.k, cache.v = k.data_ptr(), v.data_ptr()
+    return cache
 
 
 def _table(page_table, B, dev):
@@ -291,7 +301,9 @@ def cache_append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_ne
 def _row_view(x, shape):
     """The spec_rows of rows [(num_layers,) B, N, heads, head_dim] that _rows gave."""
     strides = x.stride()
-    return _abi.spec_rows(x.data_ptr(), *((0, *strides[:3]) if len(shape) == 4 else strides[:4]))
+    if len(shape) == 4:
+        return _abi.spec_rows(x.data_ptr(), 0, strides[0], strides[1], strides[2])
+    return _abi.spec_rows(x.data_ptr(), *strides[:4])
 
 
 _NO_ROWS = _abi.spec_rows(None, 0, 0, 0, 0)

@@ -25,10 +25,10 @@
 // the spread).  The weights of 8 keys and 8 rows cross from the scores' layout to the
 // products' by one transposing move.
 //
-// Bound by instructions and the latencies of a warp's turn, about 430 instructions for 32
-// keys and values, of which half go to units that issue every other cycle: 256 sequences of
-// 1 to 4096 tokens, one token each, 32/8 heads of 128: 158 us, 4.28 TB/s; the copies alone
-// take 115.  Twelve warps an SM (three thread blocks; sixteen with fewer registers 179 us).
+// Bound by instructions and the latencies between them: 680 for 32 keys and values, issued
+// in every second cycle by the three warps a scheduler has registers for (sixteen warps an
+// SM instead of twelve, with fewer registers: 179 us).  256 sequences of 1 to 4096 tokens,
+// one token each, 32/8 heads of 128: 158 us, 4.28 TB/s; the copies alone take 115.
 #include <algorithm>
 
 #include "q4_copies.cuh"

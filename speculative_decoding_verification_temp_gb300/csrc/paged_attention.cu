@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // a CTA looks at 32 of them.  Their units of few pieces are dealt over its warps row by row;
 // the pieces of larger ones are shared by all warps, a row after the other.  (1824 workers,
 // both kernels of a call together, a CTA a worker and 32: 8 units of 32 tiles 16.4 us and
-// 13.2, 8 of 3072 tiles, 7 rows 58.7 and 45.2, but 2048 units 158 and 166.)
+// 13.2, 8 of about 3000 tiles, 7 rows 58.7 and 45.2, but 2048 units 158 and 166.)
 constexpr int kManyThreads = 512, kManyWorkers = 32, kFewPieces = 16;
 template <typename TE>
 __global__ void __launch_bounds__(kManyThreads) join_many_kernel(const __grid_constant__ AttnParams p) {

@@ -21,7 +21,8 @@ namespace sv {
 
 namespace {
 
-// Two warpgroups of softmax, six warps that make operands, two that issue products.
+// For more than 32 rows: two warpgroups of softmax, six warps that make operands, one that
+// issues products; the last of the fourth warpgroup has nothing to do.
 constexpr int kThreads4 = 512, kMakers = 6, kIssuer = 8 + kMakers;
 // Registers of a softmax thread and of the others: 256 * 184 + 256 * 72 are the 512 * 128
 // that the CTA is launched with.

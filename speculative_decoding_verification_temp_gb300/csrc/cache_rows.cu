@@ -11,9 +11,13 @@
 // (kRotThreads / pairs at most): one thread per (token, pair) finds the angle, and all
 // of the tokens' heads use it from shared memory.
 //
-// All kernels here are bound by HBM: rows are read once and written once, in 16-byte
-// pieces, a thread holding both pieces of its pairs, so that queries may be rotated in
-// place.
+// Rows are read once and written once, in 16-byte pieces, a thread holding both pieces of
+// its pairs, so that queries may be rotated in place.  Two rows a thread in flight (one 64 us,
+// four 61) on six thread blocks an SM (three 61, eight 64): 16384 tokens' 40 heads of 128,
+// bf16, 55 us, 0.90 of the copy rate.  Appends find their slots through three loads one behind
+// another before they read: five prompts of up to 4001 tokens, 32/8 heads of 128, f16, 60 us,
+// 0.61 of it.  4-bit rows are bound by instructions, a minimum, a maximum and a code per value:
+// 8192 tokens, 32/8 heads of 64, 28 us with the queries' rotation.
 #include <algorithm>
 
 #include "paged_attention.cuh"
@@ -61,7 +65,8 @@ __device__ __forceinline__ unsigned long long turn_of(double frequency) {
 
 // Where a pair's angle is: neighbouring lanes take neighbouring pieces of kEach pairs, and
 // of a piece one pair at a time, so that the first pairs of all pieces come first, then the
-// second ones (pairs in order: four lanes meet a bank; prompts' rows 84 us, 69 so).
+// second ones (pairs in order, of which four lanes meet a bank, and a row at a time: prompts'
+// rows 84 us, 61 so with four rows at once).
 template <int kEach>
 __device__ __forceinline__ int angle_at(int pairs, int pair) {
   return pair % kEach * (pairs / kEach) + pair / kEach;

@@ -975,7 +975,10 @@ cudaError_t start_join(const AttnParams &p, cudaStream_t stream) {
   if constexpr (sizeof(TE) == 2)
     if (p.workers > 8 * kSms && p.workers > 4ll * p.S.B * p.C.heads * tiles && p.D <= 128) return launch_behind(
         join_many_kernel<TE>, dim3((p.workers + kManyWorkers - 1) / kManyWorkers, rows), kManyThreads, 0, stream, p);
-  return launch_behind(join_kernel<TE>, dim3(p.workers, rows), kJoinThreads, 0, stream, p);
+  // many workers have few rows each: a warp a row (1824 workers, one token at B = 256 155 us, with
+  // four blocks for the four rows 158; two tokens, eight rows, at B = 64 63.6 us and 68.8)
+  return launch_behind(join_kernel<TE>, dim3(p.workers, p.workers > 8 * kSms ? (rows + 3) / 4 : rows), kJoinThreads,
+                       0, stream, p);
 }
 cudaError_t launch_join(const AttnParams &p, int dtype, cudaStream_t stream) {
   if (dtype == SPEC_F32) return start_join<float>(p, stream);

@@ -28,7 +28,7 @@
 // Bound by instructions and the latencies between them: 680 for 32 keys and values, issued
 // in every second cycle by the three warps a scheduler has registers for (sixteen warps an
 // SM instead of twelve, with fewer registers: 179 us).  256 sequences of 1 to 4096 tokens,
-// one token each, 32/8 heads of 128: 158 us, 4.28 TB/s; the copies alone take 115.
+// one token each, 32/8 heads of 128: 155 us, 4.37 TB/s; the copies alone take 112.
 #include <algorithm>
 
 #include "q4_copies.cuh"

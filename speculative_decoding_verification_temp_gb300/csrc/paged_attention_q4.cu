@@ -692,10 +692,9 @@ size_t attention_q4_workspace_bytes(int N, int G, int D) { return plan_bytes(q4_
 cudaError_t launch_attention_q4(AttnParams &p, int dtype, void *workspace, cudaStream_t stream) {
   const bool wide = q4_wide(p.S.N, p.G);
   take_plan(p, q4_plan(p.S.N, p.G), workspace);
-  // row tiles of a tree see the same keys, those of a chain end at their own; a CTA's
-  // workers are on one line
+  // row tiles of a tree see the same keys, those of a chain end at their own
   const int tiles = (p.S.N * p.G + p.rows - 1) / p.rows;
-  if (p.mask && tiles <= 8 && (wide || p.workers / 4 % tiles == 0)) p.row_lines = tiles;
+  if (wide && p.mask && tiles <= 8) p.row_lines = tiles;
   const cudaError_t e = wide          ? launch_attention_q4_wide(p, dtype, stream)
                         : p.rows == 4 ? start4<4>(p, dtype, stream)
                                       : start4<8>(p, dtype, stream);

@@ -410,3 +410,39 @@ def test_no_query_heads():
     for x, y in ((got.k, want), (got.v, new)):
         span = (y.float().amax() - y.float().amin()).item()
         assert ((x.float() - y.float()).abs() <= span / 30 * 1.1 + 1e-2).all() and x.abs().sum() > 0
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_offsets_beyond_32_bits(four):
+    """Pages more than 2^32 bytes into the cache: append, read, compaction and attention."""
+    page, heads, D, pages = 16, 8, 128, 160_000 if not four else 450_000
+    if four:
+        k, v = (torch.empty(pages, heads, page, 80, dtype=torch.uint8, device="cuda").transpose(1, 2) for _ in "kv")
+    else:
+        k, v = (torch.empty(pages, page, heads, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    assert k.numel() * k.element_size() > 2 ** 32
+    gen = torch.Generator("cuda")
+    gen.manual_seed(5)
+    new = lambda n: torch.randn(2, n, heads, D, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    table = torch.tensor([[pages - 1, 3, pages - 7], [pages - 2, pages - 5, 0]], dtype=torch.int32, device="cuda")
+    small = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32, device="cuda")
+    ks, vs = sv.cache_4bit(6, page, heads, D) if four else (k[:6].clone().zero_(), v[:6].clone().zero_())
+    f, _ = sv.rotary_frequency(D)
+    ctx = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    rows, more = (new(36), new(36)), (new(5), new(5))
+    at = torch.tensor([36, 36], dtype=torch.int32, device="cuda")
+    path = torch.tensor([[0, 2, 4], [0, 3, -1]], dtype=torch.int32, device="cuda")
+    taken = torch.tensor([2, 1], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 5, 32, D, generator=gen, device="cuda").to(torch.bfloat16)
+    got = []
+    for kc, vc, t in ((k, v, table), (ks, vs, small)):
+        out = []
+        sv.cache_append_rotary(*rows, kc, vc, t, ctx, f)
+        sv.cache_append_rotary(*more, kc, vc, t, at, f)
+        out += sv.paged_attention(q, kc, vc, t, at, return_lse=True)[:2]
+        out += sv.paged_attention(q[:, :1], kc, vc, t, at, return_lse=True)[:2]
+        sv.cache_compact(kc, vc, t, at, path, taken)
+        out += sv.cache_read(kc, vc, t, ctx, 39)[:2]
+        got.append(out)
+    for x, y in zip(*got):
+        assert torch.equal(x, y)

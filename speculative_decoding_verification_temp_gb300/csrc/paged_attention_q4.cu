@@ -681,7 +681,9 @@ AttnPlan q4_plan_of() {
 bool q4_wide(int N, int G) { return N * G > 8 && G <= 128; }
 AttnPlan q4_plan(int N, int G) {
   if (q4_wide(N, G))
-    return N * G > 32 ? AttnPlan{kSms4, 2 * wide_tile_rows(G), 7, 8, 16} : AttnPlan{kSms4, 32, 7, 4, 8};
+    return N * G <= 32                  ? AttnPlan{kSms4, 32, 7, 4, 8}
+           : N * G <= wide_tile_rows(G) ? AttnPlan{kSms4, wide_tile_rows(G), 7, 4, 8}
+                                        : AttnPlan{kSms4, 2 * wide_tile_rows(G), 7, 8, 16};
   return N * G <= 4 ? q4_plan_of<4>() : q4_plan_of<8>();
 }
 

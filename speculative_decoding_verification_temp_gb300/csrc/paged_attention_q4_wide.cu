@@ -1,7 +1,7 @@
 // Attention over a paged cache of 4-bit rows (q4.cuh) for more than 8 rows of queries, on
-// the fifth-generation tensor cores: units of at most 32 rows, which the four quarters of
-// the lanes hold each, or pairs of row tiles of at most 128 rows (new tokens times the
-// group's heads), as solo_kernel and pair_kernel of the 16-bit caches.
+// the fifth-generation tensor cores: units of one row tile, at most 128 rows (new tokens
+// times the group's heads; at most 32 are held by each of the four quarters of the lanes),
+// or pairs of tiles, as solo_kernel and pair_kernel of the 16-bit caches.
 //
 // Six warps make the products' operands: each copies 32 keys and then their values for
 // itself, reads the codes into registers and writes the values m + s n as float16 into the
@@ -69,8 +69,8 @@ struct PairCtl4 {
   uint32_t tmem;
   int dead, bad;
 };
-template <int D>
-struct SplitCtl4 {
+template <int D, int kThreads>
+struct SoloCtl4 {
   Ring4<D == 128 ? 4 : 8> ring;
   // of a group's even and odd tiles, in turn: outputs of a tile that is not the last one
   // are waited for only where they are scaled, and its phase is not mistaken for the one
@@ -79,7 +79,7 @@ struct SplitCtl4 {
     unsigned long long s_full[2], p_full[2], o_done[2], q_full, q_empty, meet;
   } group[2];
   unsigned long long drain;
-  RunScratch<kSplitThreads, 1> runs;
+  RunScratch<kThreads, 1> runs;
   uint32_t tmem;
   int dead, bad;
 };
@@ -94,7 +94,7 @@ struct Shape4 {
   static constexpr int kSplitEntries = kQ, kSplitRaw = kSplitEntries + kRing * Entry<D>::kBytes;
   static constexpr int kMeet = kSplitRaw + kSplitMakers * Raw4<D>::kWarp;
   static constexpr int kSplitCtl = kMeet + 2 * static_cast<int>(sizeof(Quarters));
-  static constexpr int kSplit = kSplitCtl + static_cast<int>(sizeof(SplitCtl4<D>));
+  static constexpr int kSplit = kSplitCtl + static_cast<int>(sizeof(SoloCtl4<D, kThreads4>));
   static_assert(kPair <= 227 * 1024 && kSplit <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -206,7 +206,7 @@ __device__ __forceinline__ void weigh_rows(const AttnParams &p, const Line &line
       if (works) {
         const uint4 valid = *reinterpret_cast<const uint4 *>(ring.valid[(tiles + i) % kValidRing]);
         softmax_tile<F16, D>(c, mine, tile_masked(p, u, at0, valid), both(seen, valid), s_at, o_at,
-                             i == 0, m, l);
+                             i == 0, m, l, [] { return true; });
       }
       tc_before();
       __syncwarp();
@@ -444,16 +444,19 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
   void_run<E, D, kThreads4>(p, line);
 }
 
-// Units of at most 32 rows: each quarter of the lanes holds them all and weighs a quarter
-// of a tile's keys, and the quarters are added at the unit's end.  Scores have two places:
+// Units of one row tile.  kSplit: of at most 32 rows: each quarter of the lanes holds them
+// all and weighs a quarter of a tile's keys, and the quarters are added at the unit's end.
+// Otherwise a thread has a row (sixteen tokens of 32/8 heads at B = 64 148 us, as one
+// stream of pair4_kernel 167).  Scores have two places:
 // a tile's products with the keys run while the tile before is in its softmax.  Two
 // warpgroups take the units in turn: one writes a unit while the other has the next.
-template <class E, int D>
-__global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_constant__ AttnParams p) {
+template <class E, int D, bool kSplit>
+__global__ void __launch_bounds__(kSplit ? kSplitThreads : kThreads4, 1)
+    solo4_kernel(const __grid_constant__ AttnParams p) {
   using W = Entry<D>;
   using Shape = Shape4<D>;
-  using Ctl = SplitCtl4<D>;
-  constexpr int kRing = Shape::kRing;
+  constexpr int kRing = Shape::kRing, kThreads = kSplit ? kSplitThreads : kThreads4;
+  using Ctl = SoloCtl4<D, kThreads>;
   extern __shared__ __align__(1024) char wide4_s[];
   Ctl &ctl = *reinterpret_cast<Ctl *>(wide4_s + Shape::kSplitCtl);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -494,7 +497,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_c
 
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
-    const int g = warp >> 2, part = warp & 3;
+    if constexpr (!kSplit) more_regs<kSoftRegs4>();
+    const int g = warp >> 2, part = warp & 3, row = kSplit ? lane : part * 32 + lane;
     auto &x = ctl.group[g];
     const uint32_t lanes = tmem + (static_cast<uint32_t>(part * 32) << 16), o_at = lanes + 256 + g * 128;
     Quarters &quarters = reinterpret_cast<Quarters *>(wide4_s + Shape::kMeet)[g];
@@ -507,8 +511,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_c
         t += n_tiles;
         continue;
       }
-      const bool mine = lane < live;
-      const int r = u.r0 + min(lane, live - 1), n = r / p.G;
+      const bool mine = row < live, works = kSplit || part * 32 < live;
+      const int r = u.r0 + min(row, live - 1), n = r / p.G;
       // once the products of the unit before, the other group's, have read theirs
       const float c = put_query<E, D>(
           p.q + u.b * p.q_seq + n * p.q_token + (u.h * p.G + r - n * p.G) * p.q_head, mine, p.scale_log2, wide4_s,
@@ -524,17 +528,27 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_c
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n_tiles; ++i, ++t, ++own) {
         const int at0 = key_tile(u.k, u.i0 + i) * kTileKeys;
-        const uint32_t seen =
-            all_seen(p, u.k, at0, kTileKeys) ? 0xFFFFFFFFu : seen_word(p, u.k, u.b, n, at0 + part * 32);
+        uint4 seen = make_uint4(0, 0, 0, 0);
+        if (kSplit) {
+          seen.x = all_seen(p, u.k, at0, kTileKeys) ? 0xFFFFFFFFu : seen_word(p, u.k, u.b, n, at0 + part * 32);
+        } else if (works) {
+          seen = seen_tile(p, u, n, at0);
+        }
         if (!(ok = warp_wait(&x.s_full[own & 1], (own >> 1) & 1u, &ctl.dead))) break;
         const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.ring.valid[t % kValidRing]);
-        const uint32_t word = ctl.ring.valid[t % kValidRing][part];
-        softmax_part<F16, D>(c, mine, tile_masked(p, u, at0, valid), seen & word, part, lanes + (t & 1) * 128,
-                             o_at, i == 0, m, l, [&] {
-                               outputs_done(own - 1);
-                               tc_after();
-                               return ok;
-                             });
+        const bool masked = tile_masked(p, u, at0, valid);
+        const uint32_t s_at = lanes + (t & 1) * 128;
+        auto whole = [&] {
+          outputs_done(own - 1);
+          tc_after();
+          return ok;
+        };
+        if (kSplit) {
+          const uint32_t word = ctl.ring.valid[t % kValidRing][part];
+          softmax_part<F16, D>(c, mine, masked, seen.x & word, part, s_at, o_at, i == 0, m, l, whole);
+        } else if (works) {
+          softmax_tile<F16, D>(c, mine, masked, both(seen, valid), s_at, o_at, i == 0, m, l, whole);
+        }
         if (!ok) break;
         tc_before();
         __syncwarp();
@@ -542,16 +556,23 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_c
       }
       // the other group goes on with the next unit meanwhile
       if (!ok || !outputs_done(own - 1)) break;
-      if (!(ok = write_split<E, D, true>(p, u, line.worker, part, lane, o_at, m, l, quarters, &x.meet, met,
-                                         &ctl.dead, &ctl.bad)))
-        break;
+      if constexpr (kSplit) {
+        if (!(ok = write_split<E, D, true>(p, u, line.worker, part, lane, o_at, m, l, quarters, &x.meet, met,
+                                           &ctl.dead, &ctl.bad)))
+          break;
+      } else if (works) {
+        write_row<E, D, true>(p, u, line.worker, row, n, mine, o_at, m, l,
+                              *reinterpret_cast<volatile int *>(&ctl.bad) != 0);
+      }
     } while (u.next(p, line));
-  } else if (warp < kSplitIssuer) {
+  } else {
+   if constexpr (!kSplit) fewer_regs<kRestRegs4>();
+   if (warp < kSplitIssuer) {
     // ------------------------------------------------- operands of the products
     const int maker = warp - 8;
     make_operands<D, kSplitMakers>(p, line, u, maker, lane, wide4_s + Shape::kSplitRaw + maker * Raw4<D>::kWarp,
                                    entries, ctl.ring, &ctl.dead, &ctl.bad);
-  } else {
+   } else if (warp == kSplitIssuer) {
     // ------------------------------------------------------------- products
     uint32_t t = 0, own[2] = {0, 0}, units = 0;  // tiles, of each group
     const uint32_t entries_at = smem_u32(entries), q_at = smem_u32(wide4_s);
@@ -587,10 +608,11 @@ __global__ void __launch_bounds__(kSplitThreads, 1) split4_kernel(const __grid_c
     // nothing is in flight when the tensor memory goes back
     issue_commit(&ctl.drain);
     bar_linger(&ctl.drain, 0u);
+   }
   }
   tm_free<kSplitIssuer>(tmem, warp);
   if (!ctl.dead) return;
-  void_run<E, D, kSplitThreads>(p, line);
+  void_run<E, D, kThreads>(p, line);
 }
 
 namespace {
@@ -602,8 +624,9 @@ cudaError_t start_wide4(int smem, int threads, const AttnParams &p, cudaStream_t
 }
 template <class E, int D>
 cudaError_t start_wide4(const AttnParams &p, cudaStream_t stream) {
-  return p.rows <= 32 ? start_wide4<split4_kernel<E, D>>(Shape4<D>::kSplit, kSplitThreads, p, stream)
-                      : start_wide4<pair4_kernel<E, D>>(Shape4<D>::kPair, kThreads4, p, stream);
+  if (p.rows > wide_tile_rows(p.G)) return start_wide4<pair4_kernel<E, D>>(Shape4<D>::kPair, kThreads4, p, stream);
+  return p.rows <= 32 ? start_wide4<solo4_kernel<E, D, true>>(Shape4<D>::kSplit, kSplitThreads, p, stream)
+                      : start_wide4<solo4_kernel<E, D, false>>(Shape4<D>::kSplit, kThreads4, p, stream);
 }
 
 }  // namespace

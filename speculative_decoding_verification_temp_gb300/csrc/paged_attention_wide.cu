@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                                o_at + lanes, i == 0, m, l, [] { return true; });
           } else if (works) {
             softmax_tile<E, D>(p.scale_log2, mine, masked, both(seen, valid), s_at + lanes,
-                               o_at + lanes, i == 0, m, l);
+                               o_at + lanes, i == 0, m, l, [] { return true; });
           }
           if (masked && (idle == 0 || !works)) {
             const uint32_t e = 2 * tiles + 1;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (works) {
           const uint4 valid = *reinterpret_cast<const uint4 *>(ctl.valid[(tiles + i) % kValidRing]);
           softmax_tile<E, D>(p.scale_log2, mine, tile_masked(p, u, at0, valid), both(seen, valid),
-                             s_at, o_at, i == 0, m, l);
+                             s_at, o_at, i == 0, m, l, [] { return true; });
         }
         tc_before();
         __syncwarp();

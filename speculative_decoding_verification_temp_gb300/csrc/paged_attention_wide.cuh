@@ -364,11 +364,12 @@ __device__ __forceinline__ uint4 seen_tile(const AttnParams &p, const UnitWalk &
 
 // One row per thread: the scores of a tile become weights, m and l go on, the
 // row's outputs so far are rescaled where m is raised (`first`: there are none).
-// seen: the keys that the row sees; masked: some are missing in some row.
-template <class E, int D>
+// seen: the keys that the row sees; masked: some are missing in some row; outputs_whole:
+// called by whole warps before the outputs so far are scaled, false where a wait gave up.
+template <class E, int D, class F>
 __device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, uint4 seen,
                                              uint32_t s_at, uint32_t o_at, bool first, float &m,
-                                             float &l) {
+                                             float &l, const F &outputs_whole) {
   tc_after();
   uint32_t s[4][32];
   float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -395,8 +396,7 @@ __device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, ui
     const float f = m == -INFINITY ? 0.f : fast_exp2(m - to);
     l *= f;
     m = to;
-    if (!first) {
-      // the products before S's are complete: O is whole
+    if (!first && outputs_whole()) {
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
         uint32_t o[16];
@@ -434,8 +434,7 @@ __device__ __forceinline__ void softmax_tile(float c, bool mine, bool masked, ui
 }
 
 // The same for a quarter of the tile's keys, those of the warp's part: weights of
-// zero for the other quarters' keys.  seen: of the 32 keys; outputs_whole: called by
-// whole warps before the outputs so far are scaled, false where a wait gave up.
+// zero for the other quarters' keys.  seen: of the 32 keys.
 template <class E, int D, class F>
 __device__ __forceinline__ void softmax_part(float c, bool mine, bool masked, uint32_t seen,
                                              int part, uint32_t s_at, uint32_t o_at, bool first,

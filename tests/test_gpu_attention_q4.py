@@ -363,13 +363,14 @@ def test_groups_of_many_heads(N, Hq, Hkv, D):
     s.check(s.call(), only=sorted({0, N - 1}))
 
 
-@pytest.mark.parametrize("N,G", [(2, 8), (3, 3), (32, 1), (11, 3), (8, 4), (9, 1), (16, 2)])
-def test_rows_spread_over_the_quarters(N, G):
-    """Between nine and 33 rows: many short sequences, so that a thread block has units of
+@pytest.mark.parametrize("N,G", [(2, 8), (3, 3), (32, 1), (11, 3), (8, 4), (9, 1), (16, 2), (12, 4), (25, 5),
+                                 (64, 2), (100, 1), (2, 64), (16, 4)])
+def test_units_of_one_row_tile(N, G):
+    """Between nine and 128 rows: many short sequences, so that a thread block has units of
     one tile and of several behind one another, and long ones cut between blocks."""
     ctx = np.random.default_rng(22).integers(0, 90, 700)
     ctx[::97] = 3000 + np.arange(len(ctx[::97])) * 31
-    s = Setup(22, ctx, N, 2 * G, 2, 64, 16, "f16", max_pages=3300 // 16)
+    s = Setup(22, ctx, N, 2 * G, 2, 64, 16, "f16", max_pages=3400 // 16)
     res = s.call()
     again = s.call()
     assert torch.equal(res.out, again.out) and torch.equal(res.lse, again.lse)

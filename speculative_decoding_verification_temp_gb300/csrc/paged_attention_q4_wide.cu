@@ -447,9 +447,9 @@ __global__ void __launch_bounds__(kThreads4, 1) pair4_kernel(const __grid_consta
 // Units of one row tile.  kSplit: of at most 32 rows: each quarter of the lanes holds them
 // all and weighs a quarter of a tile's keys, and the quarters are added at the unit's end.
 // Otherwise a thread has a row (sixteen tokens of 32/8 heads at B = 64 148 us, as one
-// stream of pair4_kernel 167).  Scores have two places:
-// a tile's products with the keys run while the tile before is in its softmax.  Two
-// warpgroups take the units in turn: one writes a unit while the other has the next.
+// stream of pair4_kernel 167).  Scores have two places: a tile's products with the keys run
+// while the tile before is in its softmax.  Two warpgroups take the units in turn: one
+// writes a unit while the other has the next.
 template <class E, int D, bool kSplit>
 __global__ void __launch_bounds__(kSplit ? kSplitThreads : kThreads4, 1)
     solo4_kernel(const __grid_constant__ AttnParams p) {
@@ -566,13 +566,13 @@ __global__ void __launch_bounds__(kSplit ? kSplitThreads : kThreads4, 1)
       }
     } while (u.next(p, line));
   } else {
-   if constexpr (!kSplit) fewer_regs<kRestRegs4>();
-   if (warp < kSplitIssuer) {
+    if constexpr (!kSplit) fewer_regs<kRestRegs4>();
+    if (warp < kSplitIssuer) {
     // ------------------------------------------------- operands of the products
     const int maker = warp - 8;
     make_operands<D, kSplitMakers>(p, line, u, maker, lane, wide4_s + Shape::kSplitRaw + maker * Raw4<D>::kWarp,
                                    entries, ctl.ring, &ctl.dead, &ctl.bad);
-   } else if (warp == kSplitIssuer) {
+    } else if (warp == kSplitIssuer) {
     // ------------------------------------------------------------- products
     uint32_t t = 0, own[2] = {0, 0}, units = 0;  // tiles, of each group
     const uint32_t entries_at = smem_u32(entries), q_at = smem_u32(wide4_s);
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kSplit ? kSplitThreads : kThreads4, 1)
     // nothing is in flight when the tensor memory goes back
     issue_commit(&ctl.drain);
     bar_linger(&ctl.drain, 0u);
-   }
+    }
   }
   tm_free<kSplitIssuer>(tmem, warp);
   if (!ctl.dead) return;

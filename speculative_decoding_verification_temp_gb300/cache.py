@@ -310,14 +310,22 @@ _NO_ROWS = _abi.spec_rows(None, 0, 0, 0, 0)
 _NO_ROTATION = _abi.spec_rotation(None, 0, 0, 0, 1.0)
 
 
+@functools.lru_cache(maxsize=256)
+def _rotation_layout(dtype, shape, head_dim, interleaved, inverse, amplitude):
+    """The spec_rotation of frequencies of this shape."""
+    if dtype != torch.float64 or len(shape) != 1 or not 1 <= shape[0] <= min(256, head_dim // 2):
+        raise ValueError("frequency must be float64 [dim / 2], dim at most head_dim and 512")
+    return _abi.spec_rotation(None, 2 * shape[0], interleaved, inverse, amplitude)
+
+
 def _rotation(frequency, head_dim, dev, interleaved, inverse, amplitude):
     _on(frequency, dev, "frequency")
-    if frequency.dtype != torch.float64 or frequency.dim() != 1 or \
-            not 1 <= frequency.shape[0] <= min(256, head_dim // 2):
-        raise ValueError("frequency must be float64 [dim / 2], dim at most head_dim and 512")
-    frequency = frequency.contiguous()
-    return frequency, _abi.spec_rotation(frequency.data_ptr(), 2 * frequency.shape[0], bool(interleaved),
-                                         bool(inverse), float(amplitude))
+    turn = _abi.spec_rotation.from_buffer_copy(_rotation_layout(
+        frequency.dtype, frequency.shape, head_dim, bool(interleaved), bool(inverse), float(amplitude)))
+    if not frequency.is_contiguous():
+        frequency = frequency.contiguous()
+    turn.frequency = frequency.data_ptr()
+    return frequency, turn
 
 
 def _append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_new, rotation, return_flags,
@@ -486,12 +494,21 @@ def rotary_frequency(dim, base=10000.0, scaling=None, factor=1.0, context=4096, 
     return RotaryFrequency(f.to(device), amplitude)
 
 
-def _loose_rows(x):
-    """x with the last dimension contiguous and rows apart, a copy where they are not."""
-    strides, shape = x.stride(), x.shape
+@functools.lru_cache(maxsize=512)
+def _rotary_rows(dtype, shape, strides):
+    """Of heads to rotate, their type's code, B, N, heads, head_dim and the spec_rows of
+    tensors with these strides; None where rows are not apart, or their last dimension is
+    not contiguous."""
+    code, dims = _KV_DTYPES.get(dtype), len(shape)
+    if code is None or not 2 <= dims <= 4:
+        raise ValueError("x must be [B, N, heads, D], [N, heads, D] or [heads, D], float32, bfloat16 or "
+                         "float16")
+    _sizes(shape)
+    lead = 4 - dims
+    rows = None
     if strides[-1] == 1 and all(n <= 1 or s >= shape[-1] for n, s in zip(shape[:-1], strides[:-1])):
-        return x
-    return x.clone(memory_format=torch.contiguous_format)
+        rows = _abi.spec_rows(None, 0, *(0,) * lead, *strides[:-1])
+    return code, ((1,) * lead + tuple(shape)), rows
 
 
 def rotary(x, position, frequency, interleaved=False, amplitude=1.0, inverse=False, out=None):
@@ -509,31 +526,34 @@ def rotary(x, position, frequency, interleaved=False, amplitude=1.0, inverse=Fal
         raise ValueError("x must be a CUDA tensor")
     _forward_only(x)
     dev, shape = x.device, x.shape
-    if x.dtype not in _KV_DTYPES or not 2 <= x.dim() <= 4:
-        raise ValueError("x must be [B, N, heads, D], [N, heads, D] or [heads, D], float32, bfloat16 or "
-                         "float16")
-    _sizes(shape)
-    frequency, turn = _rotation(frequency, shape[-1], dev, interleaved, inverse, amplitude)
+    code, sizes, rows = _rotary_rows(x.dtype, shape, x.stride())
+    frequency, turn = _rotation(frequency, sizes[3], dev, interleaved, inverse, amplitude)
     _on(position, dev, "position")
-    if x.dim() == 4 and position.dim() == 1:
-        position, pos_stride = _ints(position, shape[1:2], dev, "position"), 0
+    pos_stride = 0
+    if len(shape) == 4 and position.dim() == 1:
+        position = _ints(position, shape[1:2], dev, "position")
     else:
         position = _ints(position, shape[:-2], dev, "position")
-        pos_stride = shape[1] if x.dim() == 4 else 0
-    x = _loose_rows(x)
+        if len(shape) == 4:
+            pos_stride = sizes[1]
+    if rows is None:
+        x = x.clone(memory_format=torch.contiguous_format)
+        rows = _rotary_rows(x.dtype, shape, x.stride())[2]
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out_rows = _rotary_rows(x.dtype, shape, out.stride())[2]
     else:
         _on(out, dev, "out")
         _forward_only(out)
-        if out.shape != shape or out.dtype != x.dtype or _loose_rows(out) is not out:
+        out_rows = None
+        if out.shape == shape and out.dtype == x.dtype:
+            out_rows = _rotary_rows(x.dtype, shape, out.stride())[2]
+        if out_rows is None:
             raise ValueError("out must be like x, its last dimension contiguous")
-    lead = (1,) * (4 - len(shape))
-    view = lambda t: _abi.spec_rows(t.data_ptr(), 0, *(0,) * len(lead), *t.stride()[:-1])  # noqa: E731
-    B, N, H, D = (*lead, *shape)
     if x.numel():
-        _run(dev, _abi.load().spec_rotary, view(x), view(out), _KV_DTYPES[x.dtype], B, N, H, D,
-             position.data_ptr(), pos_stride, turn)
+        x_view, out_view = (_abi.spec_rows.from_buffer_copy(r) for r in (rows, out_rows))
+        x_view.data, out_view.data = x.data_ptr(), out.data_ptr()
+        _run(dev, _abi.load().spec_rotary, x_view, out_view, code, *sizes, position.data_ptr(), pos_stride, turn)
     return out
 
 

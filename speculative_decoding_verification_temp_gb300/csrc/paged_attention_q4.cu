@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
         const bool copied = (valid >> lane) & 1u;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (!copied || !q4_finite(q4_pair(w[j]))) {
+          if (!copied || !q4_finite(w[j])) {
             bad |= copied;
             w[j] = 0u;
           }

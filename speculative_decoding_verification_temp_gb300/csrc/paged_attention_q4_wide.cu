@@ -293,7 +293,7 @@ __device__ __forceinline__ void make_operands(const AttnParams &p, const Line &l
             const bool copied = (there >> key) & 1u;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              if (!copied || (values && !q4_finite(q4_pair(pair[j])))) {
+              if (!copied || (values && !q4_finite(pair[j]))) {
                 if (copied) *reinterpret_cast<volatile int *>(bad) = 1;
                 pair[j] = 0u;
               }

@@ -502,9 +502,8 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
 
 __device__ __forceinline__ uint32_t word_at(const char *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
-// Two outputs of token n that the keys' values which are not finite (beyond float16
-// too) add, from the parts of tiles that some row does not see whole; see
-// nonfinite_values.
+// Two outputs of token n that the keys' values which are not finite add, from the parts
+// of tiles that some row does not see whole; see nonfinite_values.
 template <int D, int kSlice>
 static __device__ __noinline__ float2 nonfinite_values_q4(const AttnParams &p, const UnitWalk u, int n,
                                                           int d) {
@@ -521,14 +520,12 @@ static __device__ __noinline__ float2 nonfinite_values_q4(const AttnParams &p, c
         if (!page_ok(p.C, page) || !sees(p, u.k, u.b, n, at)) continue;
         const char *row = p.C.v + page * p.C.v_page + (at - index * p.C.page_size) * p.C.v_token +
                           u.h * p.C.v_head;
-        const float2 s = q4_pair(word_at(row + D / 2 + d / (D / 4) * 4));
-        if (q4_finite(s)) continue;
+        const uint32_t pair = word_at(row + D / 2 + d / (D / 4) * 4);
+        if (q4_finite(pair)) continue;
+        const float2 s = q4_pair(pair);
         float x[8];
         q4_codes(word_at(row + d / 8 * 4), x);
-        for (int j = 0; j < 2; ++j) {
-          const float v = fmaf(s.x, x[d % 8 + j], s.y);
-          a[j] += fabsf(v) < 65520.f ? 0.f : (isnan(v) ? v : copysignf(INFINITY, v));
-        }
+        for (int j = 0; j < 2; ++j) a[j] += fmaf(s.x, x[d % 8 + j], s.y);
       }
     }
   }

@@ -35,9 +35,12 @@ __device__ __forceinline__ float2 q4_pair(uint32_t scale_min) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&scale_min));
 }
 
-// Whether every value of a group with this scale and minimum is one of float16's.
-__device__ __forceinline__ bool q4_finite(float2 scale_min) {
-  return fabsf(scale_min.y) + 15.f * fabsf(scale_min.x) < 65520.f;
+// Whether a group with this (scale, minimum) pair stands for numbers: both are finite, and
+// then m + s n is for every code (below 2^20, whose sixteenth is still one of float16's).
+// Otherwise none of its values is: an infinite or unknown scale times any code, 0 too, is
+// not finite.
+__device__ __forceinline__ bool q4_finite(uint32_t scale_min) {
+  return (((scale_min & 0x7C007C00u) + 0x04000400u) & 0x80008000u) == 0;
 }
 
 // Values that are the same float32 operations in a group's every thread: the codes

@@ -331,8 +331,10 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
       }
       // scales of 2^(cap + 1) and more: the weights are lowered
       if (__any_sync(0xFFFFFFFFu, ((s.x | s.y) | (s.z | s.w)) & 0x4000u)) {
-        const uint32_t top = max(max(s.x & 0x7FFFu, s.y & 0x7FFFu), max(s.z & 0x7FFFu, s.w & 0x7FFFu));
-        const uint32_t finite = __reduce_max_sync(0xFFFFFFFFu, top < 0x7C00u ? top : 0u);
+        // (each by itself: a scale that is not finite may stand beside a large one)
+        auto finite_scale = [](uint32_t x) { return (x & 0x7C00u) == 0x7C00u ? 0u : x & 0x7FFFu; };
+        const uint32_t top = max(max(finite_scale(s.x), finite_scale(s.y)), max(finite_scale(s.z), finite_scale(s.w)));
+        const uint32_t finite = __reduce_max_sync(0xFFFFFFFFu, top);
         const int more = static_cast<int>(finite >> 10) - 15 - cap;
         if (more > 0) {
           cap += more;

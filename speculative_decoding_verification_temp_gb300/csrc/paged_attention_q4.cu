@@ -20,9 +20,11 @@
 // subnormals.  The scales go into the weights, one product of float16 per key, row and
 // group instead of one per key and value; sums of the weights times the minima are two
 // more columns.  Weights are float16 as in the tensor-memory kernels: lifted, so that
-// those rounded to zero are below 2^-32 of the row's largest; the product with a scale
+// those rounded to zero are below 2^-31 of the row's largest; the product with a scale
 // rounds once more (half a step of 2^-11, against quantisation by half a step of 1/15 of
-// the spread).  The weights of 8 keys and 8 rows cross from the scores' layout to the
+// the spread).  Powers of two keep both in float16's range whatever the scales are
+// (bring_near_one): a product is lost below 2^-24 of the row's largest weight times the
+// group's usual scale.  The weights of 8 keys and 8 rows cross from the scores' layout to the
 // products' by one transposing move.
 //
 // Bound by instructions and the latencies between them: 680 for 32 keys and values, issued
@@ -39,8 +41,7 @@ namespace {
 
 constexpr int kQ4Tile = kQ4Keys;  // of a tile
 constexpr int kSms4 = 152;
-// Weights reach 2^(kLift4 + kSlack) = 2^14, and times scales below 2 stay in float16;
-// larger scales lower the weights (see cap).
+// Weights reach 2^(kLift4 + kSlack) = 2^14, and times scales below 2 stay in float16.
 constexpr float kLift4 = 6.f;
 
 // R: rows of a unit, 4 or 8.
@@ -57,7 +58,8 @@ struct Rows4 {
   // of the queries: two operands a step, two for the sums, the factors; two steps a piece
   static constexpr int kQPieces = kSteps / 2 + 1;
   static constexpr int kQBytes = kQPieces * 32 * 16;
-  static constexpr int kWarp = 2 * kStage + kQBytes;
+  static constexpr int kDowns = 2 * kStage + kQBytes;  // usual_downs of the unit
+  static constexpr int kWarp = kDowns + 16;
   static constexpr int kSmem = kWarps * kWarp;
   static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "shared memory of an SM");
 };
@@ -108,6 +110,67 @@ __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_ca
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 __device__ __forceinline__ float scale_at(const char *p) { return __half2float(*reinterpret_cast<const __half *>(p)); }
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // nibbles of two halves
+
+// The products of weights and scales are float16, so a key's scales are brought near one, and
+// its weight times the same power of two takes their place in the row's running maximum:
+// neither small scales nor a key of large ones costs the other keys' weights their bits.
+// Tiles of scales within [1/128, 2) stay as they are (others cost 85 instructions more).
+
+// Not zero where a scale lies outside of [1/128, 2): its exponent field outside of 8 to 15.
+__device__ __forceinline__ uint32_t scale_far(uint32_t pair) { return (pair ^ 0x2000u) & 0x6000u; }
+__device__ __forceinline__ bool scales_far(uint4 s) {
+  return (scale_far(s.x) | scale_far(s.y) | scale_far(s.z) | scale_far(s.w)) != 0u;
+}
+// Exponent field of a scale; -1: zero, or not finite.
+__device__ __forceinline__ int scale_field(uint32_t pair) {
+  const uint32_t x = pair & 0x7FFFu;
+  return x != 0u && x < 0x7C00u ? static_cast<int>(x >> 10) : -1;
+}
+// Groups whose scales are usually smaller than another group's: by how many powers of two, a
+// byte a group, at most 7, so that keys whose groups are alike are not brought further apart
+// than the groups of tiles that stay as they are.  By a whole warp, from a tile's keys.
+__device__ __forceinline__ uint32_t usual_downs(uint4 s) {
+  const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+  int mean[4], top = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int field = scale_field(w[j]);
+    const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, field < 0 ? 0u : 0x10000u + field);
+    const int n = sum >> 16;
+    mean[j] = n ? (static_cast<int>(sum & 0xFFFFu) + n / 2) / n : -1;
+    top = max(top, mean[j]);
+  }
+  uint32_t downs = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    downs |= static_cast<uint32_t>(mean[j] < 0 ? 0 : min(top - mean[j], 7)) << (8 * j);
+  return downs;
+}
+__device__ __forceinline__ int down_exponent(uint32_t downs, int group) { return downs >> (8 * group) & 255; }
+__device__ __forceinline__ float down_of(uint32_t downs, int group) {
+  return __int_as_float((127 - down_exponent(downs, group)) << 23);
+}
+// Brings the largest of a key's scales, times 2^downs, into [1, 2), and its minima with them;
+// returns the power of two that its weight takes instead.  Small scales are raised no further
+// than float16 holds the minima.
+__device__ __forceinline__ int bring_near_one(uint4 &s, uint32_t downs) {
+  uint32_t *w = reinterpret_cast<uint32_t *>(&s);
+  int high = -1, low = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int field = scale_field(w[j]), minimum = w[j] >> 26 & 31;
+    if (field >= 0) high = max(high, field + down_exponent(downs, j));
+    if (minimum < 31) low = max(low, minimum);
+  }
+  const int by = high < 0 ? 0 : max(high - 15, low - 30);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = q4_pair(w[j]);
+    w[j] = F16::pack(x.x * __int_as_float((127 + down_exponent(downs, j) - by) << 23),
+                     x.y * __int_as_float((127 - by) << 23));
+  }
+  return by;
+}
 
 // A lane's operands of the scores' products, of the unit's queries as eight columns
 // (four with kQuad), into pieces of 16 bytes [step / 2][lane]:
@@ -272,7 +335,9 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
   };
 
   if (busy) copies.begin(p, u, key_tile(u.k, u.i0) * kQ4Tile, lane);
+  uint32_t *unit_downs = reinterpret_cast<uint32_t *>(ring + L::kDowns);
   while (busy) {
+      if (lane == 0) *unit_downs = 0u;
       prepare_queries<E, D, kQuad>(p, u, lane, queries);
     __syncwarp();
     uint32_t qs[2];
@@ -293,8 +358,6 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
 #pragma unroll
       for (int i = 0; i < kOuts; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }
-    // scales are below 2^(cap + 1)
-    int cap = 0;
     bool bad = false;
 
     // two tiles are on their way while one is weighed
@@ -315,42 +378,37 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
       uint4 *scales = reinterpret_cast<uint4 *>(v_s + lane * kRow + D / 2);
       uint4 s = *scales;
       const bool masked = valid != 0xFFFFFFFFu || !all_seen(p, u.k, at0, kQ4Tile);
+      bool far = scales_far(s);
       if (masked) {
         // rows that were not copied stand for zeros, and so do groups that are not
         // finite, which nonfinite_values_q4 adds
         uint32_t *w = reinterpret_cast<uint32_t *>(&s);
         const bool copied = (valid >> lane) & 1u;
+        uint32_t apart = 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (!copied || !q4_finite(w[j])) {
             bad |= copied;
             w[j] = 0u;
+          } else {
+            apart |= scale_far(w[j]);
           }
+        far = apart != 0u;
+      }
+      uint32_t downs = *unit_downs;
+      const bool moved = __any_sync(0xFFFFFFFFu, far || downs != 0u);
+      int by = 0;  // of this lane's key
+      if (moved) {
+        // (where no row has a maximum the outputs so far are zeros, whatever they were times)
+        if (__all_sync(0xFFFFFFFFu, m[0] == -INFINITY && m[1] == -INFINITY)) {
+          downs = usual_downs(s);
+          *unit_downs = downs;  // the same in every lane
+        }
+        by = bring_near_one(s, downs);
+      }
+      if (masked || moved) {
         *scales = s;
         __syncwarp();
-      }
-      // scales of 2^(cap + 1) and more: the weights are lowered
-      if (__any_sync(0xFFFFFFFFu, ((s.x | s.y) | (s.z | s.w)) & 0x4000u)) {
-        // (each by itself: a scale that is not finite may stand beside a large one)
-        auto finite_scale = [](uint32_t x) { return (x & 0x7C00u) == 0x7C00u ? 0u : x & 0x7FFFu; };
-        const uint32_t top = max(max(finite_scale(s.x), finite_scale(s.y)), max(finite_scale(s.z), finite_scale(s.w)));
-        const uint32_t finite = __reduce_max_sync(0xFFFFFFFFu, top);
-        const int more = static_cast<int>(finite >> 10) - 15 - cap;
-        if (more > 0) {
-          cap += more;
-          const float f = __int_as_float((127 - more) << 23);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            m[e] += static_cast<float>(more);
-            l[e] *= f;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            om[e] *= f;
-#pragma unroll
-            for (int j = 0; j < kOuts; ++j) o[j][e] *= f;
-          }
-        }
       }
       // (once in the code: unrolled, its instructions do not stay in the cache, 12 % slower)
 #pragma unroll 1
@@ -456,18 +514,29 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
             }
         }
         // ------------------------------------------------------------ weights
-        const float lift = kLift4 - static_cast<float>(cap);
+        // the product with a key's scales takes its weight times 2^by; their sum takes it as it is
+        float back[kKeys];
+#pragma unroll
+        for (int h = 0; h < kKeys; ++h) {
+          back[h] = 1.f;
+          if (moved) {
+            const int up = __shfl_sync(0xFFFFFFFFu, by, blk * 16 + key_of(h));
+            y[2 * h] += static_cast<float>(up);
+            y[2 * h + 1] += static_cast<float>(up);
+            back[h] = __int_as_float((127 - up) << 23);
+          }
+        }
         auto top_of = [&](int e) { return kQuad ? y[e] : fmaxf(y[e], y[2 * (kKeys - 1) + e]); };
         bool up = false;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) up |= top_of(e) - lift > m[e] + kSlack;
+          for (int e = 0; e < 2; ++e) up |= top_of(e) - kLift4 > m[e] + kSlack;
         if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float top = top_of(e);
 #pragma unroll
               for (int x = kQuad ? 2 : 4; x <= 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-              top -= lift;
+              top -= kLift4;
               const float to = top > m[e] + kSlack ? top : m[e];
               const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - to);
               m[e] = to;
@@ -488,8 +557,8 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
 #pragma unroll
         for (int h = 0; h < kKeys; ++h) {
           const float p0 = fast_exp2(y[2 * h] - u0), p1 = fast_exp2(y[2 * h + 1] - u1);
-          l[0] += p0;
-          l[1] += p1;
+          l[0] = fmaf(p0, back[h], l[0]);
+          l[1] = fmaf(p1, back[h], l[1]);
           w[h] = transposed(F16::pack(p0, p1));
         }
         if constexpr (kQuad) {
@@ -584,6 +653,8 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
     // row_of(e): dimensions d0, d0 + 1, d1, d1 + 1
     const bool whole = v.whole();
     bad = __any_sync(0xFFFFFFFFu, bad);
+    const uint32_t downs = *unit_downs;
+    __syncwarp();
     float *slot = p.part + piece_slot(v, line.worker) * slot_floats(p.rows, D);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -606,9 +677,9 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
             // dimensions of it
             const int group = D == 128 ? j : 2 * j + (g >> 2);
             const float lo = __shfl_sync(0xFFFFFFFFu, om[e], (2 * group + 1) * 4 + t);
-            const float x0 = fmaf(o[2 * j][e], 16777216.f, lo), x1 = fmaf(o[2 * j][2 + e], 1048576.f, lo);
-            const float x2 = fmaf(o[2 * j + 1][e], 16777216.f, lo);
-            const float x3 = fmaf(o[2 * j + 1][2 + e], 1048576.f, lo);
+            const float even = 16777216.f * down_of(downs, group), odds = even * 0.0625f;
+            const float x0 = fmaf(o[2 * j][e], even, lo), x1 = fmaf(o[2 * j][2 + e], odds, lo);
+            const float x2 = fmaf(o[2 * j + 1][e], even, lo), x3 = fmaf(o[2 * j + 1][2 + e], odds, lo);
             const bool odd = g & 1;
             const float z0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x2, 4);
             const float z1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? x1 : x3, 4);
@@ -619,8 +690,9 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
             const float lo = __shfl_sync(0xFFFFFFFFu, om[e], (4 * j + 1) * 4 + t);
             const float hi = __shfl_sync(0xFFFFFFFFu, om[e], (4 * j + 3) * 4 + t);
             const float f = g & 1 ? 1048576.f : 16777216.f;
-            y = make_float4(fmaf(o[2 * j][e], f, lo), fmaf(o[2 * j][2 + e], f, lo),
-                            fmaf(o[2 * j + 1][e], f, hi), fmaf(o[2 * j + 1][2 + e], f, hi));
+            const float f0 = f * down_of(downs, 2 * j), f1 = f * down_of(downs, 2 * j + 1);
+            y = make_float4(fmaf(o[2 * j][e], f0, lo), fmaf(o[2 * j][2 + e], f0, lo),
+                            fmaf(o[2 * j + 1][e], f1, hi), fmaf(o[2 * j + 1][2 + e], f1, hi));
             d0 = 32 * j + 2 * g;
             d1 = d0 + 16;
           }

@@ -104,21 +104,22 @@ __device__ __forceinline__ uint32_t word_of(__half2 x) { return *reinterpret_cas
 // The operands are values times kFourth (paged_attention_wide.cuh), 2^-4.  A nibble at
 // bits 6 to 9 is a float16 below its normal ones, n 2^-18, exactly: with a scale of s 2^14,
 // for s below 4 (a group that spans less than 60), a value takes a shift, a mask and half
-// of a fused multiply and add.  (The nibble as 1024 + n, less 1024, before that: twice the
+// of a fused multiply and add.  (Any form that takes larger scales too has twice the
 // instructions of float16, which run at a quarter of the rate.)
 __device__ __forceinline__ uint4 word_values(uint32_t w, __half2 scale, __half2 low) {
   auto value = [&](uint32_t x) { return word_of(__hfma2(half2_of(x & 0x03C003C0u), scale, low)); };
   return make_uint4(value(w << 6), value(w << 2), value(w >> 2), value(w >> 6));
 }
-// For any scale.
+// A scale of 4 and more is taken as it is, with n 2^-4 instead.
+__device__ __forceinline__ bool large_scale(uint32_t pair) { return (pair & 0x7FFFu) >= 0x4400u; }
+// Large scales and others, in groups of one row or in rows of one warp.
 __device__ __forceinline__ uint4 word_values_any(uint32_t w, uint32_t pair) {
-  const __half2 x = half2_of(pair), part = __float2half2_rn(kFourth);
-  const __half2 scale = __hmul2(__low2half2(x), part), low = __hmul2(__high2half2(x), part);
-  uint32_t v[4];
-  for (int i = 0; i < 4; ++i)
-    v[i] = word_of(__hfma2(__hsub2(half2_of((w >> 4 * i & 0x000F000Fu) | 0x64006400u), half2_of(0x64006400u)),
-                           scale, low));
-  return make_uint4(v[0], v[1], v[2], v[3]);
+  const bool large = large_scale(pair);
+  const __half2 up = __float2half2_rn(large ? 16384.f : 1.f);
+  const __half2 f = __hmul2(half2_of(pair), __floats2half2_rn(large ? 1.f : kFourth * 262144.f, kFourth));
+  const __half2 scale = __low2half2(f), low = __high2half2(f);
+  auto value = [&](uint32_t x) { return word_of(__hfma2(__hmul2(half2_of(x & 0x03C003C0u), up), scale, low)); };
+  return make_uint4(value(w << 6), value(w << 2), value(w >> 2), value(w >> 6));
 }
 
 // A row of queries as float16 into its place of a tile (panels of 64 values, the
@@ -303,9 +304,7 @@ __device__ __forceinline__ void make_operands(const AttnParams &p, const Line &l
           auto put = [&](int j, uint4 v) {
             *reinterpret_cast<uint4 *>(to + ((((piece & 1) * 4 + j) ^ r) << 4)) = v;
           };
-          // (as integers: scales are not below zero; not-a-number counts as large)
-          const uint32_t large = max(pair[0] & 0xFFFFu, pair[1] & 0xFFFFu);
-          if (__any_sync(0xFFFFFFFFu, large >= 0x4400u)) {
+          if (__any_sync(0xFFFFFFFFu, large_scale(pair[0]) || large_scale(pair[1]))) {
 #pragma unroll 1
             for (int j = 0; j < 4; ++j)
               put(j, word_values_any(word_at(row + piece * 16 + j * 4), j < 2 ? pair[0] : pair[1]));

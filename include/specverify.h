@@ -703,14 +703,14 @@ spec_status spec_cache_read(spec_kv_cache cache, spec_page_table pages, const in
 /* spec_paged_attention over a cache of 4-bit rows (cache.dtype SPEC_Q4): keys and values
  * are what the rows stand for.  dtype: of q and out, SPEC_BF16 or SPEC_F16.  Arguments,
  * masks, windows, flags, errors and limits as for spec_paged_attention otherwise; a query
- * that is not finite makes its row NaN.  Up to 8 rows (N times the group's query heads),
- * and groups of more than 128 heads, take the codes as they are: weights are float16, and
- * so are their products with the scales, both brought into its range by powers of two
- * where a scale lies outside of 2^-7 .. 2.  Weights below 2^-31 of a row's largest are zero
- * (both times their keys' largest scales there), products below 2^-24 of that weight times
- * the scale that the group usually has (of groups within 2^14 of one another).  More rows
- * take keys and values rounded to float16 (those below 2^-10 to multiples of 2^-20) and
- * weights that are zero below 2^-32. */
+ * that is not finite makes its row NaN where it sees a key.  Up to 8 rows (N times the
+ * group's query heads), and groups of more than 128 heads, take the codes as they are:
+ * weights are float16, and so are their products with the scales, both brought into its
+ * range by powers of two where a scale lies outside of 2^-7 .. 2.  Weights below 2^-31 of a
+ * row's largest are zero (both times their keys' largest scales there), products below
+ * 2^-24 of that weight times the scale that the group usually has (of groups within 2^14 of
+ * one another).  More rows take keys and values rounded to float16 (those below 2^-10 to
+ * multiples of 2^-20) and weights that are zero below 2^-32. */
 size_t spec_paged_attention_q4_workspace_size(int B, int N, int num_q_heads, int num_kv_heads,
                                               int head_dim, spec_dtype dtype);
 spec_status spec_paged_attention_q4(

@@ -221,7 +221,7 @@ __device__ __forceinline__ void prepare_queries(const AttnParams &p, const UnitW
   // to [2^8, 2^9); rows of zeros, and those far below what matters, stay
   const int exponent = top > 1e-30f ? min(max(8 - ilogbf(top), -126), 126) : 0;
   const float up = __int_as_float((127 + exponent) << 23);
-  // a query that is not finite makes its row NaN
+  // a query that is not finite makes its row's scores NaN, those that the mask leaves
   const float factor = odd ? __int_as_float(0x7FC00000)
                            : p.scale_log2 * __int_as_float((127 - exponent) << 23);
   float sum[kParts];

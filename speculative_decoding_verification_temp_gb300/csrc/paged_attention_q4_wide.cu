@@ -146,8 +146,8 @@ __device__ __forceinline__ float put_query(const char *from, bool mine, float sc
       top = fmaxf(top, x);
     }
   const int exponent = top > 16384.f || (top > 1e-30f && top < 0.0625f) ? min(max(8 - ilogbf(top), -126), 126) : 0;
-  // a query that is not finite makes its row NaN
-  const float up = odd ? 0.f : __int_as_float((127 + exponent) << 23);
+  // a query that is not finite makes its row's scores NaN, those that the mask leaves
+  const float up = __int_as_float((127 + exponent) << 23);
   if (!ready()) return 0.f;
 #pragma unroll
   for (int i = 0; mine && i < D / 8; ++i) {
@@ -155,12 +155,12 @@ __device__ __forceinline__ float put_query(const char *from, bool mine, float sc
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const TE *x = reinterpret_cast<const TE *>(&v[i]) + 2 * e;
-      h[e] = odd ? 0u : F16::pack(E::to(x[0]) * up, E::to(x[1]) * up);
+      h[e] = odd ? 0x7E007E00u : F16::pack(E::to(x[0]) * up, E::to(x[1]) * up);
     }
     *reinterpret_cast<uint4 *>(tile + i / 8 * panel_bytes + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
         make_uint4(h[0], h[1], h[2], h[3]);
   }
-  return odd ? __int_as_float(0x7FC00000) : scale * (1.f / kFourth) * __int_as_float((127 - exponent) << 23);
+  return scale * (1.f / kFourth) * (odd ? 1.f : __int_as_float((127 - exponent) << 23));
 }
 
 // The rows of a stream, a thread each: their queries, their weights and their outputs.

@@ -639,8 +639,9 @@ spec_status spec_cache_fork(spec_page_pool pool, spec_kv_cache cache, int32_t *c
  * * frequency[i], (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t); inverse: by
  * -t.  Pair i is (i, i + dim / 2), interleaved: (2i, 2i + 1).  frequency: dim / 2 values
  * in device memory (radians per token, float64); the angle is wrapped in 64-bit fixed
- * point, so that far positions are as exact as near ones; sine, cosine, products and
- * sums are float32.  A frequency that is not finite makes its pairs NaN.  dim: even,
+ * point, off by 2^-64 turns per token of position (by 2^-106 of the frequency where that
+ * is above 2^53), so that far positions are as exact as near ones; sine, cosine, products
+ * and sums are float32.  A frequency that is not finite makes its pairs NaN.  dim: even,
  * 2..512, at most head_dim (SPEC_ERR_INVALID_ARG otherwise).  Where dim / 2 values
  * (interleaved: dim) are no multiple of 16 bytes, rows take a scalar path. */
 typedef struct {

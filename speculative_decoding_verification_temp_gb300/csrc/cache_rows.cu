@@ -6,7 +6,7 @@
 // b cos t), t = position * frequency.  Far positions times frequencies lose their
 // angle in float32, and float64 is slow here, so a frequency becomes the fraction of
 // a turn per token in 64-bit fixed point once per thread; an integer product that
-// wraps is then the angle itself, off by 2^-54 turns per token of position, and
+// wraps is then the angle itself, off by 2^-64 turns per token of position, and
 // sine and cosine see a float32 in [-1/2, 1/2] turns.  A CTA takes a batch of tokens
 // (kRotThreads / pairs at most): one thread per (token, pair) finds the angle, and all
 // of the tokens' heads use it from shared memory.
@@ -56,11 +56,28 @@ struct Piece {
   }
 };
 
-// A thread's frequency as turns per token, in units of 2^-64 turns.
+// A thread's frequency as turns per token, in units of 2^-64 turns, wrapped.  1 / (2 pi) has
+// 128 bits behind the point, times a mantissa of 53: good to that unit for frequencies up to
+// 2^53, and by integers faster than the same by float64 (16384 tokens' 40 heads 59 us for
+// 57).  Larger ones, by sums of two float64: good to 2^-106 of themselves.
 __device__ __forceinline__ unsigned long long turn_of(double frequency) {
-  const double r = frequency * 0.15915494309189533577;  // 1 / (2 pi)
-  return static_cast<unsigned long long>(
-      static_cast<long long>(__double2ull_rd((r - floor(r)) * 18446744073709551616.0)));
+  constexpr unsigned long long kHigh = 0x28BE60DB9391054Aull, kLow = 0x7F09D5F47D4D3770ull;
+  const long long bits = __double_as_longlong(frequency);
+  const int exponent = static_cast<int>(bits >> 52 & 2047) - 1023;
+  unsigned long long turn;
+  if (exponent <= 52) {
+    const unsigned long long mantissa = (bits & ((1ll << 52) - 1)) | 1ll << 52;
+    const unsigned long long carry = __umul64hi(mantissa, kLow), part = mantissa * kHigh, low = part + carry;
+    const unsigned long long high = __umul64hi(mantissa, kHigh) + (low < part ? 1 : 0);
+    const int down = 52 - exponent;
+    turn = down >= 64 ? (down < 128 ? high >> (down - 64) : 0) : (low >> down | (down ? high << (64 - down) : 0));
+  } else {
+    constexpr double kUnits = 18446744073709551616.0;
+    const double x = fabs(frequency), a = x * 0.15915494309189535, b = fma(x, -9.839338337591243e-18, fma(x, 0.15915494309189535, -a));
+    turn = static_cast<unsigned long long>(__double2ll_rn((a - rint(a)) * kUnits)) +
+           static_cast<unsigned long long>(__double2ll_rn((b - rint(b)) * kUnits));
+  }
+  return bits < 0 ? 0 - turn : turn;
 }
 
 // Where a pair's angle is: neighbouring lanes take neighbouring pieces of kEach pairs, and

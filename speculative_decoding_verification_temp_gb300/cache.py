@@ -320,6 +320,7 @@ def _rotation_layout(dtype, shape, head_dim, interleaved, inverse, amplitude):
 
 def _rotation(frequency, head_dim, dev, interleaved, inverse, amplitude):
     _on(frequency, dev, "frequency")
+    _forward_only(frequency)
     turn = _abi.spec_rotation.from_buffer_copy(_rotation_layout(
         frequency.dtype, frequency.shape, head_dim, bool(interleaved), bool(inverse), float(amplitude)))
     if not frequency.is_contiguous():

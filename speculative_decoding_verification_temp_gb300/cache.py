@@ -234,6 +234,7 @@ def paged_attention(q, k_cache, v_cache, page_table, context_len, scale=None, nu
         tree_mask = tree_mask.contiguous()
         mask_stride = N * words if tree_mask.dim() == 3 else 0
     if position is not None:
+        _on(position, dev, "position")
         pos_stride = N if position.dim() == 2 else 0
         position = _ints(position, (B, N) if position.dim() == 2 else (N,), dev, "position")
     if out is None:
@@ -373,6 +374,7 @@ def _append(k_new, v_new, k_cache, v_cache, page_table, context_len, num_new, ro
         frequency, turn = _rotation(rotation[0], D, dev, rotation[1], False, rotation[2])
     pos_stride = 0
     if position is not None:
+        _on(position, dev, "position")
         pos_stride = N if position.dim() == 2 else 0
         position = _ints(position, (B, N) if position.dim() == 2 else (N,), dev, "position")
     page_table, table = _table(page_table, B, dev)

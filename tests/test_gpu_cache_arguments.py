@@ -27,3 +27,13 @@ def test_frequencies_that_require_gradients():
     assert not k.any() and not v.any()
     with torch.no_grad():
         assert torch.equal(sv.rotary(new[0], position, f), new[0])
+
+
+@pytest.mark.parametrize("position", [[0, 1], 0, torch.zeros(2, dtype=torch.int32)], ids=["list", "number", "cpu"])
+def test_positions_that_are_no_tensors_of_the_device(position):
+    k, v, new, table, ctx, f = setup()
+    with pytest.raises(ValueError):
+        sv.cache_append_rotary(*new, k, v, table, ctx, f, position=position)
+    with pytest.raises(ValueError):
+        sv.paged_attention(new[0], k, v, table, ctx, position=position)
+    assert not k.any() and not v.any()

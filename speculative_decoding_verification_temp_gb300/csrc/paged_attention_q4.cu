@@ -58,8 +58,10 @@ struct Rows4 {
   // of the queries: two operands a step, two for the sums, the factors; two steps a piece
   static constexpr int kQPieces = kSteps / 2 + 1;
   static constexpr int kQBytes = kQPieces * 32 * 16;
-  static constexpr int kDowns = 2 * kStage + kQBytes;  // usual_downs of the unit
-  static constexpr int kWarp = kDowns + 16;
+  // usual_downs of the unit; bring_near_one of the tile's keys
+  static constexpr int kDowns = 2 * kStage + kQBytes;
+  static constexpr int kBy = kDowns + 16;
+  static constexpr int kWarp = kBy + 4 * kQ4Tile;
   static constexpr int kSmem = kWarps * kWarp;
   static_assert(kCtas * (kSmem + 2048) <= 227 * 1024, "shared memory of an SM");
 };
@@ -397,14 +399,13 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
       }
       uint32_t downs = *unit_downs;
       const bool moved = __any_sync(0xFFFFFFFFu, far || downs != 0u);
-      int by = 0;  // of this lane's key
       if (moved) {
         // (where no row has a maximum the outputs so far are zeros, whatever they were times)
         if (__all_sync(0xFFFFFFFFu, m[0] == -INFINITY && m[1] == -INFINITY)) {
           downs = usual_downs(s);
           *unit_downs = downs;  // the same in every lane
         }
-        by = bring_near_one(s, downs);
+        reinterpret_cast<int *>(ring + L::kBy)[lane] = bring_near_one(s, downs);
       }
       if (masked || moved) {
         *scales = s;
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(Rows4<D, R>::kThreads, Rows4<D, R>::kCtas)
         for (int h = 0; h < kKeys; ++h) {
           back[h] = 1.f;
           if (moved) {
-            const int up = __shfl_sync(0xFFFFFFFFu, by, blk * 16 + key_of(h));
+            const int up = reinterpret_cast<int *>(ring + L::kBy)[blk * 16 + key_of(h)];
             y[2 * h] += static_cast<float>(up);
             y[2 * h + 1] += static_cast<float>(up);
             back[h] = __int_as_float((127 - up) << 23);

@@ -444,7 +444,8 @@ def cache_read(k_cache, v_cache, page_table, start, N, num=None, dtype=None, ret
 
 def cache_4bit(num_pages, page_size, num_heads, head_dim, num_layers=None, device="cuda"):
     """An empty cache of 4-bit rows: k and v, uint8 [(num_layers,) num_pages, page_size,
-    num_heads, head_dim / 2 + 16], with a head's tokens of a page one behind another."""
+    num_heads, head_dim / 2 + 16], with a head's tokens of a page one behind another: with
+    pages of a power of two tokens, the layout that attention reads fastest."""
     if head_dim not in (64, 128):
         raise ValueError("4-bit caches have head_dim 64 or 128")
     lead = (num_pages,) if num_layers is None else (num_layers, num_pages)
@@ -519,7 +520,7 @@ def rotary(x, position, frequency, interleaved=False, amplitude=1.0, inverse=Fal
 
     x [B, N, heads, D], [N, heads, D] or [heads, D], float32, bfloat16 or float16;
     position: integers of x's shape without its last two dimensions, or [N] for all
-    sequences.  frequency float64 [dim / 2], radians per token (rotary_frequency); the
+    sequences (beyond 32 bits: as their largest or smallest).  frequency float64 [dim / 2], radians per token (rotary_frequency); the
     values of a head behind the first dim are copied.  Pairs are (i, i + dim / 2), or
     interleaved (2i, 2i + 1).  amplitude: a factor of the rotated values.  inverse:
     turns back (with amplitude 1 the inverse, and the gradient).  out: where the

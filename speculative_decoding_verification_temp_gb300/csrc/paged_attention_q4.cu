@@ -27,10 +27,10 @@
 // group's usual scale.  The weights of 8 keys and 8 rows cross from the scores' layout to the
 // products' by one transposing move.
 //
-// Bound by instructions and the latencies between them: 680 for 32 keys and values, issued
+// Bound by instructions and the latencies between them: 690 for 32 keys and values, issued
 // in every second cycle by the three warps a scheduler has registers for (sixteen warps an
 // SM instead of twelve, with fewer registers: 179 us).  256 sequences of 1 to 4096 tokens,
-// one token each, 32/8 heads of 128: 155 us, 4.37 TB/s; the copies alone take 112.
+// one token each, 32/8 heads of 128: 158 us, 4.27 TB/s; the copies alone take 112.
 #include <algorithm>
 
 #include "q4_copies.cuh"
@@ -116,7 +116,8 @@ constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;  // nibbles of two h
 // The products of weights and scales are float16, so a key's scales are brought near one, and
 // its weight times the same power of two takes their place in the row's running maximum:
 // neither small scales nor a key of large ones costs the other keys' weights their bits.
-// Tiles of scales within [1/128, 2) stay as they are (others cost 85 instructions more).
+// Tiles of scales within [1/128, 2) stay as they are (others take 180 us where those take 161:
+// one token at B = 256, 1 to 4096 tokens).
 
 // Not zero where a scale lies outside of [1/128, 2): its exponent field outside of 8 to 15.
 __device__ __forceinline__ uint32_t scale_far(uint32_t pair) { return (pair ^ 0x2000u) & 0x6000u; }

@@ -14,7 +14,7 @@
 // Bound by the turns of making, scores, softmax and outputs, not by a unit of the SM
 // (issue slots 0.33, tensor pipe 0.23 active).  A tile of 128 keys of one unit of eight
 // tokens (32/8 heads of 128, B = 64, 1..4096 tokens: 118 us) takes about 3200 cycles, without
-// its making 2700; of a pair (60-node trees, B = 32: 121 us) 4900, without it 4700.
+// its making 2700; of a pair (60-node trees, B = 32: 119 us) 4900, without it 4700.
 #include "q4_copies.cuh"
 
 namespace sv {
